@@ -92,8 +92,13 @@ typedef enum muon_kernel_kind {
   MUON_K_ADAM = 6,       /* DistAdam update of non-matrix parameters            */
   MUON_K_FUSED_NS = 7,   /* all NS rounds, one CTA pair per matrix, 64<=m<=256,
                             n<=512 (see muon_set_fused_ns)                      */
-  MUON_K_ROUNDS = 8      /* all Gram/Poly/Update stages of every round in one
+  MUON_K_ROUNDS = 8,     /* all Gram/Poly/Update stages of every round in one
                             persistent launch (see muon_set_persistent_rounds)  */
+  MUON_K_NORM_ROPE = 9,      /* norm and rotation of the query and key heads    */
+  MUON_K_NORM_ROPE_BWD = 10, /* its gradients                                   */
+  MUON_K_ATTENTION = 11,     /* attention, forward                              */
+  MUON_K_ATTENTION_DQ = 12,  /* attention, gradient of the queries              */
+  MUON_K_ATTENTION_DKV = 13  /* attention, gradients of the keys and values     */
 } muon_kernel_kind;
 
 /* Workspace bytes for one muon_step()/muon_ns5() call on [batch, rows, cols].
@@ -231,6 +236,114 @@ typedef struct muon_adam_tensor {
 muon_status muon_adam_step(const muon_adam_tensor* tensors, int n_tensors, int step, float lr,
                            float beta1, float beta2, float eps, float weight_decay,
                            void* stream);
+
+/*
+ * The attention path of a GPT block, the block whose c_q, c_k, c_v and proj
+ * weights muon_step trains: the norm and rotation of the query and key heads,
+ * and the attention itself, each with its gradients.  The pages name the model
+ * ([MCS] section 2.1) and print none of this; it is an addition.
+ *
+ * Heads are passed as strided views, so that the columns of a fused q, k, v
+ * projection's output (and of its gradient) are used in place: element d of
+ * head h of token t lies at data[t token_stride + h head_stride + d].  Strides
+ * are in elements.  data and both strides are 16-byte aligned (a stride whose
+ * dimension has one entry is ignored); rows of different (t, h) do not overlap
+ * in an output.  head_dim is a multiple of 8.
+ */
+typedef struct muon_heads {
+  void* data;
+  long long token_stride;
+  long long head_stride;
+} muon_heads;
+
+/*
+ * For every token t and head x of q (q_heads of them) and of k (k_heads):
+ *   n = x (mean_d x_d^2 + eps)^-1/2 w     (norm != 0; w = 1 where the weight is
+ *                                          NULL; n = x where norm == 0)
+ *   y_a = n_a c_i - n_b s_i,  y_b = n_b c_i + n_a s_i   for the pairs
+ *         i < rot_dim / 2: (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ *         interleaved != 0; elements from rot_dim on pass unrotated,
+ * with c_i, s_i row positions[t] (t itself where positions is NULL) of the
+ * tables cos, sin ([table_len, rot_dim / 2] fp32, contiguous).  Scalings for
+ * long contexts are a matter of the tables.  A position outside the tables
+ * makes the token's outputs NaN.  All in fp32, rounded once to the outputs' type.
+ */
+typedef struct muon_norm_rope {
+  int dtype;               /* muon_dtype of every muon_heads of the call          */
+  int tokens;              /* >= 0; tokens (q_heads + k_heads) < 2^31             */
+  int q_heads, k_heads;    /* 0..65535, not both 0 (the views of none are unused) */
+  int head_dim;            /* multiple of 8, 8..256                               */
+  int rot_dim;             /* multiple of 8, 0..head_dim                          */
+  int norm, interleaved;   /* 0 or 1                                              */
+  float eps;               /* finite, >= 0                                        */
+  int table_len;           /* rows of cos and sin, >= 1 if rot_dim > 0            */
+  const float* cos;        /* 16-byte aligned; unused if rot_dim == 0             */
+  const float* sin;
+  const int* positions;    /* [tokens] or NULL                                    */
+  const float* q_weight;   /* [head_dim] or NULL; NULL if norm == 0; 16-byte      */
+  const float* k_weight;   /*   aligned                                           */
+} muon_norm_rope;
+
+muon_status muon_qk_norm_rope(const muon_norm_rope* spec, muon_heads q, muon_heads k,
+                              muon_heads q_out, muon_heads k_out, void* stream);
+
+/*
+ * Gradients of muon_qk_norm_rope: dq, dk (the inputs') from dq_out, dk_out (the
+ * outputs'), and the weights' in fp32 where the weight is given (dq_weight and
+ * dk_weight are then required: [head_dim], overwritten).  Sums over tokens and
+ * heads are taken in a fixed order: repeated calls give equal bits.
+ */
+size_t muon_norm_rope_workspace_bytes(int head_dim);
+muon_status muon_qk_norm_rope_backward(const muon_norm_rope* spec, muon_heads dq_out,
+                                       muon_heads dk_out, muon_heads q, muon_heads k,
+                                       muon_heads dq, muon_heads dk, float* dq_weight,
+                                       float* dk_weight, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * Causal attention over sequences packed along the tokens.  Sequence s holds the
+ * tokens cu_seqlens[s] <= t < cu_seqlens[s + 1] (n_seqs + 1 ascending int32 on the
+ * device, from 0 to at most `tokens`; empty sequences are allowed; NULL with
+ * n_seqs = 0: one sequence of all tokens).  Query head h reads key/value head
+ * h / (q_heads / kv_heads).  For token i of a sequence that starts at a:
+ *   s_ij = scale q_i . k_j,  a <= j <= i;   lse_i = log sum_j exp(s_ij)
+ *   out_i = sum_j exp(s_ij - lse_i) v_j
+ * Tokens past the last sequence get out = 0 and lse = -inf, and no gradient.
+ * A token's results depend on its own sequence's tokens up to it alone: Inf or
+ * NaN elsewhere does not reach them.  Offsets that do not ascend give undefined
+ * results (no access leaves the tensors).
+ * bf16 heads; products in bf16 with fp32 sums, softmax in fp32; the weights
+ * exp(s_ij - m) are rounded to bf16 for their product with v.
+ */
+typedef struct muon_attention_spec {
+  int tokens;              /* >= 0; tokens q_heads < 2^31                         */
+  int q_heads, kv_heads;   /* 1..65535; q_heads a multiple of kv_heads            */
+  int head_dim;            /* multiple of 8, 8..128                               */
+  int n_seqs;              /* >= 0                                                */
+  const int* cu_seqlens;   /* [n_seqs + 1] device memory, or NULL                 */
+  float scale;             /* finite, > 0                                         */
+} muon_attention_spec;
+
+/* Workspace bytes of muon_attention and muon_attention_backward; 0 if invalid. */
+size_t muon_attention_workspace_bytes(int tokens, int q_heads, int kv_heads, int head_dim);
+
+/* out: bf16 heads (q_heads of them); lse: [q_heads, tokens] fp32, natural log. */
+muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_heads k,
+                           muon_heads v, muon_heads out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of muon_attention's out with respect to q, k and v, from its out and
+ * lse.  With delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
+ *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
+ * (dk and dv summed over the query heads that share the key/value head, in fp32).
+ * Fixed summation order, no atomics: repeated calls give equal bits.
+ */
+muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads dout,
+                                    muon_heads q, muon_heads k, muon_heads v, muon_heads out,
+                                    const float* lse, muon_heads dq, muon_heads dk,
+                                    muon_heads dv, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /*
  * Path selection (no counterpart on the pages).  With enable = 1 (the default)

@@ -11,11 +11,16 @@ Entry points mirror the C ABI:
   step(p, g, buf, ...)           one Muon step on a stack of same-shape weights
   step_grouped([(p, g, buf)...]) one Muon step on every group of a model
   adam_step([(p, g, m, v)...])   one DistAdam step on the non-matrix parameters
+  qk_norm_rope(q, k, cos, sin)   RMS norm and rotary positions of the query and key heads
+  attention(q, k, v, cu_seqlens) causal attention over packed sequences, grouped heads
+with qk_norm_rope_backward and attention_backward for their gradients.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -28,6 +33,8 @@ __all__ = [
     "kernel_launch_count", "trace_begin", "trace_end",
     "set_fused_ns", "fused_ns", "set_persistent_rounds", "persistent_rounds",
     "set_streamed_apply", "streamed_apply", "KERNEL_KINDS",
+    "ROPE_EPS", "rope_tables", "qk_norm_rope", "qk_norm_rope_backward",
+    "norm_rope_workspace_bytes", "attention", "attention_backward", "attention_workspace_bytes",
 ]
 
 # Quintic coefficients and rounds as printed in "Muon Custom Sizing 实战", section 2.3.
@@ -41,7 +48,8 @@ ADAM_BETAS = (0.8, 0.95)
 ADAM_EPS = 1e-8
 
 KERNEL_KINDS = {0: "prologue", 1: "small_ns", 2: "gram", 3: "poly", 4: "update", 5: "apply",
-                6: "adam", 7: "fused_ns", 8: "rounds"}
+                6: "adam", 7: "fused_ns", 8: "rounds", 9: "norm_rope", 10: "norm_rope_backward",
+                11: "attention", 12: "attention_dq", 13: "attention_dkv"}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "timeout",
            5: "workspace"}
 
@@ -71,6 +79,26 @@ class _AdamTensor(ctypes.Structure):
                 ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("numel", ctypes.c_longlong), ("g_dtype", ctypes.c_int),
                 ("lr_scale", ctypes.c_float), ("wd_scale", ctypes.c_float)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class _NormRope(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("tokens", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("k_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("norm", ctypes.c_int), ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
+                ("table_len", ctypes.c_int), ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class _AttentionSpec(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("cu_seqlens", ctypes.c_void_p), ("scale", ctypes.c_float)]
 
 
 class _TraceRecord(ctypes.Structure):
@@ -111,6 +139,19 @@ def load_library():
     L.muon_selftest_wait_timeout.restype = ci
     L.muon_adam_step.argtypes = [ctypes.POINTER(_AdamTensor), ci, ci, cf, cf, cf, cf, cf, vp]
     L.muon_adam_step.restype = ci
+    rope, spec, hd = ctypes.POINTER(_NormRope), ctypes.POINTER(_AttentionSpec), _Heads
+    L.muon_qk_norm_rope.argtypes = [rope, hd, hd, hd, hd, vp]
+    L.muon_qk_norm_rope.restype = ci
+    L.muon_norm_rope_workspace_bytes.argtypes = [ci]
+    L.muon_norm_rope_workspace_bytes.restype = sz
+    L.muon_qk_norm_rope_backward.argtypes = [rope, hd, hd, hd, hd, hd, hd, vp, vp, vp, sz, vp]
+    L.muon_qk_norm_rope_backward.restype = ci
+    L.muon_attention_workspace_bytes.argtypes = [ci, ci, ci, ci]
+    L.muon_attention_workspace_bytes.restype = sz
+    L.muon_attention.argtypes = [spec, hd, hd, hd, hd, vp, vp, sz, vp]
+    L.muon_attention.restype = ci
+    L.muon_attention_backward.argtypes = [spec, hd, hd, hd, hd, hd, vp, hd, hd, hd, vp, sz, vp]
+    L.muon_attention_backward.restype = ci
     L.muon_set_persistent_rounds.argtypes = [ci]
     L.muon_set_persistent_rounds.restype = ci
     L.muon_set_fused_ns.argtypes = [ci]
@@ -388,6 +429,253 @@ def adam_step(tensors, step: int, *, lr: float = ADAM_LR, betas=ADAM_BETAS, eps:
     """One DistAdam update, in place, of every (param, grad, exp_avg, exp_avg_sq[, lr_scale
     [, wd_scale]]) entry at step count `step` (>= 1)."""
     AdamStep(tensors, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)(step, stream)
+
+
+# ------------------------------------------------------------ attention path
+ROPE_EPS = 1e-6
+
+
+def rope_tables(length: int, rot_dim: int, *, base: float = 10000.0, scale: float = 1.0,
+                device=None):
+    """cos and sin of the angles (position / scale) base^(-2i / rot_dim), i < rot_dim / 2, for
+    the positions 0..length-1: two [length, rot_dim / 2] fp32 tensors.  scale > 1 spreads the
+    angles of a context it times as long over the trained range."""
+    inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / max(1, rot_dim))
+    ang = (torch.arange(length, dtype=torch.float64) / scale)[:, None] * inv[None, :]
+    device = device if device is not None else "cuda"
+    return ang.cos().float().to(device), ang.sin().float().to(device)
+
+
+def _head_view(t: torch.Tensor, name: str, like=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along head_dim")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    return t
+
+
+def _shaped(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _plain(t, name: str, device, dtype, shape=None):
+    """A contiguous tensor argument of one dtype (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _heads(t: torch.Tensor) -> _Heads:
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """Makes `device` and the stream of the call current, so that what the call allocates
+    belongs to that stream; yields the stream's handle."""
+    if stream is None and device.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream(device).cuda_stream
+        return
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+_stream_ws = {}
+
+
+def _stream_workspace(ws, need: int, device, handle: int) -> Workspace:
+    """The caller's workspace, or one kept for each device and stream: calls on different
+    streams may overlap, and must not share one."""
+    if ws is not None:
+        return ws
+    key = (device.index, handle)
+    w = _stream_ws.get(key)
+    if w is None or w.nbytes < need:
+        w = _stream_ws[key] = Workspace(need, device)
+    return w
+
+
+def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
+    _head_view(q, "q")
+    _head_view(k, "k", q)
+    if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"q and k must agree in tokens and head_dim, got {tuple(q.shape)} and "
+                         f"{tuple(k.shape)}")
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError("cos and sin must be [length, rot_dim / 2] of one shape")
+    t, hq, d = q.shape
+    dev = q.device
+    _plain(cos, "cos", dev, torch.float32)
+    _plain(sin, "sin", dev, torch.float32)
+    _plain(positions, "positions", dev, torch.int32, (t,))
+    _plain(q_weight, "q_weight", dev, torch.float32, (d,))
+    _plain(k_weight, "k_weight", dev, torch.float32, (d,))
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to the norm: norm=False takes none")
+    dtype = {torch.float32: 0, torch.bfloat16: 1}.get(q.dtype)
+    if dtype is None:
+        raise TypeError(f"q and k must be float32 or bfloat16, got {q.dtype}")
+    return _NormRope(dtype, t, hq, k.shape[1], d, 2 * cos.shape[1], int(bool(norm)),
+                     int(bool(interleaved)), eps, cos.shape[0], cos.data_ptr(), sin.data_ptr(),
+                     _ptr(positions), _ptr(q_weight), _ptr(k_weight))
+
+
+def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None,
+                 norm: bool = True, eps: float = ROPE_EPS, interleaved: bool = False,
+                 q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim]
+    (bf16 or fp32, strided along tokens and heads), times q_weight / k_weight ([head_dim] fp32),
+    then the rotation of its first 2 * cos.shape[1] elements by rows `positions` (int32; the
+    token's index when None) of the tables cos, sin (see rope_tables).  Pairs are (i, i + half),
+    or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves."""
+    L = load_library()
+    spec = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    with _launch_on(q.device, stream) as handle:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _shaped(_head_view(q_out, "q_out", q), "q_out", q)
+        _shaped(_head_view(k_out, "k_out", q), "k_out", k)
+        _raise(L.muon_qk_norm_rope(spec, _heads(q), _heads(k), _heads(q_out), _heads(k_out),
+                                   handle), "muon_qk_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_workspace_bytes(head_dim: int) -> int:
+    return int(load_library().muon_norm_rope_workspace_bytes(head_dim))
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_weight=None,
+                          positions=None, norm: bool = True, eps: float = ROPE_EPS,
+                          interleaved: bool = False, dq=None, dk=None,
+                          workspace: Workspace | None = None, stream=None):
+    """Gradients of qk_norm_rope: from those of its outputs, and its inputs, returns (dq, dk,
+    dq_weight, dk_weight); the weights' are fp32, and None where no weight is given."""
+    L = load_library()
+    spec = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    _shaped(_head_view(dq_out, "dq_out", q), "dq_out", q)
+    _shaped(_head_view(dk_out, "dk_out", q), "dk_out", k)
+    with _launch_on(q.device, stream) as handle:
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _shaped(_head_view(dq, "dq", q), "dq", q)
+        _shaped(_head_view(dk, "dk", q), "dk", k)
+        dqw = torch.empty_like(q_weight) if q_weight is not None else None
+        dkw = torch.empty_like(k_weight) if k_weight is not None else None
+        ws = _stream_workspace(workspace, L.muon_norm_rope_workspace_bytes(q.shape[2]), q.device,
+                               handle)
+        _raise(L.muon_qk_norm_rope_backward(
+            spec, _heads(dq_out), _heads(dk_out), _heads(q), _heads(k), _heads(dq), _heads(dk),
+            _ptr(dqw), _ptr(dkw), ws.ptr, ws.nbytes, handle), "muon_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+def attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load_library().muon_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
+
+
+def _attention_spec(q, k, v, cu_seqlens, scale):
+    _head_view(q, "q")
+    _head_view(k, "k", q)
+    _shaped(_head_view(v, "v", q), "v", k)
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q, k and v must be bfloat16, got {q.dtype}")
+    t, hq, d = q.shape
+    hk = k.shape[1]
+    if k.shape[0] != t or k.shape[2] != d:
+        raise ValueError(f"q and k must agree in tokens and head_dim, got {tuple(q.shape)} and "
+                         f"{tuple(k.shape)}")
+    if hk == 0 or hq == 0 or hq % hk:
+        raise ValueError(f"q heads ({hq}) must be a multiple of k heads ({hk})")
+    n_seqs = 0
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [sequences + 1]")
+        _plain(cu_seqlens, "cu_seqlens", q.device, torch.int32)
+        n_seqs = cu_seqlens.numel() - 1
+    return _AttentionSpec(t, hq, hk, d, n_seqs, _ptr(cu_seqlens),
+                          1.0 / math.sqrt(d) if scale is None else scale)
+
+
+def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None, lse=None,
+              workspace: Workspace | None = None, stream=None):
+    """Causal attention of bf16 heads over sequences packed along the tokens: q [tokens, q_heads,
+    head_dim], k and v [tokens, kv_heads, head_dim] (strided along tokens and heads), cu_seqlens
+    int32 [sequences + 1] on the device (None: one sequence).  scale is 1 / sqrt(head_dim) when
+    None.  Returns (out, lse): out like q, lse [q_heads, tokens] fp32.  Tokens past the last
+    sequence get out 0 and lse -inf."""
+    L = load_library()
+    spec = _attention_spec(q, k, v, cu_seqlens, scale)
+    with _launch_on(q.device, stream) as handle:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((spec.q_heads, spec.tokens), dtype=torch.float32, device=q.device)
+        _shaped(_head_view(out, "out", q), "out", q)
+        _plain(lse, "lse", q.device, torch.float32, (spec.q_heads, spec.tokens))
+        ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
+            spec.tokens, spec.q_heads, spec.kv_heads, spec.head_dim), q.device, handle)
+        _raise(L.muon_attention(spec, _heads(q), _heads(k), _heads(v), _heads(out),
+                                lse.data_ptr(), ws.ptr, ws.nbytes, handle), "muon_attention")
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float | None = None,
+                       dq=None, dk=None, dv=None, workspace: Workspace | None = None,
+                       stream=None):
+    """Gradients of attention's out: from dout, the inputs, and its out and lse, returns (dq, dk,
+    dv) in bf16 (dk and dv summed over the query heads of a group)."""
+    L = load_library()
+    spec = _attention_spec(q, k, v, cu_seqlens, scale)
+    _shaped(_head_view(dout, "dout", q), "dout", q)
+    _shaped(_head_view(out, "out", q), "out", q)
+    _plain(lse, "lse", q.device, torch.float32, (spec.q_heads, spec.tokens))
+    with _launch_on(q.device, stream) as handle:
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        if dv is None:
+            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
+            _shaped(_head_view(t, name, q), name, like)
+        ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
+            spec.tokens, spec.q_heads, spec.kv_heads, spec.head_dim), q.device, handle)
+        _raise(L.muon_attention_backward(
+            spec, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
+            _heads(dq), _heads(dk), _heads(dv), ws.ptr, ws.nbytes, handle),
+            "muon_attention_backward")
+    return dq, dk, dv
 
 
 def workspace_status(workspace: Workspace, clear: bool = False, stream=None) -> int:

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <functional>
+
 #include "../../include/muon_gb300.h"
 
 namespace muon {
@@ -29,6 +31,7 @@ enum DeviceError : unsigned int {
   kErrTimeoutFused = 16u,
   kErrTimeoutDepend = 32u,
   kErrTimeoutApply = 64u,
+  kErrTimeoutAttention = 128u,
 };
 
 // What the prologue computes from (g, buf).
@@ -256,6 +259,46 @@ struct AdamLaunch {
   float beta1, beta2, eps;
 };
 
+// ---- attention path (norm_rope.cu, attention*.cu, attention_api.cu)
+// Heads as strided views (element strides), as in muon_heads.
+template <typename T>
+struct Heads {
+  T* p;
+  long long ts, hs;
+  __host__ __device__ __forceinline__ T* row(int t, int h) const {
+    return p + t * ts + h * hs;
+  }
+};
+
+constexpr int kRopeMaxDim = 256;
+constexpr int kRopeMaxBlocks = 608;   // partial sums of the weights' gradients
+
+struct NormRopeLaunch {
+  Heads<void> x[2], y[2], dy[2];    // [0] queries, [1] keys; backward: y is dx
+  const float* w[2];
+  float* dw[2];
+  int heads[2];
+  int tokens, dim, rot, norm, interleaved, bf16;
+  int table_len;
+  float eps;
+  const float *cos, *sin;
+  const int* pos;
+  float* parts;                     // backward: [blocks][2][dim]
+  unsigned int* ticket;             // backward: zero before and after the launch
+  const unsigned int* status;
+};
+
+struct AttentionLaunch {
+  Heads<const __nv_bfloat16> q, k, v, o, dout;
+  Heads<__nv_bfloat16> out, dq, dk, dv;
+  float* lse;                       // [hq, T]
+  float* stats;                     // backward workspace
+  const int* cu;
+  int n_seqs, T, hq, hk, group, dim;
+  float scale;
+  unsigned int* status;
+};
+
 // Launchers (defined next to their kernels).  Each returns a cudaError_t from
 // the launch; grid sizes come from the caller's SM count.
 // The prologue may be launched as a programmatic dependent of the kernel
@@ -281,6 +324,19 @@ cudaError_t launch_adam(const AdamLaunch& l, int blocks, cudaStream_t s);
 // dependent of the kernel before it (the prologue), whose output it reads
 // after griddepcontrol.wait.
 cudaError_t launch_fused(const FusedLaunch& l, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeLaunch& l, bool backward, int sms, cudaStream_t s);
+cudaError_t launch_attention(const AttentionLaunch& l, cudaStream_t s);
+cudaError_t launch_attention_dq(const AttentionLaunch& l, cudaStream_t s);
+cudaError_t launch_attention_dkv(const AttentionLaunch& l, cudaStream_t s);
+
+// Host services of muon_api.cu for the other entry points' files.
+// Runs `fn` (which launches one kernel), counting and tracing it.
+cudaError_t counted_launch(cudaStream_t st, int kind, double flops, double bytes,
+                           const std::function<cudaError_t()>& fn);
+// SM count of the current device; MUON_ERR_UNSUPPORTED unless it is sm_103a.
+muon_status device_sms(int* sms);
+constexpr size_t kStatusBytes = 256;  // status block at the start of a workspace
+
 int adam_blocks_per_sm();  // resident Adam blocks per SM on the current device (0 on error)
 
 // muon_step whose workspace's sticky error word is cleared on the stream after

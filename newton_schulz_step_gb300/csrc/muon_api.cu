@@ -183,7 +183,6 @@ struct GPlan {
   int ctr = 0;  // first per-matrix completion counter (rounds kernel, streamed write)
 };
 
-constexpr size_t kStatusBytes = 256;
 constexpr int kMaxDim = 65536;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -849,6 +848,13 @@ muon_status step_clearing_status(float* params, const void* grads, int g_dtype,
     return MUON_ERR_CUDA;
   }
 }
+
+cudaError_t counted_launch(cudaStream_t st, int kind, double flops, double bytes,
+                           const std::function<cudaError_t()>& fn) {
+  return tracked_launch(st, {kind, -1, flops, bytes}, fn);
+}
+
+muon_status device_sms(int* sms) { return current_device(sms); }
 
 }  // namespace muon
 

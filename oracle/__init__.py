@@ -19,3 +19,4 @@ from .muon_oracle import (  # noqa: F401
     rescale_factor,
 )
 from .adam_oracle import ADAM_BETAS, ADAM_EPS, ADAM_LR, adam_step  # noqa: F401,E402
+from . import attention_oracle  # noqa: F401,E402

@@ -1,0 +1,173 @@
+"""Host-only checks of the attention path's C entry points and of the binding: refusals
+before anything is enqueued, workspace sizes."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+import newton_schulz_step_gb300 as muon
+
+OK, INVALID, UNSUPPORTED, CUDA, TIMEOUT, WORKSPACE = range(6)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(muon.library_path()):
+        from newton_schulz_step_gb300 import build
+        build.build()
+    return muon.load_library()
+
+
+def _view(data=0x1000, ts=512, hs=64):
+    return muon._Heads(data, ts, hs)
+
+
+def _rope_spec(**kw):
+    a = dict(dtype=1, tokens=16, q_heads=8, k_heads=4, head_dim=64, rot_dim=64, norm=1,
+             interleaved=0, eps=1e-6, table_len=16, cos=0x1000, sin=0x2000, positions=None,
+             q_weight=None, k_weight=None)
+    a.update(kw)
+    return muon._NormRope(*[a[n] for n, _ in muon._NormRope._fields_])
+
+
+ROPE_BAD = [dict(dtype=2), dict(tokens=-1), dict(q_heads=-1), dict(q_heads=0, k_heads=0),
+            dict(q_heads=70000), dict(head_dim=0), dict(head_dim=60), dict(head_dim=264),
+            dict(rot_dim=-8), dict(rot_dim=72), dict(rot_dim=20), dict(norm=2),
+            dict(interleaved=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(table_len=0),
+            dict(table_len=15), dict(cos=None), dict(sin=None), dict(cos=0x1004),
+            dict(q_weight=0x1004), dict(norm=0, q_weight=0x1000), dict(norm=0, k_weight=0x1000)]
+VIEW_BAD = [dict(data=None), dict(data=0x1008), dict(ts=0), dict(ts=-512), dict(ts=516),
+            dict(hs=4), dict(hs=0), dict(hs=-64)]
+
+
+@pytest.mark.parametrize("kw", ROPE_BAD)
+def test_norm_rope_refuses_a_bad_spec(lib, kw):
+    v = _view()
+    assert lib.muon_qk_norm_rope(_rope_spec(**kw), v, v, v, v, None) == INVALID
+    assert lib.muon_qk_norm_rope_backward(_rope_spec(**kw), v, v, v, v, v, v, None, None, 0x10000,
+                                          1 << 30, None) == INVALID
+
+
+@pytest.mark.parametrize("at", range(4))
+@pytest.mark.parametrize("kw", VIEW_BAD)
+def test_norm_rope_refuses_a_bad_view(lib, at, kw):
+    views = [_view() for _ in range(4)]
+    views[at] = _view(**kw)
+    assert lib.muon_qk_norm_rope(_rope_spec(), *views, None) == INVALID
+
+
+def test_norm_rope_refuses_overlapping_output_rows(lib):
+    v = _view()
+    # heads 64 apart but tokens only 256 apart: 8 heads of one token span 512
+    assert lib.muon_qk_norm_rope(_rope_spec(), v, v, _view(ts=256), v, None) == INVALID
+    assert lib.muon_qk_norm_rope(_rope_spec(), v, v, _view(hs=32), v, None) == INVALID
+    # [heads, tokens, dim] storage is fine (refused later here, for want of a GPU)
+    if not torch.cuda.is_available():
+        assert lib.muon_qk_norm_rope(_rope_spec(), v, v, _view(ts=64, hs=1024), v, None) in (
+            UNSUPPORTED, CUDA)
+
+
+def test_norm_rope_sizes(lib):
+    v = _view()
+    assert lib.muon_qk_norm_rope(None, v, v, v, v, None) == INVALID
+    assert lib.muon_qk_norm_rope(_rope_spec(tokens=0), v, v, v, v, None) == OK
+    assert lib.muon_qk_norm_rope(_rope_spec(tokens=2 ** 31 - 1, table_len=2 ** 31 - 1), v, v, v, v,
+                                 None) == UNSUPPORTED
+    assert lib.muon_norm_rope_workspace_bytes(64) == 256 + 640 * 2 * 64 * 4
+    for bad in (0, -8, 12, 264):
+        assert lib.muon_norm_rope_workspace_bytes(bad) == 0
+
+
+def test_norm_rope_backward_needs_its_workspace_and_gradients(lib):
+    v = _view()
+
+    def call(spec, dqw=None, dkw=None, ws=0x10000, n=1 << 30):
+        return lib.muon_qk_norm_rope_backward(spec, v, v, v, v, v, v, dqw, dkw, ws, n, None)
+
+    assert call(_rope_spec(), ws=None) == WORKSPACE
+    assert call(_rope_spec(), ws=0x10010) == WORKSPACE
+    assert call(_rope_spec(), n=4096) == WORKSPACE
+    # a weight and its gradient come together
+    assert call(_rope_spec(q_weight=0x1000)) == INVALID
+    assert call(_rope_spec(), dkw=0x1000) == INVALID
+
+
+def _attn_spec(**kw):
+    a = dict(tokens=16, q_heads=8, kv_heads=4, head_dim=64, n_seqs=2, cu_seqlens=0x1000,
+             scale=0.125)
+    a.update(kw)
+    return muon._AttentionSpec(*[a[n] for n, _ in muon._AttentionSpec._fields_])
+
+
+def _attn(lib, spec, views=None, lse=0x1000, ws=0x10000, n=1 << 30):
+    views = views or [_view()] * 4
+    return lib.muon_attention(spec, *views, lse, ws, n, None)
+
+
+def _attn_back(lib, spec, views=None, lse=0x1000, ws=0x10000, n=1 << 30):
+    w = views or [_view()] * 8
+    return lib.muon_attention_backward(spec, *w[:5], lse, *w[5:], ws, n, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(tokens=-1), dict(q_heads=0), dict(kv_heads=0), dict(kv_heads=3), dict(q_heads=70000),
+    dict(head_dim=0), dict(head_dim=60), dict(head_dim=136), dict(n_seqs=-1),
+    dict(cu_seqlens=None), dict(cu_seqlens=0x1002), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(tokens=2 ** 31 - 1)])
+def test_attention_refuses_a_bad_spec(lib, kw):
+    assert _attn(lib, _attn_spec(**kw)) == INVALID
+    assert _attn_back(lib, _attn_spec(**kw)) == INVALID
+
+
+@pytest.mark.parametrize("kw", VIEW_BAD)
+def test_attention_refuses_a_bad_view(lib, kw):
+    for at in range(4):
+        views = [_view() for _ in range(4)]
+        views[at] = _view(**kw)
+        assert _attn(lib, _attn_spec(), views) == INVALID
+    for at in range(8):
+        views = [_view() for _ in range(8)]
+        views[at] = _view(**kw)
+        assert _attn_back(lib, _attn_spec(), views) == INVALID
+
+
+def test_attention_refuses_overlap_lse_and_workspace(lib):
+    v, bad = _view(), _view(ts=256)
+    assert _attn(lib, _attn_spec(), [v, v, v, bad]) == INVALID
+    assert _attn_back(lib, _attn_spec(), [v] * 5 + [bad, v, v]) == INVALID
+    assert _attn(lib, _attn_spec(), lse=None) == INVALID
+    assert _attn_back(lib, _attn_spec(), lse=0x1004) == INVALID
+    for call in (_attn, _attn_back):
+        assert call(lib, None) == INVALID
+        assert call(lib, _attn_spec(), ws=None) == WORKSPACE
+        assert call(lib, _attn_spec(), ws=0x10010) == WORKSPACE
+        assert call(lib, _attn_spec(), n=128) == WORKSPACE
+        assert call(lib, _attn_spec(tokens=0)) == OK
+
+
+def test_attention_workspace_bytes(lib):
+    f = lib.muon_attention_workspace_bytes
+    assert f(0, 8, 4, 64) >= 256
+    assert f(1000, 8, 4, 64) <= f(2000, 8, 4, 64)
+    for bad in ((-1, 8, 4, 64), (10, 8, 3, 64), (10, 0, 0, 64), (10, 8, 4, 65), (10, 8, 4, 256)):
+        assert f(*bad) == 0
+
+
+def test_binding_refuses_cpu_tensors(lib):
+    q = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
+    c = torch.zeros(4, 32)
+    with pytest.raises(ValueError):
+        muon.attention(q, q, q)
+    with pytest.raises(ValueError):
+        muon.qk_norm_rope(q, q, c, c)
+
+
+def test_rope_tables_scale_the_positions():
+    c1, s1 = muon.rope_tables(64, 16, device="cpu")
+    c2, s2 = muon.rope_tables(256, 16, scale=4.0, device="cpu")
+    assert c1.shape == (64, 8) and c1.dtype == torch.float32
+    assert torch.equal(c2[::4], c1) and torch.equal(s2[::4], s1)
+    assert torch.equal(c1[0], torch.ones(8)) and torch.equal(s1[0], torch.zeros(8))
+    assert ctypes.sizeof(muon._Heads) == 24
