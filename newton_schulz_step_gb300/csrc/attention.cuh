@@ -1,5 +1,6 @@
 // attention.cuh -- what the attention kernels share: the sequence that a token
-// belongs to, and one row of each result computed by a warp from its definition.
+// belongs to, shared-memory tiles, bounded waits, and one row of each result
+// computed by a warp from its definition.
 #pragma once
 
 #include "internal.h"
@@ -9,6 +10,15 @@ namespace muon {
 namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBlock = 128;            // rows of a tile (keys or queries)
+constexpr uint32_t kSlab = 16384;      // 128 rows x 64 bf16, 128-byte swizzle
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // First token and end (one past the last token) of the sequence that holds token i,
 // or an empty range for a token past the last sequence.  Clamped around i, so that
@@ -27,7 +37,115 @@ __device__ __forceinline__ Span sequence_of(const AttentionLaunch& L, int i) {
   return {min(max(__ldg(L.cu + lo), 0), i), min(max(__ldg(L.cu + lo + 1), i + 1), L.T)};
 }
 
+// Tokens that belong to a sequence: those past them are padding.
+__device__ __forceinline__ int tokens_in_use(const AttentionLaunch& L) {
+  return L.cu == nullptr ? L.T : min(max(__ldg(L.cu + L.n_seqs), 0), L.T);
+}
+
+// ---- bounded waits ------------------------------------------------------
+// Every wait of a CTA goes through its abort flag and the workspace's status word:
+// a wait that gives up sets both, which ends the waits of the CTA's other roles.
+struct Guard {
+  volatile int* bad;
+  unsigned int* status;
+  unsigned int role;                     // DeviceError bit of the waiting role
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+    return ptx::mbar_wait(bar, parity, bad, status);
+  }
+  __device__ __forceinline__ void fail() const {
+    if (!*bad) atomicOr(status, kErrTimeoutAttention | role);
+    *bad = 1;
+  }
+  // One thread's wait; records a failure.
+  __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity) const {
+    if (wait(bar, parity)) return true;
+    fail();
+    return false;
+  }
+  // A whole warp's wait (the lanes agree on the result).
+  __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) const {
+    const bool ok = __all_sync(0xffffffffu, wait(bar, parity));
+    if (!ok) fail();
+    return ok;
+  }
+};
+// What a role still has in flight when it gives up is waited for, within this limit.
+constexpr uint64_t kDrainNs = 100ull * 1000ull * 1000ull;
+
+// Registers move from the warps that only issue work to those that compute: a block of
+// 384 threads is launched with 168 each (64512), of which 4 warps keep kIssueRegs and 8
+// get kComputeRegs.  The issuing roles must fit kIssueRegs as compiled without the split
+// (they take at most 64): below that the compiler's allocation was seen to break (waits
+// ran into their limit with 40).
+constexpr int kThreads = 384;
+constexpr int kIssueRegs = 72, kComputeRegs = 216;
+static_assert(128 * kIssueRegs + 256 * kComputeRegs == kThreads * 168,
+              "no more registers than at launch");
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+}
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+}
+
+// ---- tiles --------------------------------------------------------------
+// A tile is 128 rows of one head in DP / 64 slabs of 64 columns, 128-byte swizzle:
+// as a matrix operand it can be read along the head (K-major: 16 columns a step) or
+// along its rows (MN-major: 16 rows a step).
+template <int DP>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row,
+                                          uint64_t* bar) {
+  ptx::mbar_arrive_expect_tx(bar, DP / 64 * kSlab);
+#pragma unroll
+  for (int s = 0; s < DP / 64; ++s) ptx::tma_load_3d(dst + s * kSlab, map, 64 * s, head, row, bar);
+}
+// Operand descriptors (ptx::smem_desc_sw128) with the tile's address added last, so that
+// the steps of a product differ by a constant.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int step) {   // 16 columns from 16 step
+  return ptx::smem_desc_sw128(0, 16, 1024) +
+         ((tile + (step >> 2) * kSlab + (step & 3) * 32) >> 4);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int step) {  // 16 rows from 16 step
+  return ptx::smem_desc_sw128(0, kSlab, 1024) + ((tile + step * 2048) >> 4);
+}
+// The address, computed where it is used: descriptors of every tile kept over a whole
+// loop would cost the issuing role its registers.
+__device__ __forceinline__ uint32_t here(uint32_t tile) {
+  asm volatile("" : "+r"(tile));
+  return tile;
+}
+// byte offset of 8 elements (row, column 8 c) of a tile
+__device__ __forceinline__ uint32_t tile_off(int row, int c) {
+  return static_cast<uint32_t>(c >> 3) * kSlab + static_cast<uint32_t>(row) * 128u +
+         ((static_cast<uint32_t>(c & 7) ^ static_cast<uint32_t>(row & 7)) << 4);
+}
+// Zeroes row `row` of a tile: padding may hold anything, and zero weights do not stop
+// Inf or NaN in a product.  (fence_proxy_async_smem before the product reads it.)
+template <int DP>
+__device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
+#pragma unroll
+  for (int c = 0; c < DP / 8; ++c)
+    *reinterpret_cast<uint4*>(tile + tile_off(row, c)) = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+// 32 fp32 values as bf16 into columns 8 c .. 8 c + 31 of a row
+__device__ __forceinline__ void store_row32(uint8_t* tile, int row, int c, const float (&f)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(tile + tile_off(row, c + q)) =
+        make_uint4(pack2(f[8 * q], f[8 * q + 1]), pack2(f[8 * q + 2], f[8 * q + 3]),
+                   pack2(f[8 * q + 4], f[8 * q + 5]), pack2(f[8 * q + 6], f[8 * q + 7]));
+}
+
 // ---- rows by definition -------------------------------------------------
+// A matrix product over a tile multiplies invisible pairs by a weight of zero, and
+// zero times Inf or NaN is NaN.  A result row that is not finite is therefore
+// computed again from its visible pairs alone, by one warp: rows that depend on a
+// non-finite value stay non-finite, the others lose what leaked into them.  Nothing
+// of this runs on finite data.
 // A lane holds the elements 2 lane, 2 lane + 1 of each 64-element half of a head.
 struct Row { float v[4]; };
 
@@ -60,25 +178,32 @@ __device__ __forceinline__ void axpy(Row& acc, float f, const Row& x) {
   for (int j = 0; j < 4; ++j) acc.v[j] = fmaf(f, x.v[j], acc.v[j]);
 }
 
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const Row& r, int dim) {
+// Every element of the row is NaN: further terms cannot change it.
+__device__ __forceinline__ bool all_nan(const Row& r, int dim) {
   const int lane = threadIdx.x & 31;
+  bool n = true;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int d = 64 * h + 2 * lane;
-    if (d < dim)
-      *reinterpret_cast<__nv_bfloat162*>(p + d) =
-          __floats2bfloat162_rn(r.v[2 * h], r.v[2 * h + 1]);
-  }
+  for (int j = 0; j < 4; ++j) n &= 64 * (j >> 1) + 2 * lane >= dim || isnan(r.v[j]);
+  return __all_sync(0xffffffffu, n);
 }
 
-// Output row i of query head h (and its log-sum-exp) over the keys begin..i.
-__device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int i, int begin,
-                                    float* lse) {
+// The row as bf16 into row `row` of a shared-memory tile.
+__device__ __forceinline__ void put_row(uint8_t* tile, int row, const Row& r, int slabs) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (h < slabs)
+      *reinterpret_cast<uint32_t*>(tile + tile_off(row, 8 * h + (lane >> 2)) + 4 * (lane & 3)) =
+          pack2(r.v[2 * h], r.v[2 * h + 1]);
+}
+
+// Output row i of query head h over the keys begin..i.
+static __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int i, int begin) {
   const int kh = h / L.group;
   const Row q = load_row(L.q.row(i, h), L.dim);
   Row acc = {{0.f, 0.f, 0.f, 0.f}};
   float m = -INFINITY, l = 0.f;
-  for (int j = begin; j <= i; ++j) {
+  for (int j = i; j >= begin && !all_nan(acc, L.dim); --j) {
     const float s = L.scale * dot_row(q, load_row(L.k.row(j, kh), L.dim));
     const float mn = fmaxf(m, s);
     const float base = mn == -INFINITY ? 0.f : mn;
@@ -89,7 +214,6 @@ __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int i, int 
     axpy(acc, p, load_row(L.v.row(j, kh), L.dim));
     m = mn;
   }
-  *lse = l == 0.f ? -INFINITY : m + logf(l);
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc.v[e] *= inv;
@@ -97,14 +221,14 @@ __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int i, int 
 }
 
 // Query gradient row i of head h.
-__device__ __noinline__ Row dq_row(const AttentionLaunch& L, int h, int i, int begin) {
+static __device__ __noinline__ Row dq_row(const AttentionLaunch& L, int h, int i, int begin) {
   const int kh = h / L.group;
   const Row q = load_row(L.q.row(i, h), L.dim);
   const Row g = load_row(L.dout.row(i, h), L.dim);
   const float delta = dot_row(g, load_row(L.o.row(i, h), L.dim));
   const float lse = L.lse[static_cast<size_t>(h) * L.T + i];
   Row acc = {{0.f, 0.f, 0.f, 0.f}};
-  for (int j = begin; j <= i; ++j) {
+  for (int j = i; j >= begin && !all_nan(acc, L.dim); --j) {
     const Row k = load_row(L.k.row(j, kh), L.dim);
     const float p = __expf(L.scale * dot_row(q, k) - lse);
     axpy(acc, p * (dot_row(g, load_row(L.v.row(j, kh), L.dim)) - delta), k);
@@ -115,13 +239,13 @@ __device__ __noinline__ Row dq_row(const AttentionLaunch& L, int h, int i, int b
 }
 
 // Key and value gradient rows j of key head kh, over the queries j..end-1 of its group.
-__device__ __noinline__ void dkv_row(const AttentionLaunch& L, int kh, int j, int end, Row& dk,
+static __device__ __noinline__ void dkv_row(const AttentionLaunch& L, int kh, int j, int end, Row& dk,
                                      Row& dv) {
   const Row k = load_row(L.k.row(j, kh), L.dim);
   const Row v = load_row(L.v.row(j, kh), L.dim);
   dk = dv = {{0.f, 0.f, 0.f, 0.f}};
   for (int h = kh * L.group; h < (kh + 1) * L.group; ++h)
-    for (int i = j; i < end; ++i) {
+    for (int i = j; i < end && !(all_nan(dk, L.dim) && all_nan(dv, L.dim)); ++i) {
       const Row q = load_row(L.q.row(i, h), L.dim);
       const Row g = load_row(L.dout.row(i, h), L.dim);
       const float delta = dot_row(g, load_row(L.o.row(i, h), L.dim));

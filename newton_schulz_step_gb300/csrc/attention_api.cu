@@ -255,11 +255,15 @@ muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_h
     L.v = view<const __nv_bfloat16>(v);
     L.out = view<__nv_bfloat16>(out);
     L.lse = lse;
+    AttentionMaps M;
+    if (!heads_tmap(&M.q, q, L.T, L.hq, L.dim) || !heads_tmap(&M.k, k, L.T, L.hk, L.dim) ||
+        !heads_tmap(&M.v, v, L.T, L.hk, L.dim) || !heads_tmap(&M.out, out, L.T, L.hq, L.dim))
+      return MUON_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double heads = 2.0 * L.T * (2.0 * L.hq + 2.0 * L.hk) * L.dim;
     const cudaError_t e =
         counted_launch(st, MUON_K_ATTENTION, 4.0 * L.dim * pair_bound(L), heads,
-                       [&] { return launch_attention(L, st); });
+                       [&] { return launch_attention(M, L, st); });
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   } catch (...) {
     return MUON_ERR_CUDA;

@@ -299,6 +299,12 @@ struct AttentionLaunch {
   unsigned int* status;
 };
 
+// Tensor maps of the heads as (head_dim, heads, tokens), boxes of 64 x 1 x 128 with
+// 128-byte swizzle; columns past head_dim and tokens past the last read as zero.
+struct AttentionMaps {
+  CUtensorMap q, k, v, out;           // forward
+};
+
 // Launchers (defined next to their kernels).  Each returns a cudaError_t from
 // the launch; grid sizes come from the caller's SM count.
 // The prologue may be launched as a programmatic dependent of the kernel
@@ -325,7 +331,7 @@ cudaError_t launch_adam(const AdamLaunch& l, int blocks, cudaStream_t s);
 // after griddepcontrol.wait.
 cudaError_t launch_fused(const FusedLaunch& l, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeLaunch& l, bool backward, int sms, cudaStream_t s);
-cudaError_t launch_attention(const AttentionLaunch& l, cudaStream_t s);
+cudaError_t launch_attention(const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s);
 cudaError_t launch_attention_dq(const AttentionLaunch& l, cudaStream_t s);
 cudaError_t launch_attention_dkv(const AttentionLaunch& l, cudaStream_t s);
 
@@ -333,6 +339,8 @@ cudaError_t launch_attention_dkv(const AttentionLaunch& l, cudaStream_t s);
 // Runs `fn` (which launches one kernel), counting and tracing it.
 cudaError_t counted_launch(cudaStream_t st, int kind, double flops, double bytes,
                            const std::function<cudaError_t()>& fn);
+// Tensor map of bf16 heads (see AttentionMaps); false if the driver refuses it.
+bool heads_tmap(CUtensorMap* tm, const muon_heads& v, int tokens, int heads, int dim);
 // SM count of the current device; MUON_ERR_UNSUPPORTED unless it is sm_103a.
 muon_status device_sms(int* sms);
 constexpr size_t kStatusBytes = 256;  // status block at the start of a workspace

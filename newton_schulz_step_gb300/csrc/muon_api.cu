@@ -854,6 +854,20 @@ cudaError_t counted_launch(cudaStream_t st, int kind, double flops, double bytes
   return tracked_launch(st, {kind, -1, flops, bytes}, fn);
 }
 
+bool heads_tmap(CUtensorMap* tm, const muon_heads& v, int tokens, int heads, int dim) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(v.head_stride) * 2,
+                                 static_cast<cuuint64_t>(v.token_stride) * 2};
+  const cuuint32_t box[3] = {64u, 1u, 128u}, estr[3] = {1u, 1u, 1u};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.data, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 muon_status device_sms(int* sms) { return current_device(sms); }
 
 }  // namespace muon
