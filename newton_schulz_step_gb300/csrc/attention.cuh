@@ -140,6 +140,11 @@ __device__ __forceinline__ void store_row32(uint8_t* tile, int row, int c, const
                    pack2(f[8 * q + 4], f[8 * q + 5]), pack2(f[8 * q + 6], f[8 * q + 7]));
 }
 
+// 64 consecutive TMEM columns
+__device__ __forceinline__ void load64(uint32_t t, uint32_t (&a)[2][32]) {
+  ptx::tmem_ld32x2_sync(t, t + 32, a[0], a[1]);
+}
+
 // ---- rows by definition -------------------------------------------------
 // A matrix product over a tile multiplies invisible pairs by a weight of zero, and
 // zero times Inf or NaN is NaN.  A result row that is not finite is therefore

@@ -132,7 +132,10 @@ bool attention_shape_ok(int tokens, int hq, int hk, int dim) {
          hq % hk == 0 && dim >= 8 && dim <= 128 && dim % 8 == 0 && 1ll * tokens * hq <= INT_MAX;
 }
 
-size_t attention_workspace(int, int) { return kStatusBytes; }
+// Status block, then per query head and 128 tokens: 128 log-sum-exps, 128 deltas.
+size_t attention_workspace(int tokens, int hq) {
+  return kStatusBytes + static_cast<size_t>(hq) * ((tokens + 127) / 128) * 1024;
+}
 
 muon_status attention_launch(AttentionLaunch& L, const muon_attention_spec* s, void* ws,
                              size_t ws_bytes) {
@@ -301,15 +304,22 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
     L.dk = view<__nv_bfloat16>(dk);
     L.dv = view<__nv_bfloat16>(dv);
     L.lse = const_cast<float*>(lse);
+    L.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+    AttentionMaps M;
+    if (!heads_tmap(&M.q, q, L.T, L.hq, L.dim) || !heads_tmap(&M.k, k, L.T, L.hk, L.dim) ||
+        !heads_tmap(&M.v, v, L.T, L.hk, L.dim) || !heads_tmap(&M.dout, dout, L.T, L.hq, L.dim) ||
+        !heads_tmap(&M.dq, dq, L.T, L.hq, L.dim) || !heads_tmap(&M.dk, dk, L.T, L.hk, L.dim) ||
+        !heads_tmap(&M.dv, dv, L.T, L.hk, L.dim))
+      return MUON_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double row = 2.0 * L.T * L.dim;
     cudaError_t e = counted_launch(
         st, MUON_K_ATTENTION_DQ, 6.0 * L.dim * pair_bound(L), row * (4.0 * L.hq + 2.0 * L.hk),
-        [&] { return launch_attention_dq(L, st); });
+        [&] { return launch_attention_dq(M, L, st); });
     if (e != cudaSuccess) return MUON_ERR_CUDA;
     e = counted_launch(st, MUON_K_ATTENTION_DKV, 8.0 * L.dim * pair_bound(L),
                        row * (2.0 * L.hq + 4.0 * L.hk),
-                       [&] { return launch_attention_dkv(L, st); });
+                       [&] { return launch_attention_dkv(M, L, st); });
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   } catch (...) {
     return MUON_ERR_CUDA;

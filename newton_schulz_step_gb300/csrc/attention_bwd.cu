@@ -1,53 +1,680 @@
 // attention_bwd.cu -- gradients of causal attention over packed sequences with grouped
-// key/value heads: one warp computes one row from the definition.
+// key/value heads, on the tensor cores.
+//
+// With p_ij = exp(scale q_i . k_j - lse_i) and delta_i = dout_i . out_i,
+//   ds_ij = p_ij (dout_i . v_j - delta_i),
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i.
+// Two kernels, each of which holds its sums in TMEM from the first block to the last:
+// one owns 128 queries and walks their keys (dq), one owns 128 keys and walks their
+// queries, over all query heads of the group (dk, dv).  S and dP are computed in both:
+// seven products a block instead of five.  In return nothing is added in global memory:
+// no fp32 dq buffer of 2 x (4 + 4) bytes an element and key block to move, no atomics,
+// the same bits in every run.
+// p and ds are rounded to bf16, the tensor cores' input; everything else is fp32.
+//
+// 384 threads: warps 0-3 and 4-7 compute, warp 8 issues the copies, warp 9 the products.
+// A compute thread owns a row (TMEM lane) of S and dP, warps 0-3 its columns 0-63, warps
+// 4-7 its columns 64-127.  P and dS overwrite S or dP as bf16 pairs, each half within its
+// own columns, and are the A operand of the accumulating product from there.
 #include "attention.cuh"
 
 namespace muon {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kWarps = kRowThreads / 32;
+using namespace attn;
 
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const attn::Row& r, int dim) {
-  const int lane = threadIdx.x & 31;
-  for (int h = 0; h < 2; ++h)
-    if (64 * h + 2 * lane < dim)
-      *reinterpret_cast<uint32_t*>(p + 64 * h + 2 * lane) =
-          attn::pack2(r.v[2 * h], r.v[2 * h + 1]);
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr uint32_t kStatBytes = 1024;      // a block's 128 log-sum-exps and 128 deltas
+
+__device__ __forceinline__ void compute_barrier() {   // the 256 compute threads
+  asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kRowThreads)
-    attention_dq_kernel(const __grid_constant__ AttentionLaunch L) {
-  if (ptx::status_set(L.status)) return;
-  const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (w >= static_cast<long long>(L.T) * L.hq) return;
-  const int i = static_cast<int>(w / L.hq), h = static_cast<int>(w % L.hq);
-  store_row(L.dq.row(i, h), attn::dq_row(L, h, i, attn::sequence_of(L, i).begin), L.dim);
+// Address of step i (16 columns of A) of the bf16 pairs that the two halves of the
+// compute threads left at `t` and `t + 64`.
+__device__ __forceinline__ uint32_t a_step(uint32_t t, int i) {
+  return t + (i < 4 ? 8 * i : 64 + 8 * (i - 4));
 }
 
-__global__ void __launch_bounds__(kRowThreads)
-    attention_dkv_kernel(const __grid_constant__ AttentionLaunch L) {
-  if (ptx::status_set(L.status)) return;
-  const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (w >= static_cast<long long>(L.T) * L.hk) return;
-  const int j = static_cast<int>(w / L.hk), kh = static_cast<int>(w % L.hk);
-  attn::Row dk, dv;
-  attn::dkv_row(L, kh, j, attn::sequence_of(L, j).end, dk, dv);
-  store_row(L.dk.row(j, kh), dk, L.dim);
-  store_row(L.dv.row(j, kh), dv, L.dim);
+// D (+)= A B^T over the head: both tiles K-major
+template <int DP>
+__device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t kId = ptx::idesc_bf16(128, 128, false);
+  a = here(a);
+  b = here(b);
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) ptx::mma_bf16(d, desc_k(a, i), desc_k(b, i), kId, i > 0);
+}
+// D += A[tmem] B over the 128 rows of B
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+  constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
+  b = here(b);
+#pragma unroll
+  for (int i = 0; i < kBlock / 16; ++i)
+    ptx::mma_bf16_ts(d, a_step(a, i), desc_mn(b, i), kId, accumulate || i > 0);
 }
 
-int blocks_for(long long rows) { return static_cast<int>((rows + kWarps - 1) / kWarps); }
+// ------------------------------------------------------------------ dq
+// TMEM: S of even and odd blocks (0, 128), dP (256), dq (384).  Per block, in the
+// tensor cores' order: dP of the next block, dq += dS K, S of the block after next; so
+// the exponentials of a block run beside the products of the one before.
+template <int DP> struct DqCfg {
+  static constexpr uint32_t kTile = DP / 64 * kSlab;
+  static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
+  static constexpr uint32_t kDo = kTile, kKRing = 2 * kTile, kVRing = kKRing + kK * kTile;
+  static constexpr uint32_t kMisc = kVRing + kV * kTile;
+  static constexpr uint32_t kSmem = kMisc + 1536 + 1024;
+};
+
+struct DqMisc {
+  uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], dp_full, ds_full, dq_full, drain;
+  uint32_t tmem;
+  int bad, skip;
+  int first, last;                 // begin of the tile's first and last row
+  unsigned int repair[4];          // rows to compute again, by warp of the tile
+  float delta[2][128];             // halves of delta
+};
+static_assert(sizeof(DqMisc) <= 1536, "misc block");
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dq_kernel(const __grid_constant__ AttentionMaps M,
+                        const __grid_constant__ AttentionLaunch L) {
+  using C = DqCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  DqMisc& X = *reinterpret_cast<DqMisc*>(sm + C::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // the last tiles hold the most keys: they go first
+  const int tiles = (L.T + 127) / 128;
+  const int h = static_cast<int>(blockIdx.x) % L.hq;
+  const int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
+  const int row0 = 128 * tile, kh = h / L.group;
+
+  if (tid < 2) {
+    const int b = sequence_of(L, tid ? min(row0 + 127, L.T - 1) : row0).begin;
+    if (tid) X.last = b;
+    else X.first = b;
+  }
+  if (tid < 4) X.repair[tid] = 0;
+  if (warp == kProducerWarp && lane == 0) {
+    ptx::mbar_init(&X.q_full, 2);
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(&X.k_full[s], 1);
+      ptx::mbar_init(&X.k_empty[s], 1);
+      ptx::mbar_init(&X.v_full[s], 1);
+      ptx::mbar_init(&X.v_empty[s], 1);
+    }
+    ptx::mbar_init(&X.s_full[0], 1);
+    ptx::mbar_init(&X.s_full[1], 1);
+    ptx::mbar_init(&X.dp_full, 1);
+    ptx::mbar_init(&X.ds_full, 8);
+    ptx::mbar_init(&X.dq_full, 1);
+    ptx::mbar_init(&X.drain, 1);
+    X.bad = 0;
+    X.skip = ptx::status_set(L.status);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&M.q);
+    ptx::prefetch_tmap(&M.dout);
+    ptx::prefetch_tmap(&M.k);
+    ptx::prefetch_tmap(&M.v);
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&X.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = X.tmem;
+  const Guard guard{&X.bad, L.status,
+                    warp == kProducerWarp ? kErrTimeoutProducer
+                    : warp == kMmaWarp    ? kErrTimeoutMma
+                                          : kErrTimeoutEpilogue};
+  const bool run = !X.skip;
+  const int begin = X.first / kBlock, n = tile + 1 - begin;     // key blocks
+
+  if (warp >= kProducerWarp) {
+    registers_down();
+    if (run && warp == kProducerWarp) {
+      if (lane == 0) {
+        load_tile<DP>(sm, &M.q, h, row0, &X.q_full);
+        load_tile<DP>(sm + C::kDo, &M.dout, h, row0, &X.q_full);
+        int j = 0;
+        bool ok = true;
+        for (; j < n && ok; ++j) {
+          const int ks = j % C::kK, vs = j % C::kV, row = (begin + j) * kBlock;
+          if (j >= C::kK) ok = guard.wait_or_fail(&X.k_empty[ks], (j / C::kK - 1) & 1);
+          if (!ok) break;
+          load_tile<DP>(sm + C::kKRing + ks * C::kTile, &M.k, kh, row, &X.k_full[ks]);
+          if (j >= C::kV) ok = guard.wait_or_fail(&X.v_empty[vs], (j / C::kV - 1) & 1);
+          if (!ok) break;
+          load_tile<DP>(sm + C::kVRing + vs * C::kTile, &M.v, kh, row, &X.v_full[vs]);
+        }
+        if (!ok) {                       // copies in flight land before the CTA ends
+          ptx::mbar_wait(&X.q_full, 0, nullptr, nullptr, kDrainNs);
+          for (int i = j > C::kK ? j - C::kK : 0; i <= j; ++i) {
+            ptx::mbar_wait(&X.k_full[i % C::kK], (i / C::kK) & 1, nullptr, nullptr, kDrainNs);
+            if (i < j)
+              ptx::mbar_wait(&X.v_full[i % C::kV], (i / C::kV) & 1, nullptr, nullptr, kDrainNs);
+          }
+        }
+      }
+    } else if (run && warp == kMmaWarp) {
+      if (lane == 0) {
+        const uint32_t base = ptx::smem_u32(sm);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          ok = ok && guard.wait_or_fail(bar, parity);
+          if (ok) ptx::tc_fence_after();
+          return ok;
+        };
+        auto scores = [&](int j) {
+          const int s = j % C::kK;
+          if (!wait(&X.k_full[s], (j / C::kK) & 1)) return;
+          mma_heads<DP>(tmem + 128 * (j & 1), base, base + C::kKRing + s * C::kTile);
+          ptx::mma_commit(&X.s_full[j & 1]);
+        };
+        auto dp = [&](int j) {
+          const int s = j % C::kV;
+          if (!wait(&X.v_full[s], (j / C::kV) & 1)) return;
+          mma_heads<DP>(tmem + 256, base + C::kDo, base + C::kVRing + s * C::kTile);
+          ptx::mma_commit(&X.dp_full);
+          ptx::mma_commit(&X.v_empty[s]);
+        };
+        wait(&X.q_full, 0);
+        if (ok) scores(0);
+        if (ok) dp(0);
+        if (ok && n > 1) scores(1);
+        for (int j = 0; j < n && ok; ++j) {
+          if (!wait(&X.ds_full, j & 1)) break;
+          if (j + 1 < n) dp(j + 1);
+          if (!ok) break;
+          const int s = j % C::kK;
+          mma_rows<DP>(tmem + 384, tmem + 128 * (j & 1), base + C::kKRing + s * C::kTile, j > 0);
+          ptx::mma_commit(&X.k_empty[s]);
+          if (j + 1 == n) ptx::mma_commit(&X.dq_full);
+          if (j + 2 < n) scores(j + 2);
+        }
+        if (!ok) {                       // products in flight end before TMEM is freed
+          ptx::mma_commit(&X.drain);
+          ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        }
+      }
+    }
+  } else {
+    registers_up();
+    if (run) {
+      const int half = warp >> 2, r = tid & 127, row = row0 + r;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const int used = tokens_in_use(L);
+      const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
+      const int last_begin = X.last;
+      const float c = L.scale * kLog2e;
+      // delta, half the columns each; lse in base 2, +inf (p = 0) for rows without keys
+      float delta = 0.f, lse2 = INFINITY;
+      if (row < used) {
+        const __nv_bfloat16 *o = L.o.row(row, h), *g = L.dout.row(row, h);
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          const int d = DP / 2 * half + 8 * i;
+          if (d < L.dim) {
+            const uint4 a = *reinterpret_cast<const uint4*>(o + d);
+            const uint4 b = *reinterpret_cast<const uint4*>(g + d);
+            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              delta = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), delta);
+              delta = fmaf(__uint_as_float(x[e] & 0xffff0000u),
+                           __uint_as_float(y[e] & 0xffff0000u), delta);
+            }
+          }
+        }
+        lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
+      }
+      X.delta[half][r] = delta;
+      compute_barrier();
+      delta = X.delta[0][r] + X.delta[1][r];
+      {
+        float* st = L.stats + (static_cast<size_t>(h) * tiles + tile) * 256 + r;
+        if (half == 0) st[0] = lse2;
+        else st[128] = delta;
+      }
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        const int k0 = (begin + j) * kBlock;
+        const bool masked = k0 < last_begin || j + 1 == n;
+        const int lo = row_begin - k0 - 64 * half, hi = row - k0 - 64 * half;
+        const uint32_t ts = tmem + lanes + 128 * (j & 1) + 64 * half;
+        ok = guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float p[64];
+        {
+          uint32_t s[2][32];
+          load64(ts, s);
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            p[i] = ex2(fmaf(__uint_as_float(s[i >> 5][i & 31]), c, -lse2));
+        }
+        ok = guard.warp_wait(&X.dp_full, j & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        {
+          uint32_t g[2][32];
+          load64(tmem + lanes + 256 + 64 * half, g);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(g[i >> 5][i & 31]) - delta;
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo || i > hi) p[i] = 0.f;
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+        ptx::tmem_st32(ts, w);
+        if (used < min(k0 + kBlock, L.T)) {            // the block holds padding: clear its K
+          const int s = j % C::kK;                     // (landed: S has read it)
+          if (half == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
+          ptx::fence_proxy_async_smem();
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+      }
+      if (ok) ok = guard.warp_wait(&X.dq_full, 0);
+      if (ok) {
+        ptx::tc_fence_after();
+        // Q has been read for the last time: dq goes through its place
+        float test = 0.f;                              // NaN if an element is not finite
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i) {
+          const int col = DP / 2 * half + 32 * i;
+          uint32_t o[32];
+          ptx::tmem_ld32_sync(tmem + lanes + 384 + col, o);
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            f[e] = __uint_as_float(o[e]) * L.scale;
+            test = fmaf(f[e], 0.f, test);
+          }
+          store_row32(sm, r, col / 8, f);
+        }
+        const unsigned int bad = __ballot_sync(0xffffffffu, row < used && test != 0.f);
+        if (bad && lane == 0) atomicOr(&X.repair[warp & 3], bad);
+      }
+      compute_barrier();                               // (reached by every compute thread)
+      if (ok) {
+        // each half of a row's elements may be bad alone: both warps of the rows look
+        // at the joint set and take every other row
+        unsigned int bad = X.repair[warp & 3] & (half ? 0xaaaaaaaau : 0x55555555u);
+        while (bad) {
+          const int src = __ffs(bad) - 1;
+          bad &= bad - 1;
+          put_row(sm, r - lane + src,
+                  dq_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
+                  DP / 64);
+        }
+        ptx::fence_proxy_async_smem();
+      }
+      compute_barrier();
+      if (ok && tid == 0 && !X.bad) {
+#pragma unroll
+        for (int i = 0; i < DP / 64; ++i)
+          ptx::tma_store_3d(&M.dq, 64 * i, h, row0, sm + i * kSlab);
+        ptx::bulk_commit();
+        ptx::bulk_wait<0>();
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dk, dv
+// Scores are transposed here (rows are keys): P^T and dS^T are A operands as they come,
+// without an exchange.  TMEM: S^T (0), dP^T (128), dv (256), dk (256 + DP).  Per block,
+// in the tensor cores' order: dv += P^T dO, S^T of the next block, dk += dS^T Q, dP^T of
+// the next block; so P of a block is computed beside the last two products of the one
+// before, and dS beside the first two of its own.
+template <int DP> struct DkvCfg {
+  static constexpr uint32_t kTile = DP / 64 * kSlab;
+  static constexpr int kStages = DP == 128 ? 2 : 4;          // of Q (with its stats) and dO
+  static constexpr uint32_t kV = kTile, kQRing = 2 * kTile, kDoRing = kQRing + kStages * kTile;
+  static constexpr uint32_t kStats = kDoRing + kStages * kTile;
+  static constexpr uint32_t kMisc = kStats + kStages * kStatBytes;
+  static constexpr uint32_t kSmem = kMisc + 512 + 1024;
+};
+
+struct DkvMisc {
+  uint64_t kv_full, q_full[4], q_empty[4], do_full[4], do_empty[4];
+  uint64_t s_full, dp_full, p_full, ds_full, done, drain;
+  uint32_t tmem;
+  int bad, skip;
+  int first_end, blocks;           // end of the first key's sequence; query blocks per head
+};
+static_assert(sizeof(DkvMisc) <= 512, "misc block");
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dkv_kernel(const __grid_constant__ AttentionMaps M,
+                         const __grid_constant__ AttentionLaunch L) {
+  using C = DkvCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  DkvMisc& X = *reinterpret_cast<DkvMisc*>(sm + C::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // the first tiles are seen by the most queries: they go first
+  const int tiles = (L.T + 127) / 128;
+  const int kh = static_cast<int>(blockIdx.x) % L.hk;
+  const int tile = static_cast<int>(blockIdx.x) / L.hk;
+  const int key0 = 128 * tile;
+
+  if (tid == 0) {
+    const int used = tokens_in_use(L);
+    int end = 0;
+    if (key0 < used) end = sequence_of(L, min(key0 + 127, used - 1)).end;
+    X.first_end = sequence_of(L, key0).end;
+    X.blocks = end > key0 ? (end - 1) / kBlock + 1 - tile : 0;
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    ptx::mbar_init(&X.kv_full, 2);
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(&X.q_full[s], 1);
+      ptx::mbar_init(&X.q_empty[s], 1);
+      ptx::mbar_init(&X.do_full[s], 1);
+      ptx::mbar_init(&X.do_empty[s], 1);
+    }
+    ptx::mbar_init(&X.s_full, 1);
+    ptx::mbar_init(&X.dp_full, 1);
+    ptx::mbar_init(&X.p_full, 8);
+    ptx::mbar_init(&X.ds_full, 8);
+    ptx::mbar_init(&X.done, 1);
+    ptx::mbar_init(&X.drain, 1);
+    X.bad = 0;
+    X.skip = ptx::status_set(L.status);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&M.q);
+    ptx::prefetch_tmap(&M.dout);
+    ptx::prefetch_tmap(&M.k);
+    ptx::prefetch_tmap(&M.v);
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&X.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = X.tmem;
+  const Guard guard{&X.bad, L.status,
+                    warp == kProducerWarp ? kErrTimeoutProducer
+                    : warp == kMmaWarp    ? kErrTimeoutMma
+                                          : kErrTimeoutEpilogue};
+  const bool run = !X.skip;
+  const int blocks = X.blocks, n = blocks * L.group;     // query blocks of all heads
+
+  if (warp >= kProducerWarp) {
+    registers_down();
+    if (run && n > 0 && warp == kProducerWarp) {
+      if (lane == 0) {
+        load_tile<DP>(sm, &M.k, kh, key0, &X.kv_full);
+        load_tile<DP>(sm + C::kV, &M.v, kh, key0, &X.kv_full);
+        int i = 0, h = kh * L.group, b = tile;
+        bool ok = true;
+        for (; i < n; ++i) {
+          const int s = i % C::kStages;
+          if (i >= C::kStages) ok = guard.wait_or_fail(&X.q_empty[s], (i / C::kStages - 1) & 1);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(&X.q_full[s], C::kTile + kStatBytes);
+#pragma unroll
+          for (int e = 0; e < DP / 64; ++e)
+            ptx::tma_load_3d(sm + C::kQRing + s * C::kTile + e * kSlab, &M.q, 64 * e, h,
+                             b * kBlock, &X.q_full[s]);
+          ptx::bulk_load(sm + C::kStats + s * kStatBytes,
+                         L.stats + (static_cast<size_t>(h) * tiles + b) * 256, kStatBytes,
+                         &X.q_full[s]);
+          if (i >= C::kStages) ok = guard.wait_or_fail(&X.do_empty[s], (i / C::kStages - 1) & 1);
+          if (!ok) break;
+          load_tile<DP>(sm + C::kDoRing + s * C::kTile, &M.dout, h, b * kBlock, &X.do_full[s]);
+          if (++b == tile + blocks) {
+            b = tile;
+            ++h;
+          }
+        }
+        if (!ok) {                       // copies in flight land before the CTA ends
+          ptx::mbar_wait(&X.kv_full, 0, nullptr, nullptr, kDrainNs);
+          for (int e = i > C::kStages ? i - C::kStages : 0; e <= i; ++e) {
+            const uint32_t parity = (e / C::kStages) & 1;
+            ptx::mbar_wait(&X.q_full[e % C::kStages], parity, nullptr, nullptr, kDrainNs);
+            if (e < i)
+              ptx::mbar_wait(&X.do_full[e % C::kStages], parity, nullptr, nullptr, kDrainNs);
+          }
+        }
+      }
+    } else if (run && n > 0 && warp == kMmaWarp) {
+      if (lane == 0) {
+        const uint32_t base = ptx::smem_u32(sm);
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          ok = ok && guard.wait_or_fail(bar, parity);
+          if (ok) ptx::tc_fence_after();
+          return ok;
+        };
+        auto scores = [&](int i) {
+          const int s = i % C::kStages;
+          if (!wait(&X.q_full[s], (i / C::kStages) & 1)) return;
+          mma_heads<DP>(tmem, base, base + C::kQRing + s * C::kTile);
+          ptx::mma_commit(&X.s_full);
+        };
+        auto dp = [&](int i) {
+          const int s = i % C::kStages;
+          if (!wait(&X.do_full[s], (i / C::kStages) & 1)) return;
+          mma_heads<DP>(tmem + 128, base + C::kV, base + C::kDoRing + s * C::kTile);
+          ptx::mma_commit(&X.dp_full);
+        };
+        wait(&X.kv_full, 0);
+        if (ok) scores(0);
+        if (ok) dp(0);
+        for (int i = 0; i < n && ok; ++i) {
+          const int s = i % C::kStages;
+          if (!wait(&X.p_full, i & 1)) break;
+          mma_rows<DP>(tmem + 256, tmem, base + C::kDoRing + s * C::kTile, i > 0);
+          ptx::mma_commit(&X.do_empty[s]);
+          if (i + 1 < n) scores(i + 1);
+          if (!ok || !wait(&X.ds_full, i & 1)) break;
+          mma_rows<DP>(tmem + 256 + DP, tmem + 128, base + C::kQRing + s * C::kTile, i > 0);
+          ptx::mma_commit(&X.q_empty[s]);
+          if (i + 1 == n) ptx::mma_commit(&X.done);
+          if (i + 1 < n) dp(i + 1);
+        }
+        if (!ok) {                       // products in flight end before TMEM is freed
+          ptx::mma_commit(&X.drain);
+          ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        }
+      }
+    }
+  } else {
+    registers_up();
+    if (run) {
+      const int half = warp >> 2, r = tid & 127, key = key0 + r;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const int used = tokens_in_use(L);
+      const int key_end = key < used ? sequence_of(L, key).end : key;
+      const int first_end = X.first_end;
+      const float c = L.scale * kLog2e;
+      bool ok = true;
+      int b = tile;
+      for (int i = 0; i < n; ++i) {
+        const int s = i % C::kStages, q0 = b * kBlock;
+        const bool masked = b == tile || q0 + kBlock > first_end;
+        const int lo = key - q0 - 64 * half, hi = key_end - q0 - 64 * half;   // lo <= col < hi
+        const uint32_t ts = tmem + lanes + 64 * half;
+        const float4* lse2 =
+            reinterpret_cast<const float4*>(sm + C::kStats + s * kStatBytes) + 16 * half;
+        const float4* delta = lse2 + 32;
+        ok = guard.warp_wait(&X.q_full[s], (i / C::kStages) & 1) &&   // the stats
+             guard.warp_wait(&X.s_full, i & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        float p[64];
+        {
+          uint32_t x[2][32];
+          load64(ts, x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 z = lse2[e];
+            const int a = e >> 3, o = 4 * (e & 7);
+            p[4 * e] = ex2(fmaf(__uint_as_float(x[a][o]), c, -z.x));
+            p[4 * e + 1] = ex2(fmaf(__uint_as_float(x[a][o + 1]), c, -z.y));
+            p[4 * e + 2] = ex2(fmaf(__uint_as_float(x[a][o + 2]), c, -z.z));
+            p[4 * e + 3] = ex2(fmaf(__uint_as_float(x[a][o + 3]), c, -z.w));
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < lo || e >= hi) p[e] = 0.f;
+        }
+        {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = pack2(p[2 * e], p[2 * e + 1]);
+          ptx::tmem_st32(ts, w);
+        }
+        if (used < min(q0 + kBlock, L.T)) {      // the block holds padding: clear its Q and dO
+          ok = guard.warp_wait(&X.do_full[s], (i / C::kStages) & 1);
+          if (!ok) break;
+          if (q0 + r >= used)
+            zero_row<DP>(sm + (half ? C::kDoRing : C::kQRing) + s * C::kTile, r);
+          ptx::fence_proxy_async_smem();
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&X.p_full);
+
+        ok = guard.warp_wait(&X.dp_full, i & 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        {
+          uint32_t x[2][32];
+          load64(ts + 128, x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 z = delta[e];
+            const int a = e >> 3, o = 4 * (e & 7);
+            p[4 * e] *= __uint_as_float(x[a][o]) - z.x;
+            p[4 * e + 1] *= __uint_as_float(x[a][o + 1]) - z.y;
+            p[4 * e + 2] *= __uint_as_float(x[a][o + 2]) - z.z;
+            p[4 * e + 3] *= __uint_as_float(x[a][o + 3]) - z.w;
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e < lo || e >= hi) p[e] = 0.f;
+        }
+        {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) w[e] = pack2(p[2 * e], p[2 * e + 1]);
+          ptx::tmem_st32(ts + 128, w);
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+        if (++b == tile + blocks) b = tile;
+      }
+      if (ok && n > 0) ok = guard.warp_wait(&X.done, 0);
+      if (ok) {
+        ptx::tc_fence_after();
+        // V and K have been read for the last time: dv goes through V's place (warps
+        // 0-3), dk through K's (warps 4-7)
+        uint8_t* stage = half ? sm : sm + C::kV;
+        const float f0 = half ? L.scale : 1.f;
+        float test = 0.f;                              // NaN if an element is not finite
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          uint32_t o[32];
+          ptx::tmem_ld32_sync(tmem + lanes + 256 + DP * half + 32 * i, o);
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            f[e] = key < used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+            test = fmaf(f[e], 0.f, test);
+          }
+          store_row32(stage, r, 4 * i, f);
+        }
+        __syncwarp();
+        unsigned int bad = __ballot_sync(0xffffffffu, key < used && test != 0.f);
+        while (bad) {
+          const int src = __ffs(bad) - 1;
+          bad &= bad - 1;
+          Row dk, dv;
+          dkv_row(L, kh, key - lane + src, __shfl_sync(0xffffffffu, key_end, src), dk, dv);
+          put_row(stage, r - lane + src, half ? dk : dv, DP / 64);
+        }
+        ptx::fence_proxy_async_smem();
+        if (half) asm volatile("bar.sync 2, 128;" ::: "memory");
+        else asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (r == 0) {
+#pragma unroll
+          for (int i = 0; i < DP / 64; ++i)
+            ptx::tma_store_3d(half ? &M.dk : &M.dv, 64 * i, kh, key0, stage + i * kSlab);
+          ptx::bulk_commit();
+          ptx::bulk_wait<0>();
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename K>
+cudaError_t launch(K kernel, int blocks, uint32_t smem, const AttentionMaps& m,
+                   const AttentionLaunch& l, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, kThreads, smem, s>>>(m, l);
+  return cudaGetLastError();
+}
+static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shared memory");
 
 }  // namespace
 
-cudaError_t launch_attention_dq(const AttentionLaunch& l, cudaStream_t s) {
-  attention_dq_kernel<<<blocks_for(1ll * l.T * l.hq), kRowThreads, 0, s>>>(l);
-  return cudaGetLastError();
+cudaError_t launch_attention_dq(const AttentionMaps& m, const AttentionLaunch& l,
+                                cudaStream_t s) {
+  const int blocks = (l.T + 127) / 128 * l.hq;
+  return l.dim <= 64 ? launch(attention_dq_kernel<64>, blocks, DqCfg<64>::kSmem, m, l, s)
+                     : launch(attention_dq_kernel<128>, blocks, DqCfg<128>::kSmem, m, l, s);
 }
-cudaError_t launch_attention_dkv(const AttentionLaunch& l, cudaStream_t s) {
-  attention_dkv_kernel<<<blocks_for(1ll * l.T * l.hk), kRowThreads, 0, s>>>(l);
-  return cudaGetLastError();
+
+cudaError_t launch_attention_dkv(const AttentionMaps& m, const AttentionLaunch& l,
+                                 cudaStream_t s) {
+  const int blocks = (l.T + 127) / 128 * l.hk;
+  return l.dim <= 64 ? launch(attention_dkv_kernel<64>, blocks, DkvCfg<64>::kSmem, m, l, s)
+                     : launch(attention_dkv_kernel<128>, blocks, DkvCfg<128>::kSmem, m, l, s);
 }
 
 }  // namespace muon

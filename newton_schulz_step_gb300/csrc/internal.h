@@ -292,7 +292,7 @@ struct AttentionLaunch {
   Heads<const __nv_bfloat16> q, k, v, o, dout;
   Heads<__nv_bfloat16> out, dq, dk, dv;
   float* lse;                       // [hq, T]
-  float* stats;                     // backward workspace
+  float* stats;                     // backward workspace: [hq][ceil(T / 128)][2][128]
   const int* cu;
   int n_seqs, T, hq, hk, group, dim;
   float scale;
@@ -302,7 +302,9 @@ struct AttentionLaunch {
 // Tensor maps of the heads as (head_dim, heads, tokens), boxes of 64 x 1 x 128 with
 // 128-byte swizzle; columns past head_dim and tokens past the last read as zero.
 struct AttentionMaps {
-  CUtensorMap q, k, v, out;           // forward
+  CUtensorMap q, k, v;
+  CUtensorMap out;                    // forward
+  CUtensorMap dout, dq, dk, dv;       // backward
 };
 
 // Launchers (defined next to their kernels).  Each returns a cudaError_t from
@@ -332,8 +334,10 @@ cudaError_t launch_adam(const AdamLaunch& l, int blocks, cudaStream_t s);
 cudaError_t launch_fused(const FusedLaunch& l, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeLaunch& l, bool backward, int sms, cudaStream_t s);
 cudaError_t launch_attention(const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s);
-cudaError_t launch_attention_dq(const AttentionLaunch& l, cudaStream_t s);
-cudaError_t launch_attention_dkv(const AttentionLaunch& l, cudaStream_t s);
+cudaError_t launch_attention_dq(const AttentionMaps& m, const AttentionLaunch& l,
+                                cudaStream_t s);
+cudaError_t launch_attention_dkv(const AttentionMaps& m, const AttentionLaunch& l,
+                                 cudaStream_t s);
 
 // Host services of muon_api.cu for the other entry points' files.
 // Runs `fn` (which launches one kernel), counting and tracing it.
