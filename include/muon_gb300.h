@@ -270,7 +270,7 @@ typedef struct muon_heads {
  */
 typedef struct muon_norm_rope {
   int dtype;               /* muon_dtype of every muon_heads of the call          */
-  int tokens;              /* >= 0; tokens (q_heads + k_heads) < 2^31             */
+  int tokens;              /* >= 0; tokens (q_heads + k_heads) < 2^31 - 2^16      */
   int q_heads, k_heads;    /* 0..65535, not both 0 (the views of none are unused) */
   int head_dim;            /* multiple of 8, 8..256                               */
   int rot_dim;             /* multiple of 8, 0..head_dim                          */
@@ -316,7 +316,7 @@ muon_status muon_qk_norm_rope_backward(const muon_norm_rope* spec, muon_heads dq
  * exp(s_ij - m) are rounded to bf16 for their product with v.
  */
 typedef struct muon_attention_spec {
-  int tokens;              /* >= 0; tokens q_heads < 2^31                         */
+  int tokens;              /* >= 0; tokens q_heads < 2^31 - 2^16                  */
   int q_heads, kv_heads;   /* 1..65535; q_heads a multiple of kv_heads            */
   int head_dim;            /* multiple of 8, 8..128                               */
   int n_seqs;              /* >= 0                                                */

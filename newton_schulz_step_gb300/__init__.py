@@ -446,66 +446,81 @@ def rope_tables(length: int, rot_dim: int, *, base: float = 10000.0, scale: floa
     return ang.cos().float().to(device), ang.sin().float().to(device)
 
 
-def _head_view(t: torch.Tensor, name: str, like=None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _cuda_device(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _refuse_heads(t, name, shape, dtype, device):
+    """Says what is wrong with a [tokens, heads, head_dim] argument."""
+    _cuda_device(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name} must be contiguous along head_dim")
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return t
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous along head_dim")
 
 
-def _shaped(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    return t
+def _heads(t, name: str, shape, dtype, device) -> _Heads:
+    """The view of a [tokens, heads, head_dim] tensor of the given shape, dtype and device."""
+    if t.dtype is not dtype or t.device != device or t.shape != shape or len(shape) != 3:
+        _refuse_heads(t, name, shape, dtype, device)
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        _refuse_heads(t, name, shape, dtype, device)
+    return _Heads(t.data_ptr(), st, sh)
 
 
-def _plain(t, name: str, device, dtype, shape=None):
-    """A contiguous tensor argument of one dtype (None passes)."""
+def _out_heads(t, name: str, shape, dtype, device):
+    """(tensor, view) of an output: the caller's, or a new contiguous one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+    return t, _heads(t, name, shape, dtype, device)
+
+
+def _ptr(t, name: str, device, dtype, shape=None):
+    """Pointer of a contiguous tensor argument of one dtype (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _heads(t: torch.Tensor) -> _Heads:
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
 def _launch_on(device, stream):
     """Makes `device` and the stream of the call current, so that what the call allocates
-    belongs to that stream; yields the stream's handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream(device).cuda_stream
-        return
+    belongs to that stream."""
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
+            yield
             return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            yield
 
+
+# (the public current_stream() builds a Stream object, 2 us a call)
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _stream_ws = {}
 
@@ -523,28 +538,26 @@ def _stream_workspace(ws, need: int, device, handle: int) -> Workspace:
 
 
 def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
-    _head_view(q, "q")
-    _head_view(k, "k", q)
-    if q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
-        raise ValueError(f"q and k must agree in tokens and head_dim, got {tuple(q.shape)} and "
-                         f"{tuple(k.shape)}")
+    """The spec of a call and its views of q and k."""
+    dev, shape, dtype = _cuda_device(q, "q"), q.shape, q.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"q and k must be float32 or bfloat16, got {dtype}")
+    vq = _heads(q, "q", shape, dtype, dev)
+    t, hq, d = shape
+    if k.dim() != 3:
+        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(k.shape)}")
+    vk = _heads(k, "k", torch.Size((t, k.shape[1], d)), dtype, dev)
     if cos.dim() != 2 or cos.shape != sin.shape:
         raise ValueError("cos and sin must be [length, rot_dim / 2] of one shape")
-    t, hq, d = q.shape
-    dev = q.device
-    _plain(cos, "cos", dev, torch.float32)
-    _plain(sin, "sin", dev, torch.float32)
-    _plain(positions, "positions", dev, torch.int32, (t,))
-    _plain(q_weight, "q_weight", dev, torch.float32, (d,))
-    _plain(k_weight, "k_weight", dev, torch.float32, (d,))
     if not norm and (q_weight is not None or k_weight is not None):
         raise ValueError("weights belong to the norm: norm=False takes none")
-    dtype = {torch.float32: 0, torch.bfloat16: 1}.get(q.dtype)
-    if dtype is None:
-        raise TypeError(f"q and k must be float32 or bfloat16, got {q.dtype}")
-    return _NormRope(dtype, t, hq, k.shape[1], d, 2 * cos.shape[1], int(bool(norm)),
-                     int(bool(interleaved)), eps, cos.shape[0], cos.data_ptr(), sin.data_ptr(),
-                     _ptr(positions), _ptr(q_weight), _ptr(k_weight))
+    f32 = torch.float32
+    return _NormRope(1 if dtype is torch.bfloat16 else 0, t, hq, k.shape[1], d, 2 * cos.shape[1],
+                     1 if norm else 0, 1 if interleaved else 0, eps, cos.shape[0],
+                     _ptr(cos, "cos", dev, f32), _ptr(sin, "sin", dev, f32),
+                     _ptr(positions, "positions", dev, torch.int32, (t,)),
+                     _ptr(q_weight, "q_weight", dev, f32, (d,)),
+                     _ptr(k_weight, "k_weight", dev, f32, (d,))), vq, vk
 
 
 def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None,
@@ -556,16 +569,18 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
     token's index when None) of the tables cos, sin (see rope_tables).  Pairs are (i, i + half),
     or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves."""
     L = load_library()
-    spec = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    with _launch_on(q.device, stream) as handle:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _shaped(_head_view(q_out, "q_out", q), "q_out", q)
-        _shaped(_head_view(k_out, "k_out", q), "k_out", k)
-        _raise(L.muon_qk_norm_rope(spec, _heads(q), _heads(k), _heads(q_out), _heads(k_out),
-                                   handle), "muon_qk_norm_rope")
+    spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
+                              interleaved)
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launch_on(dev, stream):
+            return qk_norm_rope(q, k, cos, sin, q_weight=q_weight, k_weight=k_weight,
+                                positions=positions, norm=norm, eps=eps, interleaved=interleaved,
+                                q_out=q_out, k_out=k_out)
+    q_out, vqo = _out_heads(q_out, "q_out", q.shape, q.dtype, dev)
+    k_out, vko = _out_heads(k_out, "k_out", k.shape, q.dtype, dev)
+    _raise(L.muon_qk_norm_rope(spec, vq, vk, vqo, vko, _current_handle(dev.index)),
+           "muon_qk_norm_rope")
     return q_out, k_out
 
 
@@ -580,23 +595,27 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_we
     """Gradients of qk_norm_rope: from those of its outputs, and its inputs, returns (dq, dk,
     dq_weight, dk_weight); the weights' are fp32, and None where no weight is given."""
     L = load_library()
-    spec = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    _shaped(_head_view(dq_out, "dq_out", q), "dq_out", q)
-    _shaped(_head_view(dk_out, "dk_out", q), "dk_out", k)
-    with _launch_on(q.device, stream) as handle:
-        if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if dk is None:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _shaped(_head_view(dq, "dq", q), "dq", q)
-        _shaped(_head_view(dk, "dk", q), "dk", k)
-        dqw = torch.empty_like(q_weight) if q_weight is not None else None
-        dkw = torch.empty_like(k_weight) if k_weight is not None else None
-        ws = _stream_workspace(workspace, L.muon_norm_rope_workspace_bytes(q.shape[2]), q.device,
-                               handle)
-        _raise(L.muon_qk_norm_rope_backward(
-            spec, _heads(dq_out), _heads(dk_out), _heads(q), _heads(k), _heads(dq), _heads(dk),
-            _ptr(dqw), _ptr(dkw), ws.ptr, ws.nbytes, handle), "muon_qk_norm_rope_backward")
+    spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
+                              interleaved)
+    dev, dtype = q.device, q.dtype
+    if _elsewhere(dev, stream):
+        with _launch_on(dev, stream):
+            return qk_norm_rope_backward(
+                dq_out, dk_out, q, k, cos, sin, q_weight=q_weight, k_weight=k_weight,
+                positions=positions, norm=norm, eps=eps, interleaved=interleaved, dq=dq, dk=dk,
+                workspace=workspace)
+    vdqo = _heads(dq_out, "dq_out", q.shape, dtype, dev)
+    vdko = _heads(dk_out, "dk_out", k.shape, dtype, dev)
+    dq, vdq = _out_heads(dq, "dq", q.shape, dtype, dev)
+    dk, vdk = _out_heads(dk, "dk", k.shape, dtype, dev)
+    dqw = torch.empty_like(q_weight) if q_weight is not None else None
+    dkw = torch.empty_like(k_weight) if k_weight is not None else None
+    handle = _current_handle(dev.index)
+    ws = _stream_workspace(workspace, L.muon_norm_rope_workspace_bytes(spec.head_dim), dev, handle)
+    _raise(L.muon_qk_norm_rope_backward(
+        spec, vdqo, vdko, vq, vk, vdq, vdk, None if dqw is None else dqw.data_ptr(),
+        None if dkw is None else dkw.data_ptr(), ws.ptr, ws.nbytes, handle),
+        "muon_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
 
 
@@ -605,26 +624,29 @@ def attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim
 
 
 def _attention_spec(q, k, v, cu_seqlens, scale):
-    _head_view(q, "q")
-    _head_view(k, "k", q)
-    _shaped(_head_view(v, "v", q), "v", k)
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q, k and v must be bfloat16, got {q.dtype}")
-    t, hq, d = q.shape
+    """The spec of a call and its views of q, k and v."""
+    dev, shape, dtype = _cuda_device(q, "q"), q.shape, q.dtype
+    if dtype is not torch.bfloat16:
+        raise TypeError(f"q, k and v must be bfloat16, got {dtype}")
+    vq = _heads(q, "q", shape, dtype, dev)
+    t, hq, d = shape
+    if k.dim() != 3:
+        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(k.shape)}")
     hk = k.shape[1]
-    if k.shape[0] != t or k.shape[2] != d:
-        raise ValueError(f"q and k must agree in tokens and head_dim, got {tuple(q.shape)} and "
-                         f"{tuple(k.shape)}")
     if hk == 0 or hq == 0 or hq % hk:
         raise ValueError(f"q heads ({hq}) must be a multiple of k heads ({hk})")
-    n_seqs = 0
+    kv_shape = torch.Size((t, hk, d))
+    vk = _heads(k, "k", kv_shape, dtype, dev)
+    vv = _heads(v, "v", kv_shape, dtype, dev)
+    n_seqs, cu = 0, None
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [sequences + 1]")
-        _plain(cu_seqlens, "cu_seqlens", q.device, torch.int32)
+        cu = _ptr(cu_seqlens, "cu_seqlens", dev, torch.int32)
         n_seqs = cu_seqlens.numel() - 1
-    return _AttentionSpec(t, hq, hk, d, n_seqs, _ptr(cu_seqlens),
-                          1.0 / math.sqrt(d) if scale is None else scale)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d) if d else 1.0
+    return _AttentionSpec(t, hq, hk, d, n_seqs, cu, scale), vq, vk, vv
 
 
 def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None, lse=None,
@@ -635,18 +657,22 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     None.  Returns (out, lse): out like q, lse [q_heads, tokens] fp32.  Tokens past the last
     sequence get out 0 and lse -inf."""
     L = load_library()
-    spec = _attention_spec(q, k, v, cu_seqlens, scale)
-    with _launch_on(q.device, stream) as handle:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty((spec.q_heads, spec.tokens), dtype=torch.float32, device=q.device)
-        _shaped(_head_view(out, "out", q), "out", q)
-        _plain(lse, "lse", q.device, torch.float32, (spec.q_heads, spec.tokens))
-        ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
-            spec.tokens, spec.q_heads, spec.kv_heads, spec.head_dim), q.device, handle)
-        _raise(L.muon_attention(spec, _heads(q), _heads(k), _heads(v), _heads(out),
-                                lse.data_ptr(), ws.ptr, ws.nbytes, handle), "muon_attention")
+    spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _launch_on(dev, stream):
+            return attention(q, k, v, cu_seqlens, scale=scale, out=out, lse=lse,
+                             workspace=workspace)
+    t, hq, _ = q.shape
+    out, vo = _out_heads(out, "out", q.shape, q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
+    p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
+    handle = _current_handle(dev.index)
+    ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
+        t, hq, spec.kv_heads, spec.head_dim), dev, handle)
+    _raise(L.muon_attention(spec, vq, vk, vv, vo, p_lse, ws.ptr, ws.nbytes, handle),
+           "muon_attention")
     return out, lse
 
 
@@ -656,25 +682,24 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
     """Gradients of attention's out: from dout, the inputs, and its out and lse, returns (dq, dk,
     dv) in bf16 (dk and dv summed over the query heads of a group)."""
     L = load_library()
-    spec = _attention_spec(q, k, v, cu_seqlens, scale)
-    _shaped(_head_view(dout, "dout", q), "dout", q)
-    _shaped(_head_view(out, "out", q), "out", q)
-    _plain(lse, "lse", q.device, torch.float32, (spec.q_heads, spec.tokens))
-    with _launch_on(q.device, stream) as handle:
-        if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if dk is None:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        if dv is None:
-            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-        for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
-            _shaped(_head_view(t, name, q), name, like)
-        ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
-            spec.tokens, spec.q_heads, spec.kv_heads, spec.head_dim), q.device, handle)
-        _raise(L.muon_attention_backward(
-            spec, _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
-            _heads(dq), _heads(dk), _heads(dv), ws.ptr, ws.nbytes, handle),
-            "muon_attention_backward")
+    spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
+    dev, dtype = q.device, q.dtype
+    if _elsewhere(dev, stream):
+        with _launch_on(dev, stream):
+            return attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=scale, dq=dq,
+                                      dk=dk, dv=dv, workspace=workspace)
+    t, hq, _ = q.shape
+    vg = _heads(dout, "dout", q.shape, dtype, dev)
+    vo = _heads(out, "out", q.shape, dtype, dev)
+    p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
+    dq, vdq = _out_heads(dq, "dq", q.shape, dtype, dev)
+    dk, vdk = _out_heads(dk, "dk", k.shape, dtype, dev)
+    dv, vdv = _out_heads(dv, "dv", k.shape, dtype, dev)
+    handle = _current_handle(dev.index)
+    ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
+        t, hq, spec.kv_heads, spec.head_dim), dev, handle)
+    _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws.ptr,
+                                     ws.nbytes, handle), "muon_attention_backward")
     return dq, dk, dv
 
 

@@ -74,7 +74,7 @@ muon_status rope_launch(NormRopeLaunch& L, const muon_norm_rope* s, muon_heads (
   if (s->tokens < 0 || s->q_heads < 0 || s->k_heads < 0 || s->q_heads > kMaxHeads ||
       s->k_heads > kMaxHeads || s->q_heads + s->k_heads == 0)
     return MUON_ERR_INVALID_ARG;
-  if (1ll * s->tokens * (s->q_heads + s->k_heads) > INT_MAX) return MUON_ERR_UNSUPPORTED;
+  if (1ll * s->tokens * (s->q_heads + s->k_heads) > INT_MAX - 65536) return MUON_ERR_UNSUPPORTED;
   if (!rope_dim_ok(s->head_dim) || s->rot_dim < 0 || s->rot_dim > s->head_dim ||
       s->rot_dim % 8 != 0)
     return MUON_ERR_INVALID_ARG;
@@ -129,7 +129,8 @@ double rope_bytes(const NormRopeLaunch& L, int passes) {
 // ------------------------------------------------------------ attention
 bool attention_shape_ok(int tokens, int hq, int hk, int dim) {
   return tokens >= 0 && hq >= 1 && hk >= 1 && hq <= kMaxHeads && hk <= kMaxHeads &&
-         hq % hk == 0 && dim >= 8 && dim <= 128 && dim % 8 == 0 && 1ll * tokens * hq <= INT_MAX;
+         hq % hk == 0 && dim >= 8 && dim <= 128 && dim % 8 == 0 &&
+         1ll * tokens * hq <= INT_MAX - 65536;
 }
 
 // Status block, then per query head and 128 tokens: 128 log-sum-exps, 128 deltas.
