@@ -108,11 +108,33 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t tile, int step) {   // 16 co
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int step) {  // 16 rows from 16 step
   return ptx::smem_desc_sw128(0, kSlab, 1024) + ((tile + step * 2048) >> 4);
 }
-// The address, computed where it is used: descriptors of every tile kept over a whole
-// loop would cost the issuing role its registers.
-__device__ __forceinline__ uint32_t here(uint32_t tile) {
-  asm volatile("" : "+r"(tile));
-  return tile;
+// Position in a ring of `kN` slots.
+template <int kN> struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kN) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+// Products, issued by one elected lane of a warp in step.  A CTA holds all 512 TMEM
+// columns, so their addresses start at 0.
+// D = A B^T over the head: both tiles K-major
+template <int DP>
+__device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t kId = ptx::idesc_bf16(128, 128, false);
+#pragma unroll
+  for (int i = 0; i < DP / 16; ++i) ptx::mma_bf16(d, desc_k(a, i), desc_k(b, i), kId, i > 0);
+}
+// D (+)= A[tmem] B over the 128 rows of B; a: the columns' address by step
+template <int DP, typename A>
+__device__ __forceinline__ void mma_rows(uint32_t d, A&& a, uint32_t b, bool accumulate) {
+  constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
+#pragma unroll
+  for (int i = 0; i < kBlock / 16; ++i)
+    ptx::mma_bf16_ts(d, a(i), desc_mn(b, i), kId, accumulate || i > 0);
 }
 // byte offset of 8 elements (row, column 8 c) of a tile
 __device__ __forceinline__ uint32_t tile_off(int row, int c) {

@@ -36,25 +36,6 @@ __device__ __forceinline__ uint32_t a_step(uint32_t t, int i) {
   return t + (i < 4 ? 8 * i : 64 + 8 * (i - 4));
 }
 
-// D (+)= A B^T over the head: both tiles K-major
-template <int DP>
-__device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t kId = ptx::idesc_bf16(128, 128, false);
-  a = here(a);
-  b = here(b);
-#pragma unroll
-  for (int i = 0; i < DP / 16; ++i) ptx::mma_bf16(d, desc_k(a, i), desc_k(b, i), kId, i > 0);
-}
-// D += A[tmem] B over the 128 rows of B
-template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
-  constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
-  b = here(b);
-#pragma unroll
-  for (int i = 0; i < kBlock / 16; ++i)
-    ptx::mma_bf16_ts(d, a_step(a, i), desc_mn(b, i), kId, accumulate || i > 0);
-}
-
 // ------------------------------------------------------------------ dq
 // TMEM: S of even and odd blocks (0, 128), dP (256), dq (384).  Per block, in the
 // tensor cores' order: dP of the next block, dq += dS K, S of the block after next; so
@@ -87,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   DqMisc& X = *reinterpret_cast<DqMisc*>(sm + C::kMisc);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // the last tiles hold the most keys: they go first
   const int tiles = (L.T + 127) / 128;
@@ -130,13 +112,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = X.tmem;
   const Guard guard{&X.bad, L.status,
                     warp == kProducerWarp ? kErrTimeoutProducer
                     : warp == kMmaWarp    ? kErrTimeoutMma
                                           : kErrTimeoutEpilogue};
   const bool run = !X.skip;
-  const int begin = X.first / kBlock, n = tile + 1 - begin;     // key blocks
+  const int begin = __shfl_sync(0xffffffffu, X.first, 0) / kBlock;
+  const int n = tile + 1 - begin;                               // key blocks
 
   if (warp >= kProducerWarp) {
     registers_down();
@@ -165,45 +147,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (run && warp == kMmaWarp) {
-      if (lane == 0) {
-        const uint32_t base = ptx::smem_u32(sm);
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && guard.wait_or_fail(bar, parity);
-          if (ok) ptx::tc_fence_after();
-          return ok;
-        };
-        auto scores = [&](int j) {
-          const int s = j % C::kK;
-          if (!wait(&X.k_full[s], (j / C::kK) & 1)) return;
-          mma_heads<DP>(tmem + 128 * (j & 1), base, base + C::kKRing + s * C::kTile);
+      const uint32_t base = ptx::smem_u32(sm);
+      Ring<C::kK> at_s, at_q;            // K tiles as read by S and by dq
+      Ring<C::kV> at_v;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && guard.warp_wait(bar, parity);
+        if (ok) ptx::tc_fence_after();
+        return ok;
+      };
+      auto scores = [&](int j) {
+        if (!wait(&X.k_full[at_s.slot], at_s.parity)) return;
+        if (ptx::elect_one()) {
+          mma_heads<DP>(128 * (j & 1), base, base + C::kKRing + at_s.slot * C::kTile);
           ptx::mma_commit(&X.s_full[j & 1]);
-        };
-        auto dp = [&](int j) {
-          const int s = j % C::kV;
-          if (!wait(&X.v_full[s], (j / C::kV) & 1)) return;
-          mma_heads<DP>(tmem + 256, base + C::kDo, base + C::kVRing + s * C::kTile);
+        }
+        at_s.next();
+      };
+      auto dp = [&] {
+        if (!wait(&X.v_full[at_v.slot], at_v.parity)) return;
+        if (ptx::elect_one()) {
+          mma_heads<DP>(256, base + C::kDo, base + C::kVRing + at_v.slot * C::kTile);
           ptx::mma_commit(&X.dp_full);
-          ptx::mma_commit(&X.v_empty[s]);
-        };
-        wait(&X.q_full, 0);
-        if (ok) scores(0);
-        if (ok) dp(0);
-        if (ok && n > 1) scores(1);
-        for (int j = 0; j < n && ok; ++j) {
-          if (!wait(&X.ds_full, j & 1)) break;
-          if (j + 1 < n) dp(j + 1);
-          if (!ok) break;
-          const int s = j % C::kK;
-          mma_rows<DP>(tmem + 384, tmem + 128 * (j & 1), base + C::kKRing + s * C::kTile, j > 0);
-          ptx::mma_commit(&X.k_empty[s]);
+          ptx::mma_commit(&X.v_empty[at_v.slot]);
+        }
+        at_v.next();
+      };
+      wait(&X.q_full, 0);
+      if (ok) scores(0);
+      if (ok) dp();
+      if (ok && n > 1) scores(1);
+      for (int j = 0; j < n && ok; ++j) {
+        if (!wait(&X.ds_full, j & 1)) break;
+        if (j + 1 < n) dp();
+        if (!ok) break;
+        const uint32_t s = 128 * (j & 1);
+        if (ptx::elect_one()) {
+          mma_rows<DP>(384, [s](int i) { return a_step(s, i); },
+                       base + C::kKRing + at_q.slot * C::kTile, j > 0);
+          ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
-          if (j + 2 < n) scores(j + 2);
         }
-        if (!ok) {                       // products in flight end before TMEM is freed
-          ptx::mma_commit(&X.drain);
-          ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
-        }
+        at_q.next();
+        if (j + 2 < n) scores(j + 2);
+      }
+      if (!ok) {                         // products in flight end before TMEM is freed
+        if (ptx::elect_one()) ptx::mma_commit(&X.drain);
+        ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        __syncwarp();
       }
     }
   } else {
@@ -249,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k0 = (begin + j) * kBlock;
         const bool masked = k0 < last_begin || j + 1 == n;
         const int lo = row_begin - k0 - 64 * half, hi = row - k0 - 64 * half;
-        const uint32_t ts = tmem + lanes + 128 * (j & 1) + 64 * half;
+        const uint32_t ts = lanes + 128 * (j & 1) + 64 * half;
         ok = guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -266,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         {
           uint32_t g[2][32];
-          load64(tmem + lanes + 256 + 64 * half, g);
+          load64(lanes + 256 + 64 * half, g);
 #pragma unroll
           for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(g[i >> 5][i & 31]) - delta;
         }
@@ -298,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < DP / 64; ++i) {
           const int col = DP / 2 * half + 32 * i;
           uint32_t o[32];
-          ptx::tmem_ld32_sync(tmem + lanes + 384 + col, o);
+          ptx::tmem_ld32_sync(lanes + 384 + col, o);
           float f[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -338,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(X.tmem, 512);
   }
 }
 
@@ -375,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   DkvMisc& X = *reinterpret_cast<DkvMisc*>(sm + C::kMisc);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // the first tiles are seen by the most queries: they go first
   const int tiles = (L.T + 127) / 128;
@@ -419,13 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = X.tmem;
   const Guard guard{&X.bad, L.status,
                     warp == kProducerWarp ? kErrTimeoutProducer
                     : warp == kMmaWarp    ? kErrTimeoutMma
                                           : kErrTimeoutEpilogue};
   const bool run = !X.skip;
-  const int blocks = X.blocks, n = blocks * L.group;     // query blocks of all heads
+  const int blocks = __shfl_sync(0xffffffffu, X.blocks, 0);
+  const int n = blocks * L.group;                        // query blocks of all heads
 
   if (warp >= kProducerWarp) {
     registers_down();
@@ -466,45 +458,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (run && n > 0 && warp == kMmaWarp) {
-      if (lane == 0) {
-        const uint32_t base = ptx::smem_u32(sm);
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && guard.wait_or_fail(bar, parity);
-          if (ok) ptx::tc_fence_after();
-          return ok;
-        };
-        auto scores = [&](int i) {
-          const int s = i % C::kStages;
-          if (!wait(&X.q_full[s], (i / C::kStages) & 1)) return;
-          mma_heads<DP>(tmem, base, base + C::kQRing + s * C::kTile);
+      const uint32_t base = ptx::smem_u32(sm);
+      Ring<C::kStages> at_s, at_p, at_v, at_k;   // tiles as read by S, dP, dv and dk
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && guard.warp_wait(bar, parity);
+        if (ok) ptx::tc_fence_after();
+        return ok;
+      };
+      auto scores = [&] {
+        if (!wait(&X.q_full[at_s.slot], at_s.parity)) return;
+        if (ptx::elect_one()) {
+          mma_heads<DP>(0, base, base + C::kQRing + at_s.slot * C::kTile);
           ptx::mma_commit(&X.s_full);
-        };
-        auto dp = [&](int i) {
-          const int s = i % C::kStages;
-          if (!wait(&X.do_full[s], (i / C::kStages) & 1)) return;
-          mma_heads<DP>(tmem + 128, base + C::kV, base + C::kDoRing + s * C::kTile);
+        }
+        at_s.next();
+      };
+      auto dp = [&] {
+        if (!wait(&X.do_full[at_p.slot], at_p.parity)) return;
+        if (ptx::elect_one()) {
+          mma_heads<DP>(128, base + C::kV, base + C::kDoRing + at_p.slot * C::kTile);
           ptx::mma_commit(&X.dp_full);
-        };
-        wait(&X.kv_full, 0);
-        if (ok) scores(0);
-        if (ok) dp(0);
-        for (int i = 0; i < n && ok; ++i) {
-          const int s = i % C::kStages;
-          if (!wait(&X.p_full, i & 1)) break;
-          mma_rows<DP>(tmem + 256, tmem, base + C::kDoRing + s * C::kTile, i > 0);
-          ptx::mma_commit(&X.do_empty[s]);
-          if (i + 1 < n) scores(i + 1);
-          if (!ok || !wait(&X.ds_full, i & 1)) break;
-          mma_rows<DP>(tmem + 256 + DP, tmem + 128, base + C::kQRing + s * C::kTile, i > 0);
-          ptx::mma_commit(&X.q_empty[s]);
+        }
+        at_p.next();
+      };
+      wait(&X.kv_full, 0);
+      if (ok) scores();
+      if (ok) dp();
+      for (int i = 0; i < n && ok; ++i) {
+        if (!wait(&X.p_full, i & 1)) break;
+        if (ptx::elect_one()) {
+          mma_rows<DP>(256, [](int e) { return a_step(0, e); },
+                       base + C::kDoRing + at_v.slot * C::kTile, i > 0);
+          ptx::mma_commit(&X.do_empty[at_v.slot]);
+        }
+        at_v.next();
+        if (i + 1 < n) scores();
+        if (!ok || !wait(&X.ds_full, i & 1)) break;
+        if (ptx::elect_one()) {
+          mma_rows<DP>(256 + DP, [](int e) { return a_step(128, e); },
+                       base + C::kQRing + at_k.slot * C::kTile, i > 0);
+          ptx::mma_commit(&X.q_empty[at_k.slot]);
           if (i + 1 == n) ptx::mma_commit(&X.done);
-          if (i + 1 < n) dp(i + 1);
         }
-        if (!ok) {                       // products in flight end before TMEM is freed
-          ptx::mma_commit(&X.drain);
-          ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
-        }
+        at_k.next();
+        if (i + 1 < n) dp();
+      }
+      if (!ok) {                         // products in flight end before TMEM is freed
+        if (ptx::elect_one()) ptx::mma_commit(&X.drain);
+        ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        __syncwarp();
       }
     }
   } else {
@@ -522,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = i % C::kStages, q0 = b * kBlock;
         const bool masked = b == tile || q0 + kBlock > first_end;
         const int lo = key - q0 - 64 * half, hi = key_end - q0 - 64 * half;   // lo <= col < hi
-        const uint32_t ts = tmem + lanes + 64 * half;
+        const uint32_t ts = lanes + 64 * half;
         const float4* lse2 =
             reinterpret_cast<const float4*>(sm + C::kStats + s * kStatBytes) + 16 * half;
         const float4* delta = lse2 + 32;
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i) {
           uint32_t o[32];
-          ptx::tmem_ld32_sync(tmem + lanes + 256 + DP * half + 32 * i, o);
+          ptx::tmem_ld32_sync(lanes + 256 + DP * half + 32 * i, o);
           float f[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(X.tmem, 512);
   }
 }
 

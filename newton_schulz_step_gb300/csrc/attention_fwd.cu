@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   Misc& X = *reinterpret_cast<Misc*>(sm + C::kMisc);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   // the last tiles hold the most keys: they go first
   const int pairs = (L.T + 128 * kTiles - 1) / (128 * kTiles);
@@ -104,18 +105,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = X.tmem;
   const Guard guard{&X.bad, L.status,
                     warp == kProducerWarp ? kErrTimeoutProducer
                     : warp == kMmaWarp    ? kErrTimeoutMma
                                           : kErrTimeoutEpilogue};
 
   // key blocks of each tile, [b0, b1), and of both
-  int b0[kTiles], b1[kTiles], begin = INT_MAX, end = 0;
+  int b0[kTiles], b1[kTiles], begin = INT_MAX, end = 0;   // (the same in every lane)
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
     const int r = row0 + 128 * t;
-    b0[t] = X.first[t] / kBlock;
+    b0[t] = __shfl_sync(0xffffffffu, X.first[t], 0) / kBlock;
     b1[t] = r < L.T ? r / kBlock + 1 : 0;
     if (r < L.T) {
       begin = min(begin, b0[t]);
@@ -154,59 +154,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (run && warp == kMmaWarp) {
-      if (lane == 0) {
-        constexpr uint32_t kIdS = ptx::idesc_bf16(128, 128, false);
-        constexpr uint32_t kIdO = ptx::idesc_bf16(128, DP, true);
-        const uint32_t sq = ptx::smem_u32(sm), ring = sq + C::kRing;
-        int n = 0;                       // ring slots taken
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && guard.wait_or_fail(bar, parity);
-          if (ok) ptx::tc_fence_after();
-          return ok;
-        };
-        auto take = [&] {                // waits for the next slot of the ring
-          const int s = n % C::kStages;
-          wait(&X.full[s], (n / C::kStages) & 1);
-          ++n;
-          return s;
-        };
-        auto scores = [&](int t, int b, int slot) {
-          if (b == b0[t]) wait(&X.q_full[t], 0);
-          if (!ok) return;
-          const uint32_t q = here(sq + t * C::kTile), k = here(ring + slot * C::kTile);
-#pragma unroll
-          for (int i = 0; i < DP / 16; ++i)
-            ptx::mma_bf16(tmem + 128 * t, desc_k(q, i), desc_k(k, i), kIdS, i > 0);
+      const uint32_t sq = ptx::smem_u32(sm), ring = sq + C::kRing;
+      Ring<C::kStages> at;               // next slot of the ring
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && guard.warp_wait(bar, parity);
+        if (ok) ptx::tc_fence_after();
+        return ok;
+      };
+      auto take = [&] {
+        const int s = at.slot;
+        wait(&X.full[s], at.parity);
+        at.next();
+        return s;
+      };
+      auto scores = [&](int t, int b, int slot) {
+        if (b == b0[t] && !wait(&X.q_full[t], 0)) return;
+        if (ptx::elect_one()) {
+          mma_heads<DP>(128 * t, sq + t * C::kTile, ring + slot * C::kTile);
           ptx::mma_commit(&X.s_full[t]);
-        };
-        int ks = take();
-        for (int t = 0; t < kTiles && ok; ++t)
-          if (active(t, begin)) scores(t, begin, ks);
-        if (ok) ptx::mma_commit(&X.empty[ks]);
-        for (int b = begin; b < end && ok; ++b) {
-          const int vs = take();
-          ks = b + 1 < end ? take() : -1;
-          for (int t = 0; t < kTiles && ok; ++t) {
-            if (active(t, b)) {
-              if (!wait(&X.p_full[t], (b - b0[t]) & 1)) break;
-              const uint32_t v = here(ring + vs * C::kTile);
+        }
+      };
+      int ks = take();
 #pragma unroll
-              for (int i = 0; i < kBlock / 16; ++i)
-                ptx::mma_bf16_ts(tmem + 128 * kTiles + DP * t, tmem + 128 * t + 8 * i,
-                                 desc_mn(v, i), kIdO, b > b0[t] || i > 0);
+      for (int t = 0; t < kTiles; ++t)
+        if (ok && active(t, begin)) scores(t, begin, ks);
+      if (ok && ptx::elect_one()) ptx::mma_commit(&X.empty[ks]);
+      for (int b = begin; b < end && ok; ++b) {
+        const int vs = take();
+        ks = b + 1 < end ? take() : -1;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (ok && active(t, b) && wait(&X.p_full[t], (b - b0[t]) & 1)) {
+            if (ptx::elect_one()) {
+              mma_rows<DP>(128 * kTiles + DP * t, [t](int i) { return 128u * t + 8 * i; },
+                           ring + vs * C::kTile, b > b0[t]);
               if (b + 1 == b1[t]) ptx::mma_commit(&X.o_full[t]);
             }
-            if (active(t, b + 1)) scores(t, b + 1, ks);
           }
-          if (!ok) break;
+          if (ok && active(t, b + 1)) scores(t, b + 1, ks);
+        }
+        if (!ok) break;
+        if (ptx::elect_one()) {
           ptx::mma_commit(&X.empty[vs]);
           if (ks >= 0) ptx::mma_commit(&X.empty[ks]);
         }
-        if (!ok) {                       // products in flight end before TMEM is freed
-          ptx::mma_commit(&X.drain);
-          ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
-        }
+      }
+      if (!ok) {                         // products in flight end before TMEM is freed
+        if (ptx::elect_one()) ptx::mma_commit(&X.drain);
+        ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        __syncwarp();
       }
     }
   } else {
@@ -215,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = warp >> 2, r = tid & 127;
       const int row = row0 + 128 * t + r;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 128 * kTiles + DP * t;
+      const uint32_t ts = lanes + 128 * t, to = lanes + 128 * kTiles + DP * t;
       const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
       const int last_begin = X.last[t];
       const int used = tokens_in_use(L);
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc(X.tmem, 512);
   }
 }
 
