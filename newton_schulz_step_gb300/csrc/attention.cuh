@@ -20,6 +20,38 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 values in one register pair: a product and sum, or a sum, an instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // First token and end (one past the last token) of the sequence that holds token i,
 // or an empty range for a token past the last sequence.  Clamped around i, so that
 // offsets that do not ascend cannot lead outside the tensors.
@@ -45,26 +77,39 @@ __device__ __forceinline__ int tokens_in_use(const AttentionLaunch& L) {
 // ---- bounded waits ------------------------------------------------------
 // Every wait of a CTA goes through its abort flag and the workspace's status word:
 // a wait that gives up sets both, which ends the waits of the CTA's other roles.
+// The code of the issuing roles is kept short (waiting is a call there, loops stay
+// loops): all roles share the instruction caches, and with everything unrolled every
+// step of the issuing warp was measured to wait 300 cycles for its instructions.
+static __device__ __noinline__ bool wait_call(uint64_t* bar, uint32_t parity,
+                                              const volatile int* bad, unsigned int* status) {
+  return ptx::mbar_wait(bar, parity, bad, status);
+}
+
 struct Guard {
   volatile int* bad;
   unsigned int* status;
   unsigned int role;                     // DeviceError bit of the waiting role
-  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
-    return ptx::mbar_wait(bar, parity, bad, status);
-  }
   __device__ __forceinline__ void fail() const {
     if (!*bad) atomicOr(status, kErrTimeoutAttention | role);
     *bad = 1;
   }
-  // One thread's wait; records a failure.
+  // One issuing thread's wait; records a failure.
   __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity) const {
-    if (wait(bar, parity)) return true;
+    if (ptx::mbar_try_wait(bar, parity) || wait_call(bar, parity, bad, status)) return true;
     fail();
     return false;
   }
-  // A whole warp's wait (the lanes agree on the result).
+  // An issuing warp's wait (the lanes agree on the result).
+  __device__ __forceinline__ bool issue_wait(uint64_t* bar, uint32_t parity) const {
+    for (int i = 0; i < 8; ++i)          // (a try itself waits a while)
+      if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, wait_call(bar, parity, bad, status))) return true;
+    fail();
+    return false;
+  }
+  // A compute warp's wait (a call would cost it the registers it holds).
   __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) const {
-    const bool ok = __all_sync(0xffffffffu, wait(bar, parity));
+    const bool ok = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, bad, status));
     if (!ok) fail();
     return ok;
   }
@@ -72,20 +117,11 @@ struct Guard {
 // What a role still has in flight when it gives up is waited for, within this limit.
 constexpr uint64_t kDrainNs = 100ull * 1000ull * 1000ull;
 
-// Registers move from the warps that only issue work to those that compute: a block of
-// 384 threads is launched with 168 each (64512), of which 4 warps keep kIssueRegs and 8
-// get kComputeRegs.  The issuing roles must fit kIssueRegs as compiled without the split
-// (they take at most 64): below that the compiler's allocation was seen to break (waits
-// ran into their limit with 40).
-constexpr int kThreads = 384;
-constexpr int kIssueRegs = 72, kComputeRegs = 216;
-static_assert(128 * kIssueRegs + 256 * kComputeRegs == kThreads * 168,
-              "no more registers than at launch");
-__device__ __forceinline__ void registers_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-}
-__device__ __forceinline__ void registers_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+// The dynamic shared memory starts on the 1024 bytes that the swizzled tiles need (it
+// follows the system's own 1 KB); a kernel that found it elsewhere would do nothing and
+// report a failed wait.
+__device__ __forceinline__ bool tiles_aligned(const uint8_t* sm) {
+  return (ptx::smem_u32(sm) & 1023u) == 0;
 }
 
 // ---- tiles --------------------------------------------------------------
@@ -125,16 +161,23 @@ template <int kN> struct Ring {
 template <int DP>
 __device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t kId = ptx::idesc_bf16(128, 128, false);
+#pragma unroll 1
+  for (uint32_t s = 0; s < DP / 64; ++s)
 #pragma unroll
-  for (int i = 0; i < DP / 16; ++i) ptx::mma_bf16(d, desc_k(a, i), desc_k(b, i), kId, i > 0);
+    for (int i = 0; i < 4; ++i)
+      ptx::mma_bf16(d, desc_k(a + s * kSlab, i), desc_k(b + s * kSlab, i), kId, s > 0 || i > 0);
 }
-// D (+)= A[tmem] B over the 128 rows of B; a: the columns' address by step
-template <int DP, typename A>
-__device__ __forceinline__ void mma_rows(uint32_t d, A&& a, uint32_t b, bool accumulate) {
+// D (+)= A[tmem] B over the first kRows rows of B.  A: bf16 pairs, kRun columns (of 32
+// bits) from `a`, the next from a + 2 kRun, and so on
+template <int DP, int kRows, int kRun>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
+#pragma unroll 1
+  for (uint32_t s = 0; s < kRows / 64; ++s)
 #pragma unroll
-  for (int i = 0; i < kBlock / 16; ++i)
-    ptx::mma_bf16_ts(d, a(i), desc_mn(b, i), kId, accumulate || i > 0);
+    for (int i = 0; i < 4; ++i)
+      ptx::mma_bf16_ts(d, a + 64 * s + 8 * i + 8 * i / kRun * kRun, desc_mn(b + s * 8192, i), kId,
+                       accumulate || s > 0 || i > 0);
 }
 // byte offset of 8 elements (row, column 8 c) of a tile
 __device__ __forceinline__ uint32_t tile_off(int row, int c) {
@@ -162,6 +205,12 @@ __device__ __forceinline__ void store_row32(uint8_t* tile, int row, int c, const
                    pack2(f[8 * q + 4], f[8 * q + 5]), pack2(f[8 * q + 6], f[8 * q + 7]));
 }
 
+// Columns outside lo..hi become `value`.
+__device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi, uint32_t value) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < lo || j > hi) s[j] = value;
+}
 // 64 consecutive TMEM columns
 __device__ __forceinline__ void load64(uint32_t t, uint32_t (&a)[2][32]) {
   ptx::tmem_ld32x2_sync(t, t + 32, a[0], a[1]);

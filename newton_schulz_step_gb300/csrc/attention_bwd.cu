@@ -12,10 +12,10 @@
 // the same bits in every run.
 // p and ds are rounded to bf16, the tensor cores' input; everything else is fp32.
 //
-// 384 threads: warps 0-3 and 4-7 compute, warp 8 issues the copies, warp 9 the products.
-// A compute thread owns a row (TMEM lane) of S and dP, warps 0-3 its columns 0-63, warps
-// 4-7 its columns 64-127.  P and dS overwrite S or dP as bf16 pairs, each half within its
-// own columns, and are the A operand of the accumulating product from there.
+// Warps 0-15 compute, warp 16 issues the copies, warp 17 the products.  A compute thread
+// owns a row (TMEM lane) of S and dP and 32 of its columns; each of the 4 groups of warps
+// writes P and dS over half of its own columns of S or dP, as bf16 pairs, from where they
+// are the A operand of the accumulating product.
 #include "attention.cuh"
 
 namespace muon {
@@ -23,17 +23,19 @@ namespace {
 
 using namespace attn;
 
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+// 16 compute warps in 4 groups, a warp for the copies, a warp for the products: with four
+// compute warps on each of the SM's four schedulers a thread has 96 registers, and a warp's
+// waits, exponentials and TMEM accesses run beside the others'.  (8 warps with 64 columns
+// a thread: dk/dv of 8192 tokens, 32/8 heads of 128, in 751 us instead of 663.)
+constexpr int kThreads = 576;
+constexpr int kProducerWarp = 16, kMmaWarp = 17;
 constexpr uint32_t kStatBytes = 1024;      // a block's 128 log-sum-exps and 128 deltas
 
-__device__ __forceinline__ void compute_barrier() {   // the 256 compute threads
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+__device__ __forceinline__ void compute_barrier() {   // the 16 compute warps
+  asm volatile("bar.sync 1, 512;" ::: "memory");
 }
-
-// Address of step i (16 columns of A) of the bf16 pairs that the two halves of the
-// compute threads left at `t` and `t + 64`.
-__device__ __forceinline__ uint32_t a_step(uint32_t t, int i) {
-  return t + (i < 4 ? 8 * i : 64 + 8 * (i - 4));
+__device__ __forceinline__ void half_barrier(int half) {   // the lower or upper 8 of them
+  asm volatile("bar.sync %0, 256;" ::"r"(2 + half) : "memory");
 }
 
 // ------------------------------------------------------------------ dq
@@ -44,8 +46,8 @@ template <int DP> struct DqCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
   static constexpr uint32_t kDo = kTile, kKRing = 2 * kTile, kVRing = kKRing + kK * kTile;
-  static constexpr uint32_t kMisc = kVRing + kV * kTile;
-  static constexpr uint32_t kSmem = kMisc + 1536 + 1024;
+  static constexpr uint32_t kMisc = kVRing + kV * kTile, kMiscBytes = 2560;
+  static constexpr uint32_t kSmem = kMisc + kMiscBytes;
 };
 
 struct DqMisc {
@@ -55,18 +57,16 @@ struct DqMisc {
   int bad, skip;
   int first, last;                 // begin of the tile's first and last row
   unsigned int repair[4];          // rows to compute again, by warp of the tile
-  float delta[2][128];             // halves of delta
+  float delta[4][128];             // parts of delta
 };
-static_assert(sizeof(DqMisc) <= 1536, "misc block");
+static_assert(sizeof(DqMisc) <= DqCfg<64>::kMiscBytes, "misc block");
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_dq_kernel(const __grid_constant__ AttentionMaps M,
                         const __grid_constant__ AttentionLaunch L) {
   using C = DqCfg<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   DqMisc& X = *reinterpret_cast<DqMisc*>(sm + C::kMisc);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -94,11 +94,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&X.s_full[0], 1);
     ptx::mbar_init(&X.s_full[1], 1);
     ptx::mbar_init(&X.dp_full, 1);
-    ptx::mbar_init(&X.ds_full, 8);
+    ptx::mbar_init(&X.ds_full, 16);
     ptx::mbar_init(&X.dq_full, 1);
     ptx::mbar_init(&X.drain, 1);
     X.bad = 0;
     X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&M.q);
     ptx::prefetch_tmap(&M.dout);
@@ -121,7 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = tile + 1 - begin;                               // key blocks
 
   if (warp >= kProducerWarp) {
-    registers_down();
     if (run && warp == kProducerWarp) {
       if (lane == 0) {
         load_tile<DP>(sm, &M.q, h, row0, &X.q_full);
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<C::kV> at_v;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && guard.warp_wait(bar, parity);
+        ok = ok && guard.issue_wait(bar, parity);
         if (ok) ptx::tc_fence_after();
         return ok;
       };
@@ -181,10 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(&X.ds_full, j & 1)) break;
         if (j + 1 < n) dp();
         if (!ok) break;
-        const uint32_t s = 128 * (j & 1);
         if (ptx::elect_one()) {
-          mma_rows<DP>(384, [s](int i) { return a_step(s, i); },
-                       base + C::kKRing + at_q.slot * C::kTile, j > 0);
+          mma_rows<DP, 128, 16>(384, 128 * (j & 1), base + C::kKRing + at_q.slot * C::kTile, j > 0);
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
         }
@@ -197,132 +198,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else {
-    registers_up();
-    if (run) {
-      const int half = warp >> 2, r = tid & 127, row = row0 + r;
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const int used = tokens_in_use(L);
-      const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
-      const int last_begin = X.last;
-      const float c = L.scale * kLog2e;
-      // delta, half the columns each; lse in base 2, +inf (p = 0) for rows without keys
-      float delta = 0.f, lse2 = INFINITY;
-      if (row < used) {
-        const __nv_bfloat16 *o = L.o.row(row, h), *g = L.dout.row(row, h);
+  } else if (run) {
+    const int group = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane, row = row0 + r;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const int used = tokens_in_use(L);
+    const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
+    const int last_begin = X.last;
+    const float c = L.scale * kLog2e;
+    // delta, a quarter of the columns each; lse in base 2, +inf (p = 0) for rows without keys
+    float delta = 0.f, lse2 = INFINITY;
+    if (row < used) {
+      const __nv_bfloat16 *o = L.o.row(row, h), *g = L.dout.row(row, h);
 #pragma unroll
-        for (int i = 0; i < DP / 16; ++i) {
-          const int d = DP / 2 * half + 8 * i;
-          if (d < L.dim) {
-            const uint4 a = *reinterpret_cast<const uint4*>(o + d);
-            const uint4 b = *reinterpret_cast<const uint4*>(g + d);
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+      for (int i = 0; i < DP / 32; ++i) {
+        const int d = DP / 4 * group + 8 * i;
+        if (d < L.dim) {
+          const uint4 a = *reinterpret_cast<const uint4*>(o + d);
+          const uint4 b = *reinterpret_cast<const uint4*>(g + d);
+          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              delta = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), delta);
-              delta = fmaf(__uint_as_float(x[e] & 0xffff0000u),
-                           __uint_as_float(y[e] & 0xffff0000u), delta);
-            }
+          for (int e = 0; e < 4; ++e) {
+            delta = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), delta);
+            delta = fmaf(__uint_as_float(x[e] & 0xffff0000u),
+                         __uint_as_float(y[e] & 0xffff0000u), delta);
           }
         }
-        lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
       }
-      X.delta[half][r] = delta;
-      compute_barrier();
-      delta = X.delta[0][r] + X.delta[1][r];
-      {
-        float* st = L.stats + (static_cast<size_t>(h) * tiles + tile) * 256 + r;
-        if (half == 0) st[0] = lse2;
-        else st[128] = delta;
+      lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
+    }
+    X.delta[group][r] = delta;
+    compute_barrier();
+    delta = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
+    if (group < 2)
+      L.stats[(static_cast<size_t>(h) * tiles + tile) * 256 + 128 * group + r] =
+          group ? delta : lse2;
+    const uint64_t c2 = pair(c, c), lse22 = pair(-lse2, -lse2), delta2 = pair(-delta, -delta);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int k0 = (begin + j) * kBlock;
+      const uint32_t ts = lanes + 128 * (j & 1) + 32 * group;
+      ok = guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      uint32_t x[32];
+      uint64_t p[16];
+      ptx::tmem_ld32_sync(ts, x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 y = unpair(
+            fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, lse22));
+        p[i] = pair(ex2(y.x), ex2(y.y));
       }
-      bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        const int k0 = (begin + j) * kBlock;
-        const bool masked = k0 < last_begin || j + 1 == n;
-        const int lo = row_begin - k0 - 64 * half, hi = row - k0 - 64 * half;
-        const uint32_t ts = lanes + 128 * (j & 1) + 64 * half;
-        ok = guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float p[64];
-        {
-          uint32_t s[2][32];
-          load64(ts, s);
+      ok = guard.warp_wait(&X.dp_full, j & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      ptx::tmem_ld32_sync(lanes + 256 + 32 * group, x);
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            p[i] = ex2(fmaf(__uint_as_float(s[i >> 5][i & 31]), c, -lse2));
-        }
-        ok = guard.warp_wait(&X.dp_full, j & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        {
-          uint32_t g[2][32];
-          load64(lanes + 256 + 64 * half, g);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) p[i] *= __uint_as_float(g[i >> 5][i & 31]) - delta;
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i < lo || i > hi) p[i] = 0.f;
-        }
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
-        ptx::tmem_st32(ts, w);
-        if (used < min(k0 + kBlock, L.T)) {            // the block holds padding: clear its K
-          const int s = j % C::kK;                     // (landed: S has read it)
-          if (half == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
-          ptx::fence_proxy_async_smem();
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+      for (int i = 0; i < 16; ++i) {
+        const float2 y = unpair(mul2(
+            p[i], add2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), delta2)));
+        x[2 * i] = __float_as_uint(y.x);
+        x[2 * i + 1] = __float_as_uint(y.y);
       }
-      if (ok) ok = guard.warp_wait(&X.dq_full, 0);
-      if (ok) {
-        ptx::tc_fence_after();
-        // Q has been read for the last time: dq goes through its place
-        float test = 0.f;                              // NaN if an element is not finite
+      if (k0 < last_begin || j + 1 == n)
+        hide(x, row_begin - k0 - 32 * group, row - k0 - 32 * group, 0u);
+      uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < DP / 64; ++i) {
-          const int col = DP / 2 * half + 32 * i;
-          uint32_t o[32];
-          ptx::tmem_ld32_sync(lanes + 384 + col, o);
-          float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            f[e] = __uint_as_float(o[e]) * L.scale;
-            test = fmaf(f[e], 0.f, test);
-          }
-          store_row32(sm, r, col / 8, f);
-        }
-        const unsigned int bad = __ballot_sync(0xffffffffu, row < used && test != 0.f);
-        if (bad && lane == 0) atomicOr(&X.repair[warp & 3], bad);
-      }
-      compute_barrier();                               // (reached by every compute thread)
-      if (ok) {
-        // each half of a row's elements may be bad alone: both warps of the rows look
-        // at the joint set and take every other row
-        unsigned int bad = X.repair[warp & 3] & (half ? 0xaaaaaaaau : 0x55555555u);
-        while (bad) {
-          const int src = __ffs(bad) - 1;
-          bad &= bad - 1;
-          put_row(sm, r - lane + src,
-                  dq_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
-                  DP / 64);
-        }
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+      ptx::tmem_st16(ts, w);
+      if (used < min(k0 + kBlock, L.T)) {              // the block holds padding: clear its K
+        const int s = j % C::kK;                       // (landed: S has read it)
+        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
         ptx::fence_proxy_async_smem();
       }
-      compute_barrier();
-      if (ok && tid == 0 && !X.bad) {
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+    }
+    if (ok) ok = guard.warp_wait(&X.dq_full, 0);
+    if (ok && 32 * group < DP) {
+      ptx::tc_fence_after();
+      // Q has been read for the last time: dq goes through its place
+      float test = 0.f;                                // NaN if an element is not finite
+      uint32_t o[32];
+      ptx::tmem_ld32_sync(lanes + 384 + 32 * group, o);
+      float f[32];
 #pragma unroll
-        for (int i = 0; i < DP / 64; ++i)
-          ptx::tma_store_3d(&M.dq, 64 * i, h, row0, sm + i * kSlab);
-        ptx::bulk_commit();
-        ptx::bulk_wait<0>();
+      for (int e = 0; e < 32; ++e) {
+        f[e] = __uint_as_float(o[e]) * L.scale;
+        test = fmaf(f[e], 0.f, test);
       }
+      store_row32(sm, r, 4 * group, f);
+      const unsigned int bad = __ballot_sync(0xffffffffu, row < used && test != 0.f);
+      if (bad && lane == 0) atomicOr(&X.repair[quarter], bad);
+    }
+    compute_barrier();                                 // (reached by every compute thread)
+    if (ok) {
+      // any part of a row may be bad: the four warps of the rows share the joint set
+      unsigned int bad = X.repair[quarter] & (0x11111111u << group);
+      while (bad) {
+        const int src = __ffs(bad) - 1;
+        bad &= bad - 1;
+        put_row(sm, r - lane + src,
+                dq_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
+                DP / 64);
+      }
+      ptx::fence_proxy_async_smem();
+    }
+    compute_barrier();
+    if (ok && tid == 0 && !X.bad) {
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i)
+        ptx::tma_store_3d(&M.dq, 64 * i, h, row0, sm + i * kSlab);
+      ptx::bulk_commit();
+      ptx::bulk_wait<0>();
     }
   }
   ptx::tc_fence_before();
@@ -345,7 +337,7 @@ template <int DP> struct DkvCfg {
   static constexpr uint32_t kV = kTile, kQRing = 2 * kTile, kDoRing = kQRing + kStages * kTile;
   static constexpr uint32_t kStats = kDoRing + kStages * kTile;
   static constexpr uint32_t kMisc = kStats + kStages * kStatBytes;
-  static constexpr uint32_t kSmem = kMisc + 512 + 1024;
+  static constexpr uint32_t kSmem = kMisc + 512;
 };
 
 struct DkvMisc {
@@ -354,6 +346,7 @@ struct DkvMisc {
   uint32_t tmem;
   int bad, skip;
   int first_end, blocks;           // end of the first key's sequence; query blocks per head
+  unsigned int repair[2][4];       // rows of dv, dk to compute again, by warp of the tile
 };
 static_assert(sizeof(DkvMisc) <= 512, "misc block");
 
@@ -362,9 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_dkv_kernel(const __grid_constant__ AttentionMaps M,
                          const __grid_constant__ AttentionLaunch L) {
   using C = DkvCfg<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   DkvMisc& X = *reinterpret_cast<DkvMisc*>(sm + C::kMisc);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -382,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     X.first_end = sequence_of(L, key0).end;
     X.blocks = end > key0 ? (end - 1) / kBlock + 1 - tile : 0;
   }
+  if (tid < 8) X.repair[tid >> 2][tid & 3] = 0;
   if (warp == kProducerWarp && lane == 0) {
     ptx::mbar_init(&X.kv_full, 2);
     for (int s = 0; s < 4; ++s) {
@@ -392,12 +384,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(&X.s_full, 1);
     ptx::mbar_init(&X.dp_full, 1);
-    ptx::mbar_init(&X.p_full, 8);
-    ptx::mbar_init(&X.ds_full, 8);
+    ptx::mbar_init(&X.p_full, 16);
+    ptx::mbar_init(&X.ds_full, 16);
     ptx::mbar_init(&X.done, 1);
     ptx::mbar_init(&X.drain, 1);
     X.bad = 0;
     X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&M.q);
     ptx::prefetch_tmap(&M.dout);
@@ -420,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = blocks * L.group;                        // query blocks of all heads
 
   if (warp >= kProducerWarp) {
-    registers_down();
     if (run && n > 0 && warp == kProducerWarp) {
       if (lane == 0) {
         load_tile<DP>(sm, &M.k, kh, key0, &X.kv_full);
@@ -462,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<C::kStages> at_s, at_p, at_v, at_k;   // tiles as read by S, dP, dv and dk
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && guard.warp_wait(bar, parity);
+        ok = ok && guard.issue_wait(bar, parity);
         if (ok) ptx::tc_fence_after();
         return ok;
       };
@@ -488,16 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n && ok; ++i) {
         if (!wait(&X.p_full, i & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP>(256, [](int e) { return a_step(0, e); },
-                       base + C::kDoRing + at_v.slot * C::kTile, i > 0);
+          mma_rows<DP, 128, 16>(256, 0, base + C::kDoRing + at_v.slot * C::kTile, i > 0);
           ptx::mma_commit(&X.do_empty[at_v.slot]);
         }
         at_v.next();
         if (i + 1 < n) scores();
         if (!ok || !wait(&X.ds_full, i & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP>(256 + DP, [](int e) { return a_step(128, e); },
-                       base + C::kQRing + at_k.slot * C::kTile, i > 0);
+          mma_rows<DP, 128, 16>(256 + DP, 128, base + C::kQRing + at_k.slot * C::kTile, i > 0);
           ptx::mma_commit(&X.q_empty[at_k.slot]);
           if (i + 1 == n) ptx::mma_commit(&X.done);
         }
@@ -510,139 +503,144 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else {
-    registers_up();
-    if (run) {
-      const int half = warp >> 2, r = tid & 127, key = key0 + r;
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const int used = tokens_in_use(L);
-      const int key_end = key < used ? sequence_of(L, key).end : key;
-      const int first_end = X.first_end;
-      const float c = L.scale * kLog2e;
-      bool ok = true;
-      int b = tile;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % C::kStages, q0 = b * kBlock;
-        const bool masked = b == tile || q0 + kBlock > first_end;
-        const int lo = key - q0 - 64 * half, hi = key_end - q0 - 64 * half;   // lo <= col < hi
-        const uint32_t ts = lanes + 64 * half;
-        const float4* lse2 =
-            reinterpret_cast<const float4*>(sm + C::kStats + s * kStatBytes) + 16 * half;
-        const float4* delta = lse2 + 32;
-        ok = guard.warp_wait(&X.q_full[s], (i / C::kStages) & 1) &&   // the stats
-             guard.warp_wait(&X.s_full, i & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        float p[64];
-        {
-          uint32_t x[2][32];
-          load64(ts, x);
+  } else if (run) {
+    const int group = warp >> 2, quarter = warp & 3;
+    const int r = 32 * quarter + lane, key = key0 + r;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t ts = lanes + 32 * group;
+    const int used = tokens_in_use(L);
+    const int key_end = key < used ? sequence_of(L, key).end : key;
+    const int first_end = X.first_end;
+    const float c = L.scale * kLog2e;
+    const uint64_t c2 = pair(c, c);
+    bool ok = true;
+    int b = tile;
+    Ring<C::kStages> at;
+    for (int i = 0; i < n; ++i) {
+      const int q0 = b * kBlock;
+      const bool masked = b == tile || q0 + kBlock > first_end;
+      const int lo = key - q0 - 32 * group, hi = key_end - 1 - q0 - 32 * group;
+      const float4* lse2 =
+          reinterpret_cast<const float4*>(sm + C::kStats + at.slot * kStatBytes) + 8 * group;
+      ok = guard.warp_wait(&X.q_full[at.slot], at.parity) &&          // the stats
+           guard.warp_wait(&X.s_full, i & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      uint32_t x[32];
+      uint64_t p[16];
+      ptx::tmem_ld32_sync(ts, x);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 z = lse2[e];
-            const int a = e >> 3, o = 4 * (e & 7);
-            p[4 * e] = ex2(fmaf(__uint_as_float(x[a][o]), c, -z.x));
-            p[4 * e + 1] = ex2(fmaf(__uint_as_float(x[a][o + 1]), c, -z.y));
-            p[4 * e + 2] = ex2(fmaf(__uint_as_float(x[a][o + 2]), c, -z.z));
-            p[4 * e + 3] = ex2(fmaf(__uint_as_float(x[a][o + 3]), c, -z.w));
-          }
-        }
-        if (masked) {
+      for (int e = 0; e < 8; ++e) {
+        const float4 z = lse2[e];
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < lo || e >= hi) p[e] = 0.f;
+        for (int k = 0; k < 2; ++k) {
+          const int o = 4 * e + 2 * k;
+          const float2 y =
+              unpair(fma2(pair(__uint_as_float(x[o]), __uint_as_float(x[o + 1])), c2,
+                          k ? pair(-z.z, -z.w) : pair(-z.x, -z.y)));
+          x[o] = __float_as_uint(ex2(y.x));
+          x[o + 1] = __float_as_uint(ex2(y.y));
         }
-        {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pack2(p[2 * e], p[2 * e + 1]);
-          ptx::tmem_st32(ts, w);
-        }
-        if (used < min(q0 + kBlock, L.T)) {      // the block holds padding: clear its Q and dO
-          ok = guard.warp_wait(&X.do_full[s], (i / C::kStages) & 1);
-          if (!ok) break;
-          if (q0 + r >= used)
-            zero_row<DP>(sm + (half ? C::kDoRing : C::kQRing) + s * C::kTile, r);
-          ptx::fence_proxy_async_smem();
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&X.p_full);
-
-        ok = guard.warp_wait(&X.dp_full, i & 1);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        {
-          uint32_t x[2][32];
-          load64(ts + 128, x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 z = delta[e];
-            const int a = e >> 3, o = 4 * (e & 7);
-            p[4 * e] *= __uint_as_float(x[a][o]) - z.x;
-            p[4 * e + 1] *= __uint_as_float(x[a][o + 1]) - z.y;
-            p[4 * e + 2] *= __uint_as_float(x[a][o + 2]) - z.z;
-            p[4 * e + 3] *= __uint_as_float(x[a][o + 3]) - z.w;
-          }
-        }
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e < lo || e >= hi) p[e] = 0.f;
-        }
-        {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = pack2(p[2 * e], p[2 * e + 1]);
-          ptx::tmem_st32(ts + 128, w);
-        }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&X.ds_full);
-        if (++b == tile + blocks) b = tile;
       }
-      if (ok && n > 0) ok = guard.warp_wait(&X.done, 0);
-      if (ok) {
-        ptx::tc_fence_after();
-        // V and K have been read for the last time: dv goes through V's place (warps
-        // 0-3), dk through K's (warps 4-7)
-        uint8_t* stage = half ? sm : sm + C::kV;
-        const float f0 = half ? L.scale : 1.f;
-        float test = 0.f;                              // NaN if an element is not finite
+      if (masked) hide(x, lo, hi, 0u);
+      {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < DP / 32; ++i) {
-          uint32_t o[32];
-          ptx::tmem_ld32_sync(lanes + 256 + DP * half + 32 * i, o);
-          float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            f[e] = key < used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
-            test = fmaf(f[e], 0.f, test);
-          }
-          store_row32(stage, r, 4 * i, f);
+        for (int e = 0; e < 16; ++e) {
+          w[e] = pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+          p[e] = pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         }
-        __syncwarp();
-        unsigned int bad = __ballot_sync(0xffffffffu, key < used && test != 0.f);
-        while (bad) {
-          const int src = __ffs(bad) - 1;
-          bad &= bad - 1;
-          Row dk, dv;
-          dkv_row(L, kh, key - lane + src, __shfl_sync(0xffffffffu, key_end, src), dk, dv);
-          put_row(stage, r - lane + src, half ? dk : dv, DP / 64);
-        }
+        ptx::tmem_st16(ts, w);
+      }
+      if (used < min(q0 + kBlock, L.T)) {        // the block holds padding: clear its Q and dO
+        ok = guard.warp_wait(&X.do_full[at.slot], at.parity);
+        if (!ok) break;
+        if (group < 2 && q0 + r >= used)
+          zero_row<DP>(sm + (group ? C::kDoRing : C::kQRing) + at.slot * C::kTile, r);
         ptx::fence_proxy_async_smem();
-        if (half) asm volatile("bar.sync 2, 128;" ::: "memory");
-        else asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (r == 0) {
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&X.p_full);
+
+      ok = guard.warp_wait(&X.dp_full, i & 1);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      ptx::tmem_ld32_sync(ts + 128, x);
 #pragma unroll
-          for (int i = 0; i < DP / 64; ++i)
-            ptx::tma_store_3d(half ? &M.dk : &M.dv, 64 * i, kh, key0, stage + i * kSlab);
-          ptx::bulk_commit();
-          ptx::bulk_wait<0>();
+      for (int e = 0; e < 8; ++e) {
+        const float4 z = lse2[32 + e];           // delta
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int o = 4 * e + 2 * k;
+          const float2 y =
+              unpair(mul2(p[2 * e + k], add2(pair(__uint_as_float(x[o]), __uint_as_float(x[o + 1])),
+                                             k ? pair(-z.z, -z.w) : pair(-z.x, -z.y))));
+          x[o] = __float_as_uint(y.x);
+          x[o + 1] = __float_as_uint(y.y);
         }
       }
+      if (masked) hide(x, lo, hi, 0u);
+      {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+        ptx::tmem_st16(ts + 128, w);
+      }
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+      at.next();
+      if (++b == tile + blocks) b = tile;
+    }
+    // V and K have been read for the last time: dv goes through V's place (groups 0, 1),
+    // dk through K's (groups 2, 3)
+    const int which = group >> 1, side = group & 1;
+    uint8_t* stage = which ? sm : sm + C::kV;
+    if (ok && n > 0) ok = guard.warp_wait(&X.done, 0);
+    if (ok) {
+      ptx::tc_fence_after();
+      const float f0 = which ? L.scale : 1.f;
+      float test = 0.f;                                // NaN if an element is not finite
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        const int col = DP / 2 * side + 32 * i;
+        uint32_t o[32];
+        ptx::tmem_ld32_sync(lanes + 256 + DP * which + col, o);
+        float f[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          f[e] = key < used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+          test = fmaf(f[e], 0.f, test);
+        }
+        store_row32(stage, r, col / 8, f);
+      }
+      const unsigned int bad = __ballot_sync(0xffffffffu, key < used && test != 0.f);
+      if (bad && lane == 0) atomicOr(&X.repair[which][quarter], bad);
+    }
+    half_barrier(which);                               // (reached by every compute thread)
+    if (ok) {
+      // either side of a row may be bad: the two warps take every other row of the joint set
+      unsigned int bad = X.repair[which][quarter] & (side ? 0xaaaaaaaau : 0x55555555u);
+      while (bad) {
+        const int src = __ffs(bad) - 1;
+        bad &= bad - 1;
+        Row dk, dv;
+        dkv_row(L, kh, key - lane + src, __shfl_sync(0xffffffffu, key_end, src), dk, dv);
+        put_row(stage, r - lane + src, which ? dk : dv, DP / 64);
+      }
+      ptx::fence_proxy_async_smem();
+    }
+    half_barrier(which);
+    if (ok && side == 0 && r == 0 && !X.bad) {
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i)
+        ptx::tma_store_3d(which ? &M.dk : &M.dv, 64 * i, kh, key0, stage + i * kSlab);
+      ptx::bulk_commit();
+      ptx::bulk_wait<0>();
     }
   }
   ptx::tc_fence_before();

@@ -10,17 +10,20 @@
 // begin to its own diagonal block, and only blocks that hold a begin or the diagonal
 // are masked.  No table of tiles is needed, and short sequences share tiles.
 //
-// A CTA takes 256 rows of one head as two tiles of 128.  While a warpgroup turns one
-// tile's S into P, the tensor cores run the other tile's products:
+// A CTA takes 256 rows of one head as two tiles of 128.  While the compute warps turn
+// one tile's S into P, the tensor cores run the other tile's products:
 //   warps 0-3, 4-7  softmax of tile 0, 1 (a thread owns a row), then the epilogue
 //   warp 8          TMA: Q once, then K and V blocks through a ring
 //   warp 9          MMA: per block and tile  O += P V, then S of the next block
 //   warps 10, 11    leave their registers to the softmax
-// TMEM: S of each tile (128 columns; P overwrites its first 64 as bf16 pairs, the A
-// operand of P V), O of each tile.  tcgen05 ops of one thread run in order, so the
-// commit that announces S of block b + 1 also says that P V of block b is done: O may
-// be rescaled before P of block b + 1 is handed over.  O is rescaled only when the
-// maximum grows by more than 2^8 (P stays below 2^8; fp32 sums and O hold that
+// (Two threads a row, with 16 warps for the softmax, were measured slower: 2204 against
+// 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs more than
+// the other warps hide.)
+// TMEM: S of each tile (128 columns; P overwrites the first 64 as bf16 pairs, the A operand
+// of P V, handed over in two halves), O of each tile.  tcgen05 ops of one thread run in
+// order, so the commit that announces S of block b + 1 also says that P V of block b is
+// done: O may be rescaled before P of block b + 1 is handed over.  O is rescaled only when
+// the maximum grows by more than 2^8 (P stays below 2^8; fp32 sums and O hold that
 // easily), so nearly never after the first blocks.
 // P is rounded to bf16, the tensor cores' input; l sums the unrounded values.
 #include <climits>
@@ -33,35 +36,69 @@ namespace {
 using namespace attn;
 
 constexpr int kTiles = 2;
-constexpr int kProducerWarp = 4 * kTiles, kMmaWarp = kProducerWarp + 1;
 constexpr float kRescale = 8.f;        // log2 growth of the maximum that triggers a rescale
+
+constexpr int kProducerWarp = 4 * kTiles, kMmaWarp = kProducerWarp + 1;
+constexpr int kThreads = 384;
+constexpr uint32_t kMiscBytes = 512;
+
+// Registers move from the warps that only issue work to those that compute: a block is
+// launched with 168 a thread (64512), of which 4 warps keep kIssueRegs and 8 get
+// kComputeRegs.  The issuing roles must fit kIssueRegs as compiled without the split (62):
+// with 40 the compiler's allocation was seen to break (waits ran into their limit).
+constexpr int kIssueRegs = 104, kComputeRegs = 200;
+static_assert(128 * kIssueRegs + 256 * kComputeRegs == kThreads * 168,
+              "no more registers than at launch");
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+}
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+}
 
 template <int DP> struct Cfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kStages = DP == 128 ? 5 : 8;
   static constexpr uint32_t kRing = kTiles * kTile;          // after Q
   static constexpr uint32_t kMisc = kRing + kStages * kTile;
-  static constexpr uint32_t kSmem = kMisc + 512 + 1024;
+  static constexpr uint32_t kSmem = kMisc + kMiscBytes;
 };
 
 struct Misc {
   uint64_t full[8], empty[8];
-  uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], o_full[kTiles];
+  uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles][2], o_full[kTiles];
   uint64_t drain;
   uint32_t tmem;
   int bad, skip;                       // abort flag; the workspace had failed before
   int first[kTiles], last[kTiles];     // begin of the first and last row of each tile
 };
-static_assert(sizeof(Misc) <= 512, "misc block");
+static_assert(sizeof(Misc) <= kMiscBytes, "misc block");
+
+__device__ __forceinline__ float row_max(const uint32_t (&s)[32]) {
+  float x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    x[j] = max3(__uint_as_float(s[j]), __uint_as_float(s[j + 4]), __uint_as_float(s[j + 8]));
+#pragma unroll
+  for (int j = 12; j < 28; j += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      x[e] = max3(x[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + 4 + e]));
+  const float a = max3(x[0], __uint_as_float(s[28]), __uint_as_float(s[29]));
+  const float b = max3(x[1], __uint_as_float(s[30]), __uint_as_float(s[31]));
+  return max3(a, b, fmaxf(x[2], x[3]));
+}
+
+__device__ __forceinline__ void tile_barrier(int t) {   // the four warps of a tile
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_fwd_kernel(const __grid_constant__ AttentionMaps M,
                          const __grid_constant__ AttentionLaunch L) {
   using C = Cfg<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   Misc& X = *reinterpret_cast<Misc*>(sm + C::kMisc);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -87,12 +124,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < kTiles; ++t) {
       ptx::mbar_init(&X.q_full[t], 1);
       ptx::mbar_init(&X.s_full[t], 1);
-      ptx::mbar_init(&X.p_full[t], 4);
+      ptx::mbar_init(&X.p_full[t][0], 4);
+      ptx::mbar_init(&X.p_full[t][1], 4);
       ptx::mbar_init(&X.o_full[t], 1);
     }
     ptx::mbar_init(&X.drain, 1);
     X.bad = 0;
     X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&M.q);
     ptx::prefetch_tmap(&M.k);
@@ -158,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<C::kStages> at;               // next slot of the ring
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && guard.warp_wait(bar, parity);
+        ok = ok && guard.issue_wait(bar, parity);
         if (ok) ptx::tc_fence_after();
         return ok;
       };
@@ -185,10 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ks = b + 1 < end ? take() : -1;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-          if (ok && active(t, b) && wait(&X.p_full[t], (b - b0[t]) & 1)) {
-            if (ptx::elect_one()) {
-              mma_rows<DP>(128 * kTiles + DP * t, [t](int i) { return 128u * t + 8 * i; },
-                           ring + vs * C::kTile, b > b0[t]);
+          if (ok && active(t, b)) {
+            const uint32_t parity = (b - b0[t]) & 1, v = ring + vs * C::kTile;
+            if (wait(&X.p_full[t][0], parity) && ptx::elect_one())
+              mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t, v, b > b0[t]);
+            if (wait(&X.p_full[t][1], parity) && ptx::elect_one()) {
+              mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t + 32, v + 8192, true);
               if (b + 1 == b1[t]) ptx::mma_commit(&X.o_full[t]);
             }
           }
@@ -209,40 +253,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     registers_up();
     if (run) {
-      const int t = warp >> 2, r = tid & 127;
-      const int row = row0 + 128 * t + r;
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const int t = warp >> 2, r = tid & 127, row = row0 + 128 * t + r;
+      const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       const uint32_t ts = lanes + 128 * t, to = lanes + 128 * kTiles + DP * t;
       const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
-      const int last_begin = X.last[t];
+      const int last_begin = X.last[t], first_block = b0[t], blocks_end = b1[t];
       const int used = tokens_in_use(L);
       const float c = L.scale * kLog2e;
+      const uint64_t c2 = pair(c, c);
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int b = b0[t]; b < b1[t]; ++b) {
-        ok = guard.warp_wait(&X.s_full[t], (b - b0[t]) & 1);
+      for (int b = first_block; b < blocks_end; ++b) {
+        const int k0 = b * kBlock;
+        ok = guard.warp_wait(&X.s_full[t], (b - first_block) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
         uint32_t s[4][32];
-        ptx::tmem_ld128_sync(ts, s);
-        const int k0 = b * kBlock;
-        if (k0 < last_begin || b + 1 == b1[t]) {
-          const int lo = row_begin - k0, hi = row - k0;      // visible columns
+        ptx::tmem_ld32x2_sync(ts, ts + 32, s[0], s[1]);
+        ptx::tmem_ld32x2_sync(ts + 64, ts + 96, s[2], s[3]);
+        if (k0 < last_begin || b + 1 == blocks_end) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * i + j < lo || 32 * i + j > hi) s[i][j] = 0xff800000u;
+            hide(s[i], row_begin - k0 - 32 * i, row - k0 - 32 * i, 0xff800000u);
         }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-          for (int j = 1; j < 32; ++j) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][j]));
-        }
-        const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (b == b0[t]) {
+        const float mb = fmaxf(fmaxf(row_max(s[0]), row_max(s[1])),
+                               fmaxf(row_max(s[2]), row_max(s[3])));
+        if (b == first_block) {
           m = mb;
         } else {
           const bool grow = mb > m && !((mb - m) * c <= kRescale);
@@ -250,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = grow ? ex2((m - mb) * c) : 1.f;
             if (grow) m = mb;
             l *= f;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < DP / 32; ++i) {
               uint32_t o[32];
               ptx::tmem_ld32_sync(to + 32 * i, o);
@@ -260,21 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float mc = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t p[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x = ex2(fmaf(__uint_as_float(s[i][2 * j]), c, -mc));
-            const float y = ex2(fmaf(__uint_as_float(s[i][2 * j + 1]), c, -mc));
-            sum[j & 3] += x + y;
-            p[j] = pack2(x, y);
-          }
-          ptx::tmem_st16(ts + 16 * i, p);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         if (used < min(k0 + kBlock, L.T)) {            // the block holds padding: clear its V
           const int n = 2 * (b - begin) + 1, slot = n % C::kStages;
           ok = guard.warp_wait(&X.full[slot], (n / C::kStages) & 1);
@@ -282,53 +303,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k0 + r >= used) zero_row<DP>(sm + C::kRing + slot * C::kTile, r);
           ptx::fence_proxy_async_smem();
         }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&X.p_full[t]);
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const uint64_t mc2 = pair(-mc, -mc);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = unpair(fma2(pair(__uint_as_float(s[i][2 * j]),
+                                              __uint_as_float(s[i][2 * j + 1])), c2, mc2));
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            sum[j & 1] = add2(sum[j & 1], pair(y.x, y.y));
+            p[j] = pack2(y.x, y.y);
+          }
+          ptx::tmem_st16(ts + 16 * i, p);
+          if (i & 1) {                                 // half of P is ready for its product
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&X.p_full[t][i >> 1]);
+          }
+        }
+        const float2 a = unpair(add2(sum[0], sum[1]));
+        l += a.x + a.y;
       }
-      if (ok && b1[t] > 0) {
-        ok = guard.warp_wait(&X.o_full[t], 0);
+      if (ok && blocks_end > 0) ok = guard.warp_wait(&X.o_full[t], 0);
+      if (ok && blocks_end > 0) {
         ptx::tc_fence_after();
-        if (ok) {
-          // Q of this tile has been read for the last time: out goes through its place
-          uint8_t* stage = sm + t * C::kTile;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          float test = 0.f;                            // NaN if an element is not finite
+        // Q of this tile has been read for the last time: out goes through its place
+        uint8_t* stage = sm + t * C::kTile;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float test = 0.f;                              // NaN if an element is not finite
 #pragma unroll
-          for (int i = 0; i < DP / 32; ++i) {
-            uint32_t o[32];
-            ptx::tmem_ld32_sync(to + 32 * i, o);
-            float f[32];
+        for (int i = 0; i < DP / 32; ++i) {
+          uint32_t o[32];
+          ptx::tmem_ld32_sync(to + 32 * i, o);
+          float f[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              f[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
-              test = fmaf(f[j], 0.f, test);
-            }
-            store_row32(stage, r, 4 * i, f);
+          for (int j = 0; j < 32; ++j) {
+            f[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
+            test = fmaf(f[j], 0.f, test);
           }
-          if (row < L.T)
-            L.lse[static_cast<size_t>(h) * L.T + row] =
-                l == 0.f ? -INFINITY : m * L.scale + __logf(l);
-          __syncwarp();
-          unsigned int bad = __ballot_sync(0xffffffffu, row < L.T && test != 0.f);
-          while (bad) {
-            const int src = __ffs(bad) - 1;
-            bad &= bad - 1;
-            const int i = row - lane + src;
-            put_row(stage, r - lane + src,
-                    out_row(L, h, i, __shfl_sync(0xffffffffu, row_begin, src)), DP / 64);
-          }
-          ptx::fence_proxy_async_smem();
-          if (t == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
-          else asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (r == 0) {
+          store_row32(stage, r, 4 * i, f);
+        }
+        if (row < L.T)
+          L.lse[static_cast<size_t>(h) * L.T + row] =
+              l == 0.f ? -INFINITY : m * L.scale + __logf(l);
+        __syncwarp();
+        unsigned int bad = __ballot_sync(0xffffffffu, row < L.T && test != 0.f);
+        while (bad) {
+          const int src = __ffs(bad) - 1;
+          bad &= bad - 1;
+          put_row(stage, r - lane + src,
+                  out_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
+                  DP / 64);
+        }
+        ptx::fence_proxy_async_smem();
+      }
+      if (blocks_end > 0) {
+        tile_barrier(t);                               // (reached by every thread of the tile)
+        if (ok && r == 0 && !X.bad) {
 #pragma unroll
-            for (int i = 0; i < DP / 64; ++i)
-              ptx::tma_store_3d(&M.out, 64 * i, h, row0 + 128 * t, stage + i * kSlab);
-            ptx::bulk_commit();
-            ptx::bulk_wait<0>();
-          }
+          for (int i = 0; i < DP / 64; ++i)
+            ptx::tma_store_3d(&M.out, 64 * i, h, row0 + 128 * t, sm + t * C::kTile + i * kSlab);
+          ptx::bulk_commit();
+          ptx::bulk_wait<0>();
         }
       }
     }
