@@ -14,8 +14,10 @@
 // one tile's S into P, the tensor cores run the other tile's products:
 //   warps 0-3, 4-7  softmax of tile 0, 1 (a thread owns a row), then the epilogue
 //   warp 8          TMA: Q once, then K and V blocks through a ring
-//   warp 9          MMA: per block and tile  O += P V, then S of the next block
-//   warps 10, 11    leave their registers to the softmax
+//   warps 9, 10     MMA of tile 0, 1: per block  O += P V, then S of the next block.  (One
+//                   warp for both took 1500 cycles of waits and commits between its
+//                   products, with the tensor cores idle.)
+//   warp 11         leaves its registers to the softmax
 // (Two threads a row, with 16 warps for the softmax, were measured slower: 2204 against
 // 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs more than
 // the other warps hide.)
@@ -38,7 +40,7 @@ using namespace attn;
 constexpr int kTiles = 2;
 constexpr float kRescale = 8.f;        // log2 growth of the maximum that triggers a rescale
 
-constexpr int kProducerWarp = 4 * kTiles, kMmaWarp = kProducerWarp + 1;
+constexpr int kProducerWarp = 4 * kTiles, kMmaWarp = kProducerWarp + 1;   // and one a tile
 constexpr int kThreads = 384;
 constexpr uint32_t kMiscBytes = 512;
 
@@ -67,7 +69,7 @@ template <int DP> struct Cfg {
 struct Misc {
   uint64_t full[8], empty[8];
   uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles][2], o_full[kTiles];
-  uint64_t drain;
+  uint64_t drain[kTiles];
   uint32_t tmem;
   int bad, skip;                       // abort flag; the workspace had failed before
   int first[kTiles], last[kTiles];     // begin of the first and last row of each tile
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&X.full[s], 1);
-      ptx::mbar_init(&X.empty[s], 1);
+      ptx::mbar_init(&X.empty[s], kTiles);
     }
     for (int t = 0; t < kTiles; ++t) {
       ptx::mbar_init(&X.q_full[t], 1);
@@ -127,8 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&X.p_full[t][0], 4);
       ptx::mbar_init(&X.p_full[t][1], 4);
       ptx::mbar_init(&X.o_full[t], 1);
+      ptx::mbar_init(&X.drain[t], 1);
     }
-    ptx::mbar_init(&X.drain, 1);
     X.bad = 0;
     X.skip = ptx::status_set(L.status);
     if (!tiles_aligned(sm)) {
@@ -195,13 +197,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                            kDrainNs);
         }
       }
-    } else if (run && warp == kMmaWarp) {
-      const uint32_t sq = ptx::smem_u32(sm), ring = sq + C::kRing;
+    } else if (run && warp < kMmaWarp + kTiles) {
+      const int t = warp - kMmaWarp;
+      const int first = b0[t], last = b1[t];
+      const uint32_t q = ptx::smem_u32(sm) + t * C::kTile;
+      const uint32_t ring = ptx::smem_u32(sm) + C::kRing;
       Ring<C::kStages> at;               // next slot of the ring
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && guard.issue_wait(bar, parity);
-        if (ok) ptx::tc_fence_after();
         return ok;
       };
       auto take = [&] {
@@ -210,43 +214,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.next();
         return s;
       };
-      auto scores = [&](int t, int b, int slot) {
-        if (b == b0[t] && !wait(&X.q_full[t], 0)) return;
+      // S of a block (if the tile has it), then the K slot is free
+      auto scores = [&](int b, int slot) {
+        const bool mine = b >= first && b < last;
+        if (mine && b == first) wait(&X.q_full[t], 0);
+        if (!ok) return;
+        ptx::tc_fence_after();
         if (ptx::elect_one()) {
-          mma_heads<DP>(128 * t, sq + t * C::kTile, ring + slot * C::kTile);
-          ptx::mma_commit(&X.s_full[t]);
+          if (mine) {
+            mma_heads<DP>(128 * t, q, ring + slot * C::kTile);
+            ptx::mma_commit(&X.s_full[t]);
+          }
+          ptx::mma_commit(&X.empty[slot]);
         }
       };
-      int ks = take();
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-        if (ok && active(t, begin)) scores(t, begin, ks);
-      if (ok && ptx::elect_one()) ptx::mma_commit(&X.empty[ks]);
+      if (begin < end) scores(begin, take());
       for (int b = begin; b < end && ok; ++b) {
         const int vs = take();
-        ks = b + 1 < end ? take() : -1;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (ok && active(t, b)) {
-            const uint32_t parity = (b - b0[t]) & 1, v = ring + vs * C::kTile;
-            if (wait(&X.p_full[t][0], parity) && ptx::elect_one())
-              mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t, v, b > b0[t]);
-            if (wait(&X.p_full[t][1], parity) && ptx::elect_one()) {
-              mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t + 32, v + 8192, true);
-              if (b + 1 == b1[t]) ptx::mma_commit(&X.o_full[t]);
-            }
+        const int ks = b + 1 < end ? take() : -1;
+        if (ok && b >= first && b < last) {
+          const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
+          if (!wait(&X.p_full[t][0], parity)) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one())
+            mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t, v, b > first);
+          if (!wait(&X.p_full[t][1], parity)) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t + 32, v + 8192, true);
+            if (b + 1 == last) ptx::mma_commit(&X.o_full[t]);
           }
-          if (ok && active(t, b + 1)) scores(t, b + 1, ks);
         }
-        if (!ok) break;
-        if (ptx::elect_one()) {
-          ptx::mma_commit(&X.empty[vs]);
-          if (ks >= 0) ptx::mma_commit(&X.empty[ks]);
-        }
+        if (ks >= 0) scores(b + 1, ks);
+        if (ok && ptx::elect_one()) ptx::mma_commit(&X.empty[vs]);
       }
       if (!ok) {                         // products in flight end before TMEM is freed
-        if (ptx::elect_one()) ptx::mma_commit(&X.drain);
-        ptx::mbar_wait(&X.drain, 0, nullptr, nullptr, kDrainNs);
+        if (ptx::elect_one()) ptx::mma_commit(&X.drain[t]);
+        ptx::mbar_wait(&X.drain[t], 0, nullptr, nullptr, kDrainNs);
         __syncwarp();
       }
     }
