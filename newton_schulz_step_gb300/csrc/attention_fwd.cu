@@ -14,9 +14,11 @@
 // one tile's S into P, the tensor cores run the other tile's products:
 //   warps 0-3, 4-7  softmax of tile 0, 1 (a thread owns a row), then the epilogue
 //   warp 8          TMA: Q once, then K and V blocks through a ring
-//   warps 9, 10     MMA of tile 0, 1: per block  O += P V, then S of the next block.  (One
-//                   warp for both took 1500 cycles of waits and commits between its
-//                   products, with the tensor cores idle.)
+//   warps 9, 10     MMA of tile 0, 1: per block  O += P V, then S of the next block, in
+//                   turns, so that one tile's softmax falls on the other's products.
+//                   (One warp for both took 1500 cycles of waits and commits between its
+//                   products, with the tensor cores idle; without turns the tiles fall
+//                   into step.)
 //   warp 11         leaves its registers to the softmax
 // (Two threads a row, with 16 warps for the softmax, were measured slower: 2204 against
 // 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs more than
@@ -69,7 +71,7 @@ template <int DP> struct Cfg {
 struct Misc {
   uint64_t full[8], empty[8];
   uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles][2], o_full[kTiles];
-  uint64_t drain[kTiles];
+  uint64_t drain[kTiles], turn[kTiles];
   uint32_t tmem;
   int bad, skip;                       // abort flag; the workspace had failed before
   int first[kTiles], last[kTiles];     // begin of the first and last row of each tile
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&X.p_full[t][1], 4);
       ptx::mbar_init(&X.o_full[t], 1);
       ptx::mbar_init(&X.drain[t], 1);
+      ptx::mbar_init(&X.turn[t], 1);
     }
     X.bad = 0;
     X.skip = ptx::status_set(L.status);
@@ -232,9 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = begin; b < end && ok; ++b) {
         const int vs = take();
         const int ks = b + 1 < end ? take() : -1;
-        if (ok && b >= first && b < last) {
-          const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
-          if (!wait(&X.p_full[t][0], parity)) break;
+        const bool mine = b >= first && b < last;
+        const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
+        if (mine) wait(&X.p_full[t][0], parity);
+        // the tiles take turns: tile 0 waits for tile 1's last block, tile 1 for this one
+        if (!wait(&X.turn[t], ((b - begin) & 1) ^ (t == 0 ? 1 : 0))) break;
+        if (mine) {
           ptx::tc_fence_after();
           if (ptx::elect_one())
             mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t, v, b > first);
@@ -246,7 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (ks >= 0) scores(b + 1, ks);
-        if (ok && ptx::elect_one()) ptx::mma_commit(&X.empty[vs]);
+        if (ok && ptx::elect_one()) {
+          ptx::mbar_arrive(&X.turn[t ^ 1]);
+          ptx::mma_commit(&X.empty[vs]);
+        }
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain[t]);
