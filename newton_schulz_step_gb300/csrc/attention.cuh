@@ -167,6 +167,17 @@ __device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b) {
     for (int i = 0; i < 4; ++i)
       ptx::mma_bf16(d, desc_k(a + s * kSlab, i), desc_k(b + s * kSlab, i), kId, s > 0 || i > 0);
 }
+// The same with A in TMEM (bf16 pairs, DP / 2 columns): a product from shared memory alone
+// reads 8 KB of it for 64 cycles of a 128 x 128 x 16 step, all that it delivers.
+template <int DP>
+__device__ __forceinline__ void mma_heads_ts(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t kId = ptx::idesc_bf16(128, 128, false);
+#pragma unroll 1
+  for (uint32_t s = 0; s < DP / 64; ++s)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ptx::mma_bf16_ts(d, a + 32 * s + 8 * i, desc_k(b + s * kSlab, i), kId, s > 0 || i > 0);
+}
 // D (+)= A[tmem] B over the first kRows rows of B.  A: bf16 pairs, kRun columns (of 32
 // bits) from `a`, the next from a + 2 kRun, and so on
 template <int DP, int kRows, int kRun>

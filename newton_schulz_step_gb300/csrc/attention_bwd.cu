@@ -39,20 +39,23 @@ __device__ __forceinline__ void half_barrier(int half) {   // the lower or upper
 }
 
 // ------------------------------------------------------------------ dq
-// TMEM: S of even and odd blocks (0, 128), dP (256), dq (384).  Per block, in the
-// tensor cores' order: dP of the next block, dq += dS K, S of the block after next; so
-// the exponentials of a block run beside the products of the one before.
+// TMEM: S (0), dP (128; dS over it), dq (256), Q and dO (384, 448) as bf16 pairs: as the A
+// operands of S and dP from there, those products read half as much shared memory (from
+// shared memory they ran at 106 cycles a step instead of 64, dq of 8192 tokens, 32/8
+// heads of 128, in 632 us).  Per block, in the tensor cores' order: S of the next block,
+// dq += dS K, dP of the next block; so S and the exponentials of a block run beside the
+// work on the one before.
 template <int DP> struct DqCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
-  static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
-  static constexpr uint32_t kDo = kTile, kKRing = 2 * kTile, kVRing = kKRing + kK * kTile;
+  static constexpr int kK = 4, kV = 3;                       // ring slots
+  static constexpr uint32_t kVRing = kK * kTile;
   static constexpr uint32_t kMisc = kVRing + kV * kTile, kMiscBytes = 2560;
   static constexpr uint32_t kSmem = kMisc + kMiscBytes;
 };
 
 struct DqMisc {
-  uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], dp_full, ds_full, dq_full, drain;
+  uint64_t q_ready, k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full, s_read, dp_full, ds_full, dq_full, drain;
   uint32_t tmem;
   int bad, skip;
   int first, last;                 // begin of the tile's first and last row
@@ -84,15 +87,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid < 4) X.repair[tid] = 0;
   if (warp == kProducerWarp && lane == 0) {
-    ptx::mbar_init(&X.q_full, 2);
+    ptx::mbar_init(&X.q_ready, 16);
     for (int s = 0; s < 4; ++s) {
       ptx::mbar_init(&X.k_full[s], 1);
       ptx::mbar_init(&X.k_empty[s], 1);
       ptx::mbar_init(&X.v_full[s], 1);
       ptx::mbar_init(&X.v_empty[s], 1);
     }
-    ptx::mbar_init(&X.s_full[0], 1);
-    ptx::mbar_init(&X.s_full[1], 1);
+    ptx::mbar_init(&X.s_full, 1);
+    ptx::mbar_init(&X.s_read, 16);
     ptx::mbar_init(&X.dp_full, 1);
     ptx::mbar_init(&X.ds_full, 16);
     ptx::mbar_init(&X.dq_full, 1);
@@ -104,8 +107,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       X.skip = 1;
     }
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&M.q);
-    ptx::prefetch_tmap(&M.dout);
     ptx::prefetch_tmap(&M.k);
     ptx::prefetch_tmap(&M.v);
   }
@@ -127,21 +128,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducerWarp) {
     if (run && warp == kProducerWarp) {
       if (lane == 0) {
-        load_tile<DP>(sm, &M.q, h, row0, &X.q_full);
-        load_tile<DP>(sm + C::kDo, &M.dout, h, row0, &X.q_full);
         int j = 0;
         bool ok = true;
         for (; j < n && ok; ++j) {
           const int ks = j % C::kK, vs = j % C::kV, row = (begin + j) * kBlock;
           if (j >= C::kK) ok = guard.wait_or_fail(&X.k_empty[ks], (j / C::kK - 1) & 1);
           if (!ok) break;
-          load_tile<DP>(sm + C::kKRing + ks * C::kTile, &M.k, kh, row, &X.k_full[ks]);
+          load_tile<DP>(sm + ks * C::kTile, &M.k, kh, row, &X.k_full[ks]);
           if (j >= C::kV) ok = guard.wait_or_fail(&X.v_empty[vs], (j / C::kV - 1) & 1);
           if (!ok) break;
           load_tile<DP>(sm + C::kVRing + vs * C::kTile, &M.v, kh, row, &X.v_full[vs]);
         }
         if (!ok) {                       // copies in flight land before the CTA ends
-          ptx::mbar_wait(&X.q_full, 0, nullptr, nullptr, kDrainNs);
           for (int i = j > C::kK ? j - C::kK : 0; i <= j; ++i) {
             ptx::mbar_wait(&X.k_full[i % C::kK], (i / C::kK) & 1, nullptr, nullptr, kDrainNs);
             if (i < j)
@@ -159,38 +157,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ptx::tc_fence_after();
         return ok;
       };
-      auto scores = [&](int j) {
+      auto scores = [&] {
         if (!wait(&X.k_full[at_s.slot], at_s.parity)) return;
         if (ptx::elect_one()) {
-          mma_heads<DP>(128 * (j & 1), base, base + C::kKRing + at_s.slot * C::kTile);
-          ptx::mma_commit(&X.s_full[j & 1]);
+          mma_heads_ts<DP>(0, 384, base + at_s.slot * C::kTile);
+          ptx::mma_commit(&X.s_full);
         }
         at_s.next();
       };
       auto dp = [&] {
         if (!wait(&X.v_full[at_v.slot], at_v.parity)) return;
         if (ptx::elect_one()) {
-          mma_heads<DP>(256, base + C::kDo, base + C::kVRing + at_v.slot * C::kTile);
+          mma_heads_ts<DP>(128, 448, base + C::kVRing + at_v.slot * C::kTile);
           ptx::mma_commit(&X.dp_full);
           ptx::mma_commit(&X.v_empty[at_v.slot]);
         }
         at_v.next();
       };
-      wait(&X.q_full, 0);
-      if (ok) scores(0);
+      wait(&X.q_ready, 0);
+      if (ok) scores();
       if (ok) dp();
-      if (ok && n > 1) scores(1);
       for (int j = 0; j < n && ok; ++j) {
-        if (!wait(&X.ds_full, j & 1)) break;
-        if (j + 1 < n) dp();
-        if (!ok) break;
+        if (j + 1 < n && wait(&X.s_read, j & 1)) scores();
+        if (!ok || !wait(&X.ds_full, j & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP, 128, 16>(384, 128 * (j & 1), base + C::kKRing + at_q.slot * C::kTile, j > 0);
+          mma_rows<DP, 128, 16>(256, 128, base + at_q.slot * C::kTile, j > 0);
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
         }
         at_q.next();
-        if (j + 2 < n) scores(j + 2);
+        if (j + 1 < n) dp();
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain);
@@ -206,27 +202,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
     const int last_begin = X.last;
     const float c = L.scale * kLog2e;
-    // delta, a quarter of the columns each; lse in base 2, +inf (p = 0) for rows without keys
+    // Q and dO to TMEM, 32 columns of a row each, with their part of delta; lse in base 2,
+    // +inf (p = 0) for rows without keys
     float delta = 0.f, lse2 = INFINITY;
-    if (row < used) {
-      const __nv_bfloat16 *o = L.o.row(row, h), *g = L.dout.row(row, h);
+    if (32 * group < DP) {
+      uint32_t a[16], g[16];
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        const int d = DP / 4 * group + 8 * i;
-        if (d < L.dim) {
-          const uint4 a = *reinterpret_cast<const uint4*>(o + d);
-          const uint4 b = *reinterpret_cast<const uint4*>(g + d);
-          const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+      for (int i = 0; i < 16; ++i) a[i] = g[i] = 0u;
+      if (row < L.T) {
+        const __nv_bfloat16 *q = L.q.row(row, h), *o = L.o.row(row, h), *w = L.dout.row(row, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            delta = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), delta);
-            delta = fmaf(__uint_as_float(x[e] & 0xffff0000u),
-                         __uint_as_float(y[e] & 0xffff0000u), delta);
+        for (int i = 0; i < 4; ++i) {
+          const int d = 32 * group + 8 * i;
+          if (d < L.dim) {
+            const uint4 x = *reinterpret_cast<const uint4*>(q + d);
+            const uint4 y = *reinterpret_cast<const uint4*>(w + d);
+            const uint4 z = *reinterpret_cast<const uint4*>(o + d);
+            a[4 * i] = x.x; a[4 * i + 1] = x.y; a[4 * i + 2] = x.z; a[4 * i + 3] = x.w;
+            g[4 * i] = y.x; g[4 * i + 1] = y.y; g[4 * i + 2] = y.z; g[4 * i + 3] = y.w;
+            const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              delta = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(g[4 * i + e] << 16), delta);
+              delta = fmaf(__uint_as_float(u[e] & 0xffff0000u),
+                           __uint_as_float(g[4 * i + e] & 0xffff0000u), delta);
+            }
           }
         }
       }
-      lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
+      ptx::tmem_st16(lanes + 384 + 16 * group, a);
+      ptx::tmem_st16(lanes + 448 + 16 * group, g);
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&X.q_ready);
+    if (row < used) lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
+    else delta = 0.f;
     X.delta[group][r] = delta;
     compute_barrier();
     delta = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
@@ -237,13 +249,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int k0 = (begin + j) * kBlock;
-      const uint32_t ts = lanes + 128 * (j & 1) + 32 * group;
-      ok = guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1);
+      ok = guard.warp_wait(&X.s_full, j & 1);
       if (!ok) break;
       ptx::tc_fence_after();
       uint32_t x[32];
       uint64_t p[16];
-      ptx::tmem_ld32_sync(ts, x);
+      ptx::tmem_ld32_sync(lanes + 32 * group, x);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&X.s_read);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 y = unpair(
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = guard.warp_wait(&X.dp_full, j & 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      ptx::tmem_ld32_sync(lanes + 256 + 32 * group, x);
+      ptx::tmem_ld32_sync(lanes + 128 + 32 * group, x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 y = unpair(mul2(
@@ -267,10 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-      ptx::tmem_st16(ts, w);
+      ptx::tmem_st16(lanes + 128 + 32 * group, w);
       if (used < min(k0 + kBlock, L.T)) {              // the block holds padding: clear its K
         const int s = j % C::kK;                       // (landed: S has read it)
-        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
+        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + s * C::kTile, r);
         ptx::fence_proxy_async_smem();
       }
       ptx::tmem_st_wait();
@@ -281,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) ok = guard.warp_wait(&X.dq_full, 0);
     if (ok && 32 * group < DP) {
       ptx::tc_fence_after();
-      // Q has been read for the last time: dq goes through its place
+      // K has been read for the last time: dq goes through its place
       float test = 0.f;                                // NaN if an element is not finite
       uint32_t o[32];
-      ptx::tmem_ld32_sync(lanes + 384 + 32 * group, o);
+      ptx::tmem_ld32_sync(lanes + 256 + 32 * group, o);
       float f[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < DP / 64; ++i)
         ptx::tma_store_3d(&M.dq, 64 * i, h, row0, sm + i * kSlab);
       ptx::bulk_commit();
-      ptx::bulk_wait<0>();
+      ptx::bulk_wait_read<0>();
     }
   }
   ptx::tc_fence_before();
@@ -640,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < DP / 64; ++i)
         ptx::tma_store_3d(which ? &M.dk : &M.dv, 64 * i, kh, key0, stage + i * kSlab);
       ptx::bulk_commit();
-      ptx::bulk_wait<0>();
+      ptx::bulk_wait_read<0>();
     }
   }
   ptx::tc_fence_before();

@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < DP / 64; ++i)
             ptx::tma_store_3d(&M.out, 64 * i, h, row0 + 128 * t, sm + t * C::kTile + i * kSlab);
           ptx::bulk_commit();
-          ptx::bulk_wait<0>();
+          ptx::bulk_wait_read<0>();
         }
       }
     }
