@@ -267,7 +267,7 @@ muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_h
     const double heads = 2.0 * L.T * (2.0 * L.hq + 2.0 * L.hk) * L.dim;
     const cudaError_t e =
         counted_launch(st, MUON_K_ATTENTION, 4.0 * L.dim * pair_bound(L), heads,
-                       [&] { return launch_attention(M, L, st); });
+                       [&] { return launch_attention(M, L, sms, st); });
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   } catch (...) {
     return MUON_ERR_CUDA;
@@ -316,11 +316,11 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
     const double row = 2.0 * L.T * L.dim;
     cudaError_t e = counted_launch(
         st, MUON_K_ATTENTION_DQ, 6.0 * L.dim * pair_bound(L), row * (4.0 * L.hq + 2.0 * L.hk),
-        [&] { return launch_attention_dq(M, L, st); });
+        [&] { return launch_attention_dq(M, L, sms, st); });
     if (e != cudaSuccess) return MUON_ERR_CUDA;
     e = counted_launch(st, MUON_K_ATTENTION_DKV, 8.0 * L.dim * pair_bound(L),
                        row * (2.0 * L.hq + 4.0 * L.hk),
-                       [&] { return launch_attention_dkv(M, L, st); });
+                       [&] { return launch_attention_dkv(M, L, sms, st); });
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   } catch (...) {
     return MUON_ERR_CUDA;

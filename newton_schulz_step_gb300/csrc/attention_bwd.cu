@@ -74,10 +74,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  // the last tiles hold the most keys: they go first
+  // of one sequence, the last tiles hold the most keys: they go first
   const int tiles = (L.T + 127) / 128;
   const int h = static_cast<int>(blockIdx.x) % L.hq;
-  const int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
+  int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
+  if (L.ranked)
+    tile = ranked_tile(tiles, static_cast<int>(blockIdx.x) / L.hq, reinterpret_cast<int*>(sm),
+                       [&](int i) { return i - sequence_of(L, 128 * i).begin / kBlock; });
   const int row0 = 128 * tile, kh = h / L.group;
 
   if (tid < 2) {
@@ -374,10 +377,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  // the first tiles are seen by the most queries: they go first
+  // of one sequence, the first tiles are seen by the most queries: they go first
   const int tiles = (L.T + 127) / 128;
   const int kh = static_cast<int>(blockIdx.x) % L.hk;
-  const int tile = static_cast<int>(blockIdx.x) / L.hk;
+  int tile = static_cast<int>(blockIdx.x) / L.hk;
+  if (L.ranked)
+    tile = ranked_tile(tiles, tile, reinterpret_cast<int*>(sm), [&](int i) {
+      const Span s = sequence_of(L, min(128 * i + 127, L.T - 1));
+      return s.end / kBlock - i;
+    });
   const int key0 = 128 * tile;
 
   if (tid == 0) {
@@ -666,30 +674,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename K>
-cudaError_t launch(K kernel, int blocks, uint32_t smem, const AttentionMaps& m,
-                   const AttentionLaunch& l, cudaStream_t s) {
+cudaError_t launch(K kernel, int heads, uint32_t smem, const AttentionMaps& m,
+                   AttentionLaunch& l, int sms, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, kThreads, smem, s>>>(m, l);
+  const int tiles = (l.T + 127) / 128;
+  l.ranked = l.n_seqs > 1 && tiles <= kRankedTiles && tiles * heads > sms;
+  kernel<<<tiles * heads, kThreads, smem, s>>>(m, l);
   return cudaGetLastError();
 }
 static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shared memory");
 
 }  // namespace
 
-cudaError_t launch_attention_dq(const AttentionMaps& m, const AttentionLaunch& l,
+cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, int sms,
                                 cudaStream_t s) {
-  const int blocks = (l.T + 127) / 128 * l.hq;
-  return l.dim <= 64 ? launch(attention_dq_kernel<64>, blocks, DqCfg<64>::kSmem, m, l, s)
-                     : launch(attention_dq_kernel<128>, blocks, DqCfg<128>::kSmem, m, l, s);
+  return l.dim <= 64 ? launch(attention_dq_kernel<64>, l.hq, DqCfg<64>::kSmem, m, l, sms, s)
+                     : launch(attention_dq_kernel<128>, l.hq, DqCfg<128>::kSmem, m, l, sms, s);
 }
 
-cudaError_t launch_attention_dkv(const AttentionMaps& m, const AttentionLaunch& l,
+cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
                                  cudaStream_t s) {
-  const int blocks = (l.T + 127) / 128 * l.hk;
-  return l.dim <= 64 ? launch(attention_dkv_kernel<64>, blocks, DkvCfg<64>::kSmem, m, l, s)
-                     : launch(attention_dkv_kernel<128>, blocks, DkvCfg<128>::kSmem, m, l, s);
+  return l.dim <= 64 ? launch(attention_dkv_kernel<64>, l.hk, DkvCfg<64>::kSmem, m, l, sms, s)
+                     : launch(attention_dkv_kernel<128>, l.hk, DkvCfg<128>::kSmem, m, l, sms, s);
 }
 
 }  // namespace muon

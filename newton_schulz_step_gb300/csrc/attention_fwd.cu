@@ -107,11 +107,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  // the last tiles hold the most keys: they go first
+  // of one sequence, the last tiles hold the most keys: they go first
   const int pairs = (L.T + 128 * kTiles - 1) / (128 * kTiles);
-  const int h = static_cast<int>(blockIdx.x) % L.hq;
-  const int row0 = (pairs - 1 - static_cast<int>(blockIdx.x) / L.hq) * (128 * kTiles);
-  const int kh = h / L.group;
+  const int h = static_cast<int>(blockIdx.x) % L.hq, kh = h / L.group;
+  int row0 = (pairs - 1 - static_cast<int>(blockIdx.x) / L.hq) * (128 * kTiles);
+  if (L.ranked)
+    row0 = 128 * kTiles *
+           ranked_tile(pairs, static_cast<int>(blockIdx.x) / L.hq, reinterpret_cast<int*>(sm),
+                       [&](int i) {
+                         const int r = 128 * kTiles * i;
+                         return min(r + 128, L.T - 1) / kBlock - sequence_of(L, r).begin / kBlock;
+                       });
 
   if (tid < 2 * kTiles) {
     const int r = row0 + 128 * (tid >> 1);
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[4][32];
         ptx::tmem_ld32x2_sync(ts, ts + 32, s[0], s[1]);
         ptx::tmem_ld32x2_sync(ts + 64, ts + 96, s[2], s[3]);
-        if (k0 < last_begin || b + 1 == blocks_end) {
+        if (__builtin_expect(k0 < last_begin || b + 1 == blocks_end, 0)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             hide(s[i], row_begin - k0 - 32 * i, row - k0 - 32 * i, 0xff800000u);
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mb;
         } else {
           const bool grow = mb > m && !((mb - m) * c <= kRescale);
-          if (__any_sync(0xffffffffu, grow)) {
+          if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
             const float f = grow ? ex2((m - mb) * c) : 1.f;
             if (grow) m = mb;
             l *= f;
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (used < min(k0 + kBlock, L.T)) {            // the block holds padding: clear its V
+        if (__builtin_expect(used < min(k0 + kBlock, L.T), 0)) {   // the block holds padding: clear its V
           const int n = 2 * (b - begin) + 1, slot = n % C::kStages;
           ok = guard.warp_wait(&X.full[slot], (n / C::kStages) & 1);
           if (!ok) break;
@@ -395,21 +401,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP>
-cudaError_t launch(const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s) {
+cudaError_t launch(const AttentionMaps& m, AttentionLaunch& l, int sms, cudaStream_t s) {
   static_assert(Cfg<DP>::kSmem <= 232448, "shared memory");
   const cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<DP>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Cfg<DP>::kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = (l.T + 128 * kTiles - 1) / (128 * kTiles);
+  l.ranked = l.n_seqs > 1 && pairs <= kRankedTiles && pairs * l.hq > sms;
   attention_fwd_kernel<DP><<<pairs * l.hq, kThreads, Cfg<DP>::kSmem, s>>>(m, l);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attention(const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s) {
-  return l.dim <= 64 ? launch<64>(m, l, s) : launch<128>(m, l, s);
+cudaError_t launch_attention(const AttentionMaps& m, AttentionLaunch l, int sms, cudaStream_t s) {
+  return l.dim <= 64 ? launch<64>(m, l, sms, s) : launch<128>(m, l, sms, s);
 }
 
 }  // namespace muon

@@ -297,6 +297,7 @@ struct AttentionLaunch {
   int n_seqs, T, hq, hk, group, dim;
   float scale;
   unsigned int* status;
+  int ranked;                       // blocks take the tiles by their work
 };
 
 // Tensor maps of the heads as (head_dim, heads, tokens), boxes of 64 x 1 x 128 with
@@ -333,10 +334,10 @@ cudaError_t launch_adam(const AdamLaunch& l, int blocks, cudaStream_t s);
 // after griddepcontrol.wait.
 cudaError_t launch_fused(const FusedLaunch& l, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeLaunch& l, bool backward, int sms, cudaStream_t s);
-cudaError_t launch_attention(const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s);
-cudaError_t launch_attention_dq(const AttentionMaps& m, const AttentionLaunch& l,
+cudaError_t launch_attention(const AttentionMaps& m, AttentionLaunch l, int sms, cudaStream_t s);
+cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, int sms,
                                 cudaStream_t s);
-cudaError_t launch_attention_dkv(const AttentionMaps& m, const AttentionLaunch& l,
+cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
                                  cudaStream_t s);
 
 // Host services of muon_api.cu for the other entry points' files.
