@@ -39,23 +39,28 @@ __device__ __forceinline__ void half_barrier(int half) {   // the lower or upper
 }
 
 // ------------------------------------------------------------------ dq
-// TMEM: S (0), dP (128; dS over it), dq (256), Q and dO (384, 448) as bf16 pairs: as the A
-// operands of S and dP from there, those products read half as much shared memory (from
-// shared memory they ran at 106 cycles a step instead of 64, dq of 8192 tokens, 32/8
-// heads of 128, in 632 us).  Per block, in the tensor cores' order: S of the next block,
-// dq += dS K, dP of the next block; so S and the exponentials of a block run beside the
-// work on the one before.
+// TMEM: S (0, with heads of 64 or less two buffers: 0 and 320), dP (128; dS over it), dq
+// (256), Q and dO (from 512 - DP) as bf16 pairs.  The first block's S and dP take Q and dO
+// from where the copies left them; meanwhile the compute warps put both in TMEM for the
+// other blocks, whose products then read half as much shared memory (with Q and dO from
+// there a step ran 106 cycles instead of 64).
+// Per block, in the tensor cores' order, one buffer of S: S of the next block (once the
+// exponentials have read this one), dq += dS K, dP of the next block; two buffers: dq,
+// dP of the next block, S of the one after.
 template <int DP> struct DqCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
-  static constexpr int kK = 4, kV = 3;                       // ring slots
-  static constexpr uint32_t kVRing = kK * kTile;
+  static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
+  static constexpr uint32_t kDo = kTile, kKRing = 2 * kTile, kVRing = kKRing + kK * kTile;
   static constexpr uint32_t kMisc = kVRing + kV * kTile, kMiscBytes = 2560;
   static constexpr uint32_t kSmem = kMisc + kMiscBytes;
+  static constexpr bool kTwoS = DP == 64;
+  static constexpr uint32_t kQCol = 512 - DP, kDoCol = kQCol + DP / 2;
+  static __device__ __forceinline__ uint32_t s_col(int j) { return kTwoS && (j & 1) ? 320 : 0; }
 };
 
 struct DqMisc {
-  uint64_t q_ready, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full, s_read, dp_full, ds_full, dq_full, drain;
+  uint64_t q_full, q_ready, k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], s_read, dp_full, ds_full, dq_full, drain;
   uint32_t tmem;
   int bad, skip;
   int first, last;                 // begin of the tile's first and last row
@@ -90,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid < 4) X.repair[tid] = 0;
   if (warp == kProducerWarp && lane == 0) {
+    ptx::mbar_init(&X.q_full, 2);
     ptx::mbar_init(&X.q_ready, 16);
     for (int s = 0; s < 4; ++s) {
       ptx::mbar_init(&X.k_full[s], 1);
@@ -97,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&X.v_full[s], 1);
       ptx::mbar_init(&X.v_empty[s], 1);
     }
-    ptx::mbar_init(&X.s_full, 1);
+    ptx::mbar_init(&X.s_full[0], 1);
+    ptx::mbar_init(&X.s_full[1], 1);
     ptx::mbar_init(&X.s_read, 16);
     ptx::mbar_init(&X.dp_full, 1);
     ptx::mbar_init(&X.ds_full, 16);
@@ -110,6 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       X.skip = 1;
     }
     ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&M.q);
+    ptx::prefetch_tmap(&M.dout);
     ptx::prefetch_tmap(&M.k);
     ptx::prefetch_tmap(&M.v);
   }
@@ -131,18 +140,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducerWarp) {
     if (run && warp == kProducerWarp) {
       if (lane == 0) {
+        load_tile<DP>(sm, &M.q, h, row0, &X.q_full);
+        load_tile<DP>(sm + C::kDo, &M.dout, h, row0, &X.q_full);
         int j = 0;
         bool ok = true;
         for (; j < n && ok; ++j) {
           const int ks = j % C::kK, vs = j % C::kV, row = (begin + j) * kBlock;
           if (j >= C::kK) ok = guard.wait_or_fail(&X.k_empty[ks], (j / C::kK - 1) & 1);
           if (!ok) break;
-          load_tile<DP>(sm + ks * C::kTile, &M.k, kh, row, &X.k_full[ks]);
+          load_tile<DP>(sm + C::kKRing + ks * C::kTile, &M.k, kh, row, &X.k_full[ks]);
           if (j >= C::kV) ok = guard.wait_or_fail(&X.v_empty[vs], (j / C::kV - 1) & 1);
           if (!ok) break;
           load_tile<DP>(sm + C::kVRing + vs * C::kTile, &M.v, kh, row, &X.v_full[vs]);
         }
         if (!ok) {                       // copies in flight land before the CTA ends
+          ptx::mbar_wait(&X.q_full, 0, nullptr, nullptr, kDrainNs);
           for (int i = j > C::kK ? j - C::kK : 0; i <= j; ++i) {
             ptx::mbar_wait(&X.k_full[i % C::kK], (i / C::kK) & 1, nullptr, nullptr, kDrainNs);
             if (i < j)
@@ -160,36 +172,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ptx::tc_fence_after();
         return ok;
       };
-      auto scores = [&] {
+      auto scores = [&](int j) {
         if (!wait(&X.k_full[at_s.slot], at_s.parity)) return;
+        const uint32_t k = base + C::kKRing + at_s.slot * C::kTile;
         if (ptx::elect_one()) {
-          mma_heads_ts<DP>(0, 384, base + at_s.slot * C::kTile);
-          ptx::mma_commit(&X.s_full);
+          if (j == 0) mma_heads<DP>(0, base, k);
+          else mma_heads_ts<DP>(C::s_col(j), C::kQCol, k);
+          ptx::mma_commit(&X.s_full[C::kTwoS ? j & 1 : 0]);
         }
         at_s.next();
       };
-      auto dp = [&] {
+      auto dp = [&](int j) {
         if (!wait(&X.v_full[at_v.slot], at_v.parity)) return;
+        const uint32_t v = base + C::kVRing + at_v.slot * C::kTile;
         if (ptx::elect_one()) {
-          mma_heads_ts<DP>(128, 448, base + C::kVRing + at_v.slot * C::kTile);
+          if (j == 0) mma_heads<DP>(128, base + C::kDo, v);
+          else mma_heads_ts<DP>(128, C::kDoCol, v);
           ptx::mma_commit(&X.dp_full);
           ptx::mma_commit(&X.v_empty[at_v.slot]);
         }
         at_v.next();
       };
-      wait(&X.q_ready, 0);
-      if (ok) scores();
-      if (ok) dp();
+      wait(&X.q_full, 0);
+      if (ok) scores(0);
+      if (ok) dp(0);
+      if (n > 1) wait(&X.q_ready, 0);
+      if (ok && C::kTwoS && n > 1) scores(1);
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n && wait(&X.s_read, j & 1)) scores();
+        if (!C::kTwoS && j + 1 < n && wait(&X.s_read, j & 1)) scores(j + 1);
         if (!ok || !wait(&X.ds_full, j & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP, 128, 16>(256, 128, base + at_q.slot * C::kTile, j > 0);
+          mma_rows<DP, 128, 16>(256, 128, base + C::kKRing + at_q.slot * C::kTile, j > 0);
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
         }
         at_q.next();
-        if (j + 1 < n) dp();
+        if (j + 1 < n) dp(j + 1);
+        if (ok && C::kTwoS && j + 2 < n) scores(j + 2);
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain);
@@ -205,62 +224,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
     const int last_begin = X.last;
     const float c = L.scale * kLog2e;
-    // Q and dO to TMEM, 32 columns of a row each, with their part of delta; lse in base 2,
-    // +inf (p = 0) for rows without keys
+    // delta, 32 columns of a row each; lse in base 2, +inf (p = 0) for rows without keys
     float delta = 0.f, lse2 = INFINITY;
-    if (32 * group < DP) {
-      uint32_t a[16], g[16];
+    uint4 o[4];
+    const bool columns = 32 * group < DP;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = g[i] = 0u;
-      if (row < L.T) {
-        const __nv_bfloat16 *q = L.q.row(row, h), *o = L.o.row(row, h), *w = L.dout.row(row, h);
+    for (int i = 0; i < 4; ++i) o[i] = make_uint4(0, 0, 0, 0);
+    if (row < used) {
+      const __nv_bfloat16* out = L.o.row(row, h) + 32 * group;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = 32 * group + 8 * i;
-          if (d < L.dim) {
-            const uint4 x = *reinterpret_cast<const uint4*>(q + d);
-            const uint4 y = *reinterpret_cast<const uint4*>(w + d);
-            const uint4 z = *reinterpret_cast<const uint4*>(o + d);
-            a[4 * i] = x.x; a[4 * i + 1] = x.y; a[4 * i + 2] = x.z; a[4 * i + 3] = x.w;
-            g[4 * i] = y.x; g[4 * i + 1] = y.y; g[4 * i + 2] = y.z; g[4 * i + 3] = y.w;
-            const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+      for (int i = 0; i < 4; ++i)
+        if (columns && 32 * group + 8 * i < L.dim)
+          o[i] = *reinterpret_cast<const uint4*>(out + 8 * i);
+      lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
+    }
+    bool ok = guard.warp_wait(&X.q_full, 0);
+    if (ok && columns) {
+      uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              delta = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(g[4 * i + e] << 16), delta);
-              delta = fmaf(__uint_as_float(u[e] & 0xffff0000u),
-                           __uint_as_float(g[4 * i + e] & 0xffff0000u), delta);
-            }
-          }
+      for (int i = 0; i < 4; ++i) {
+        const uint4 g = *reinterpret_cast<const uint4*>(sm + C::kDo + tile_off(r, 4 * group + i));
+        w[4 * i] = g.x; w[4 * i + 1] = g.y; w[4 * i + 2] = g.z; w[4 * i + 3] = g.w;
+        const uint32_t u[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          delta = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(w[4 * i + e] << 16), delta);
+          delta = fmaf(__uint_as_float(u[e] & 0xffff0000u),
+                       __uint_as_float(w[4 * i + e] & 0xffff0000u), delta);
         }
       }
-      ptx::tmem_st16(lanes + 384 + 16 * group, a);
-      ptx::tmem_st16(lanes + 448 + 16 * group, g);
+      ptx::tmem_st16(lanes + C::kDoCol + 16 * group, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(sm + tile_off(r, 4 * group + i));
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+      }
+      ptx::tmem_st16(lanes + C::kQCol + 16 * group, w);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&X.q_ready);
-    if (row < used) lse2 = L.lse[static_cast<size_t>(h) * L.T + row] * kLog2e;
-    else delta = 0.f;
-    X.delta[group][r] = delta;
+    X.delta[group][r] = row < used ? delta : 0.f;
     compute_barrier();
     delta = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
     if (group < 2)
       L.stats[(static_cast<size_t>(h) * tiles + tile) * 256 + 128 * group + r] =
           group ? delta : lse2;
     const uint64_t c2 = pair(c, c), lse22 = pair(-lse2, -lse2), delta2 = pair(-delta, -delta);
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < n && ok; ++j) {
       const int k0 = (begin + j) * kBlock;
-      ok = guard.warp_wait(&X.s_full, j & 1);
+      ok = C::kTwoS ? guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1)
+                    : guard.warp_wait(&X.s_full[0], j & 1);
       if (!ok) break;
       ptx::tc_fence_after();
       uint32_t x[32];
       uint64_t p[16];
-      ptx::tmem_ld32_sync(lanes + 32 * group, x);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&X.s_read);
+      ptx::tmem_ld32_sync(lanes + C::s_col(j) + 32 * group, x);
+      if (!C::kTwoS) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&X.s_read);
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float2 y = unpair(
@@ -287,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_st16(lanes + 128 + 32 * group, w);
       if (used < min(k0 + kBlock, L.T)) {              // the block holds padding: clear its K
         const int s = j % C::kK;                       // (landed: S has read it)
-        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + s * C::kTile, r);
+        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
         ptx::fence_proxy_async_smem();
       }
       ptx::tmem_st_wait();
@@ -298,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) ok = guard.warp_wait(&X.dq_full, 0);
     if (ok && 32 * group < DP) {
       ptx::tc_fence_after();
-      // K has been read for the last time: dq goes through its place
+      // Q has been read for the last time: dq goes through its place
       float test = 0.f;                                // NaN if an element is not finite
       uint32_t o[32];
       ptx::tmem_ld32_sync(lanes + 256 + 32 * group, o);
