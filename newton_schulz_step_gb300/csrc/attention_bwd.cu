@@ -369,10 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ dk, dv
 // Scores are transposed here (rows are keys): P^T and dS^T are A operands as they come,
-// without an exchange.  TMEM: S^T (0), dP^T (128), dv (256), dk (256 + DP).  Per block,
-// in the tensor cores' order: dv += P^T dO, S^T of the next block, dk += dS^T Q, dP^T of
-// the next block; so P of a block is computed beside the last two products of the one
-// before, and dS beside the first two of its own.
+// without an exchange.  TMEM: S^T (0; with heads of 64 or less a second buffer: 384),
+// dP^T (128), dv (256), dk (256 + DP).  Per block, in the tensor cores' order:
+// dv += P^T dO, S^T of the next block (two buffers: of the one after), dk += dS^T Q, dP^T
+// of the next block; so P of a block is computed beside the last two products of the one
+// before, and dS beside the first two of its own.  With heads of 128 the four products
+// run at 87 % of the rate that a library product reaches; with 64 the exponentials bound
+// the kernel, and the second buffer keeps the compute warps from waiting for S.
 template <int DP> struct DkvCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kStages = DP == 128 ? 2 : 4;          // of Q (with its stats) and dO
@@ -380,11 +383,14 @@ template <int DP> struct DkvCfg {
   static constexpr uint32_t kStats = kDoRing + kStages * kTile;
   static constexpr uint32_t kMisc = kStats + kStages * kStatBytes;
   static constexpr uint32_t kSmem = kMisc + 512;
+  static constexpr bool kTwoS = DP == 64;
+  static constexpr int kAhead = kTwoS ? 2 : 1;   // S of which block follows dv of one
+  static __device__ __forceinline__ uint32_t s_col(int i) { return kTwoS && (i & 1) ? 384 : 0; }
 };
 
 struct DkvMisc {
   uint64_t kv_full, q_full[4], q_empty[4], do_full[4], do_empty[4];
-  uint64_t s_full, dp_full, p_full, ds_full, done, drain;
+  uint64_t s_full[2], dp_full, p_full[2], ds_full, done, drain;
   uint32_t tmem;
   int bad, skip;
   int first_end, blocks;           // end of the first key's sequence; query blocks per head
@@ -429,9 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&X.do_full[s], 1);
       ptx::mbar_init(&X.do_empty[s], 1);
     }
-    ptx::mbar_init(&X.s_full, 1);
+    ptx::mbar_init(&X.s_full[0], 1);
+    ptx::mbar_init(&X.s_full[1], 1);
     ptx::mbar_init(&X.dp_full, 1);
-    ptx::mbar_init(&X.p_full, 16);
+    ptx::mbar_init(&X.p_full[0], 16);
+    ptx::mbar_init(&X.p_full[1], 16);
     ptx::mbar_init(&X.ds_full, 16);
     ptx::mbar_init(&X.done, 1);
     ptx::mbar_init(&X.drain, 1);
@@ -508,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ptx::tc_fence_after();
         return ok;
       };
-      auto scores = [&] {
+      auto scores = [&](int i) {
         if (!wait(&X.q_full[at_s.slot], at_s.parity)) return;
         if (ptx::elect_one()) {
-          mma_heads<DP>(0, base, base + C::kQRing + at_s.slot * C::kTile);
-          ptx::mma_commit(&X.s_full);
+          mma_heads<DP>(C::s_col(i), base, base + C::kQRing + at_s.slot * C::kTile);
+          ptx::mma_commit(&X.s_full[C::kTwoS ? i & 1 : 0]);
         }
         at_s.next();
       };
@@ -525,16 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         at_p.next();
       };
       wait(&X.kv_full, 0);
-      if (ok) scores();
+      if (ok) scores(0);
       if (ok) dp();
+      if (ok && C::kTwoS && n > 1) scores(1);
       for (int i = 0; i < n && ok; ++i) {
-        if (!wait(&X.p_full, i & 1)) break;
+        if (!(C::kTwoS ? wait(&X.p_full[i & 1], (i >> 1) & 1) : wait(&X.p_full[0], i & 1))) break;
         if (ptx::elect_one()) {
-          mma_rows<DP, 128, 16>(256, 0, base + C::kDoRing + at_v.slot * C::kTile, i > 0);
+          mma_rows<DP, 128, 16>(256, C::s_col(i), base + C::kDoRing + at_v.slot * C::kTile, i > 0);
           ptx::mma_commit(&X.do_empty[at_v.slot]);
         }
         at_v.next();
-        if (i + 1 < n) scores();
+        if (i + C::kAhead < n) scores(i + C::kAhead);
         if (!ok || !wait(&X.ds_full, i & 1)) break;
         if (ptx::elect_one()) {
           mma_rows<DP, 128, 16>(256 + DP, 128, base + C::kQRing + at_k.slot * C::kTile, i > 0);
@@ -554,7 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = warp >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane, key = key0 + r;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t ts = lanes + 32 * group;
     const int used = tokens_in_use(L);
     const int key_end = key < used ? sequence_of(L, key).end : key;
     const int first_end = X.first_end;
@@ -570,11 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* lse2 =
           reinterpret_cast<const float4*>(sm + C::kStats + at.slot * kStatBytes) + 8 * group;
       ok = guard.warp_wait(&X.q_full[at.slot], at.parity) &&          // the stats
-           guard.warp_wait(&X.s_full, i & 1);
+           (C::kTwoS ? guard.warp_wait(&X.s_full[i & 1], (i >> 1) & 1)
+                     : guard.warp_wait(&X.s_full[0], i & 1));
       if (!ok) break;
       ptx::tc_fence_after();
       uint32_t x[32];
       uint64_t p[16];
+      const uint32_t ts = lanes + C::s_col(i) + 32 * group, tp = lanes + 128 + 32 * group;
       ptx::tmem_ld32_sync(ts, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -609,12 +619,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&X.p_full);
+      if (lane == 0) ptx::mbar_arrive(&X.p_full[C::kTwoS ? i & 1 : 0]);
 
       ok = guard.warp_wait(&X.dp_full, i & 1);
       if (!ok) break;
       ptx::tc_fence_after();
-      ptx::tmem_ld32_sync(ts + 128, x);
+      ptx::tmem_ld32_sync(tp, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float4 z = lse2[32 + e];           // delta
@@ -634,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           w[e] = pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-        ptx::tmem_st16(ts + 128, w);
+        ptx::tmem_st16(tp, w);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
