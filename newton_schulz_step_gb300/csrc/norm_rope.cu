@@ -14,9 +14,12 @@
 // loads before it uses the first.  With the half layout a lane's 8 elements are 4 + 4,
 // rot / 2 apart, so that both members of a pair are in one thread: the rotation needs
 // no exchange, and only the sum of squares (backward: also the mean of G h) crosses
-// lanes.  The table rows are read for every head, from L1 after a token's first.
-// Waiting rows stay in their storage type, which keeps a thread within 64 registers
-// and 32 warps on an SM: that many loads in flight cover the memory's latency.
+// lanes.  Waiting rows stay in their storage type (80 registers, 24 warps on an SM), the
+// arithmetic is on fp32 pairs.
+// What held earlier forms back was the chain position -> table row -> first row: without
+// it the forward of 32768 tokens, 32 + 8 heads of 128, took 111 us instead of 146 (the
+// bytes alone: 101).  So a position is read a step ahead, and the table row with the rows
+// it belongs to: 138 us; backward of 16384 tokens, 16 + 16 heads of 128: 111 us (127).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -27,14 +30,36 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // rows of a lane at a time: 4 x 16 bytes in flight (backward: 2 x 2 x 16)
 template <typename T, bool kBackward> constexpr int kIter = (kBackward ? 4 : 8) / sizeof(T);
-template <bool kBackward> constexpr int kResident = kBackward ? 3 : 4;   // blocks on an SM
+constexpr int kResident = 3;         // blocks on an SM
 constexpr int kPartGroups = 32;      // first level of the weight gradients' sum
 constexpr int kGroupMax = kRopeMaxBlocks / kPartGroups;   // blocks per group
 static_assert(kGroupMax * kPartGroups == kRopeMaxBlocks, "groups cover the blocks");
 
-struct Vec8 { float v[8]; };
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+using ptx::pair;
+using ptx::unpair;
 
-// 8 elements of a row as stored: two groups of 4, or 8 contiguous ones.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) {   // two bf16
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t bf16_of(uint64_t v) {
+  const float2 f = unpair(v);
+  const __nv_bfloat162 x = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  const float2 f = unpair(v);
+  return pair(f.y, f.x);
+}
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
+}
+
+// 8 elements of a row as stored, in two groups of 4 (kWhole: 8 contiguous ones); in
+// fp32 they are four pairs.
 template <typename T> struct Raw;
 template <> struct Raw<float> {
   float4 a, b;
@@ -43,14 +68,17 @@ template <> struct Raw<float> {
     a = *reinterpret_cast<const float4*>(p + ea);
     b = *reinterpret_cast<const float4*>(p + eb);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
+    v[0] = pair(a.x, a.y); v[1] = pair(a.z, a.w);
+    v[2] = pair(b.x, b.y); v[3] = pair(b.z, b.w);
   }
   template <bool kWhole>
-  static __device__ __forceinline__ void store(float* p, int ea, int eb, const float (&v)[8]) {
-    *reinterpret_cast<float4*>(p + ea) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + eb) = make_float4(v[4], v[5], v[6], v[7]);
+  static __device__ __forceinline__ void store(float* p, int ea, int eb, const uint64_t (&v)[4]) {
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = unpair(v[i]);
+    *reinterpret_cast<float4*>(p + ea) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    *reinterpret_cast<float4*>(p + eb) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
 };
 template <> struct Raw<__nv_bfloat16> {
@@ -67,23 +95,16 @@ template <> struct Raw<__nv_bfloat16> {
       b = *reinterpret_cast<const uint2*>(p + eb);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const unsigned int w[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
+    v[0] = pair_of(a.x); v[1] = pair_of(a.y);
+    v[2] = pair_of(b.x); v[3] = pair_of(b.y);
   }
   template <bool kWhole>
   static __device__ __forceinline__ void store(__nv_bfloat16* p, int ea, int eb,
-                                               const float (&v)[8]) {
-    unsigned int w[4];
+                                               const uint64_t (&v)[4]) {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const unsigned int*>(&x);
-    }
+    for (int i = 0; i < 4; ++i) w[i] = bf16_of(v[i]);
     if constexpr (kWhole) {
       *reinterpret_cast<uint4*>(p + ea) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
@@ -93,17 +114,58 @@ template <> struct Raw<__nv_bfloat16> {
   }
 };
 
-// index in Vec8 of the first and second member of pair j
-template <bool kInterleaved> __device__ __forceinline__ constexpr int first(int j) {
-  return kInterleaved ? 2 * j : j;
-}
-template <bool kInterleaved> __device__ __forceinline__ constexpr int second(int j) {
-  return kInterleaved ? 2 * j + 1 : j + 4;
-}
+// The rotation of a lane's four (a, b) by angles with cosines c and sines s.  Half
+// layout: pairs 0, 1 hold the a, pairs 2, 3 the b.  Interleaved: a pair holds (a, b), and
+// the cosines and sines come doubled, the sines of a with their sign changed.
+template <bool kInterleaved> struct Angles;
+template <> struct Angles<false> {
+  uint64_t c[2], s[2], ms[2];
+  __device__ __forceinline__ void set(const float4& x, const float4& y) {
+    c[0] = pair(x.x, x.y); c[1] = pair(x.z, x.w);
+    s[0] = pair(y.x, y.y); s[1] = pair(y.z, y.w);
+    ms[0] = pair(-y.x, -y.y); ms[1] = pair(-y.z, -y.w);
+  }
+  __device__ __forceinline__ void turn(uint64_t (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t a = v[i], b = v[2 + i];
+      v[i] = fma2(b, ms[i], mul2(a, c[i]));
+      v[2 + i] = fma2(a, s[i], mul2(b, c[i]));
+    }
+  }
+  __device__ __forceinline__ void turn_back(uint64_t (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t a = v[i], b = v[2 + i];
+      v[i] = fma2(b, s[i], mul2(a, c[i]));
+      v[2 + i] = fma2(a, ms[i], mul2(b, c[i]));
+    }
+  }
+};
+template <> struct Angles<true> {
+  uint64_t c[4], s[4];
+  __device__ __forceinline__ void set(const float4& x, const float4& y) {
+    c[0] = pair(x.x, x.x); c[1] = pair(x.y, x.y); c[2] = pair(x.z, x.z); c[3] = pair(x.w, x.w);
+    s[0] = pair(-y.x, y.x); s[1] = pair(-y.y, y.y);
+    s[2] = pair(-y.z, y.z); s[3] = pair(-y.w, y.w);
+  }
+  __device__ __forceinline__ void turn(uint64_t (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fma2(swapped(v[i]), s[i], mul2(v[i], c[i]));
+  }
+  __device__ __forceinline__ void turn_back(uint64_t (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fma2(swapped(v[i]), swapped(s[i]), mul2(v[i], c[i]));
+  }
+};
 
-// Sum over the `g` (power of two) lanes of a head.
+// Sum over the `g` (power of two) lanes of a row.
 __device__ __forceinline__ float head_sum(float x, int g) {
-  for (int o = g >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    if (o < g) x += y;
+  }
   return x;
 }
 
@@ -121,7 +183,7 @@ __device__ __forceinline__ float sum_rows(const float* parts, int r0, int r1, in
 }
 
 template <typename T, bool kBackward, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, kResident<kBackward>)
+__global__ void __launch_bounds__(kThreads, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeLaunch L) {
   constexpr int kN = kIter<T, kBackward>;
   __shared__ float s_dw[kBackward ? kWarps * 2 * kRopeMaxDim : 1];
@@ -147,130 +209,147 @@ __global__ void __launch_bounds__(kThreads, kResident<kBackward>)
   }
 
   int unit = blockIdx.x * kWarps + warp, passed = 0;  // work units; those of the kinds before
-#pragma unroll 1
-  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {                       // (unrolled: the strides stay constants)
     const int heads = L.heads[s];
     if (heads == 0) continue;
     const int rows = L.tokens * heads;
     const int count = (rows + kN * per - 1) / (kN * per);
     const int dt = per / heads, dh = per - dt * heads;   // from a row to the one `per` on
-    float w[8], dw[kBackward ? 8 : 1];
+    uint64_t w[4], dw[kBackward ? 4 : 1];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    for (int j = 0; j < 4; ++j) w[j] = pair(1.f, 1.f);
     if constexpr (kBackward) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+      for (int j = 0; j < 4; ++j) dw[j] = 0;
     }
     if (on && L.w[s] != nullptr) {
       Raw<float> x;
       x.template load<false>(L.w[s], ea, eb);
       x.get(w);
     }
-    for (; unit - passed < count; unit += gridDim.x * kWarps) {
-      const int row0 = (unit - passed) * (kN * per) + sub;
-      const int t0 = row0 / heads, h0 = row0 - t0 * heads;
+    // from a row to the one `per` on: a step, and a correction where the token changes
+    const long long xs = L.x[s].ts * dt + L.x[s].hs * dh, xw = L.x[s].ts - L.x[s].hs * heads;
+    const long long ys = L.y[s].ts * dt + L.y[s].hs * dh, yw = L.y[s].ts - L.y[s].hs * heads;
+    const long long gs = L.dy[s].ts * dt + L.dy[s].hs * dh, gw = L.dy[s].ts - L.dy[s].hs * heads;
+    // position of token t, -1 outside the tables
+    auto position = [&](int t) {
+      const int pos = L.pos != nullptr ? __ldg(L.pos + t) : t;
+      return pos >= 0 && pos < L.table_len ? pos : -1;
+    };
+    const int stride = gridDim.x * kWarps;
+    int row0 = (unit - passed) * (kN * per) + sub, t0 = row0 / heads;
+    int pos0 = L.rot > 0 && t0 < L.tokens ? position(t0) : 0;
+    for (; unit - passed < count; unit += stride) {
+      const int h0 = row0 - t0 * heads;
       Raw<T> x[kN], dy[kBackward ? kN : 1];
+      {
+        const T* px = static_cast<const T*>(L.x[s].p) + t0 * L.x[s].ts + h0 * L.x[s].hs;
+        const T* pg = kBackward
+            ? static_cast<const T*>(L.dy[s].p) + t0 * L.dy[s].ts + h0 * L.dy[s].hs : nullptr;
+        int h = h0;
 #pragma unroll
-      for (int i = 0, t = t0, h = h0; i < kN; ++i) {
-        const bool live = on && row0 + i * per < rows;
-        x[i].clear();
-        if (live && (!kBackward || L.norm))
-          x[i].template load<kInterleaved>(
-              static_cast<const T*>(L.x[s].p) + t * L.x[s].ts + h * L.x[s].hs, ea, eb);
-        if constexpr (kBackward) {
-          dy[i].clear();
-          if (live)
-            dy[i].template load<kInterleaved>(
-                static_cast<const T*>(L.dy[s].p) + t * L.dy[s].ts + h * L.dy[s].hs, ea, eb);
-        }
-        t += dt;
-        h += dh;
-        if (h >= heads) {
-          h -= heads;
-          ++t;
-        }
-      }
-#pragma unroll
-      for (int i = 0, t = t0, h = h0; i < kN; ++i) {
-        const bool live = on && row0 + i * per < rows;
-        float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-        float poison = 1.f;                           // NaN for a position outside the tables
-        if (L.rot > 0 && live) {
-          const int pos = L.pos != nullptr ? __ldg(L.pos + t) : t;
-          if (pos < 0 || pos >= L.table_len) {
-            poison = __int_as_float(0x7fffffff);
-          } else if (rotated) {
-            const size_t at = static_cast<size_t>(pos) * (L.rot >> 1) + 4 * u;
-            const float4 a = __ldg(reinterpret_cast<const float4*>(L.cos + at));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(L.sin + at));
-            c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-            sn[0] = b.x; sn[1] = b.y; sn[2] = b.z; sn[3] = b.w;
+        for (int i = 0; i < kN; ++i) {
+          const bool live = on && row0 + i * per < rows;
+          x[i].clear();
+          if (live && (!kBackward || L.norm)) x[i].template load<kInterleaved>(px, ea, eb);
+          if constexpr (kBackward) {
+            dy[i].clear();
+            if (live) dy[i].template load<kInterleaved>(pg, ea, eb);
+          }
+          px += xs;
+          if constexpr (kBackward) pg += gs;
+          h += dh;
+          if (h >= heads) {
+            h -= heads;
+            px += xw;
+            if constexpr (kBackward) pg += gw;
           }
         }
-        float xv[8], o[8], r = 1.f;
-        x[i].get(xv);
-        if (L.norm) {
-          float ss = 0.f;
+      }
+      // the first row's angles travel with the rows: its position was read a step ahead
+      float4 cosines = make_float4(1.f, 1.f, 1.f, 1.f), sines = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto table_row = [&](int pos) {
+        const size_t at = static_cast<size_t>(pos) * (L.rot >> 1) + 4 * u;
+        cosines = __ldg(reinterpret_cast<const float4*>(L.cos + at));
+        sines = __ldg(reinterpret_cast<const float4*>(L.sin + at));
+      };
+      if (rotated && pos0 >= 0) table_row(pos0);
+      const int next_row0 = row0 + stride * (kN * per), next_t0 = next_row0 / heads;
+      int next_pos0 = 0;
+      if (L.rot > 0 && unit - passed + stride < count && next_t0 < L.tokens)
+        next_pos0 = position(next_t0);
+      T* py = static_cast<T*>(L.y[s].p) + t0 * L.y[s].ts + h0 * L.y[s].hs;
+      Angles<kInterleaved> angles;
+      if (rotated) angles.set(cosines, sines);
+      float poison = pos0 < 0 ? __int_as_float(0x7fffffff) : 1.f;   // outside the tables: NaN
+      int t = t0, h = h0, have = t0;                  // `have`: the token of `angles`
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(xv[j], xv[j], ss);
-          r = rsqrtf(fmaf(head_sum(ss, g), inv_dim, L.eps));
+      for (int i = 0; i < kN; ++i) {
+        const bool live = on && row0 + i * per < rows;
+        if (L.rot > 0 && live && t != have) {
+          have = t;
+          const int pos = position(t);
+          poison = pos < 0 ? __int_as_float(0x7fffffff) : 1.f;
+          if (rotated && pos >= 0) {
+            table_row(pos);
+            angles.set(cosines, sines);
+          }
+        }
+        uint64_t v[4], o[4];
+        float r = 1.f;
+        x[i].get(v);
+        if (L.norm) {
+          const uint64_t ss = fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0]))));
+          r = rsqrtf(fmaf(head_sum(sum_of(ss), g), inv_dim, L.eps));
           if (!live) r = 0.f;                         // (rsqrt(0) of a row that is not there)
         }
         if constexpr (!kBackward) {
-          r *= poison;
+          const uint64_t r2 = pair(r * poison, r * poison);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = xv[j] * r * w[j];
-          if (rotated) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = o[first<kInterleaved>(j)], b = o[second<kInterleaved>(j)];
-              o[first<kInterleaved>(j)] = a * c[j] - b * sn[j];
-              o[second<kInterleaved>(j)] = b * c[j] + a * sn[j];
-            }
-          }
+          for (int j = 0; j < 4; ++j) o[j] = mul2(mul2(v[j], r2), w[j]);
+          if (rotated) angles.turn(o);
         } else {
+          const uint64_t r2 = pair(r, r), n2 = pair(poison, poison);
           dy[i].get(o);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] *= poison;
-          if (rotated) {
+          for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], n2);
+          if (rotated) angles.turn_back(o);
+          if (L.norm) {
+            uint64_t dot = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float a = o[first<kInterleaved>(j)], b = o[second<kInterleaved>(j)];
-              o[first<kInterleaved>(j)] = a * c[j] + b * sn[j];
-              o[second<kInterleaved>(j)] = b * c[j] - a * sn[j];
+              v[j] = mul2(v[j], r2);
+              if (live) dw[j] = fma2(o[j], v[j], dw[j]);
+              o[j] = mul2(o[j], w[j]);
+              dot = fma2(o[j], v[j], dot);
             }
-          }
-          if (L.norm) {
-            float dot = 0.f;
+            const float m = -head_sum(sum_of(dot), g) * inv_dim;
+            const uint64_t m2 = pair(m, m);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              xv[j] *= r;
-              dw[j] = fmaf(o[j], xv[j], dw[j]);
-              o[j] *= w[j];
-              dot = fmaf(o[j], xv[j], dot);
-            }
-            dot = head_sum(dot, g) * inv_dim;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = r * (o[j] - xv[j] * dot);
+            for (int j = 0; j < 4; ++j) o[j] = mul2(r2, fma2(v[j], m2, o[j]));
           }
         }
-        if (live)
-          Raw<T>::template store<kInterleaved>(
-              static_cast<T*>(L.y[s].p) + t * L.y[s].ts + h * L.y[s].hs, ea, eb, o);
+        if (live) Raw<T>::template store<kInterleaved>(py, ea, eb, o);
+        py += ys;
         t += dt;
         h += dh;
         if (h >= heads) {
           h -= heads;
           ++t;
+          py += yw;
         }
       }
+      row0 = next_row0;
+      t0 = next_t0;
+      pos0 = next_pos0;
     }
     passed += count;
     if constexpr (kBackward) {
       if (L.dw[s] != nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float v = dw[j];
+          float v = j & 1 ? unpair(dw[j >> 1]).y : unpair(dw[j >> 1]).x;
           for (int o = g; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
           if (sub == 0 && on) s_dw[warp * width + s * L.dim + (j < 4 ? ea + j : eb + j - 4)] = v;
         }
@@ -327,7 +406,7 @@ cudaError_t launch(const NormRopeLaunch& l, int sms, cudaStream_t s) {
   long long total = 0;
   for (int h : l.heads) total += (1ll * l.tokens * h + chunk - 1) / chunk;
   const long long want = (total + kWarps - 1) / kWarps;
-  const int cap = min(kRopeMaxBlocks, kResident<kBackward> * sms);
+  const int cap = min(kRopeMaxBlocks, kResident * sms);
   const int blocks = static_cast<int>(want < cap ? want : cap);
   if (l.interleaved) norm_rope_kernel<T, kBackward, true><<<blocks, kThreads, 0, s>>>(l);
   else norm_rope_kernel<T, kBackward, false><<<blocks, kThreads, 0, s>>>(l);
