@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -468,20 +469,20 @@ def _refuse_heads(t, name, shape, dtype, device):
 
 def _heads(t, name: str, shape, dtype, device) -> _Heads:
     """The view of a [tokens, heads, head_dim] tensor of the given shape, dtype and device."""
-    if t.dtype is not dtype or t.device != device or t.shape != shape or len(shape) != 3:
-        _refuse_heads(t, name, shape, dtype, device)
-    st, sh, sd = t.stride()
-    if sd != 1 and shape[2] > 1:
-        _refuse_heads(t, name, shape, dtype, device)
-    return _Heads(t.data_ptr(), st, sh)
+    if t.dtype is dtype and t.shape == shape and t.device == device and len(shape) == 3:
+        st, sh, sd = t.stride()
+        if sd == 1 or shape[2] <= 1:
+            return _Heads(t.data_ptr(), st, sh)
+    _refuse_heads(t, name, shape, dtype, device)
 
 
-def _out_heads(t, name: str, shape, dtype, device):
-    """(tensor, view) of an output: the caller's, or a new contiguous one."""
+def _out_heads(t, name: str, like):
+    """(tensor, view) of an output shaped like `like`: the caller's, or a new contiguous one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        shape = like.shape
+        t = like.new_empty(shape)
         return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
-    return t, _heads(t, name, shape, dtype, device)
+    return t, _heads(t, name, like.shape, like.dtype, like.device)
 
 
 def _ptr(t, name: str, device, dtype, shape=None):
@@ -526,15 +527,14 @@ _stream_ws = {}
 
 
 def _stream_workspace(ws, need: int, device, handle: int) -> Workspace:
-    """The caller's workspace, or one kept for each device and stream: calls on different
-    streams may overlap, and must not share one."""
-    if ws is not None:
-        return ws
-    key = (device.index, handle)
-    w = _stream_ws.get(key)
-    if w is None or w.nbytes < need:
-        w = _stream_ws[key] = Workspace(need, device)
-    return w
+    """Pointer and size of the caller's workspace, or of one kept for each device and stream:
+    calls on different streams may overlap, and must not share one."""
+    if ws is None:
+        key = (device.index, handle)
+        ws = _stream_ws.get(key)
+        if ws is None or ws.nbytes < need:
+            ws = _stream_ws[key] = Workspace(need, device)
+    return ws.ptr, ws.nbytes
 
 
 def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
@@ -577,13 +577,14 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
             return qk_norm_rope(q, k, cos, sin, q_weight=q_weight, k_weight=k_weight,
                                 positions=positions, norm=norm, eps=eps, interleaved=interleaved,
                                 q_out=q_out, k_out=k_out)
-    q_out, vqo = _out_heads(q_out, "q_out", q.shape, q.dtype, dev)
-    k_out, vko = _out_heads(k_out, "k_out", k.shape, q.dtype, dev)
+    q_out, vqo = _out_heads(q_out, "q_out", q)
+    k_out, vko = _out_heads(k_out, "k_out", k)
     _raise(L.muon_qk_norm_rope(spec, vq, vk, vqo, vko, _current_handle(dev.index)),
            "muon_qk_norm_rope")
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=256)
 def norm_rope_workspace_bytes(head_dim: int) -> int:
     return int(load_library().muon_norm_rope_workspace_bytes(head_dim))
 
@@ -606,19 +607,20 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_we
                 workspace=workspace)
     vdqo = _heads(dq_out, "dq_out", q.shape, dtype, dev)
     vdko = _heads(dk_out, "dk_out", k.shape, dtype, dev)
-    dq, vdq = _out_heads(dq, "dq", q.shape, dtype, dev)
-    dk, vdk = _out_heads(dk, "dk", k.shape, dtype, dev)
+    dq, vdq = _out_heads(dq, "dq", q)
+    dk, vdk = _out_heads(dk, "dk", k)
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
     handle = _current_handle(dev.index)
-    ws = _stream_workspace(workspace, L.muon_norm_rope_workspace_bytes(spec.head_dim), dev, handle)
+    ws, ws_bytes = _stream_workspace(workspace, norm_rope_workspace_bytes(spec.head_dim), dev, handle)
     _raise(L.muon_qk_norm_rope_backward(
         spec, vdqo, vdko, vq, vk, vdq, vdk, None if dqw is None else dqw.data_ptr(),
-        None if dkw is None else dkw.data_ptr(), ws.ptr, ws.nbytes, handle),
+        None if dkw is None else dkw.data_ptr(), ws, ws_bytes, handle),
         "muon_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
 
 
+@functools.lru_cache(maxsize=1024)
 def attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(load_library().muon_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim))
 
@@ -664,14 +666,16 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
             return attention(q, k, v, cu_seqlens, scale=scale, out=out, lse=lse,
                              workspace=workspace)
     t, hq, _ = q.shape
-    out, vo = _out_heads(out, "out", q.shape, q.dtype, dev)
+    out, vo = _out_heads(out, "out", q)
     if lse is None:
-        lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
-    p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
+        lse = q.new_empty((hq, t), dtype=torch.float32)
+        p_lse = lse.data_ptr()
+    else:
+        p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
     handle = _current_handle(dev.index)
-    ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
-        t, hq, spec.kv_heads, spec.head_dim), dev, handle)
-    _raise(L.muon_attention(spec, vq, vk, vv, vo, p_lse, ws.ptr, ws.nbytes, handle),
+    ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
+                                                                spec.head_dim), dev, handle)
+    _raise(L.muon_attention(spec, vq, vk, vv, vo, p_lse, ws, ws_bytes, handle),
            "muon_attention")
     return out, lse
 
@@ -692,14 +696,14 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
     vg = _heads(dout, "dout", q.shape, dtype, dev)
     vo = _heads(out, "out", q.shape, dtype, dev)
     p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
-    dq, vdq = _out_heads(dq, "dq", q.shape, dtype, dev)
-    dk, vdk = _out_heads(dk, "dk", k.shape, dtype, dev)
-    dv, vdv = _out_heads(dv, "dv", k.shape, dtype, dev)
+    dq, vdq = _out_heads(dq, "dq", q)
+    dk, vdk = _out_heads(dk, "dk", k)
+    dv, vdv = _out_heads(dv, "dv", k)
     handle = _current_handle(dev.index)
-    ws = _stream_workspace(workspace, L.muon_attention_workspace_bytes(
-        t, hq, spec.kv_heads, spec.head_dim), dev, handle)
-    _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws.ptr,
-                                     ws.nbytes, handle), "muon_attention_backward")
+    ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
+                                                                spec.head_dim), dev, handle)
+    _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws,
+                                     ws_bytes, handle), "muon_attention_backward")
     return dq, dk, dv
 
 
