@@ -10,7 +10,14 @@
 // seven products a block instead of five.  In return nothing is added in global memory:
 // no fp32 dq buffer of 2 x (4 + 4) bytes an element and key block to move, no atomics,
 // the same bits in every run.
-// p and ds are rounded to bf16, the tensor cores' input; everything else is fp32.
+// p and ds are rounded to bf16, the tensor cores' input; everything else is fp32.  What
+// these roundings (2^-9 on average) may add up to, next to the result's own:
+//   dv: p rounded -- 1.4 times the result's own rounding error
+//   dk: ds rounded, 1.4 times.  delta is not taken from the bf16 out here (that would make
+//       it 1.6): sum_j p_ij (dp_ij - delta_i) = 0 at the exact delta, so the row sums that
+//       the dq kernel ends with correct it
+//   dq: ds rounded, and delta from the bf16 out: 1.6 times; with the remainders of ds of
+//       half the columns in a second bf16, 1.4 times.
 //
 // Warps 0-15 compute, warp 16 issues the copies, warp 17 the products.  A compute thread
 // owns a row (TMEM lane) of S and dP and 32 of its columns; each of the 4 groups of warps
@@ -202,7 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!C::kTwoS && j + 1 < n && wait(&X.s_read, j & 1)) scores(j + 1);
         if (!ok || !wait(&X.ds_full, j & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP, 128, 16>(256, 128, base + C::kKRing + at_q.slot * C::kTile, j > 0);
+          const uint32_t k = base + C::kKRing + at_q.slot * C::kTile;
+          mma_rows<DP, 128, 16>(256, 128, k, j > 0);
+          constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)    // the remainders: keys 0-15 of each group's 32
+            ptx::mma_bf16_ts(256, 128 + 32 * i + 16, desc_mn(k, 2 * i), kId, 1);
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
         }
@@ -268,10 +280,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     X.delta[group][r] = row < used ? delta : 0.f;
     compute_barrier();
     delta = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
-    if (group < 2)
-      L.stats[(static_cast<size_t>(h) * tiles + tile) * 256 + 128 * group + r] =
-          group ? delta : lse2;
+    float* const stats = L.stats + (static_cast<size_t>(h) * tiles + tile) * 256 + r;
+    if (group == 0) stats[0] = lse2;
     const uint64_t c2 = pair(c, c), lse22 = pair(-lse2, -lse2), delta2 = pair(-delta, -delta);
+    uint64_t rest = 0;                                 // of the row's sum of ds
     for (int j = 0; j < n && ok; ++j) {
       const int k0 = (begin + j) * kBlock;
       ok = C::kTwoS ? guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1)
@@ -305,11 +317,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (k0 < last_begin || j + 1 == n)
         hide(x, row_begin - k0 - 32 * group, row - k0 - 32 * group, 0u);
-      uint32_t w[16];
+      uint32_t w[16], remainder[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+      for (int i = 0; i < 16; ++i) {
+        const float a = __uint_as_float(x[2 * i]), b = __uint_as_float(x[2 * i + 1]);
+        w[i] = pack2(a, b);
+        rest = add2(rest, pair(a, b));
+        if (i < 8)
+          remainder[i] = pack2(a - __uint_as_float(w[i] << 16),
+                               b - __uint_as_float(w[i] & 0xffff0000u));
+      }
       ptx::tmem_st16(lanes + 128 + 32 * group, w);
+      ptx::tmem_st8(lanes + 128 + 32 * group + 16, remainder);
       if (used < min(k0 + kBlock, L.T)) {              // the block holds padding: clear its K
         const int s = j % C::kK;                       // (landed: S has read it)
         if (group == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
@@ -337,8 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned int bad = __ballot_sync(0xffffffffu, row < used && test != 0.f);
       if (bad && lane == 0) atomicOr(&X.repair[quarter], bad);
     }
+    if (ok) {
+      const float2 a = unpair(rest);
+      X.delta[group][r] = a.x + a.y;
+    }
     compute_barrier();                                 // (reached by every compute thread)
     if (ok) {
+      if (group == 1)
+        stats[128] = delta + ((X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]));
       // any part of a row may be bad: the four warps of the rows share the joint set
       unsigned int bad = X.repair[quarter] & (0x11111111u << group);
       while (bad) {

@@ -5,9 +5,11 @@ sums and softmax in fp32, whose errors c = 2^-16 of the magnitudes entering a su
   a weight p is off by Ep p,  Ep = c (1 + scale |q| . |k|)       (error of its exponent)
   out:  u |out| + (1 + u) (u + Ep) sum p |v|                     (p rounded for the product)
   dv:   u |dv|  + (1 + u) (u + Ep) sum p |dout|
-  ds = p (dp - delta) is off by Ep |ds| + c p (|dout| . |v| + |dout| . |out|), then rounded;
+  ds = p (dp - delta) is off by Ep |ds| + (c + u) p (|dout| . |v| + |dout| . |out|), the u for
+  the bf16 out that delta may come from, then rounded;
   dq, dk: u of the result, and those errors times scale |k|, scale |q|
-The oracle takes the same bf16 inputs, and for the gradients the out and lse handed to the kernel.
+The oracle takes the same bf16 inputs, and for the gradients its own out and the lse handed to
+the kernel.
 Each result's Frobenius error is also held to 1e-2 (rounding error rms 2^-8 / sqrt 3 = 2.3e-3 for
 each of at most three roundings on a result's way, with room for cancellation).
 """
@@ -69,7 +71,8 @@ def _magnitudes(q, k, v, do, out, lse, cu, scale):
             b_out[a:b, h] = (p * (U + ep)) @ np.abs(vv)
             b_dv[a:b, g] += (p * (U + ep)).T @ np.abs(dd)
             delta = np.sum(dd * oo, 1, keepdims=True)
-            e = C * p * (np.abs(dd) @ np.abs(vv).T + np.sum(np.abs(dd * oo), 1, keepdims=True))
+            out_size = np.sum(np.abs(dd * oo), 1, keepdims=True)
+            e = p * (C * (np.abs(dd) @ np.abs(vv).T) + (C + U) * out_size)
             e += (U + ep) * p * np.abs(dd @ vv.T - delta)
             b_dq[a:b, h] = scale * (e @ np.abs(kk))
             b_dk[a:b, g] += scale * (e.T @ np.abs(qq))
@@ -85,8 +88,8 @@ def _check(q, k, v, do, lengths=None, scale=None, stream=None, cu=None):
     c = None if cu is None else cu.cpu().numpy()
     scale = q.shape[2] ** -0.5 if scale is None else scale
     r_out, r_lse = ref.attention(Q, K, V, c, scale)
-    b = _magnitudes(Q, K, V, D, f64(out), f64(lse), c, scale)
-    r_grads = ref.attention_backward(D, Q, K, V, f64(out), f64(lse), c, scale)
+    b = _magnitudes(Q, K, V, D, r_out, f64(lse), c, scale)
+    r_grads = ref.attention_backward(D, Q, K, V, r_out, f64(lse), c, scale)
     L = f64(lse)
     assert np.array_equal(np.isneginf(L), np.isneginf(r_lse))
     fin = np.isfinite(r_lse)
