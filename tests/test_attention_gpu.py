@@ -133,6 +133,13 @@ def test_parity_with_sharp_and_flat_weights(sharp, scale):
     _check(*_draw(3, 700, 2, 1, 64, sharp=sharp), [500, 200], scale=scale)
 
 
+def test_parity_over_more_than_one_wave_of_blocks():
+    # documents of different lengths: blocks take the tiles by their work
+    _check(*_draw(30, 1290, 40, 20, 16), [300, 7, 0, 511, 130, 1, 341])
+    # more tiles than are ranked in the backward kernels
+    _check(*_draw(31, 40030, 1, 1, 8), [100] * 400 + [30])
+
+
 def test_growing_scores_move_the_maximum_in_every_block():
     q, k, v, do = _draw(4, 900, 2, 1, 64, fused=False)
     k *= (1 + torch.arange(900, device="cuda")[:, None, None] / 30).to(torch.bfloat16)
