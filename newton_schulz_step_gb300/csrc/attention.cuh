@@ -70,8 +70,36 @@ __device__ __forceinline__ int ranked_tile(int tiles, int want, int* scratch, F&
     for (int k = 0; k < tiles; ++k) rank += scratch[k] > w || (scratch[k] == w && k < i);
     if (rank == want) scratch[kRankedTiles] = i;
   }
+  ptx::fence_proxy_async_smem();         // copies will land where the scratch is
   __syncthreads();
   return __shfl_sync(0xffffffffu, scratch[kRankedTiles], 0);
+}
+
+// Launch that may begin before the kernel in front of it in the stream has ended: its
+// blocks set up their barriers, then wait for that kernel (begin_after_prior) before they
+// touch global memory or take TMEM, which that kernel may still need.  The three kernels of a training pass follow each
+// other without the gap of a launch.
+template <typename K>
+cudaError_t launch_behind(K kernel, int blocks, int threads, uint32_t smem,
+                          const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m, l);
+}
+__device__ __forceinline__ void begin_after_prior() {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
 }
 
 // ---- bounded waits ------------------------------------------------------

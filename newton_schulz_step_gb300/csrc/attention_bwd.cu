@@ -86,21 +86,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  // of one sequence, the last tiles hold the most keys: they go first
-  const int tiles = (L.T + 127) / 128;
-  const int h = static_cast<int>(blockIdx.x) % L.hq;
-  int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
-  if (L.ranked)
-    tile = ranked_tile(tiles, static_cast<int>(blockIdx.x) / L.hq, reinterpret_cast<int*>(sm),
-                       [&](int i) { return i - sequence_of(L, 128 * i).begin / kBlock; });
-  const int row0 = 128 * tile, kh = h / L.group;
-
-  if (tid < 2) {
-    const int b = sequence_of(L, tid ? min(row0 + 127, L.T - 1) : row0).begin;
-    if (tid) X.last = b;
-    else X.first = b;
-  }
-  if (tid < 4) X.repair[tid] = 0;
   if (warp == kProducerWarp && lane == 0) {
     ptx::mbar_init(&X.q_full, 2);
     ptx::mbar_init(&X.q_ready, 16);
@@ -118,21 +103,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&X.dq_full, 1);
     ptx::mbar_init(&X.drain, 1);
     X.bad = 0;
-    X.skip = ptx::status_set(L.status);
-    if (!tiles_aligned(sm)) {
-      atomicOr(L.status, kErrTimeoutAttention);
-      X.skip = 1;
-    }
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&M.q);
     ptx::prefetch_tmap(&M.dout);
     ptx::prefetch_tmap(&M.k);
     ptx::prefetch_tmap(&M.v);
   }
+  begin_after_prior();
   if (warp == kMmaWarp) {
     ptx::tmem_alloc(&X.tmem, 512);
     ptx::tmem_relinquish();
   }
+  if (tid == 0) {
+    X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
+  }
+
+  // of one sequence, the last tiles hold the most keys: they go first
+  const int tiles = (L.T + 127) / 128;
+  const int h = static_cast<int>(blockIdx.x) % L.hq;
+  int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
+  if (L.ranked)
+    tile = ranked_tile(tiles, static_cast<int>(blockIdx.x) / L.hq, reinterpret_cast<int*>(sm),
+                       [&](int i) { return i - sequence_of(L, 128 * i).begin / kBlock; });
+  const int row0 = 128 * tile, kh = h / L.group;
+
+  if (tid < 2) {
+    const int b = sequence_of(L, tid ? min(row0 + 127, L.T - 1) : row0).begin;
+    if (tid) X.last = b;
+    else X.first = b;
+  }
+  if (tid < 4) X.repair[tid] = 0;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -433,6 +437,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  if (warp == kProducerWarp && lane == 0) {
+    ptx::mbar_init(&X.kv_full, 2);
+    for (int s = 0; s < 4; ++s) {
+      ptx::mbar_init(&X.q_full[s], 1);
+      ptx::mbar_init(&X.q_empty[s], 1);
+      ptx::mbar_init(&X.do_full[s], 1);
+      ptx::mbar_init(&X.do_empty[s], 1);
+    }
+    ptx::mbar_init(&X.s_full[0], 1);
+    ptx::mbar_init(&X.s_full[1], 1);
+    ptx::mbar_init(&X.dp_full, 1);
+    ptx::mbar_init(&X.p_full[0], 16);
+    ptx::mbar_init(&X.p_full[1], 16);
+    ptx::mbar_init(&X.ds_full, 16);
+    ptx::mbar_init(&X.done, 1);
+    ptx::mbar_init(&X.drain, 1);
+    X.bad = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&M.q);
+    ptx::prefetch_tmap(&M.dout);
+    ptx::prefetch_tmap(&M.k);
+    ptx::prefetch_tmap(&M.v);
+  }
+  begin_after_prior();
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&X.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 0) {
+    X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
+  }
+
   // of one sequence, the first tiles are seen by the most queries: they go first
   const int tiles = (L.T + 127) / 128;
   const int kh = static_cast<int>(blockIdx.x) % L.hk;
@@ -452,38 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     X.blocks = end > key0 ? (end - 1) / kBlock + 1 - tile : 0;
   }
   if (tid < 8) X.repair[tid >> 2][tid & 3] = 0;
-  if (warp == kProducerWarp && lane == 0) {
-    ptx::mbar_init(&X.kv_full, 2);
-    for (int s = 0; s < 4; ++s) {
-      ptx::mbar_init(&X.q_full[s], 1);
-      ptx::mbar_init(&X.q_empty[s], 1);
-      ptx::mbar_init(&X.do_full[s], 1);
-      ptx::mbar_init(&X.do_empty[s], 1);
-    }
-    ptx::mbar_init(&X.s_full[0], 1);
-    ptx::mbar_init(&X.s_full[1], 1);
-    ptx::mbar_init(&X.dp_full, 1);
-    ptx::mbar_init(&X.p_full[0], 16);
-    ptx::mbar_init(&X.p_full[1], 16);
-    ptx::mbar_init(&X.ds_full, 16);
-    ptx::mbar_init(&X.done, 1);
-    ptx::mbar_init(&X.drain, 1);
-    X.bad = 0;
-    X.skip = ptx::status_set(L.status);
-    if (!tiles_aligned(sm)) {
-      atomicOr(L.status, kErrTimeoutAttention);
-      X.skip = 1;
-    }
-    ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&M.q);
-    ptx::prefetch_tmap(&M.dout);
-    ptx::prefetch_tmap(&M.k);
-    ptx::prefetch_tmap(&M.v);
-  }
-  if (warp == kMmaWarp) {
-    ptx::tmem_alloc(&X.tmem, 512);
-    ptx::tmem_relinquish();
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -736,13 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename K>
 cudaError_t launch(K kernel, int heads, uint32_t smem, const AttentionMaps& m,
                    AttentionLaunch& l, int sms, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const int tiles = (l.T + 127) / 128;
   l.ranked = l.n_seqs > 1 && tiles <= kRankedTiles && tiles * heads > sms;
-  kernel<<<tiles * heads, kThreads, smem, s>>>(m, l);
-  return cudaGetLastError();
+  return launch_behind(kernel, tiles * heads, kThreads, smem, m, l, s);
 }
 static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shared memory");
 

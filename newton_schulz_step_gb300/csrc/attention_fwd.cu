@@ -107,6 +107,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  if (warp == kProducerWarp && lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(&X.full[s], 1);
+      ptx::mbar_init(&X.empty[s], kTiles);
+    }
+    for (int t = 0; t < kTiles; ++t) {
+      ptx::mbar_init(&X.q_full[t], 1);
+      ptx::mbar_init(&X.s_full[t], 1);
+      ptx::mbar_init(&X.p_full[t][0], 4);
+      ptx::mbar_init(&X.p_full[t][1], 4);
+      ptx::mbar_init(&X.o_full[t], 1);
+      ptx::mbar_init(&X.drain[t], 1);
+      ptx::mbar_init(&X.turn[t], 1);
+    }
+    X.bad = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&M.q);
+    ptx::prefetch_tmap(&M.k);
+    ptx::prefetch_tmap(&M.v);
+  }
+  begin_after_prior();
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&X.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  if (tid == 0) {
+    X.skip = ptx::status_set(L.status);
+    if (!tiles_aligned(sm)) {
+      atomicOr(L.status, kErrTimeoutAttention);
+      X.skip = 1;
+    }
+  }
+
   // of one sequence, the last tiles hold the most keys: they go first
   const int pairs = (L.T + 128 * kTiles - 1) / (128 * kTiles);
   const int h = static_cast<int>(blockIdx.x) % L.hq, kh = h / L.group;
@@ -125,35 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = r < L.T ? sequence_of(L, i).begin : 0;
     if (tid & 1) X.last[tid >> 1] = b;
     else X.first[tid >> 1] = b;
-  }
-  if (warp == kProducerWarp && lane == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(&X.full[s], 1);
-      ptx::mbar_init(&X.empty[s], kTiles);
-    }
-    for (int t = 0; t < kTiles; ++t) {
-      ptx::mbar_init(&X.q_full[t], 1);
-      ptx::mbar_init(&X.s_full[t], 1);
-      ptx::mbar_init(&X.p_full[t][0], 4);
-      ptx::mbar_init(&X.p_full[t][1], 4);
-      ptx::mbar_init(&X.o_full[t], 1);
-      ptx::mbar_init(&X.drain[t], 1);
-      ptx::mbar_init(&X.turn[t], 1);
-    }
-    X.bad = 0;
-    X.skip = ptx::status_set(L.status);
-    if (!tiles_aligned(sm)) {
-      atomicOr(L.status, kErrTimeoutAttention);
-      X.skip = 1;
-    }
-    ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&M.q);
-    ptx::prefetch_tmap(&M.k);
-    ptx::prefetch_tmap(&M.v);
-  }
-  if (warp == kMmaWarp) {
-    ptx::tmem_alloc(&X.tmem, 512);
-    ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -403,14 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int DP>
 cudaError_t launch(const AttentionMaps& m, AttentionLaunch& l, int sms, cudaStream_t s) {
   static_assert(Cfg<DP>::kSmem <= 232448, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<DP>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Cfg<DP>::kSmem);
-  if (e != cudaSuccess) return e;
   const int pairs = (l.T + 128 * kTiles - 1) / (128 * kTiles);
   l.ranked = l.n_seqs > 1 && pairs <= kRankedTiles && pairs * l.hq > sms;
-  attention_fwd_kernel<DP><<<pairs * l.hq, kThreads, Cfg<DP>::kSmem, s>>>(m, l);
-  return cudaGetLastError();
+  return launch_behind(attention_fwd_kernel<DP>, pairs * l.hq, kThreads, Cfg<DP>::kSmem, m, l, s);
 }
 
 }  // namespace

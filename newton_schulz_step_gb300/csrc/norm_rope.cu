@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
   constexpr int kN = kIter<T, kBackward>;
   __shared__ float s_dw[kBackward ? kWarps * 2 * kRopeMaxDim : 1];
   __shared__ int s_last;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();                 // the kernel before, which may still have been running
   if (kBackward && ptx::status_set(L.status)) return;   // the same word for every thread: set
                                                         // words stay set until the host clears
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -408,9 +410,17 @@ cudaError_t launch(const NormRopeLaunch& l, int sms, cudaStream_t s) {
   const long long want = (total + kWarps - 1) / kWarps;
   const int cap = min(kRopeMaxBlocks, kResident * sms);
   const int blocks = static_cast<int>(want < cap ? want : cap);
-  if (l.interleaved) norm_rope_kernel<T, kBackward, true><<<blocks, kThreads, 0, s>>>(l);
-  else norm_rope_kernel<T, kBackward, false><<<blocks, kThreads, 0, s>>>(l);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return l.interleaved ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, true>, l)
+                       : cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, false>, l);
 }
 
 }  // namespace
