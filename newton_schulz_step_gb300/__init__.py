@@ -668,7 +668,7 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     t, hq, _ = q.shape
     out, vo = _out_heads(out, "out", q)
     if lse is None:
-        lse = q.new_empty((hq, t), dtype=torch.float32)
+        lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
         p_lse = lse.data_ptr()
     else:
         p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))

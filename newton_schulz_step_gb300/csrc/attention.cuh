@@ -81,7 +81,8 @@ __device__ __forceinline__ int ranked_tile(int tiles, int want, int* scratch, F&
 // other without the gap of a launch.
 template <typename K>
 cudaError_t launch_behind(K kernel, int blocks, int threads, uint32_t smem,
-                          const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s) {
+                          const AttentionMaps& m, const AttentionLaunch& l, cudaStream_t s,
+                          int cluster = 1) {
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -90,11 +91,15 @@ cudaError_t launch_behind(K kernel, int blocks, int threads, uint32_t smem,
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, m, l);
 }
 __device__ __forceinline__ void begin_after_prior() {
@@ -162,6 +167,12 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
   ptx::mbar_arrive_expect_tx(bar, DP / 64 * kSlab);
 #pragma unroll
   for (int s = 0; s < DP / 64; ++s) ptx::tma_load_3d(dst + s * kSlab, map, 64 * s, head, row, bar);
+}
+// Address of a tile for descriptors: the offset in the block's own shared memory.  (In a
+// cluster, a shared-memory address also holds the block's rank, in bits that would reach
+// into the descriptor's other fields.)
+__device__ __forceinline__ uint32_t tile_address(const uint8_t* tile) {
+  return ptx::smem_u32(tile) & 0x3FFFFu;
 }
 // Operand descriptors (ptx::smem_desc_sw128) with the tile's address added last, so that
 // the steps of a product differ by a constant.

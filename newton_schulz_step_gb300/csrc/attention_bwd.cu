@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (run && warp == kMmaWarp) {
-      const uint32_t base = ptx::smem_u32(sm);
+      const uint32_t base = tile_address(sm);
       Ring<C::kK> at_s, at_q;            // K tiles as read by S and by dq
       Ring<C::kV> at_v;
       bool ok = true;
@@ -405,6 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // before, and dS beside the first two of its own.  With heads of 128 the four products
 // run at 87 % of the rate that a library product reaches; with 64 the exponentials bound
 // the kernel, and the second buffer keeps the compute warps from waiting for S.
+// Where the tiles leave SMs without work, 2 or 4 blocks of a cluster share a tile: each
+// walks its part of the queries, and they add up each other's sums through distributed
+// shared memory, in the order of their ranks.
 template <int DP> struct DkvCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kStages = DP == 128 ? 2 : 4;          // of Q (with its stats) and dO
@@ -426,6 +429,15 @@ struct DkvMisc {
   unsigned int repair[2][4];       // rows of dv, dk to compute again, by warp of the tile
 };
 static_assert(sizeof(DkvMisc) <= 512, "misc block");
+
+// Byte offset of 4 sums (columns 4 c .. 4 c + 3 of row r of dv or dk): rows of DP fp32 in
+// the place of the Q and dO rings, 16-byte columns permuted so that neither a warp's 32
+// rows nor its 32 columns meet in a bank.
+template <int DP>
+__device__ __forceinline__ uint32_t sum_off(int which, int r, int c) {
+  static_assert(2u * 128u * DP * 4u <= DkvCfg<DP>::kStats - DkvCfg<DP>::kQRing, "room for the sums");
+  return DkvCfg<DP>::kQRing + ((which * 128 + r) * (DP / 4) + (c ^ (r & (DP / 4 - 1)))) * 16;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -475,8 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // of one sequence, the first tiles are seen by the most queries: they go first
   const int tiles = (L.T + 127) / 128;
-  const int kh = static_cast<int>(blockIdx.x) % L.hk;
-  int tile = static_cast<int>(blockIdx.x) / L.hk;
+  const int rank = L.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int kh = static_cast<int>(blockIdx.x) / L.split % L.hk;
+  int tile = static_cast<int>(blockIdx.x) / L.split / L.hk;
   if (L.ranked)
     tile = ranked_tile(tiles, tile, reinterpret_cast<int*>(sm), [&](int i) {
       const Span s = sequence_of(L, min(128 * i + 127, L.T - 1));
@@ -501,14 +514,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           : kErrTimeoutEpilogue};
   const bool run = !X.skip;
   const int blocks = __shfl_sync(0xffffffffu, X.blocks, 0);
-  const int n = blocks * L.group;                        // query blocks of all heads
+  // query blocks of all heads, and this block's part of them
+  const int all = blocks * L.group;
+  const int first = all * rank / L.split, n = all * (rank + 1) / L.split - first;
 
   if (warp >= kProducerWarp) {
     if (run && n > 0 && warp == kProducerWarp) {
       if (lane == 0) {
         load_tile<DP>(sm, &M.k, kh, key0, &X.kv_full);
         load_tile<DP>(sm + C::kV, &M.v, kh, key0, &X.kv_full);
-        int i = 0, h = kh * L.group, b = tile;
+        int i = 0, h = kh * L.group + first / blocks, b = tile + first % blocks;
         bool ok = true;
         for (; i < n; ++i) {
           const int s = i % C::kStages;
@@ -541,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (run && n > 0 && warp == kMmaWarp) {
-      const uint32_t base = ptx::smem_u32(sm);
+      const uint32_t base = tile_address(sm);
       Ring<C::kStages> at_s, at_p, at_v, at_k;   // tiles as read by S, dP, dv and dk
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = L.scale * kLog2e;
     const uint64_t c2 = pair(c, c);
     bool ok = true;
-    int b = tile;
+    int b = n > 0 ? tile + first % blocks : tile;
     Ring<C::kStages> at;
     for (int i = 0; i < n; ++i) {
       const int q0 = b * kBlock;
@@ -691,7 +706,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int which = group >> 1, side = group & 1;
     uint8_t* stage = which ? sm : sm + C::kV;
     if (ok && n > 0) ok = guard.warp_wait(&X.done, 0);
-    if (ok) {
+    if (ok && L.split > 1) {
+      // the tiles of Q and dO have been read for the last time: the sums go there
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < DP / 64; ++i) {
+        uint32_t o[32];
+        ptx::tmem_ld32_sync(lanes + 256 + DP * which + DP / 2 * side + 32 * i, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float4 v = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+          if (n == 0) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          *reinterpret_cast<float4*>(
+              sm + sum_off<DP>(which, r, DP / 8 * side + 8 * i + e)) = v;
+        }
+      }
+    } else if (ok) {
       ptx::tc_fence_after();
       const float f0 = which ? L.scale : 1.f;
       float test = 0.f;                                // NaN if an element is not finite
@@ -712,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad && lane == 0) atomicOr(&X.repair[which][quarter], bad);
     }
     half_barrier(which);                               // (reached by every compute thread)
-    if (ok) {
+    if (ok && L.split == 1) {
       // either side of a row may be bad: the two warps take every other row of the joint set
       unsigned int bad = X.repair[which][quarter] & (side ? 0xaaaaaaaau : 0x55555555u);
       while (bad) {
@@ -725,13 +756,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::fence_proxy_async_smem();
     }
     half_barrier(which);
-    if (ok && side == 0 && r == 0 && !X.bad) {
+    if (ok && L.split == 1 && side == 0 && r == 0 && !X.bad) {
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i)
         ptx::tma_store_3d(which ? &M.dk : &M.dv, 64 * i, kh, key0, stage + i * kSlab);
       ptx::bulk_commit();
       ptx::bulk_wait_read<0>();
     }
+  }
+  if (L.split > 1) {
+    // (every thread of every block of the cluster comes here, in bounded time)
+    ptx::cluster_arrive();
+    ptx::cluster_wait();
+    if (run && !X.bad && warp < kProducerWarp) {
+      // a warp adds up a row, a lane 4 columns of it
+      const int used = tokens_in_use(L), rows = kBlock / L.split;
+      for (int i = warp; i < 2 * rows; i += kProducerWarp) {
+        const int which = i & 1, r = rank * rows + (i >> 1), key = key0 + r;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < DP / 4) {
+          const uint32_t at = ptx::smem_u32(sm + sum_off<DP>(which, r, lane));
+          for (int c = 0; c < L.split; ++c) {
+            const float4 x = ptx::ld_cluster_f4(ptx::mapa_shared(at, c));
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+          }
+        }
+        const float f = key >= used ? 0.f : which ? L.scale : 1.f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+        if (key >= used) v = make_float4(0.f, 0.f, 0.f, 0.f);
+        __nv_bfloat16* row = (which ? L.dk : L.dv).row(key, kh);
+        const float test = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
+        if (__any_sync(0xffffffffu, test != 0.f)) {
+          Row dk, dv;
+          dkv_row(L, kh, key, sequence_of(L, key).end, dk, dv);
+          const Row& x = which ? dk : dv;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (64 * e + 2 * lane < L.dim)
+              *reinterpret_cast<uint32_t*>(row + 64 * e + 2 * lane) =
+                  pack2(x.v[2 * e], x.v[2 * e + 1]);
+        } else if (key < L.T && 4 * lane < L.dim) {
+          *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+        }
+      }
+    }
+    ptx::cluster_arrive();                             // nobody reads this block's sums any more
+    ptx::cluster_wait();
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -742,11 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename K>
-cudaError_t launch(K kernel, int heads, uint32_t smem, const AttentionMaps& m,
+cudaError_t launch(K kernel, int heads, int split, uint32_t smem, const AttentionMaps& m,
                    AttentionLaunch& l, int sms, cudaStream_t s) {
   const int tiles = (l.T + 127) / 128;
-  l.ranked = l.n_seqs > 1 && tiles <= kRankedTiles && tiles * heads > sms;
-  return launch_behind(kernel, tiles * heads, kThreads, smem, m, l, s);
+  l.split = split;
+  l.ranked = l.n_seqs > 1 && tiles <= kRankedTiles && tiles * heads * split > sms;
+  return launch_behind(kernel, tiles * heads * split, kThreads, smem, m, l, s, split);
 }
 static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shared memory");
 
@@ -754,14 +825,20 @@ static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shar
 
 cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, int sms,
                                 cudaStream_t s) {
-  return l.dim <= 64 ? launch(attention_dq_kernel<64>, l.hq, DqCfg<64>::kSmem, m, l, sms, s)
-                     : launch(attention_dq_kernel<128>, l.hq, DqCfg<128>::kSmem, m, l, sms, s);
+  return l.dim <= 64 ? launch(attention_dq_kernel<64>, l.hq, 1, DqCfg<64>::kSmem, m, l, sms, s)
+                     : launch(attention_dq_kernel<128>, l.hq, 1, DqCfg<128>::kSmem, m, l, sms, s);
 }
 
 cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
                                  cudaStream_t s) {
-  return l.dim <= 64 ? launch(attention_dkv_kernel<64>, l.hk, DkvCfg<64>::kSmem, m, l, sms, s)
-                     : launch(attention_dkv_kernel<128>, l.hk, DkvCfg<128>::kSmem, m, l, sms, s);
+  // 2 or 4 blocks a tile while that takes no second wave: then the longest tile sets the
+  // time (in two waves it was no faster: 128 tiles of 4096 tokens, 8/4 heads of 64, 37 us
+  // either way; 80 tiles of 2048 tokens, 5 heads of 80, 28 us instead of 24)
+  const int units = (l.T + 127) / 128 * l.hk;
+  const int split = units * 4 <= sms ? 4 : units * 2 <= sms ? 2 : 1;
+  return l.dim <= 64
+             ? launch(attention_dkv_kernel<64>, l.hk, split, DkvCfg<64>::kSmem, m, l, sms, s)
+             : launch(attention_dkv_kernel<128>, l.hk, split, DkvCfg<128>::kSmem, m, l, sms, s);
 }
 
 }  // namespace muon

@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (run && warp < kMmaWarp + kTiles) {
       const int t = warp - kMmaWarp;
       const int first = b0[t], last = b1[t];
-      const uint32_t q = ptx::smem_u32(sm) + t * C::kTile;
-      const uint32_t ring = ptx::smem_u32(sm) + C::kRing;
+      const uint32_t q = tile_address(sm) + t * C::kTile;
+      const uint32_t ring = tile_address(sm) + C::kRing;
       Ring<C::kStages> at;               // next slot of the ring
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {

@@ -298,6 +298,7 @@ struct AttentionLaunch {
   float scale;
   unsigned int* status;
   int ranked;                       // blocks take the tiles by their work
+  int split;                        // dk, dv: blocks of a cluster that share a tile
 };
 
 // Tensor maps of the heads as (head_dim, heads, tokens), boxes of 64 x 1 x 128 with

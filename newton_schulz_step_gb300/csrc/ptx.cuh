@@ -257,6 +257,15 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// 16 bytes of shared memory given by its shared::cluster address (possibly another CTA's).
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 // 32-bit store into shared memory given by its shared::cluster address
 // (possibly another CTA's), e.g. to raise the peer CTA's abort flag.
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
