@@ -16,7 +16,6 @@ using ptx::pair;
 using ptx::unpair;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlock = 128;            // rows of a tile (keys or queries)
 constexpr uint32_t kSlab = 16384;      // 128 rows x 64 bf16, 128-byte swizzle
 
@@ -260,10 +259,6 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi, uint32_t
 #pragma unroll
   for (int j = 0; j < 32; ++j)
     if (j < lo || j > hi) s[j] = value;
-}
-// 64 consecutive TMEM columns
-__device__ __forceinline__ void load64(uint32_t t, uint32_t (&a)[2][32]) {
-  ptx::tmem_ld32x2_sync(t, t + 32, a[0], a[1]);
 }
 
 // ---- rows by definition -------------------------------------------------

@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const Guard guard{&X.bad, L.status,
-                    warp == kProducerWarp ? kErrTimeoutProducer
-                    : warp == kMmaWarp    ? kErrTimeoutMma
-                                          : kErrTimeoutEpilogue};
+                    warp == kProducerWarp  ? kErrTimeoutProducer
+                    : warp < kProducerWarp ? kErrTimeoutEpilogue
+                                           : kErrTimeoutMma};
 
   // key blocks of each tile, [b0, b1), and of both
   int b0[kTiles], b1[kTiles], begin = INT_MAX, end = 0;   // (the same in every lane)
