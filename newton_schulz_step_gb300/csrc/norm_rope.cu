@@ -19,7 +19,12 @@
 // What held earlier forms back was the chain position -> table row -> first row: without
 // it the forward of 32768 tokens, 32 + 8 heads of 128, took 111 us instead of 146 (the
 // bytes alone: 101).  So a position is read a step ahead, and the table row with the rows
-// it belongs to: 138 us; backward of 16384 tokens, 16 + 16 heads of 128: 111 us (127).
+// it belongs to: 138 us; with the lanes of a row known at compile time 130 us (4.3 TB/s of
+// the rows alone, 76 % of the copy rate with the tables and positions).  Backward of 16384
+// tokens, 16 + 16 heads of 128: 99 us (4.1 TB/s).  Instructions (155 a row of 8 elements
+// forward, 282 backward) hold the rest.
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -159,12 +164,14 @@ template <> struct Angles<true> {
   }
 };
 
-// Sum over the `g` (power of two) lanes of a row.
+// Sum over the `g` (power of two) lanes of a row; kLanes: g, or 0 where it is not known
+// at compile time.
+template <int kLanes>
 __device__ __forceinline__ float head_sum(float x, int g) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = kLanes ? kLanes / 2 : 16; o > 0; o >>= 1) {
     const float y = __shfl_xor_sync(0xffffffffu, x, o);
-    if (o < g) x += y;
+    if (kLanes || o < g) x += y;
   }
   return x;
 }
@@ -182,7 +189,7 @@ __device__ __forceinline__ float sum_rows(const float* parts, int r0, int r1, in
   return s;
 }
 
-template <typename T, bool kBackward, bool kInterleaved>
+template <typename T, bool kBackward, bool kInterleaved, int kLanes>
 __global__ void __launch_bounds__(kThreads, kResident)
     norm_rope_kernel(const __grid_constant__ NormRopeLaunch L) {
   constexpr int kN = kIter<T, kBackward>;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
                                                         // words stay set until the host clears
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int units = L.dim >> 3;                       // 8-element units of a row
-  const int g = units <= 1 ? 1 : 1 << (32 - __clz(units - 1));   // lanes of a row
+  const int g = kLanes ? kLanes : units <= 1 ? 1 : 1 << (32 - __clz(units - 1));   // of a row
   const int u = lane & (g - 1);                       // this lane's unit
   const int sub = lane / g, per = 32 / g;             // row within the warp, rows at a time
   const bool on = u < units;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
         x[i].get(v);
         if (L.norm) {
           const uint64_t ss = fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0]))));
-          r = rsqrtf(fmaf(head_sum(sum_of(ss), g), inv_dim, L.eps));
+          r = rsqrtf(fmaf(head_sum<kLanes>(sum_of(ss), g), inv_dim, L.eps));
           if (!live) r = 0.f;                         // (rsqrt(0) of a row that is not there)
         }
         if constexpr (!kBackward) {
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
               o[j] = mul2(o[j], w[j]);
               dot = fma2(o[j], v[j], dot);
             }
-            const float m = -head_sum(sum_of(dot), g) * inv_dim;
+            const float m = -head_sum<kLanes>(sum_of(dot), g) * inv_dim;
             const uint64_t m2 = pair(m, m);
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = mul2(r2, fma2(v[j], m2, o[j]));
@@ -419,8 +426,14 @@ cudaError_t launch(const NormRopeLaunch& l, int sms, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return l.interleaved ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, true>, l)
-                       : cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, false>, l);
+  auto with_lanes = [&](auto lanes) {
+    constexpr int k = decltype(lanes)::value;
+    return l.interleaved ? cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, true, k>, l)
+                         : cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, kBackward, false, k>, l);
+  };
+  return g == 8    ? with_lanes(std::integral_constant<int, 8>())
+         : g == 16 ? with_lanes(std::integral_constant<int, 16>())
+                   : with_lanes(std::integral_constant<int, 0>());
 }
 
 }  // namespace
