@@ -183,34 +183,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ptx::tc_fence_after();
         return ok;
       };
-      auto scores = [&](int j) {
-        if (!wait(&X.k_full[at_s.slot], at_s.parity)) return;
+      // Waits for copies stand where nothing depends on them yet, and products that follow
+      // one another go out together: every step of this warp between them costs the
+      // tensor cores 100 cycles and more.  (A commit waits for all products before it: the
+      // one that frees a tile comes right behind the product that reads it last.)
+      auto scores = [&](int j) {           // (the K tile has landed)
         const uint32_t k = base + C::kKRing + at_s.slot * C::kTile;
-        if (ptx::elect_one()) {
-          if (j == 0) mma_heads<DP>(0, base, k);
-          else mma_heads_ts<DP>(C::s_col(j), C::kQCol, k);
-          ptx::mma_commit(&X.s_full[C::kTwoS ? j & 1 : 0]);
-        }
-        at_s.next();
+        if (j == 0) mma_heads<DP>(0, base, k);
+        else mma_heads_ts<DP>(C::s_col(j), C::kQCol, k);
+        ptx::mma_commit(&X.s_full[C::kTwoS ? j & 1 : 0]);
       };
-      auto dp = [&](int j) {
-        if (!wait(&X.v_full[at_v.slot], at_v.parity)) return;
+      auto dp = [&](int j) {               // (the V tile has landed)
         const uint32_t v = base + C::kVRing + at_v.slot * C::kTile;
-        if (ptx::elect_one()) {
-          if (j == 0) mma_heads<DP>(128, base + C::kDo, v);
-          else mma_heads_ts<DP>(128, C::kDoCol, v);
-          ptx::mma_commit(&X.dp_full);
-          ptx::mma_commit(&X.v_empty[at_v.slot]);
-        }
-        at_v.next();
+        if (j == 0) mma_heads<DP>(128, base + C::kDo, v);
+        else mma_heads_ts<DP>(128, C::kDoCol, v);
+        ptx::mma_commit(&X.dp_full);
+        ptx::mma_commit(&X.v_empty[at_v.slot]);
       };
-      wait(&X.q_full, 0);
-      if (ok) scores(0);
-      if (ok) dp(0);
+      auto k_landed = [&] { return wait(&X.k_full[at_s.slot], at_s.parity); };
+      auto v_landed = [&] { return wait(&X.v_full[at_v.slot], at_v.parity); };
+      if (wait(&X.q_full, 0) && k_landed() && v_landed() && ptx::elect_one()) {
+        scores(0);
+        dp(0);
+      }
+      at_s.next();
+      at_v.next();
       if (n > 1) wait(&X.q_ready, 0);
-      if (ok && C::kTwoS && n > 1) scores(1);
+      if (C::kTwoS && n > 1) {
+        if (k_landed() && ptx::elect_one()) scores(1);
+        at_s.next();
+      }
       for (int j = 0; j < n && ok; ++j) {
-        if (!C::kTwoS && j + 1 < n && wait(&X.s_read, j & 1)) scores(j + 1);
+        if (!C::kTwoS && j + 1 < n) {
+          if (k_landed() && wait(&X.s_read, j & 1) && ptx::elect_one()) scores(j + 1);
+          at_s.next();
+        }
+        if (C::kTwoS && j + 2 < n) k_landed();
+        if (j + 1 < n) v_landed();
         if (!ok || !wait(&X.ds_full, j & 1)) break;
         if (ptx::elect_one()) {
           const uint32_t k = base + C::kKRing + at_q.slot * C::kTile;
@@ -221,10 +230,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mma_bf16_ts(256, 128 + 32 * i + 16, desc_mn(k, 2 * i), kId, 1);
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
+          if (j + 1 < n) dp(j + 1);
+          if (C::kTwoS && j + 2 < n) scores(j + 2);
         }
+        __syncwarp();
         at_q.next();
-        if (j + 1 < n) dp(j + 1);
-        if (ok && C::kTwoS && j + 2 < n) scores(j + 2);
+        at_v.next();
+        if (C::kTwoS) at_s.next();
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain);
@@ -564,42 +576,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ptx::tc_fence_after();
         return ok;
       };
-      auto scores = [&](int i) {
-        if (!wait(&X.q_full[at_s.slot], at_s.parity)) return;
-        if (ptx::elect_one()) {
-          mma_heads<DP>(C::s_col(i), base, base + C::kQRing + at_s.slot * C::kTile);
-          ptx::mma_commit(&X.s_full[C::kTwoS ? i & 1 : 0]);
-        }
+      // (With 4 tiles in a ring the waits for copies stand early, as in the dq kernel; with 2
+      // the next tile may land late, and what does not need it goes first: 784 us with early
+      // waits, 670 with late ones, for 8192 tokens, 32/8 heads of 128.)
+      constexpr bool kEarly = C::kStages > 2;
+      auto scores = [&](int i) {           // (the Q tile has landed)
+        mma_heads<DP>(C::s_col(i), base, base + C::kQRing + at_s.slot * C::kTile);
+        ptx::mma_commit(&X.s_full[C::kTwoS ? i & 1 : 0]);
+      };
+      auto dp = [&] {                      // (the dO tile has landed)
+        mma_heads<DP>(128, base + C::kV, base + C::kDoRing + at_p.slot * C::kTile);
+        ptx::mma_commit(&X.dp_full);
+      };
+      auto q_landed = [&] { return wait(&X.q_full[at_s.slot], at_s.parity); };
+      auto do_landed = [&] { return wait(&X.do_full[at_p.slot], at_p.parity); };
+      if (wait(&X.kv_full, 0) && q_landed() && ptx::elect_one()) scores(0);
+      at_s.next();
+      if (ok && do_landed() && ptx::elect_one()) dp();
+      at_p.next();
+      if (C::kTwoS && n > 1) {
+        if (ok && q_landed() && ptx::elect_one()) scores(1);
         at_s.next();
-      };
-      auto dp = [&] {
-        if (!wait(&X.do_full[at_p.slot], at_p.parity)) return;
-        if (ptx::elect_one()) {
-          mma_heads<DP>(128, base + C::kV, base + C::kDoRing + at_p.slot * C::kTile);
-          ptx::mma_commit(&X.dp_full);
-        }
-        at_p.next();
-      };
-      wait(&X.kv_full, 0);
-      if (ok) scores(0);
-      if (ok) dp();
-      if (ok && C::kTwoS && n > 1) scores(1);
+      }
       for (int i = 0; i < n && ok; ++i) {
-        if (!(C::kTwoS ? wait(&X.p_full[i & 1], (i >> 1) & 1) : wait(&X.p_full[0], i & 1))) break;
+        if (kEarly && i + C::kAhead < n) q_landed();
+        if (!ok ||
+            !(C::kTwoS ? wait(&X.p_full[i & 1], (i >> 1) & 1) : wait(&X.p_full[0], i & 1)))
+          break;
         if (ptx::elect_one()) {
           mma_rows<DP, 128, 16>(256, C::s_col(i), base + C::kDoRing + at_v.slot * C::kTile, i > 0);
           ptx::mma_commit(&X.do_empty[at_v.slot]);
+          if (kEarly && i + C::kAhead < n) scores(i + C::kAhead);
         }
+        __syncwarp();
+        if (!kEarly && i + C::kAhead < n && q_landed() && ptx::elect_one()) scores(i + C::kAhead);
         at_v.next();
-        if (i + C::kAhead < n) scores(i + C::kAhead);
+        at_s.next();
+        if (kEarly && i + 1 < n) do_landed();
         if (!ok || !wait(&X.ds_full, i & 1)) break;
         if (ptx::elect_one()) {
           mma_rows<DP, 128, 16>(256 + DP, 128, base + C::kQRing + at_k.slot * C::kTile, i > 0);
           ptx::mma_commit(&X.q_empty[at_k.slot]);
           if (i + 1 == n) ptx::mma_commit(&X.done);
+          if (kEarly && i + 1 < n) dp();
         }
+        __syncwarp();
+        if (!kEarly && i + 1 < n && do_landed() && ptx::elect_one()) dp();
         at_k.next();
-        if (i + 1 < n) dp();
+        at_p.next();
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain);

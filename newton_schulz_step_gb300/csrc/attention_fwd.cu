@@ -227,25 +227,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.next();
         return s;
       };
-      // S of a block (if the tile has it), then the K slot is free
-      auto scores = [&](int b, int slot) {
-        const bool mine = b >= first && b < last;
-        if (mine && b == first) wait(&X.q_full[t], 0);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          if (mine) {
-            mma_heads<DP>(128 * t, q, ring + slot * C::kTile);
-            ptx::mma_commit(&X.s_full[t]);
-          }
-          ptx::mma_commit(&X.empty[slot]);
-        }
+      // S of a block (the K tile has landed)
+      auto scores = [&](int slot) {
+        mma_heads<DP>(128 * t, q, ring + slot * C::kTile);
+        ptx::mma_commit(&X.s_full[t]);
       };
-      if (begin < end) scores(begin, take());
+      auto has = [&](int b) { return b >= first && b < last; };
+      if (begin < end) {
+        const int ks = take();
+        if (has(begin)) wait(&X.q_full[t], 0);
+        if (ok && ptx::elect_one()) {
+          if (has(begin)) scores(ks);
+          ptx::mma_commit(&X.empty[ks]);
+        }
+      }
       for (int b = begin; b < end && ok; ++b) {
+        // Waits for copies stand where nothing depends on them yet, and products that follow
+        // one another go out together: every step of this warp between them costs the
+        // tensor cores 100 cycles and more.
         const int vs = take();
         const int ks = b + 1 < end ? take() : -1;
-        const bool mine = b >= first && b < last;
+        if (b + 1 == first) wait(&X.q_full[t], 0);
+        const bool mine = has(b), next = has(b + 1);
         const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
         if (mine) wait(&X.p_full[t][0], parity);
         // the tiles take turns: tile 0 waits for tile 1's last block, tile 1 for this one
@@ -255,17 +258,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ptx::elect_one())
             mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t, v, b > first);
           if (!wait(&X.p_full[t][1], parity)) break;
-          ptx::tc_fence_after();
-          if (ptx::elect_one()) {
-            mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t + 32, v + 8192, true);
-            if (b + 1 == last) ptx::mma_commit(&X.o_full[t]);
-          }
         }
-        if (ks >= 0) scores(b + 1, ks);
-        if (ok && ptx::elect_one()) {
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          if (mine) mma_rows<DP, 64, 32>(128 * kTiles + DP * t, 128 * t + 32, v + 8192, true);
+          if (mine && b + 1 == last) ptx::mma_commit(&X.o_full[t]);
+          if (next) scores(ks);
           ptx::mbar_arrive(&X.turn[t ^ 1]);
           ptx::mma_commit(&X.empty[vs]);
+          if (ks >= 0) ptx::mma_commit(&X.empty[ks]);
         }
+        __syncwarp();
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain[t]);
