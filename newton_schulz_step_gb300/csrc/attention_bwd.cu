@@ -18,12 +18,21 @@
 //       the dq kernel ends with correct it
 //   dq: ds rounded, and delta from the bf16 out: 1.6 times; with the remainders of ds of
 //       half the columns in a second bf16, 1.4 times.
+// Rows that see few keys have few roundings to average, and p near 1 times the error of
+// delta: 2 to 3 times on sequences of 2 to 20 tokens.  Those rows' keys are mostly in the
+// row's own block.  There, where a sequence begins in the tile, the dq kernel takes delta
+// from the block itself (sum ds = 0), and all remainders: 1.0 times.  The dk kernel takes
+// the remainders of the block where a sequence ends in the tile: its sums over few queries
+// scatter up to 1.7 times without them.  That is a block of a walk in both cases: 8192
+// packed tokens, 16/4 heads of 128, dq 143 to 147 us, dk/dv 201 to 205.
 //
 // Warps 0-15 compute, warp 16 issues the copies, warp 17 the products.  A compute thread
 // owns a row (TMEM lane) of S and dP and 32 of its columns; each of the 4 groups of warps
 // writes P and dS over half of its own columns of S or dP, as bf16 pairs, from where they
 // are the A operand of the accumulating product.
 #include "attention.cuh"
+
+#include <type_traits>
 
 namespace muon {
 namespace {
@@ -71,6 +80,7 @@ struct DqMisc {
   uint32_t tmem;
   int bad, skip;
   int first, last;                 // begin of the tile's first and last row
+  int starts;                      // a sequence begins in the tile
   unsigned int repair[4];          // rows to compute again, by warp of the tile
   float delta[4][128];             // parts of delta
 };
@@ -136,6 +146,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid) X.last = b;
     else X.first = b;
   }
+  if (tid == 2) {
+    const int used = tokens_in_use(L);
+    X.starts = row0 < used && sequence_of(L, min(row0 + 127, used - 1)).begin >= row0;
+  }
   if (tid < 4) X.repair[tid] = 0;
   ptx::tc_fence_before();
   __syncthreads();
@@ -177,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = tile_address(sm);
       Ring<C::kK> at_s, at_q;            // K tiles as read by S and by dq
       Ring<C::kV> at_v;
+      const int starts = __shfl_sync(0xffffffffu, X.starts, 0);
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && guard.issue_wait(bar, parity);
@@ -224,10 +239,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ptx::elect_one()) {
           const uint32_t k = base + C::kKRing + at_q.slot * C::kTile;
           mma_rows<DP, 128, 16>(256, 128, k, j > 0);
-          constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
+          if (starts && j + 1 == n) {    // the remainders
+            mma_rows<DP, 128, 16>(256, 128 + 16, k, true);
+          } else {                       // of keys 0-15 of each group's 32
+            constexpr uint32_t kId = ptx::idesc_bf16(128, DP, true);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)    // the remainders: keys 0-15 of each group's 32
-            ptx::mma_bf16_ts(256, 128 + 32 * i + 16, desc_mn(k, 2 * i), kId, 1);
+            for (int i = 0; i < 4; ++i)
+              ptx::mma_bf16_ts(256, 128 + 32 * i + 16, desc_mn(k, 2 * i), kId, 1);
+          }
           ptx::mma_commit(&X.k_empty[at_q.slot]);
           if (j + 1 == n) ptx::mma_commit(&X.dq_full);
           if (j + 1 < n) dp(j + 1);
@@ -250,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     const int used = tokens_in_use(L);
     const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
-    const int last_begin = X.last;
+    const int last_begin = X.last, starts = X.starts;
     const float c = L.scale * kLog2e;
     // delta, 32 columns of a row each; lse in base 2, +inf (p = 0) for rows without keys
     float delta = 0.f, lse2 = INFINITY;
@@ -300,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (group == 0) stats[0] = lse2;
     const uint64_t c2 = pair(c, c), lse22 = pair(-lse2, -lse2), delta2 = pair(-delta, -delta);
     uint64_t rest = 0;                                 // of the row's sum of ds
-    for (int j = 0; j < n && ok; ++j) {
+    auto step = [&](int j, auto own) {                 // own: the rows' own block, with starts
       const int k0 = (begin + j) * kBlock;
       ok = C::kTwoS ? guard.warp_wait(&X.s_full[j & 1], (j >> 1) & 1)
                     : guard.warp_wait(&X.s_full[0], j & 1);
-      if (!ok) break;
+      if (!ok) return;
       ptx::tc_fence_after();
       uint32_t x[32];
       uint64_t p[16];
@@ -321,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p[i] = pair(ex2(y.x), ex2(y.y));
       }
       ok = guard.warp_wait(&X.dp_full, j & 1);
-      if (!ok) break;
+      if (!ok) return;
       ptx::tc_fence_after();
       ptx::tmem_ld32_sync(lanes + 128 + 32 * group, x);
 #pragma unroll
@@ -333,6 +352,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (k0 < last_begin || j + 1 == n)
         hide(x, row_begin - k0 - 32 * group, row - k0 - 32 * group, 0u);
+      if constexpr (decltype(own)::value) {
+        // rows that see keys of this block only: their delta is the one of sum ds = 0
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) part += __uint_as_float(x[i]);
+        compute_barrier();                             // (delta's parts have been read)
+        X.delta[group][r] = row_begin >= k0 ? part : 0.f;
+        compute_barrier();
+        const float e = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
+        delta += e;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = unpair(fma2(
+              p[i], pair(-e, -e), pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]))));
+          x[2 * i] = __float_as_uint(y.x);
+          x[2 * i + 1] = __float_as_uint(y.y);
+        }
+        hide(x, row_begin - k0 - 32 * group, row - k0 - 32 * group, 0u);
+        uint32_t remainder[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = __uint_as_float(x[16 + 2 * i]), b = __uint_as_float(x[17 + 2 * i]);
+          const uint32_t w = pack2(a, b);
+          remainder[i] =
+              pack2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+        }
+        ptx::tmem_st8(lanes + 128 + 32 * group + 24, remainder);
+      }
       uint32_t w[16], remainder[8];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -354,6 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&X.ds_full);
+    };
+    for (int j = 0; j + starts < n && ok; ++j) step(j, std::false_type{});
+    if (starts && ok) step(n - 1, std::true_type{});
+    if (starts && !ok) {        // a wait ran out: others may stand at that step's two barriers
+      compute_barrier();
+      compute_barrier();
     }
     if (ok) ok = guard.warp_wait(&X.dq_full, 0);
     if (ok && 32 * group < DP) {
@@ -570,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (run && n > 0 && warp == kMmaWarp) {
       const uint32_t base = tile_address(sm);
       Ring<C::kStages> at_s, at_p, at_v, at_k;   // tiles as read by S, dP, dv and dk
+      const int ends = __shfl_sync(0xffffffffu, X.first_end, 0) <= key0 + kBlock;
+      int b = first % blocks;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && guard.issue_wait(bar, parity);
@@ -615,7 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kEarly && i + 1 < n) do_landed();
         if (!ok || !wait(&X.ds_full, i & 1)) break;
         if (ptx::elect_one()) {
-          mma_rows<DP, 128, 16>(256 + DP, 128, base + C::kQRing + at_k.slot * C::kTile, i > 0);
+          const uint32_t q = base + C::kQRing + at_k.slot * C::kTile;
+          mma_rows<DP, 128, 16>(256 + DP, 128, q, i > 0);
+          if (ends && b == 0) mma_rows<DP, 128, 16>(256 + DP, 128 + 16, q, true);
           ptx::mma_commit(&X.q_empty[at_k.slot]);
           if (i + 1 == n) ptx::mma_commit(&X.done);
           if (kEarly && i + 1 < n) dp();
@@ -624,6 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kEarly && i + 1 < n && do_landed() && ptx::elect_one()) dp();
         at_k.next();
         at_p.next();
+        if (++b == blocks) b = 0;
       }
       if (!ok) {                         // products in flight end before TMEM is freed
         if (ptx::elect_one()) ptx::mma_commit(&X.drain);
@@ -643,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int b = n > 0 ? tile + first % blocks : tile;
     Ring<C::kStages> at;
-    for (int i = 0; i < n; ++i) {
+    auto step = [&](int i, auto own) {                 // own: the keys' own block, with ends
       const int q0 = b * kBlock;
       const bool masked = b == tile || q0 + kBlock > first_end;
       const int lo = key - q0 - 32 * group, hi = key_end - 1 - q0 - 32 * group;
@@ -652,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = guard.warp_wait(&X.q_full[at.slot], at.parity) &&          // the stats
            (C::kTwoS ? guard.warp_wait(&X.s_full[i & 1], (i >> 1) & 1)
                      : guard.warp_wait(&X.s_full[0], i & 1));
-      if (!ok) break;
+      if (!ok) return;
       ptx::tc_fence_after();
       uint32_t x[32];
       uint64_t p[16];
@@ -683,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (used < min(q0 + kBlock, L.T)) {        // the block holds padding: clear its Q and dO
         ok = guard.warp_wait(&X.do_full[at.slot], at.parity);
-        if (!ok) break;
+        if (!ok) return;
         if (group < 2 && q0 + r >= used)
           zero_row<DP>(sm + (group ? C::kDoRing : C::kQRing) + at.slot * C::kTile, r);
         ptx::fence_proxy_async_smem();
@@ -694,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(&X.p_full[C::kTwoS ? i & 1 : 0]);
 
       ok = guard.warp_wait(&X.dp_full, i & 1);
-      if (!ok) break;
+      if (!ok) return;
       ptx::tc_fence_after();
       ptx::tmem_ld32_sync(tp, x);
 #pragma unroll
@@ -717,6 +775,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 16; ++e)
           w[e] = pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
         ptx::tmem_st16(tp, w);
+        if constexpr (decltype(own)::value) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack2(__uint_as_float(x[2 * e]) - __uint_as_float(w[e] << 16),
+                         __uint_as_float(x[2 * e + 1]) - __uint_as_float(w[e] & 0xffff0000u));
+          ptx::tmem_st16(tp + 16, w);
+        }
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
@@ -724,6 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(&X.ds_full);
       at.next();
       if (++b == tile + blocks) b = tile;
+    };
+    const bool ends = first_end <= key0 + kBlock;
+    for (int i = 0; i < n && ok; ++i) {
+      if (ends && b == tile) step(i, std::true_type{});
+      else step(i, std::false_type{});
     }
     // V and K have been read for the last time: dv goes through V's place (groups 0, 1),
     // dk through K's (groups 2, 3)

@@ -121,6 +121,44 @@ def test_parity_over_heads(hq, hk, d):
     _check(*_draw(d, 300, hq, hk, d, fused=d != 96), [77, 0, 150, 73])
 
 
+@pytest.mark.parametrize("lengths", [[1], [2], [3], [2, 1], [5, 1, 2, 17], [128, 60, 3, 65],
+                                     [125, 0, 3, 1, 1, 2, 50]],
+                         ids=lambda x: ",".join(map(str, x)))
+@pytest.mark.parametrize("hq,hk,d", [(24, 8, 64), (4, 2, 128), (3, 1, 80), (8, 8, 32)])
+def test_short_sequences_round_dq_and_dk_once(lengths, hq, hk, d):
+    # Sequences inside a tile of 128 tokens: delta is sum p dp of the block, off by the errors of
+    # p and dp only, and ds goes into the products as two bf16 (U^2 = C); what is left of the
+    # bounds above is the result's own rounding and terms of C.
+    q, k, v, do = _draw(40 + sum(lengths) + d, sum(lengths), hq, hk, d)
+    cu = _cu(lengths)
+    out, lse = muon.attention(q, k, v, cu)
+    got = muon.attention_backward(do, q, k, v, out, lse, cu)[:2]
+    Q, K, V, D = (f64(x) for x in (q, k, v, do))
+    c, scale = cu.cpu().numpy(), d ** -0.5
+    r_out, _ = ref.attention(Q, K, V, c)
+    want = ref.attention_backward(D, Q, K, V, r_out, f64(lse), c)[:2]
+    bound = [np.zeros_like(Q), np.zeros_like(K)]
+    for a, b in ref.spans(c, sum(lengths)):
+        assert a // 128 == (b - 1) // 128
+        vis = np.tril(np.ones((b - a, b - a), dtype=bool))
+        for h in range(hq):
+            g = h // (hq // hk)
+            qq, kk, vv, dd = Q[a:b, h], K[a:b, g], V[a:b, g], D[a:b, h]
+            s = scale * (qq @ kk.T)
+            p = np.where(vis, np.exp(np.where(vis, s, -np.inf) - f64(lse)[h, a:b, None]), 0)
+            size = np.where(vis, scale * (np.abs(qq) @ np.abs(kk).T), 0)
+            ep = C * (1 + size.max(1, keepdims=True))
+            dp = np.abs(dd) @ np.abs(vv).T
+            # |dp - delta| <= dp + sum p dp; delta is off by 3 ep of its terms at most
+            mean = np.sum(p * dp, 1, keepdims=True)
+            e = p * (C * dp + 3 * (C + ep) * mean) + (C + ep) * p * (dp + mean)
+            bound[0][a:b, h] = scale * (e @ np.abs(kk))
+            bound[1][a:b, g] += scale * (e.T @ np.abs(qq))
+    for name, x, w, e in zip(("dq", "dk"), got, want, bound):
+        err = np.abs(f64(x) - w) - (U * np.abs(w) + (1 + U) * e + 1e-30)
+        assert np.all(err <= 0), (name, float(err.max()))
+
+
 @pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (2, 1, 128)])
 def test_parity_on_longer_sequences(hq, hk, d):
     _check(*_draw(1, 1500, hq, hk, d), [1100, 400])
