@@ -256,9 +256,11 @@ __device__ __forceinline__ void store_row32(uint8_t* tile, int row, int c, const
 
 // Columns outside lo..hi become `value`.
 __device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi, uint32_t value) {
+  const uint32_t visible = (lo > 31 ? 0u : ~0u << max(lo, 0)) &
+                           (hi < 0 ? 0u : ~0u >> (31 - min(hi, 31)));
 #pragma unroll
   for (int j = 0; j < 32; ++j)
-    if (j < lo || j > hi) s[j] = value;
+    if (!(visible >> j & 1u)) s[j] = value;
 }
 
 // ---- rows by definition -------------------------------------------------

@@ -479,7 +479,7 @@ template <int DP> struct DkvCfg {
   static constexpr uint32_t kV = kTile, kQRing = 2 * kTile, kDoRing = kQRing + kStages * kTile;
   static constexpr uint32_t kStats = kDoRing + kStages * kTile;
   static constexpr uint32_t kMisc = kStats + kStages * kStatBytes;
-  static constexpr uint32_t kSmem = kMisc + 512;
+  static constexpr uint32_t kSmem = kMisc + 1024;
   static constexpr bool kTwoS = DP == 64;
   static constexpr int kAhead = kTwoS ? 2 : 1;   // S of which block follows dv of one
   static __device__ __forceinline__ uint32_t s_col(int i) { return kTwoS && (i & 1) ? 384 : 0; }
@@ -490,10 +490,12 @@ struct DkvMisc {
   uint64_t s_full[2], dp_full, p_full[2], ds_full, done, drain;
   uint32_t tmem;
   int bad, skip;
+  int used;                        // tokens that belong to a sequence
   int first_end, blocks;           // end of the first key's sequence; query blocks per head
+  int key_end[kBlock];             // end of each key's sequence (no register is left for it)
   unsigned int repair[2][4];       // rows of dv, dk to compute again, by warp of the tile
 };
-static_assert(sizeof(DkvMisc) <= 512, "misc block");
+static_assert(sizeof(DkvMisc) <= 1024, "misc block");
 
 // Byte offset of 4 sums (columns 4 c .. 4 c + 3 of row r of dv or dk): rows of DP fp32 in
 // the place of the Q and dO rings, 16-byte columns permuted so that neither a warp's 32
@@ -566,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int used = tokens_in_use(L);
     int end = 0;
     if (key0 < used) end = sequence_of(L, min(key0 + 127, used - 1)).end;
+    X.used = used;
     X.first_end = sequence_of(L, key0).end;
     X.blocks = end > key0 ? (end - 1) / kBlock + 1 - tile : 0;
   }
@@ -693,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = warp >> 2, quarter = warp & 3;
     const int r = 32 * quarter + lane, key = key0 + r;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    const int used = tokens_in_use(L);
-    const int key_end = key < used ? sequence_of(L, key).end : key;
+    if (group == 0) X.key_end[r] = key < X.used ? sequence_of(L, key).end : key;
+    compute_barrier();
     const int first_end = X.first_end;
     const float c = L.scale * kLog2e;
     const uint64_t c2 = pair(c, c);
@@ -704,7 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto step = [&](int i, auto own) {                 // own: the keys' own block, with ends
       const int q0 = b * kBlock;
       const bool masked = b == tile || q0 + kBlock > first_end;
-      const int lo = key - q0 - 32 * group, hi = key_end - 1 - q0 - 32 * group;
+      const bool padded = masked && X.used < min(q0 + kBlock, L.T);
+      auto hide_unseen = [&](uint32_t (&s)[32]) {
+        hide(s, key - q0 - 32 * group, X.key_end[r] - 1 - q0 - 32 * group, 0u);
+      };
       const float4* lse2 =
           reinterpret_cast<const float4*>(sm + C::kStats + at.slot * kStatBytes) + 8 * group;
       ok = guard.warp_wait(&X.q_full[at.slot], at.parity) &&          // the stats
@@ -729,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[o + 1] = __float_as_uint(ex2(y.y));
         }
       }
-      if (masked) hide(x, lo, hi, 0u);
+      if (masked) hide_unseen(x);
       {
         uint32_t w[16];
 #pragma unroll
@@ -739,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_st16(ts, w);
       }
-      if (used < min(q0 + kBlock, L.T)) {        // the block holds padding: clear its Q and dO
+      if (padded) {                              // the block holds padding: clear its Q and dO
         ok = guard.warp_wait(&X.do_full[at.slot], at.parity);
         if (!ok) return;
-        if (group < 2 && q0 + r >= used)
+        if (group < 2 && q0 + r >= X.used)
           zero_row<DP>(sm + (group ? C::kDoRing : C::kQRing) + at.slot * C::kTile, r);
         ptx::fence_proxy_async_smem();
       }
@@ -768,7 +774,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[o + 1] = __float_as_uint(y.y);
         }
       }
-      if (masked) hide(x, lo, hi, 0u);
+      // (p is 0 where a key is not seen, and 0 times a dp of real data is 0; a row that NaN
+      // or Inf there reached is computed again below.  Padding may hold anything.)
+      if (padded) hide_unseen(x);
       {
         uint32_t w[16];
 #pragma unroll
@@ -828,12 +836,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float f[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          f[e] = key < used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+          f[e] = key < X.used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
           test = fmaf(f[e], 0.f, test);
         }
         store_row32(stage, r, col / 8, f);
       }
-      const unsigned int bad = __ballot_sync(0xffffffffu, key < used && test != 0.f);
+      const unsigned int bad = __ballot_sync(0xffffffffu, key < X.used && test != 0.f);
       if (bad && lane == 0) atomicOr(&X.repair[which][quarter], bad);
     }
     half_barrier(which);                               // (reached by every compute thread)
@@ -844,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int src = __ffs(bad) - 1;
         bad &= bad - 1;
         Row dk, dv;
-        dkv_row(L, kh, key - lane + src, __shfl_sync(0xffffffffu, key_end, src), dk, dv);
+        dkv_row(L, kh, key - lane + src, X.key_end[r - lane + src], dk, dv);
         put_row(stage, r - lane + src, which ? dk : dv, DP / 64);
       }
       ptx::fence_proxy_async_smem();
@@ -864,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_wait();
     if (run && !X.bad && warp < kProducerWarp) {
       // a warp adds up a row, a lane 4 columns of it
-      const int used = tokens_in_use(L), rows = kBlock / L.split;
+      const int used = X.used, rows = kBlock / L.split;
       for (int i = warp; i < 2 * rows; i += kProducerWarp) {
         const int which = i & 1, r = rank * rows + (i >> 1), key = key0 + r;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -226,6 +226,31 @@ def test_non_finite_values_reach_only_what_depends_on_them(which, value, d):
     assert np.isfinite(f64(lse)[fin]).all()
 
 
+@pytest.mark.parametrize("heads,d", [(20, 64), (40, 64), (40, 128)])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+def test_non_finite_values_with_many_heads(which, heads, d):
+    # as above where 2 blocks or 1 share a tile of the gradients (few heads: 4)
+    lengths = [60, 70, 200]
+    q, k, v, do = _draw(16, 330, heads, heads, d, fused=False)
+    x = {"q": q, "k": k, "v": v, "do": do}[which]
+    x[90, 1, 3], x[200, heads - 1, 0] = float("inf"), float("nan")
+    cu = _cu(lengths)
+    out, lse = muon.attention(q, k, v, cu)
+    grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+    some = [1, heads - 1]                 # the other heads hold finite values only
+    Q, K, V, D, O = (f64(y[:, some]) for y in (q, k, v, do, out))
+    with np.errstate(all="ignore"):
+        want = ref.attention_backward(D, Q, K, V, O, f64(lse[some]), cu.cpu().numpy())
+    for name, got, w in zip(("dq", "dk", "dv"), grads, want):
+        G = f64(got[:, some])
+        clean = np.isfinite(w).all(axis=2)
+        assert np.isfinite(G[clean]).all(), name
+        assert _rel(G[clean], w[clean]) <= REL, name
+        assert not np.isfinite(G[~clean]).all(axis=1).any(), name
+        rest = [h for h in range(heads) if h not in some]
+        assert torch.isfinite(got[:, rest]).all()
+
+
 def test_gradient_is_the_difference_quotient():
     # the oracle's forward differenced along a direction, against the kernel's gradients
     lengths = [40, 90]
