@@ -937,7 +937,11 @@ cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int 
   // time (in two waves it was no faster: 128 tiles of 4096 tokens, 8/4 heads of 64, 37 us
   // either way; 80 tiles of 2048 tokens, 5 heads of 80, 28 us instead of 24)
   const int units = (l.T + 127) / 128 * l.hk;
-  const int split = units * 4 <= sms ? 4 : units * 2 <= sms ? 2 : 1;
+  // ... but of one sequence, whose longest walk is known here to be 2 sms / ((tiles + 1) hk)
+  // times an SM's share of all walks: 4096 tokens, 8/4 heads of 64, (2.3 times) 74 us unsplit,
+  // 51 split; 8192 tokens (1.2 times) 137 and 147.
+  const bool uneven = l.n_seqs <= 1 && ((l.T + 127) / 128 + 1) * l.hk * 3 <= sms * 4;
+  const int split = units * 4 <= sms ? 4 : units * 2 <= sms || uneven ? 2 : 1;
   return l.dim <= 64
              ? launch(attention_dkv_kernel<64>, l.hk, split, DkvCfg<64>::kSmem, m, l, sms, s)
              : launch(attention_dkv_kernel<128>, l.hk, split, DkvCfg<128>::kSmem, m, l, sms, s);

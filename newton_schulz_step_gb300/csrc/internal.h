@@ -298,6 +298,7 @@ struct AttentionLaunch {
   float scale;
   unsigned int* status;
   int ranked;                       // blocks take the tiles by their work
+  int tiles;                        // forward: tiles of 128 rows a block takes
   int split;                        // dk, dv: blocks of a cluster that share a tile
 };
 
