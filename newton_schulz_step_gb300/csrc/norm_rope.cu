@@ -14,15 +14,14 @@
 // loads before it uses the first.  With the half layout a lane's 8 elements are 4 + 4,
 // rot / 2 apart, so that both members of a pair are in one thread: the rotation needs
 // no exchange, and only the sum of squares (backward: also the mean of G h) crosses
-// lanes.  Waiting rows stay in their storage type (80 registers, 24 warps on an SM), the
-// arithmetic is on fp32 pairs.
+// lanes.  Waiting rows stay in their storage type, the arithmetic is on fp32 pairs.
 // What held earlier forms back was the chain position -> table row -> first row: without
 // it the forward of 32768 tokens, 32 + 8 heads of 128, took 111 us instead of 146 (the
 // bytes alone: 101).  So a position is read a step ahead, and the table row with the rows
-// it belongs to: 138 us; with the lanes of a row known at compile time 130 us (4.3 TB/s of
-// the rows alone, 76 % of the copy rate with the tables and positions).  Backward of 16384
-// tokens, 16 + 16 heads of 128: 99 us (4.1 TB/s).  Instructions (155 a row of 8 elements
-// forward, 282 backward) hold the rest.
+// it belongs to: 138 us; with the lanes of a row known at compile time and no division
+// a step 121 us (5.7 TB/s with the tables and positions, 84 % of the copy rate).
+// Backward of 16384 tokens, 16 + 16 heads of 128: 86 us (4.8 TB/s, 70 %).  Issued
+// instructions hold the rest: about 150 for 8 elements forward, 250 backward.
 #include <type_traits>
 
 #include "internal.h"
@@ -33,9 +32,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// rows of a lane at a time: 4 x 16 bytes in flight (backward: 2 x 2 x 16)
-template <typename T, bool kBackward> constexpr int kIter = (kBackward ? 4 : 8) / sizeof(T);
-constexpr int kResident = 3;         // blocks on an SM
+// Rows of a lane at a time, and blocks on an SM: 4 x 16 bytes in flight in 24 warps, or
+// (backward) 4 x 2 x 16 in 16 warps.  (Backward with half the rows in 24 warps: 90 us
+// instead of 86 at the size above; forward with twice the rows in 16 warps: 125 instead of
+// 121.)
+template <typename T> constexpr int kIter = 8 / sizeof(T);
+template <bool kBackward> constexpr int kResident = kBackward ? 2 : 3;
 constexpr int kPartGroups = 32;      // first level of the weight gradients' sum
 constexpr int kGroupMax = kRopeMaxBlocks / kPartGroups;   // blocks per group
 static_assert(kGroupMax * kPartGroups == kRopeMaxBlocks, "groups cover the blocks");
@@ -190,9 +192,9 @@ __device__ __forceinline__ float sum_rows(const float* parts, int r0, int r1, in
 }
 
 template <typename T, bool kBackward, bool kInterleaved, int kLanes>
-__global__ void __launch_bounds__(kThreads, kResident)
+__global__ void __launch_bounds__(kThreads, kResident<kBackward>)
     norm_rope_kernel(const __grid_constant__ NormRopeLaunch L) {
-  constexpr int kN = kIter<T, kBackward>;
+  constexpr int kN = kIter<T>;
   __shared__ float s_dw[kBackward ? kWarps * 2 * kRopeMaxDim : 1];
   __shared__ int s_last;
   ptx::griddep_launch_dependents();
@@ -247,10 +249,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
       return pos >= 0 && pos < L.table_len ? pos : -1;
     };
     const int stride = gridDim.x * kWarps;
-    int row0 = (unit - passed) * (kN * per) + sub, t0 = row0 / heads;
+    int row0 = (unit - passed) * (kN * per) + sub, t0 = row0 / heads, h0 = row0 - t0 * heads;
+    const int row_step = stride * (kN * per), t_step = row_step / heads;
+    const int h_step = row_step - t_step * heads;      // (a division a step cost 25 instructions)
     int pos0 = L.rot > 0 && t0 < L.tokens ? position(t0) : 0;
     for (; unit - passed < count; unit += stride) {
-      const int h0 = row0 - t0 * heads;
       Raw<T> x[kN], dy[kBackward ? kN : 1];
       {
         const T* px = static_cast<const T*>(L.x[s].p) + t0 * L.x[s].ts + h0 * L.x[s].hs;
@@ -284,7 +287,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
         sines = __ldg(reinterpret_cast<const float4*>(L.sin + at));
       };
       if (rotated && pos0 >= 0) table_row(pos0);
-      const int next_row0 = row0 + stride * (kN * per), next_t0 = next_row0 / heads;
+      int next_t0 = t0 + t_step, next_h0 = h0 + h_step;
+      if (next_h0 >= heads) {
+        next_h0 -= heads;
+        ++next_t0;
+      }
       int next_pos0 = 0;
       if (L.rot > 0 && unit - passed + stride < count && next_t0 < L.tokens)
         next_pos0 = position(next_t0);
@@ -319,17 +326,19 @@ __global__ void __launch_bounds__(kThreads, kResident)
           for (int j = 0; j < 4; ++j) o[j] = mul2(mul2(v[j], r2), w[j]);
           if (rotated) angles.turn(o);
         } else {
-          const uint64_t r2 = pair(r, r), n2 = pair(poison, poison);
+          const uint64_t r2 = pair(r, r);
           dy[i].get(o);
+          if (__builtin_expect(poison != 1.f, 0)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = mul2(o[j], n2);
+            for (int j = 0; j < 4; ++j) o[j] = pair(poison, poison);
+          }
           if (rotated) angles.turn_back(o);
           if (L.norm) {
             uint64_t dot = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               v[j] = mul2(v[j], r2);
-              if (live) dw[j] = fma2(o[j], v[j], dw[j]);
+              dw[j] = fma2(o[j], v[j], dw[j]);       // (rows that are not there: 0)
               o[j] = mul2(o[j], w[j]);
               dot = fma2(o[j], v[j], dot);
             }
@@ -349,8 +358,9 @@ __global__ void __launch_bounds__(kThreads, kResident)
           py += yw;
         }
       }
-      row0 = next_row0;
+      row0 += row_step;
       t0 = next_t0;
+      h0 = next_h0;
       pos0 = next_pos0;
     }
     passed += count;
@@ -411,11 +421,11 @@ template <typename T, bool kBackward>
 cudaError_t launch(const NormRopeLaunch& l, int sms, cudaStream_t s) {
   int units = l.dim >> 3, g = 1;
   while (g < units) g <<= 1;
-  const long long chunk = kIter<T, kBackward> * (32 / g);
+  const long long chunk = kIter<T> * (32 / g);
   long long total = 0;
   for (int h : l.heads) total += (1ll * l.tokens * h + chunk - 1) / chunk;
   const long long want = (total + kWarps - 1) / kWarps;
-  const int cap = min(kRopeMaxBlocks, kResident * sms);
+  const int cap = min(kRopeMaxBlocks, kResident<kBackward> * sms);
   const int blocks = static_cast<int>(want < cap ? want : cap);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
