@@ -479,9 +479,12 @@ def _heads(t, name: str, shape, dtype, device) -> _Heads:
 def _out_heads(t, name: str, like):
     """(tensor, view) of an output shaped like `like`: the caller's, or a new contiguous one."""
     if t is None:
-        shape = like.shape
-        t = like.new_empty(shape)
-        return t, _Heads(t.data_ptr(), shape[1] * shape[2], shape[2])
+        t = torch.empty_like(like)        # (half the time of new_empty)
+        st, sh, _ = t.stride()
+        if not t.is_contiguous():         # it takes the strides of a dense tensor
+            t = like.new_empty(like.shape)
+            st, sh, _ = t.stride()
+        return t, _Heads(t.data_ptr(), st, sh)
     return t, _heads(t, name, like.shape, like.dtype, like.device)
 
 
@@ -489,20 +492,21 @@ def _ptr(t, name: str, device, dtype, shape=None):
     """Pointer of a contiguous tensor argument of one dtype (None passes)."""
     if t is None:
         return None
+    if (t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _elsewhere(device, stream) -> bool:
     """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != _current_device()
 
 
 @contextlib.contextmanager
@@ -519,7 +523,9 @@ def _launch_on(device, stream):
             yield
 
 
-# (the public current_stream() builds a Stream object, 2 us a call)
+# (the public current_stream() builds a Stream object, 2 us a call; current_device() looks
+# whether CUDA is up, which it is where there is a CUDA tensor)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -544,20 +550,28 @@ def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interle
         raise TypeError(f"q and k must be float32 or bfloat16, got {dtype}")
     vq = _heads(q, "q", shape, dtype, dev)
     t, hq, d = shape
-    if k.dim() != 3:
-        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(k.shape)}")
-    vk = _heads(k, "k", torch.Size((t, k.shape[1], d)), dtype, dev)
-    if cos.dim() != 2 or cos.shape != sin.shape:
+    k_shape = k.shape
+    if len(k_shape) != 3:
+        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(k_shape)}")
+    hk = k_shape[1]
+    vk = _heads(k, "k", (t, hk, d), dtype, dev)
+    table = cos.shape
+    if len(table) != 2 or table != sin.shape:
         raise ValueError("cos and sin must be [length, rot_dim / 2] of one shape")
     if not norm and (q_weight is not None or k_weight is not None):
         raise ValueError("weights belong to the norm: norm=False takes none")
     f32 = torch.float32
-    return _NormRope(1 if dtype is torch.bfloat16 else 0, t, hq, k.shape[1], d, 2 * cos.shape[1],
-                     1 if norm else 0, 1 if interleaved else 0, eps, cos.shape[0],
+    p_pos = p_qw = p_kw = None
+    if positions is not None:
+        p_pos = _ptr(positions, "positions", dev, torch.int32, (t,))
+    if q_weight is not None:
+        p_qw = _ptr(q_weight, "q_weight", dev, f32, (d,))
+    if k_weight is not None:
+        p_kw = _ptr(k_weight, "k_weight", dev, f32, (d,))
+    return _NormRope(1 if dtype is torch.bfloat16 else 0, t, hq, hk, d, 2 * table[1],
+                     1 if norm else 0, 1 if interleaved else 0, eps, table[0],
                      _ptr(cos, "cos", dev, f32), _ptr(sin, "sin", dev, f32),
-                     _ptr(positions, "positions", dev, torch.int32, (t,)),
-                     _ptr(q_weight, "q_weight", dev, f32, (d,)),
-                     _ptr(k_weight, "k_weight", dev, f32, (d,))), vq, vk
+                     p_pos, p_qw, p_kw), vq, vk
 
 
 def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None,
@@ -632,12 +646,13 @@ def _attention_spec(q, k, v, cu_seqlens, scale):
         raise TypeError(f"q, k and v must be bfloat16, got {dtype}")
     vq = _heads(q, "q", shape, dtype, dev)
     t, hq, d = shape
-    if k.dim() != 3:
-        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(k.shape)}")
-    hk = k.shape[1]
+    kv_shape = k.shape
+    if len(kv_shape) != 3:
+        raise ValueError(f"k must be [tokens, heads, head_dim], got {tuple(kv_shape)}")
+    hk = kv_shape[1]
     if hk == 0 or hq == 0 or hq % hk:
         raise ValueError(f"q heads ({hq}) must be a multiple of k heads ({hk})")
-    kv_shape = torch.Size((t, hk, d))
+    kv_shape = (t, hk, d)
     vk = _heads(k, "k", kv_shape, dtype, dev)
     vv = _heads(v, "v", kv_shape, dtype, dev)
     n_seqs, cu = 0, None
