@@ -247,8 +247,10 @@ muon_status muon_adam_step(const muon_adam_tensor* tensors, int n_tensors, int s
  * projection's output (and of its gradient) are used in place: element d of
  * head h of token t lies at data[t token_stride + h head_stride + d].  Strides
  * are in elements.  data and both strides are 16-byte aligned (a stride whose
- * dimension has one entry is ignored); rows of different (t, h) do not overlap
- * in an output.  head_dim is a multiple of 8.
+ * dimension has one entry is ignored) and strides are positive: a broadcast view
+ * (stride 0) is refused, its gradient would be a sum that no call here takes.
+ * Rows of different (t, h) do not overlap in an output.  head_dim is a multiple
+ * of 8.
  */
 typedef struct muon_heads {
   void* data;
@@ -334,7 +336,8 @@ muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_h
 
 /*
  * Gradients of muon_attention's out with respect to q, k and v, from its out and
- * lse.  With delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
+ * lse for the same q, k, v and offsets (of any other out the results are not
+ * defined: delta is corrected by what out was rounded by).  With delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
  *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
  * (dk and dv summed over the query heads that share the key/value head, in fp32).
  * Fixed summation order, no atomics: repeated calls give equal bits.

@@ -63,6 +63,10 @@ __device__ __forceinline__ void half_barrier(int half) {   // the lower or upper
 // Per block, in the tensor cores' order, one buffer of S: S of the next block (once the
 // exponentials have read this one), dq += dS K, dP of the next block; two buffers: dq,
 // dP of the next block, S of the one after.
+// What bounds it: heads of 128, the chain dP -> dS -> dq -> dP of the next block: dS is
+// written over dP, TMEM has no room for a second one.  8192 tokens, 32/8 heads: 660 us, its
+// products at 78 % of a library product's rate (tensor cores active 61 % of the cycles).
+// (Handing over dS before its remainders: 654 us.  Blocks of 64 keys: 815.)
 template <int DP> struct DqCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
@@ -468,8 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dv += P^T dO, S^T of the next block (two buffers: of the one after), dk += dS^T Q, dP^T
 // of the next block; so P of a block is computed beside the last two products of the one
 // before, and dS beside the first two of its own.  With heads of 128 the four products
-// run at 87 % of the rate that a library product reaches; with 64 the exponentials bound
-// the kernel, and the second buffer keeps the compute warps from waiting for S.
+// bound it: 88 % of the rate that a library product reaches (8192 tokens, 32/8 heads: 665
+// us).  With 64 the exponentials do, and the second buffer keeps the compute warps from
+// waiting for S.
 // Where the tiles leave SMs without work, 2 or 4 blocks of a cluster share a tile: each
 // walks its part of the queries, and they add up each other's sums through distributed
 // shared memory, in the order of their ranks.

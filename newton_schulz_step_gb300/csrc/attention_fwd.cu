@@ -20,9 +20,9 @@
 //                   products, with the tensor cores idle; without turns the tiles fall
 //                   into step.)
 //   warp 11         leaves its registers to the softmax
-// (Two threads a row, with 16 warps for the softmax, were measured slower: 2204 against
-// 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs more than
-// the other warps hide.)
+// (Two threads a row, with 16 warps for the softmax, were slower in an earlier form: 2204
+// against 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs
+// more than the other warps hide.)
 // TMEM: S of each tile (128 columns; P overwrites the first 64 as bf16 pairs, the A operand
 // of P V, handed over in two halves), O of each tile.  tcgen05 ops of one thread run in
 // order, so the commit that announces S of block b + 1 also says that P V of block b is
@@ -30,6 +30,11 @@
 // the maximum grows by more than 2^8 (P stays below 2^8; fp32 sums and O hold that
 // easily), so nearly never after the first blocks.
 // P is rounded to bf16, the tensor cores' input; l sums the unrounded values.
+// What bounds it: with heads of 128 the tensor cores.  16384 tokens, 32/8 heads of 128: 1190 us
+// for one call (1.85 PFLOP/s, as fast as a library product of that size), 1340 back to back
+// under the power limit.  With heads of 64 a block's products take half the time, and its
+// 16384 exponentials and the softmax's chain bound it; with few blocks a tile, the 5 us before
+// a block's first product and after its last.
 #include <climits>
 
 #include "attention.cuh"
