@@ -448,13 +448,15 @@ def rope_tables(length: int, rot_dim: int, *, base: float = 10000.0, scale: floa
 
 
 def _cuda_device(t, name: str):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
 
 
-def _refuse_heads(t, name, shape, dtype, device):
+# The checks below compare device indices, -1 for CPU tensors, and cost the host of a call
+# about 100 ns for each property of a tensor that they read.
+def _refuse_heads(t, name, shape, dtype, index):
     """Says what is wrong with a [tokens, heads, head_dim] argument."""
+    device = torch.device("cuda", index)
     _cuda_device(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
@@ -467,34 +469,34 @@ def _refuse_heads(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be contiguous along head_dim")
 
 
-def _heads(t, name: str, shape, dtype, device) -> _Heads:
+def _heads(t, name: str, shape, dtype, index) -> _Heads:
     """The view of a [tokens, heads, head_dim] tensor of the given shape, dtype and device."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and len(shape) == 3:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and len(shape) == 3:
         st, sh, sd = t.stride()
         if sd == 1 or shape[2] <= 1:
             return _Heads(t.data_ptr(), st, sh)
-    _refuse_heads(t, name, shape, dtype, device)
+    _refuse_heads(t, name, shape, dtype, index)
 
 
 def _out_heads(t, name: str, like):
     """(tensor, view) of an output shaped like `like`: the caller's, or a new contiguous one."""
     if t is None:
         t = torch.empty_like(like)        # (half the time of new_empty)
-        st, sh, _ = t.stride()
         if not t.is_contiguous():         # it takes the strides of a dense tensor
             t = like.new_empty(like.shape)
-            st, sh, _ = t.stride()
-        return t, _Heads(t.data_ptr(), st, sh)
-    return t, _heads(t, name, like.shape, like.dtype, like.device)
+        _, heads, dim = like.shape
+        return t, _Heads(t.data_ptr(), heads * dim, dim)
+    return t, _heads(t, name, like.shape, like.dtype, like.get_device())
 
 
-def _ptr(t, name: str, device, dtype, shape=None):
+def _ptr(t, name: str, index, dtype, shape=None):
     """Pointer of a contiguous tensor argument of one dtype (None passes)."""
     if t is None:
         return None
-    if (t.dtype is dtype and t.device == device and t.is_contiguous()
+    if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
             and (shape is None or t.shape == shape)):
         return t.data_ptr()
+    device = torch.device("cuda", index)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
@@ -502,11 +504,6 @@ def _ptr(t, name: str, device, dtype, shape=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _elsewhere(device, stream) -> bool:
-    """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != _current_device()
 
 
 @contextlib.contextmanager
@@ -532,20 +529,22 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _stream_ws = {}
 
 
-def _stream_workspace(ws, need: int, device, handle: int) -> Workspace:
+def _stream_workspace(ws, need: int, index: int, handle: int):
     """Pointer and size of the caller's workspace, or of one kept for each device and stream:
     calls on different streams may overlap, and must not share one."""
-    if ws is None:
-        key = (device.index, handle)
-        ws = _stream_ws.get(key)
-        if ws is None or ws.nbytes < need:
-            ws = _stream_ws[key] = Workspace(need, device)
-    return ws.ptr, ws.nbytes
+    if ws is not None:
+        return ws.ptr, ws.nbytes
+    kept = _stream_ws.get((index, handle))
+    if kept is None or kept[1] < need:
+        ws = Workspace(need, torch.device("cuda", index))
+        kept = _stream_ws[(index, handle)] = (ws.ptr, ws.nbytes, ws)
+    return kept[0], kept[1]
 
 
 def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
     """The spec of a call and its views of q and k."""
-    dev, shape, dtype = _cuda_device(q, "q"), q.shape, q.dtype
+    _cuda_device(q, "q")
+    dev, shape, dtype = q.get_device(), q.shape, q.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"q and k must be float32 or bfloat16, got {dtype}")
     vq = _heads(q, "q", shape, dtype, dev)
@@ -582,18 +581,18 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
     then the rotation of its first 2 * cos.shape[1] elements by rows `positions` (int32; the
     token's index when None) of the tables cos, sin (see rope_tables).  Pairs are (i, i + half),
     or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves."""
-    L = load_library()
+    L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
-    dev = q.device
-    if _elsewhere(dev, stream):
-        with _launch_on(dev, stream):
+    index = q.get_device()
+    if stream is not None or index != _current_device():
+        with _launch_on(q.device, stream):
             return qk_norm_rope(q, k, cos, sin, q_weight=q_weight, k_weight=k_weight,
                                 positions=positions, norm=norm, eps=eps, interleaved=interleaved,
                                 q_out=q_out, k_out=k_out)
     q_out, vqo = _out_heads(q_out, "q_out", q)
     k_out, vko = _out_heads(k_out, "k_out", k)
-    _raise(L.muon_qk_norm_rope(spec, vq, vk, vqo, vko, _current_handle(dev.index)),
+    _raise(L.muon_qk_norm_rope(spec, vq, vk, vqo, vko, _current_handle(index)),
            "muon_qk_norm_rope")
     return q_out, k_out
 
@@ -609,24 +608,24 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_we
                           workspace: Workspace | None = None, stream=None):
     """Gradients of qk_norm_rope: from those of its outputs, and its inputs, returns (dq, dk,
     dq_weight, dk_weight); the weights' are fp32, and None where no weight is given."""
-    L = load_library()
+    L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
-    dev, dtype = q.device, q.dtype
-    if _elsewhere(dev, stream):
-        with _launch_on(dev, stream):
+    index, dtype = q.get_device(), q.dtype
+    if stream is not None or index != _current_device():
+        with _launch_on(q.device, stream):
             return qk_norm_rope_backward(
                 dq_out, dk_out, q, k, cos, sin, q_weight=q_weight, k_weight=k_weight,
                 positions=positions, norm=norm, eps=eps, interleaved=interleaved, dq=dq, dk=dk,
                 workspace=workspace)
-    vdqo = _heads(dq_out, "dq_out", q.shape, dtype, dev)
-    vdko = _heads(dk_out, "dk_out", k.shape, dtype, dev)
+    vdqo = _heads(dq_out, "dq_out", q.shape, dtype, index)
+    vdko = _heads(dk_out, "dk_out", k.shape, dtype, index)
     dq, vdq = _out_heads(dq, "dq", q)
     dk, vdk = _out_heads(dk, "dk", k)
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
-    handle = _current_handle(dev.index)
-    ws, ws_bytes = _stream_workspace(workspace, norm_rope_workspace_bytes(spec.head_dim), dev, handle)
+    handle = _current_handle(index)
+    ws, ws_bytes = _stream_workspace(workspace, norm_rope_workspace_bytes(spec.head_dim), index, handle)
     _raise(L.muon_qk_norm_rope_backward(
         spec, vdqo, vdko, vq, vk, vdq, vdk, None if dqw is None else dqw.data_ptr(),
         None if dkw is None else dkw.data_ptr(), ws, ws_bytes, handle),
@@ -641,7 +640,8 @@ def attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim
 
 def _attention_spec(q, k, v, cu_seqlens, scale):
     """The spec of a call and its views of q, k and v."""
-    dev, shape, dtype = _cuda_device(q, "q"), q.shape, q.dtype
+    _cuda_device(q, "q")
+    dev, shape, dtype = q.get_device(), q.shape, q.dtype
     if dtype is not torch.bfloat16:
         raise TypeError(f"q, k and v must be bfloat16, got {dtype}")
     vq = _heads(q, "q", shape, dtype, dev)
@@ -673,23 +673,23 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     int32 [sequences + 1] on the device (None: one sequence).  scale is 1 / sqrt(head_dim) when
     None.  Returns (out, lse): out like q, lse [q_heads, tokens] fp32.  Tokens past the last
     sequence get out 0 and lse -inf."""
-    L = load_library()
+    L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
-    dev = q.device
-    if _elsewhere(dev, stream):
-        with _launch_on(dev, stream):
+    index = q.get_device()
+    if stream is not None or index != _current_device():
+        with _launch_on(q.device, stream):
             return attention(q, k, v, cu_seqlens, scale=scale, out=out, lse=lse,
                              workspace=workspace)
     t, hq, _ = q.shape
     out, vo = _out_heads(out, "out", q)
     if lse is None:
-        lse = torch.empty((hq, t), dtype=torch.float32, device=dev)
+        lse = torch.empty((hq, t), dtype=torch.float32, device=q.device)
         p_lse = lse.data_ptr()
     else:
-        p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
-    handle = _current_handle(dev.index)
+        p_lse = _ptr(lse, "lse", index, torch.float32, (hq, t))
+    handle = _current_handle(index)
     ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
-                                                                spec.head_dim), dev, handle)
+                                                                spec.head_dim), index, handle)
     _raise(L.muon_attention(spec, vq, vk, vv, vo, p_lse, ws, ws_bytes, handle),
            "muon_attention")
     return out, lse
@@ -700,23 +700,23 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
                        stream=None):
     """Gradients of attention's out: from dout, the inputs, and its out and lse, returns (dq, dk,
     dv) in bf16 (dk and dv summed over the query heads of a group)."""
-    L = load_library()
+    L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
-    dev, dtype = q.device, q.dtype
-    if _elsewhere(dev, stream):
-        with _launch_on(dev, stream):
+    index, dtype = q.get_device(), q.dtype
+    if stream is not None or index != _current_device():
+        with _launch_on(q.device, stream):
             return attention_backward(dout, q, k, v, out, lse, cu_seqlens, scale=scale, dq=dq,
                                       dk=dk, dv=dv, workspace=workspace)
     t, hq, _ = q.shape
-    vg = _heads(dout, "dout", q.shape, dtype, dev)
-    vo = _heads(out, "out", q.shape, dtype, dev)
-    p_lse = _ptr(lse, "lse", dev, torch.float32, (hq, t))
+    vg = _heads(dout, "dout", q.shape, dtype, index)
+    vo = _heads(out, "out", q.shape, dtype, index)
+    p_lse = _ptr(lse, "lse", index, torch.float32, (hq, t))
     dq, vdq = _out_heads(dq, "dq", q)
     dk, vdk = _out_heads(dk, "dk", k)
     dv, vdv = _out_heads(dv, "dv", k)
-    handle = _current_handle(dev.index)
+    handle = _current_handle(index)
     ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
-                                                                spec.head_dim), dev, handle)
+                                                                spec.head_dim), index, handle)
     _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws,
                                      ws_bytes, handle), "muon_attention_backward")
     return dq, dk, dv
