@@ -159,6 +159,25 @@ def test_short_sequences_round_dq_and_dk_once(lengths, hq, hk, d):
         assert np.all(err <= 0), (name, float(err.max()))
 
 
+@pytest.mark.parametrize("lengths", [[900, 700, 124], [1000, 10, 1100], [130, 1700, 300]],
+                         ids=lambda x: ",".join(map(str, x)))
+@pytest.mark.parametrize("hq,hk,d", [(80, 20, 64), (80, 40, 16), (80, 20, 128)])
+def test_parity_of_two_tiles_with_different_walks(lengths, hq, hk, d):
+    # many heads: a block takes two tiles, of which one may begin its walk blocks later
+    q, k, v, do = _draw(50 + d, sum(lengths), hq, hk, d)
+    cu = _cu(lengths)
+    out, lse = muon.attention(q, k, v, cu)
+    some = [0, hq - 1]
+    g = [h // (hq // hk) for h in some]
+    Q, K, V = f64(q[:, some]), f64(k[:, g]), f64(v[:, g])
+    r_out, r_lse = ref.attention(Q, K, V, cu.cpu().numpy())
+    b_out, b_lse, *_ = _magnitudes(Q, K, V, np.zeros_like(Q), r_out, r_lse, cu.cpu().numpy(),
+                                   d ** -0.5)
+    err = np.abs(f64(out[:, some]) - r_out) - (U * np.abs(r_out) + (1 + U) * b_out + 1e-30)
+    assert np.all(err <= 0), float(err.max())
+    assert np.all(np.abs(f64(lse[some]) - r_lse) <= b_lse + 1e-30)
+
+
 @pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (2, 1, 128)])
 def test_parity_on_longer_sequences(hq, hk, d):
     _check(*_draw(1, 1500, hq, hk, d), [1100, 400])
