@@ -14,12 +14,12 @@
 // one tile's S into P, the tensor cores run the other tile's products:
 //   warps 0-3, 4-7  softmax of tile 0, 1 (a thread owns a row), then the epilogue
 //   warp 8          TMA: Q once, then K and V blocks through a ring
-//   warps 9, 10     heads of 128: MMA of tile 0, 1: per block  O += P V, then S of the next
+//   warps 9, 10     MMA of tile 0, 1.  Heads of 128: per block  O += P V, then S of the next
 //                   block, in turns, so that one tile's softmax falls on the other's
 //                   products.  (One warp for both took 1500 cycles of waits and commits
 //                   between its products, with the tensor cores idle; without turns the
-//                   tiles fall into step.)
-//                   heads of 64: S, and P V, of both tiles (see Slots)
+//                   tiles fall into step.)  Heads of 64: S of the next block as soon as the
+//                   softmax has read this one, then O += P V
 //   warp 11         leaves its registers to the softmax
 // (Two threads a row, with 16 warps for the softmax, were slower in an earlier form: 2204
 // against 1623 us on 16384 tokens, 32/8 heads of 128 -- the exchange of the maxima costs
@@ -27,9 +27,13 @@
 // TMEM: S of each tile (128 columns; P overwrites the first 64 as bf16 pairs, the A operand
 // of P V, handed over in two halves), O of each tile.  tcgen05 ops of one thread run in
 // order, so the commit that announces S of block b + 1 also says that P V of block b is
-// done (heads of 64: a commit of its own): O may be rescaled before P of block b + 1 is
-// handed over.  O is rescaled only when the maximum grows by more than 2^8 (P stays below
-// 2^8; fp32 sums and O hold that easily), so nearly never after the first blocks.
+// done: O may be rescaled before P of block b + 1 is handed over.  O is rescaled only when
+// the maximum grows by more than 2^8 (P stays below 2^8; fp32 sums and O hold that easily),
+// so nearly never after the first blocks.  Heads of 64 leave room for P beside S: the next S
+// is ready when its softmax begins, and a commit of its own says that P V is done.  8192
+// tokens of 5 to 2400, 12 heads: 43.1 us instead of 45.6 with P over S.  (A third S instead,
+// that either tile's next block takes: 42.9, but one sequence of 8192 tokens in 158 us
+// instead of 154.)
 // P is rounded to bf16, the tensor cores' input; l sums the unrounded values.
 // What bounds it: with heads of 128 the tensor cores.  16384 tokens, 32/8 heads of 128: 1190 us
 // for one call (1.85 PFLOP/s, as fast as a library product of that size), 1340 back to back
@@ -69,9 +73,9 @@ __device__ __forceinline__ void registers_up() {
 template <int DP> struct Cfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kStages = DP == 128 ? 5 : 8;
-  static constexpr bool kThreeS = DP == 64;                  // buffers of S (see Slots)
-  static constexpr int kDepth = kThreeS ? 4 : 1;             // barriers of S and P a tile
-  static constexpr uint32_t kOCol = kThreeS ? 384 : 128 * kTiles;
+  static constexpr bool kOwnP = DP == 64;                    // P has columns of its own
+  static constexpr uint32_t kOCol = kOwnP ? 384 : 256;
+  static __device__ __forceinline__ uint32_t p_col(int t) { return kOwnP ? 256 + 64 * t : 128 * t; }
   static constexpr uint32_t kRing = kTiles * kTile;          // after Q
   static constexpr uint32_t kMisc = kRing + kStages * kTile;
   static constexpr uint32_t kSmem = kMisc + kMiscBytes;
@@ -79,7 +83,7 @@ template <int DP> struct Cfg {
 
 struct Misc {
   uint64_t full[8], empty[8];
-  uint64_t q_full[kTiles], s_full[kTiles][4], p_full[kTiles][4][2], o_full[kTiles][4];
+  uint64_t q_full[kTiles], s_full[kTiles], s_read[kTiles], p_full[kTiles][2], o_full[kTiles];
   uint64_t drain[kTiles], turn[kTiles];
   uint32_t tmem;
   int bad, skip;                       // abort flag; the workspace had failed before
@@ -102,36 +106,6 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[32]) {
   return max3(a, b, fmaxf(x[2], x[3]));
 }
 
-// Heads of 64 leave room in TMEM for a third buffer of S.  The blocks of both tiles make up
-// one row of slots (tile 0 alone from its first block on, both in turns, tile 1 alone at the
-// end); slot j takes buffer j % 3, and S of slot j + 3 follows P V of slot j: a tile finds its
-// next S ready when it has handed over P.  8192 tokens of 5 to 2400, 12 heads: 42.8 us instead
-// of 45.6 with a buffer a tile; one sequence of 8192, 16/4 heads: 157 instead of 154.  (One
-// warp for S and P V of both tiles: 52.)  The waiters of S, P and O need 4 barriers a tile:
-// with a single one, or one a buffer, two phases could end before a waiter has seen the first.
-struct Slots {
-  int b00, b01, b10, b11;              // blocks of tile 0: [b00, b10), of tile 1: [b01, b11)
-  __device__ __forceinline__ int count() const { return b10 - b00 + b11 - b01; }
-  __device__ __forceinline__ bool shared(int b) const { return b >= b01 && b < b10; }
-  __device__ __forceinline__ int of(int t, int b) const {
-    if (t == 0) return b - b00 + max(b - b01, 0);
-    return b - b00 + min(b, b10 - 1) - b01 + 1;
-  }
-  __device__ __forceinline__ void at(int j, int* t, int* b) const {
-    const int alone = b01 - b00, both = b10 - b01;
-    if (j < alone) {
-      *t = 0;
-      *b = b00 + j;
-    } else if (j < alone + 2 * both) {
-      *t = (j - alone) & 1;
-      *b = b01 + ((j - alone) >> 1);
-    } else {
-      *t = 1;
-      *b = b10 + j - alone - 2 * both;
-    }
-  }
-};
-
 __device__ __forceinline__ void tile_barrier(int t) {   // the four warps of a tile
   asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
 }
@@ -149,16 +123,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp && lane == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(&X.full[s], 1);
-      ptx::mbar_init(&X.empty[s], C::kThreeS ? 1 : kTiles);
+      ptx::mbar_init(&X.empty[s], kTiles);
     }
     for (int t = 0; t < kTiles; ++t) {
       ptx::mbar_init(&X.q_full[t], 1);
-      for (int i = 0; i < C::kDepth; ++i) {
-        ptx::mbar_init(&X.s_full[t][i], 1);
-        ptx::mbar_init(&X.p_full[t][i][0], 4);
-        ptx::mbar_init(&X.p_full[t][i][1], 4);
-        ptx::mbar_init(&X.o_full[t][i], 1);
-      }
+      ptx::mbar_init(&X.s_full[t], 1);
+      ptx::mbar_init(&X.s_read[t], 4);
+      ptx::mbar_init(&X.p_full[t][0], 4);
+      ptx::mbar_init(&X.p_full[t][1], 4);
+      ptx::mbar_init(&X.o_full[t], 1);
       ptx::mbar_init(&X.drain[t], 1);
       ptx::mbar_init(&X.turn[t], 1);
     }
@@ -208,16 +181,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     : warp < kProducerWarp ? kErrTimeoutEpilogue
                                            : kErrTimeoutMma};
 
-  // key blocks of each tile, [b0, b1), and of both (the same in every lane).  Tile 1 begins no
-  // earlier than tile 0; without a tile 1 its empty range is where tile 0 ends.
-  int b0[kTiles], b1[kTiles];
-  b0[0] = __shfl_sync(0xffffffffu, X.first[0], 0) / kBlock;
-  b0[1] = max(__shfl_sync(0xffffffffu, X.first[1], 0) / kBlock, b0[0]);
-  b1[0] = row0 / kBlock + 1;
-  b1[1] = b1[0] + 1;
-  if (L.tiles < 2 || row0 + 128 >= L.T) b0[1] = b1[1] = b1[0];
-  const int begin = b0[0], end = b1[1];
-  const Slots slots{b0[0], b0[1], b1[0], b1[1]};
+  // key blocks of each tile, [b0, b1), and of both
+  int b0[kTiles], b1[kTiles], begin = INT_MAX, end = 0;   // (the same in every lane)
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int r = row0 + 128 * t;
+    const bool used = t < L.tiles && r < L.T;
+    b0[t] = used ? __shfl_sync(0xffffffffu, X.first[t], 0) / kBlock : 0;
+    b1[t] = used ? r / kBlock + 1 : 0;
+    if (used) {
+      begin = min(begin, b0[t]);
+      end = max(end, b1[t]);
+    }
+  }
+  auto active = [&](int t, int b) { return b >= b0[t] && b < b1[t]; };
+
   const bool run = !X.skip;
   if (warp >= kProducerWarp) {
     registers_down();
@@ -234,15 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n;
         };
         for (int t = 0; t < kTiles; ++t)
-          if (b0[t] < b1[t])
-            load_tile<DP>(sm + t * C::kTile, &M.q, h, row0 + 128 * t, &X.q_full[t]);
+          if (b1[t] > 0) load_tile<DP>(sm + t * C::kTile, &M.q, h, row0 + 128 * t, &X.q_full[t]);
         for (int b = begin; b < end && ok; ++b) {
           load(&M.k, b * kBlock);
           load(&M.v, b * kBlock);
         }
         if (!ok) {                       // copies in flight land before the CTA ends
           for (int t = 0; t < kTiles; ++t)
-            if (b0[t] < b1[t]) ptx::mbar_wait(&X.q_full[t], 0, nullptr, nullptr, kDrainNs);
+            if (b1[t] > 0) ptx::mbar_wait(&X.q_full[t], 0, nullptr, nullptr, kDrainNs);
           for (int i = n > C::kStages ? n - C::kStages : 0; i < n; ++i)
             ptx::mbar_wait(&X.full[i % C::kStages], (i / C::kStages) & 1, nullptr, nullptr,
                            kDrainNs);
@@ -250,69 +227,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (run && warp < kMmaWarp + kTiles) {
       const int t = warp - kMmaWarp;
+      const int first = b0[t], last = b1[t];
+      const uint32_t q = tile_address(sm) + t * C::kTile;
       const uint32_t ring = tile_address(sm) + C::kRing;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         ok = ok && guard.issue_wait(bar, parity);
         return ok;
       };
-      if constexpr (C::kThreeS) {
-        auto slot_of = [&](int n) { return n % C::kStages; };
-        auto landed = [&](int n) {       // the n-th load of the ring
-          return wait(&X.full[slot_of(n)], (n / C::kStages) & 1);
+      // S of a block (the K tile has landed)
+      auto scores = [&](int slot) {
+        mma_heads<DP>(128 * t, q, ring + slot * C::kTile);
+        ptx::mma_commit(&X.s_full[t]);
+      };
+      auto has = [&](int b) { return b >= first && b < last; };
+      if constexpr (C::kOwnP) {
+        auto load = [&](int n) {         // the slot of the ring's n-th load, which has landed
+          wait(&X.full[n % C::kStages], (n / C::kStages) & 1);
+          return n % C::kStages;
         };
-        auto read = [&](int tile, int b, int n) {   // by a tile; the last one frees the slot
-          if (tile == 1 || !slots.shared(b)) ptx::mma_commit(&X.empty[slot_of(n)]);
-        };
-        auto scores = [&](int j, int tile, int b) {
-          const int n = 2 * (b - begin);
-          mma_heads<DP>(128 * (j % 3), tile_address(sm) + tile * C::kTile,
-                        ring + slot_of(n) * C::kTile);
-          ptx::mma_commit(&X.s_full[tile][(b - (tile ? b0[1] : b0[0])) % C::kDepth]);
-          read(tile, b, n);
-        };
-        const int count = slots.count();
-        if (t == 0) {                    // S of every slot, behind P V of the third before it
-          for (int j = 0; j < count && ok; ++j) {
-            int tile, b;
-            slots.at(j, &tile, &b);
-            landed(2 * (b - begin));
-            wait(&X.q_full[tile], 0);
-            if (j >= 3) {
-              int before, bb;
-              slots.at(j - 3, &before, &bb);
-              const int i = bb - (before ? b0[1] : b0[0]);
-              wait(&X.o_full[before][i % C::kDepth], (i / C::kDepth) & 1);
-            }
-            if (!ok) break;
+        for (int b = begin - 1; b < end && ok; ++b) {
+          if (b + 1 < end) {
+            const int ks = load(2 * (b + 1 - begin));
+            if (b + 1 == first && first < last) wait(&X.q_full[t], 0);
+            if (has(b) && has(b + 1)) wait(&X.s_read[t], (b - first) & 1);
             ptx::tc_fence_after();
-            if (ptx::elect_one()) scores(j, tile, b);
-            __syncwarp();
-          }
-        } else {                         // P V of every slot
-          for (int j = 0; j < count && ok; ++j) {
-            int tile, b;
-            slots.at(j, &tile, &b);
-            const int vn = 2 * (b - begin) + 1, i = b - (tile ? b0[1] : b0[0]);
-            const uint32_t parity = (i / C::kDepth) & 1, v = ring + slot_of(vn) * C::kTile;
-            const uint32_t o = C::kOCol + DP * tile, p = 128 * (j % 3);
-            landed(vn);
-            if (!wait(&X.p_full[tile][i % C::kDepth][0], parity)) break;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) mma_rows<DP, 64, 32>(o, p, v, i > 0);
-            if (!wait(&X.p_full[tile][i % C::kDepth][1], parity)) break;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-              mma_rows<DP, 64, 32>(o, p + 32, v + 8192, true);
-              ptx::mma_commit(&X.o_full[tile][i % C::kDepth]);
-              read(tile, b, vn);
+            if (ok && ptx::elect_one()) {
+              if (has(b + 1)) scores(ks);
+              ptx::mma_commit(&X.empty[ks]);
             }
             __syncwarp();
           }
+          if (b < begin || !ok) continue;
+          const int vs = load(2 * (b - begin) + 1);
+          const bool mine = has(b);
+          const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
+          if (mine) {
+            if (!wait(&X.p_full[t][0], parity)) break;
+            ptx::tc_fence_after();
+            if (ptx::elect_one())
+              mma_rows<DP, 64, 32>(C::kOCol + DP * t, C::p_col(t), v, b > first);
+            wait(&X.p_full[t][1], parity);
+            ptx::tc_fence_after();
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) {
+            if (mine) {
+              mma_rows<DP, 64, 32>(C::kOCol + DP * t, C::p_col(t) + 32, v + 8192, true);
+              ptx::mma_commit(&X.o_full[t]);
+            }
+            ptx::mma_commit(&X.empty[vs]);
+          }
+          __syncwarp();
         }
       } else {
-        const int first = b0[t], last = b1[t];
-        const uint32_t q = tile_address(sm) + t * C::kTile;
         Ring<C::kStages> at;             // next slot of the ring
         auto take = [&] {
           const int s = at.slot;
@@ -320,12 +288,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           at.next();
           return s;
         };
-        // S of a block (the K tile has landed)
-        auto scores = [&](int slot) {
-          mma_heads<DP>(128 * t, q, ring + slot * C::kTile);
-          ptx::mma_commit(&X.s_full[t][0]);
-        };
-        auto has = [&](int b) { return b >= first && b < last; };
         if (begin < end) {
           const int ks = take();
           if (has(begin)) wait(&X.q_full[t], 0);
@@ -343,19 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b + 1 == first && first < last) wait(&X.q_full[t], 0);
           const bool mine = has(b), next = has(b + 1);
           const uint32_t parity = (b - first) & 1, v = ring + vs * C::kTile;
-          if (mine) wait(&X.p_full[t][0][0], parity);
+          if (mine) wait(&X.p_full[t][0], parity);
           // the tiles take turns: tile 0 waits for tile 1's last block, tile 1 for this one
           if (!wait(&X.turn[t], ((b - begin) & 1) ^ (t == 0 ? 1 : 0))) break;
           if (mine) {
             ptx::tc_fence_after();
             if (ptx::elect_one())
               mma_rows<DP, 64, 32>(C::kOCol + DP * t, 128 * t, v, b > first);
-            if (!wait(&X.p_full[t][0][1], parity)) break;
+            if (!wait(&X.p_full[t][1], parity)) break;
           }
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             if (mine) mma_rows<DP, 64, 32>(C::kOCol + DP * t, 128 * t + 32, v + 8192, true);
-            if (mine && b + 1 == last) ptx::mma_commit(&X.o_full[t][0]);
+            if (mine && b + 1 == last) ptx::mma_commit(&X.o_full[t]);
             if (next) scores(ks);
             ptx::mbar_arrive(&X.turn[t ^ 1]);
             ptx::mma_commit(&X.empty[vs]);
@@ -375,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (run) {
       const int t = warp >> 2, r = tid & 127, row = row0 + 128 * t + r;
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-      uint32_t ts = lanes + 128 * t;
+      const uint32_t ts = lanes + 128 * t, tp = lanes + C::p_col(t);
       const uint32_t to = lanes + C::kOCol + DP * t;
       const int row_begin = row < L.T ? sequence_of(L, row).begin : row + 1;
       const int last_begin = X.last[t], first_block = b0[t], blocks_end = b1[t];
@@ -386,14 +348,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int b = first_block; b < blocks_end; ++b) {
         const int k0 = b * kBlock;
-        const int turn = (b - first_block) % C::kDepth;
-        if constexpr (C::kThreeS) ts = lanes + 128 * (slots.of(t, b) % 3);
-        ok = guard.warp_wait(&X.s_full[t][turn], ((b - first_block) / C::kDepth) & 1);
+        ok = guard.warp_wait(&X.s_full[t], (b - first_block) & 1);
         if (!ok) break;
         ptx::tc_fence_after();
         uint32_t s[4][32];
         ptx::tmem_ld32x2_sync(ts, ts + 32, s[0], s[1]);
         ptx::tmem_ld32x2_sync(ts + 64, ts + 96, s[2], s[3]);
+        if constexpr (C::kOwnP) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&X.s_read[t]);
+        }
         if (__builtin_expect(k0 < last_begin || b + 1 == blocks_end, 0)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -404,14 +369,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (b == first_block) {
           m = mb;
         } else {
+          if constexpr (C::kOwnP) {                    // P and O of the block before are free
+            ok = guard.warp_wait(&X.o_full[t], (b - 1 - first_block) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
           const bool grow = mb > m && !((mb - m) * c <= kRescale);
           if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
-            if constexpr (C::kThreeS) {                // P V of the block before has ended
-              const int before = b - 1 - first_block;
-              ok = guard.warp_wait(&X.o_full[t][before % C::kDepth], (before / C::kDepth) & 1);
-              if (!ok) break;
-              ptx::tc_fence_after();
-            }
             const float f = grow ? ex2((m - mb) * c) : 1.f;
             if (grow) m = mb;
             l *= f;
@@ -447,22 +411,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[j & 1] = add2(sum[j & 1], pair(y.x, y.y));
             p[j] = pack2(y.x, y.y);
           }
-          ptx::tmem_st16(ts + 16 * i, p);
+          ptx::tmem_st16(tp + 16 * i, p);
           if (i & 1) {                                 // half of P is ready for its product
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&X.p_full[t][turn][i >> 1]);
+            if (lane == 0) ptx::mbar_arrive(&X.p_full[t][i >> 1]);
           }
         }
         const float2 a = unpair(add2(sum[0], sum[1]));
         l += a.x + a.y;
       }
-      const int blocks = blocks_end - first_block;
-      const int end_turn = C::kThreeS ? blocks - 1 : 0;
-      if (ok && blocks > 0)
-        ok = guard.warp_wait(&X.o_full[t][end_turn % C::kDepth], (end_turn / C::kDepth) & 1);
-      if (ok && blocks > 0) {
+      if (ok && blocks_end > 0)
+        ok = guard.warp_wait(&X.o_full[t], C::kOwnP ? (blocks_end - 1 - first_block) & 1 : 0);
+      if (ok && blocks_end > 0) {
         ptx::tc_fence_after();
         // Q of this tile has been read for the last time: out goes through its place
         uint8_t* stage = sm + t * C::kTile;
@@ -494,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
       }
-      if (blocks > 0) {
+      if (blocks_end > 0) {
         tile_barrier(t);                               // (reached by every thread of the tile)
         if (ok && r == 0 && !X.bad) {
 #pragma unroll
