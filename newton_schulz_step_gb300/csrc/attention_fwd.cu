@@ -58,7 +58,7 @@ constexpr uint32_t kMiscBytes = 512;
 
 // Registers move from the warps that only issue work to those that compute: a block is
 // launched with 168 a thread (64512), of which 4 warps keep kIssueRegs and 8 get
-// kComputeRegs.  The issuing roles must fit kIssueRegs as compiled without the split (62):
+// kComputeRegs.  The issuing roles must fit kIssueRegs as compiled without the split (57):
 // with 40 the compiler's allocation was seen to break (waits ran into their limit).
 constexpr int kIssueRegs = 104, kComputeRegs = 200;
 static_assert(128 * kIssueRegs + 256 * kComputeRegs == kThreads * 168,
