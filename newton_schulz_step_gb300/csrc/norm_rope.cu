@@ -328,7 +328,9 @@ __global__ void __launch_bounds__(kThreads, kResident<kBackward>)
         } else {
           const uint64_t r2 = pair(r, r);
           dy[i].get(o);
-          if (__builtin_expect(poison != 1.f, 0)) {
+          // (lanes past the head, and rows that are not there, keep their zeros: they enter the
+          // sums of rows whose position is good)
+          if (__builtin_expect(live && poison != 1.f, 0)) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = pair(poison, poison);
           }

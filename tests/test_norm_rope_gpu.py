@@ -224,3 +224,23 @@ def test_refusals():
     with pytest.raises(muon.MuonError):                    # not 16-byte aligned
         muon.qk_norm_rope(torch.empty(20 * 256 + 1, dtype=q.dtype, device="cuda")[1:].view(
             20, 4, 64), k, cos, sin)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("hq,hk,d,rot", [(2, 1, 24, 16), (1, 1, 80, 80), (3, 1, 96, 64),
+                                         (2, 2, 40, 8), (1, 1, 200, 200)])
+def test_position_outside_the_tables_with_lanes_past_the_head(hq, hk, d, rot, interleaved, dtype):
+    # d / 8 is no power of two: some lanes of a row hold none of its elements
+    t = 150
+    q, k, cos, sin, w, dy, pos = _draw(18 + d, t, hq, hk, d, rot, dtype)
+    bad = torch.zeros(t, dtype=torch.bool, device="cuda")
+    bad[[0, 3, 11, 64, 149]] = True
+    p = torch.where(bad, torch.tensor(t, dtype=torch.int32, device="cuda"), pos)
+    kw = dict(q_weight=w[0], k_weight=w[1], interleaved=interleaved)
+    y = muon.qk_norm_rope(q, k, cos, sin, positions=p, **kw)
+    dx = muon.qk_norm_rope_backward(dy[0], dy[1], q, k, cos, sin, positions=p, **kw)
+    good = muon.qk_norm_rope(q, k, cos, sin, positions=pos, **kw)
+    good += muon.qk_norm_rope_backward(dy[0], dy[1], q, k, cos, sin, positions=pos, **kw)[:2]
+    for x, want in zip((*y, *dx[:2]), good):
+        assert torch.isnan(x[bad]).all() and torch.equal(x[~bad], want[~bad])
