@@ -311,6 +311,7 @@ muon_status muon_qk_norm_rope_backward(const muon_norm_rope* spec, muon_heads dq
  *   s_ij = scale q_i . k_j,  a <= j <= i;   lse_i = log sum_j exp(s_ij)
  *   out_i = sum_j exp(s_ij - lse_i) v_j
  * Tokens past the last sequence get out = 0 and lse = -inf, and no gradient.
+ * A token of a sequence whose visible scores are all -inf gets NaN in both.
  * A token's results depend on its own sequence's tokens up to it alone: Inf or
  * NaN elsewhere does not reach them.  Offsets that do not ascend give undefined
  * results (no access leaves the tensors).

@@ -340,7 +340,7 @@ static __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int 
     axpy(acc, p, load_row(L.v.row(j, kh), L.dim));
     m = mn;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = 1.f / l;               // (l = 0, all scores -inf: NaN)
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc.v[e] *= inv;
   return acc;

@@ -428,7 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         // Q of this tile has been read for the last time: out goes through its place
         uint8_t* stage = sm + t * C::kTile;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        // A row without keys (padding) is 0, -inf.  One whose visible scores are all -inf has
+        // l = 0 too, and is NaN by the definition: 0 times 1 / 0 here, and lse in its place.
+        const bool keys = row_begin <= row;
+        const float inv = 1.f / l;
         float test = 0.f;                              // NaN if an element is not finite
 #pragma unroll
         for (int i = 0; i < DP / 32; ++i) {
@@ -437,14 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            f[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * inv;
+            f[j] = keys ? __uint_as_float(o[j]) * inv : 0.f;
             test = fmaf(f[j], 0.f, test);
           }
           store_row32(stage, r, 4 * i, f);
         }
         if (row < L.T)
           L.lse[static_cast<size_t>(h) * L.T + row] =
-              l == 0.f ? -INFINITY : m * L.scale + __logf(l);
+              !keys ? -INFINITY : l == 0.f ? NAN : m * L.scale + __logf(l);
         __syncwarp();
         unsigned int bad = __ballot_sync(0xffffffffu, row < L.T && test != 0.f);
         while (bad) {

@@ -457,3 +457,30 @@ def test_refusals():
         muon.attention(*(torch.zeros(4, 1, 20, dtype=q.dtype, device="cuda") for _ in range(3)))
     with pytest.raises(ValueError):
         muon.attention_backward(do, q, k, v, out, lse[:, :3])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 3])       # of the sequence that see minus infinity only
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_rows_whose_visible_scores_are_all_minus_infinity(sign, tokens, d):
+    # exp(s - max s) is exp(-inf + inf): NaN, as by the definition; not the 0 of a row without keys
+    q, k, v, do = _draw(60 + d, 330, 4, 2, d, fused=False)
+    h0, e0, rows = 1, 3, slice(60, 60 + tokens)           # the second sequence's first tokens
+    q[rows, h0, e0] = sign * float("inf")
+    k[rows, h0 // 2, e0] = -sign
+    cu = _cu([60, 70, 150])                               # and 50 tokens of no sequence
+    out, lse = muon.attention(q, k, v, cu)
+    grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+    Q, K, V, D = (f64(x) for x in (q, k, v, do))
+    with np.errstate(all="ignore"):
+        r_out, r_lse = ref.attention(Q, K, V, cu.cpu().numpy())
+        r_grads = ref.attention_backward(D, Q, K, V, f64(out), f64(lse), cu.cpu().numpy())
+    assert np.isnan(r_out[rows, h0]).all() and np.isnan(r_lse[h0, rows]).all()
+    for name, got, want in [("out", out, r_out), *zip(("dq", "dk", "dv"), grads, r_grads)]:
+        G = f64(got)
+        clean = np.isfinite(want).all(axis=2)
+        assert np.isfinite(G[clean]).all(), name
+        assert _rel(G[clean], want[clean]) <= REL, name
+        assert not np.isfinite(G[~clean]).all(axis=1).any(), name
+    assert np.array_equal(np.isnan(f64(lse)), np.isnan(r_lse))
+    assert np.array_equal(np.isneginf(f64(lse)), np.isneginf(r_lse))
