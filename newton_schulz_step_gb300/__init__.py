@@ -23,6 +23,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 
 import torch
 
@@ -526,18 +527,26 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+# (device index, stream handle) -> (pointer, bytes, Workspace, the entry it outgrew)
 _stream_ws = {}
+_stream_ws_lock = threading.Lock()
 
 
 def _stream_workspace(ws, need: int, index: int, handle: int):
     """Pointer and size of the caller's workspace, or of one kept for each device and stream:
-    calls on different streams may overlap, and must not share one."""
+    calls on different streams may overlap, and must not share one.  A workspace that is
+    outgrown stays allocated, for another thread may be about to launch with its pointer; sizes
+    double, so that all of them together are less than twice the last."""
     if ws is not None:
         return ws.ptr, ws.nbytes
     kept = _stream_ws.get((index, handle))
     if kept is None or kept[1] < need:
-        ws = Workspace(need, torch.device("cuda", index))
-        kept = _stream_ws[(index, handle)] = (ws.ptr, ws.nbytes, ws)
+        with _stream_ws_lock:
+            kept = _stream_ws.get((index, handle))
+            if kept is None or kept[1] < need:
+                ws = Workspace(need if kept is None else max(need, 2 * kept[1]),
+                               torch.device("cuda", index))
+                kept = _stream_ws[(index, handle)] = (ws.ptr, ws.nbytes, ws, kept)
     return kept[0], kept[1]
 
 

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "internal.h"
 
@@ -314,6 +315,10 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
       return MUON_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double row = 2.0 * L.T * L.dim;
+    // dk, dv reads what dq leaves in the workspace: no other thread's launches on this stream
+    // come between the two
+    static std::mutex pair_mu;
+    std::lock_guard<std::mutex> lk(pair_mu);
     cudaError_t e = counted_launch(
         st, MUON_K_ATTENTION_DQ, 6.0 * L.dim * pair_bound(L), row * (4.0 * L.hq + 2.0 * L.hk),
         [&] { return launch_attention_dq(M, L, sms, st); });

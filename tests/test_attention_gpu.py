@@ -14,6 +14,8 @@ Each result's Frobenius error is also held to 1e-2 (rounding error rms 2^-8 / sq
 each of at most three roundings on a result's way, with room for cancellation).
 """
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -484,3 +486,32 @@ def test_rows_whose_visible_scores_are_all_minus_infinity(sign, tokens, d):
         assert not np.isfinite(G[~clean]).all(axis=1).any(), name
     assert np.array_equal(np.isnan(f64(lse)), np.isnan(r_lse))
     assert np.array_equal(np.isneginf(f64(lse)), np.isneginf(r_lse))
+
+
+def test_two_threads_on_one_stream():
+    # the two launches of a gradient call hand over through the stream's default workspace
+    data = [_draw(70 + i, 257 + 640 * i, 4, 2, 64) for i in range(2)]
+    want = []
+    for q, k, v, do in data:
+        out, lse = muon.attention(q, k, v)
+        want.append((out, lse, muon.attention_backward(do, q, k, v, out, lse)))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, start = [[], []], threading.Barrier(2)
+
+    def work(i):
+        q, k, v, do = data[i]
+        start.wait()
+        for _ in range(200):
+            grads = muon.attention_backward(do, q, k, v, *want[i][:2], stream=stream)
+            got[i].append(grads)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 200
+        assert all(torch.equal(a, b) for grads in g for a, b in zip(grads, w[2]))

@@ -2,7 +2,11 @@
 before anything is enqueued, workspace sizes."""
 
 import ctypes
+import gc
 import os
+import threading
+import time
+import weakref
 
 import pytest
 import torch
@@ -171,3 +175,60 @@ def test_rope_tables_scale_the_positions():
     assert torch.equal(c2[::4], c1) and torch.equal(s2[::4], s1)
     assert torch.equal(c1[0], torch.ones(8)) and torch.equal(s1[0], torch.zeros(8))
     assert ctypes.sizeof(muon._Heads) == 24
+
+
+class _FakeWorkspace:
+    """A Workspace without a device: its address is its own, and only while it lives."""
+
+    def __init__(self, nbytes, device=None):
+        self.nbytes = max(256, nbytes)
+        self.buf = bytearray(8)
+        self.ptr = id(self.buf)
+
+
+@pytest.fixture
+def default_workspaces(monkeypatch):
+    monkeypatch.setattr(muon, "_stream_ws", {})
+    monkeypatch.setattr(muon, "Workspace", _FakeWorkspace)
+    return muon._stream_ws
+
+
+def test_an_outgrown_default_workspace_stays_alive(default_workspaces):
+    # another thread may have looked its pointer up and be about to launch with it
+    alive = []
+
+    class Watched(_FakeWorkspace):
+        def __init__(self, *args):
+            super().__init__(*args)
+            alive.append(weakref.ref(self))
+
+    muon.Workspace = Watched                    # (undone by the fixture)
+    for need in (300, 1000, 1001, 5000, 400):
+        ptr, nbytes = muon._stream_workspace(None, need, 0, 7)[:2]
+        assert nbytes >= need and ptr == alive[-1]().ptr
+    gc.collect()
+    assert len(alive) == 4 and all(ref() is not None for ref in alive)
+    assert sum(ref().nbytes for ref in alive) < 2 * alive[-1]().nbytes
+
+
+def test_threads_on_one_stream_share_one_default_workspace(default_workspaces):
+    made, got, start = [], [], threading.Barrier(8)
+
+    class Slow(_FakeWorkspace):
+        def __init__(self, *args):
+            super().__init__(*args)
+            time.sleep(0.02)                    # a thread that also looks now finds none yet
+            made.append(self)
+
+    muon.Workspace = Slow
+
+    def look_up():
+        start.wait()
+        got.append(muon._stream_workspace(None, 1000, 0, 7)[0])
+
+    threads = [threading.Thread(target=look_up) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and got == [made[0].ptr] * 8
