@@ -533,12 +533,18 @@ _stream_ws_lock = threading.Lock()
 
 
 def _stream_workspace(ws, need: int, index: int, handle: int):
-    """Pointer and size of the caller's workspace, or of one kept for each device and stream:
-    calls on different streams may overlap, and must not share one.  A workspace that is
+    """Pointer, size and owner of the caller's workspace, or of one kept for each device and
+    stream: calls on different streams may overlap, and must not share one.  A workspace that is
     outgrown stays allocated, for another thread may be about to launch with its pointer; sizes
-    double, so that all of them together are less than twice the last."""
+    double, so that all of them together are less than twice the last.
+    A call that is being captured gets a workspace of its graph alone, which may be replayed on
+    any stream and in any order; clearing its status block is a node of that graph."""
     if ws is not None:
-        return ws.ptr, ws.nbytes
+        return ws.ptr, ws.nbytes, ws
+    if torch.cuda.is_current_stream_capturing():
+        own = torch.empty(max(256, need), dtype=torch.uint8, device=torch.device("cuda", index))
+        own[:256].zero_()
+        return own.data_ptr(), own.numel(), own
     kept = _stream_ws.get((index, handle))
     if kept is None or kept[1] < need:
         with _stream_ws_lock:
@@ -547,7 +553,7 @@ def _stream_workspace(ws, need: int, index: int, handle: int):
                 ws = Workspace(need if kept is None else max(need, 2 * kept[1]),
                                torch.device("cuda", index))
                 kept = _stream_ws[(index, handle)] = (ws.ptr, ws.nbytes, ws, kept)
-    return kept[0], kept[1]
+    return kept[:3]
 
 
 def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
@@ -634,7 +640,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_we
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None else None
     handle = _current_handle(index)
-    ws, ws_bytes = _stream_workspace(workspace, norm_rope_workspace_bytes(spec.head_dim), index, handle)
+    ws, ws_bytes, _owner = _stream_workspace(
+        workspace, norm_rope_workspace_bytes(spec.head_dim), index, handle)
     _raise(L.muon_qk_norm_rope_backward(
         spec, vdqo, vdko, vq, vk, vdq, vdk, None if dqw is None else dqw.data_ptr(),
         None if dkw is None else dkw.data_ptr(), ws, ws_bytes, handle),
@@ -697,8 +704,8 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     else:
         p_lse = _ptr(lse, "lse", index, torch.float32, (hq, t))
     handle = _current_handle(index)
-    ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
-                                                                spec.head_dim), index, handle)
+    ws, ws_bytes, _owner = _stream_workspace(
+        workspace, attention_workspace_bytes(t, hq, spec.kv_heads, spec.head_dim), index, handle)
     _raise(L.muon_attention(spec, vq, vk, vv, vo, p_lse, ws, ws_bytes, handle),
            "muon_attention")
     return out, lse
@@ -724,8 +731,8 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
     dk, vdk = _out_heads(dk, "dk", k)
     dv, vdv = _out_heads(dv, "dv", k)
     handle = _current_handle(index)
-    ws, ws_bytes = _stream_workspace(workspace, attention_workspace_bytes(t, hq, spec.kv_heads,
-                                                                spec.head_dim), index, handle)
+    ws, ws_bytes, _owner = _stream_workspace(
+        workspace, attention_workspace_bytes(t, hq, spec.kv_heads, spec.head_dim), index, handle)
     _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws,
                                      ws_bytes, handle), "muon_attention_backward")
     return dq, dk, dv

@@ -515,3 +515,46 @@ def test_two_threads_on_one_stream():
     for g, w in zip(got, want):
         assert len(g) == 200
         assert all(torch.equal(a, b) for grads in g for a, b in zip(grads, w[2]))
+
+
+def test_cuda_graphs_with_the_default_workspace():
+    # Two graphs captured on one stream, replayed in the other order, while eager calls on that
+    # stream and on another one need larger workspaces.
+    def case(seed, t):
+        q, k, v, do = _draw(seed, t, 4, 2, 64)
+        cos, sin = muon.rope_tables(t, 64)
+        w = [torch.linspace(0.5, 1.5, 64, device="cuda") for _ in range(2)]
+
+        def step():
+            qn, kn = muon.qk_norm_rope(q, k, cos, sin, q_weight=w[0], k_weight=w[1])
+            out, lse = muon.attention(qn, kn, v)
+            dq, dk, dv = muon.attention_backward(do, qn, kn, v, out, lse)
+            grads = muon.qk_norm_rope_backward(dq, dk, q, k, cos, sin, q_weight=w[0],
+                                               k_weight=w[1])
+            return (out, lse, dv, *grads)
+
+        return step
+
+    stream = torch.cuda.Stream()
+    steps = [case(80, 200), case(81, 333)]
+    want = [step() for step in steps]
+    large = case(82, 1900)
+    large_want = large()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for step in steps:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs.append(step())
+        graphs.append(graph)
+    for order in ((1, 0), (0, 1), (1, 1, 0)):
+        for x in (y for out in outs for y in out):
+            x.fill_(3.0)
+        with torch.cuda.stream(stream):
+            eager = large()
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for got, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+        assert all(torch.equal(a, b) for a, b in zip(eager, large_want))

@@ -190,6 +190,7 @@ class _FakeWorkspace:
 def default_workspaces(monkeypatch):
     monkeypatch.setattr(muon, "_stream_ws", {})
     monkeypatch.setattr(muon, "Workspace", _FakeWorkspace)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return muon._stream_ws
 
 
@@ -232,3 +233,24 @@ def test_threads_on_one_stream_share_one_default_workspace(default_workspaces):
     for t in threads:
         t.join()
     assert len(made) == 1 and got == [made[0].ptr] * 8
+
+
+def test_a_captured_call_gets_a_workspace_of_its_own(default_workspaces, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    cpu = torch.empty
+    made = []
+
+    def empty(n, dtype, device):
+        made.append(cpu(n, dtype=dtype).fill_(255))       # as memory used before
+        return made[-1]
+
+    monkeypatch.setattr(torch, "empty", empty)
+    first, second = (muon._stream_workspace(None, 1000, 0, 7) for _ in range(2))
+    assert [x[0] for x in (first, second)] == [m.data_ptr() for m in made]
+    assert len(made) == 2 and not default_workspaces
+    for ptr, nbytes, owner in (first, second):
+        assert nbytes == 1000 and owner.data_ptr() == ptr
+        assert torch.count_nonzero(owner[:256]) == 0      # error word and tickets
+    # the caller's own is used as it is
+    ws = _FakeWorkspace(400)
+    assert muon._stream_workspace(ws, 1000, 0, 7) == (ws.ptr, 400, ws)
