@@ -688,7 +688,9 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     head_dim], k and v [tokens, kv_heads, head_dim] (strided along tokens and heads), cu_seqlens
     int32 [sequences + 1] on the device (None: one sequence).  scale is 1 / sqrt(head_dim) when
     None.  Returns (out, lse): out like q, lse [q_heads, tokens] fp32.  Tokens past the last
-    sequence get out 0 and lse -inf."""
+    sequence get out 0 and lse -inf.  After a device-side wait that gave up, calls on the same
+    workspace leave their outputs as they are (new ones undefined) until workspace_status(
+    workspace, clear=True); None there is the stream's default, as here."""
     L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
     index = q.get_device()
@@ -738,10 +740,22 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
     return dq, dk, dv
 
 
-def workspace_status(workspace: Workspace, clear: bool = False, stream=None) -> int:
-    """Synchronise and read the workspace's sticky device error word (0 = ok, 4 = timeout)."""
-    return int(load_library().muon_workspace_status(workspace.ptr, workspace.nbytes,
-                                                    _stream_handle(stream), int(clear)))
+def workspace_status(workspace: Workspace | None, clear: bool = False, stream=None) -> int:
+    """Synchronise and read the workspace's sticky device error word (0 = ok, 4 = timeout).
+    With None: that of the workspace which attention, its gradients and those of qk_norm_rope
+    keep for the current device and `stream` when the caller passes none.  (The one that a call
+    captured into a CUDA graph takes is cleared by each replay and cannot be read: pass a
+    Workspace to a captured call whose failure should be seen.)"""
+    handle = _stream_handle(stream)
+    if workspace is not None:
+        return int(load_library().muon_workspace_status(workspace.ptr, workspace.nbytes, handle,
+                                                        int(clear)))
+    status, kept = 0, _stream_ws.get((_current_device(), handle))
+    while kept is not None:                   # the one in use, and those that it outgrew
+        ptr, nbytes, _, kept = kept
+        status = max(status, int(load_library().muon_workspace_status(ptr, nbytes, handle,
+                                                                      int(clear))))
+    return status
 
 
 def noalloc_status(clear: bool = False, stream=None) -> int:

@@ -558,3 +558,25 @@ def test_cuda_graphs_with_the_default_workspace():
         for got, w in zip(outs, want):
             assert all(torch.equal(a, b) for a, b in zip(got, w))
         assert all(torch.equal(a, b) for a, b in zip(eager, large_want))
+
+
+def test_a_failed_default_workspace_is_seen_and_cleared():
+    q, k, v, do = _draw(90, 200, 2, 1, 64)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, lse = muon.attention(q, k, v, stream=stream)
+    assert muon.workspace_status(None, stream=stream) == 0
+    ws = muon._stream_ws[(torch.cuda.current_device(), stream.cuda_stream)][2]
+    muon.selftest_wait_timeout(ws, limit_us=1000, stream=stream)
+    o2 = torch.full_like(out, 3.0)
+    torch.cuda.synchronize()
+    muon.attention(q, k, v, out=o2, stream=stream)
+    assert muon.workspace_status(None, stream=stream) == 4
+    assert torch.all(o2 == 3.0)
+    assert muon.workspace_status(None, clear=True, stream=stream) == 4
+    assert muon.workspace_status(None, stream=stream) == 0
+    muon.attention(q, k, v, out=o2, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(o2, out)
+    # another stream has another one
+    assert muon.workspace_status(None) == 0

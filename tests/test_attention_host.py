@@ -254,3 +254,27 @@ def test_a_captured_call_gets_a_workspace_of_its_own(default_workspaces, monkeyp
     # the caller's own is used as it is
     ws = _FakeWorkspace(400)
     assert muon._stream_workspace(ws, 1000, 0, 7) == (ws.ptr, 400, ws)
+
+
+def test_status_of_the_default_workspace(default_workspaces, monkeypatch):
+    words = {}
+
+    class Library:
+        @staticmethod
+        def muon_workspace_status(ptr, nbytes, handle, clear):
+            assert nbytes >= 256 and handle == 7
+            word = words.get(ptr, OK)
+            if clear:
+                words[ptr] = OK
+            return word
+
+    monkeypatch.setattr(muon, "load_library", lambda: Library)
+    monkeypatch.setattr(muon, "_current_device", lambda: 0)
+    assert muon.workspace_status(None, stream=7) == OK        # no call needed one yet
+    first, second = (muon._stream_workspace(None, n, 0, 7)[0] for n in (300, 9000))
+    assert muon.workspace_status(None, stream=7) == OK
+    for ptr in (first, second):                               # also of a call before it grew
+        words[ptr] = TIMEOUT
+        assert muon.workspace_status(None, stream=7) == TIMEOUT
+        assert muon.workspace_status(None, clear=True, stream=7) == TIMEOUT
+        assert muon.workspace_status(None, stream=7) == OK
