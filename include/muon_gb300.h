@@ -249,8 +249,11 @@ muon_status muon_adam_step(const muon_adam_tensor* tensors, int n_tensors, int s
  * are in elements.  data and both strides are 16-byte aligned (a stride whose
  * dimension has one entry is ignored) and strides are positive: a broadcast view
  * (stride 0) is refused, its gradient would be a sum that no call here takes.
- * Rows of different (t, h) do not overlap in an output.  head_dim is a multiple
- * of 8.
+ * Rows of different (t, h) do not overlap in an output.  An output shares no
+ * bytes with an input or another output (refused as an invalid argument; views
+ * that interleave have to have one token stride), but for muon_qk_norm_rope and
+ * its gradients, whose output may be the very view of its own input or gradient.
+ * head_dim is a multiple of 8.
  */
 typedef struct muon_heads {
   void* data;

@@ -595,7 +595,8 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
     (bf16 or fp32, strided along tokens and heads), times q_weight / k_weight ([head_dim] fp32),
     then the rotation of its first 2 * cos.shape[1] elements by rows `positions` (int32; the
     token's index when None) of the tables cos, sin (see rope_tables).  Pairs are (i, i + half),
-    or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves."""
+    or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves, and
+    overlap nothing else."""
     L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
@@ -622,7 +623,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos, sin, *, q_weight=None, k_we
                           interleaved: bool = False, dq=None, dk=None,
                           workspace: Workspace | None = None, stream=None):
     """Gradients of qk_norm_rope: from those of its outputs, and its inputs, returns (dq, dk,
-    dq_weight, dk_weight); the weights' are fp32, and None where no weight is given."""
+    dq_weight, dk_weight); the weights' are fp32, and None where no weight is given.  dq may be
+    dq_out or q itself, dk likewise."""
     L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
@@ -717,7 +719,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
                        dq=None, dk=None, dv=None, workspace: Workspace | None = None,
                        stream=None):
     """Gradients of attention's out: from dout, the inputs, and its out and lse, returns (dq, dk,
-    dv) in bf16 (dk and dv summed over the query heads of a group)."""
+    dv) in bf16 (dk and dv summed over the query heads of a group).  They overlap no input."""
     L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
     index, dtype = q.get_device(), q.dtype

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "internal.h"
@@ -44,6 +45,54 @@ bool rows_apart(const muon_heads& v, int tokens, int heads, int dim) {
   const bool head_inner = v.head_stride <= v.token_stride;
   return head_inner ? v.token_stride >= v.head_stride * (heads - 1) + dim
                     : v.head_stride >= v.token_stride * (tokens - 1) + dim;
+}
+
+// Bytes that a call reads or writes: `len` at every (token, head).
+struct Rows {
+  uintptr_t at;
+  long long ts, hs, len;                    // bytes
+  int tokens, heads;
+};
+Rows rows_of(const muon_heads& v, int tokens, int heads, int dim, int size) {
+  return {reinterpret_cast<uintptr_t>(v.data), v.token_stride * size, v.head_stride * size,
+          1ll * dim * size, tokens, heads};
+}
+Rows rows_of(const float* p, long long n) {
+  return {reinterpret_cast<uintptr_t>(p), 0, 0, n * 4, 1, 1};
+}
+uintptr_t end_of(const Rows& r) { return r.at + r.ts * (r.tokens - 1) + r.hs * (r.heads - 1) + r.len; }
+long long floor_div(long long a, long long b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// Whether the two share a byte.  Views that interleave (the columns of one fused tensor) have
+// one token stride; of others that reach into each other's range, and of more heads than a
+// check should cost, the answer is yes.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.at >= end_of(b) || b.at >= end_of(a)) return false;
+  if (a.tokens > 1 && b.tokens > 1 && a.ts != b.ts) return true;
+  if (1ll * a.heads * b.heads > 1 << 16) return true;
+  const long long ts = std::max(1ll, a.tokens > 1 ? a.ts : b.ts);
+  for (int i = 0; i < a.heads; ++i)
+    for (int j = 0; j < b.heads; ++j) {
+      // tokens d apart are off + d ts apart; they meet if -a.len < off + d ts < b.len
+      const long long off =
+          static_cast<long long>(a.at - b.at) + i * a.hs - j * b.hs;
+      const long long lo = floor_div(-a.len - off, ts) + 1, hi = -floor_div(off - b.len, ts) - 1;
+      if (std::max(lo, 1ll - b.tokens) <= std::min(hi, a.tokens - 1ll)) return true;
+    }
+  return false;
+}
+bool same_rows(const Rows& a, const Rows& b) {
+  return a.at == b.at && (a.tokens == 1 || a.ts == b.ts) && (a.heads == 1 || a.hs == b.hs);
+}
+// No output shares a byte with an input or with another output.
+bool apart(std::initializer_list<Rows> outputs, std::initializer_list<Rows> inputs) {
+  for (const Rows* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Rows& x : inputs)
+      if (overlap(*o, x)) return false;
+    for (const Rows* p = outputs.begin(); p != o; ++p)
+      if (overlap(*o, *p)) return false;
+  }
+  return true;
 }
 
 template <typename T>
@@ -123,6 +172,30 @@ muon_status rope_launch(NormRopeLaunch& L, const muon_norm_rope* s, muon_heads (
   return MUON_OK;
 }
 
+// Outputs share no bytes with inputs or with each other, but a kind's output may be its own
+// input: the lanes of a row have loaded it before they store it.
+bool rope_apart(const NormRopeLaunch& L, const muon_heads (&x)[2], const muon_heads (&y)[2],
+                const muon_heads* dy) {
+  const int size = L.bf16 ? 2 : 4;
+  auto rows = [&](const muon_heads& v, int i) {
+    return rows_of(v, L.tokens, L.heads[i], L.dim, size);
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (L.heads[i] == 0) continue;
+    const Rows out = rows(y[i], i);
+    if (i == 1 && L.heads[0] > 0 && overlap(out, rows(y[0], 0))) return false;
+    for (int j = 0; j < 2; ++j) {
+      if (L.heads[j] == 0) continue;
+      auto clash = [&](const muon_heads& v) {
+        const Rows in = rows(v, j);
+        return !(i == j && same_rows(out, in)) && overlap(out, in);
+      };
+      if (((!dy || L.norm) && clash(x[j])) || (dy && clash(dy[j]))) return false;
+    }
+  }
+  return true;
+}
+
 double rope_bytes(const NormRopeLaunch& L, int passes) {
   return 1.0 * L.tokens * (L.heads[0] + L.heads[1]) * L.dim * (L.bf16 ? 2 : 4) * passes;
 }
@@ -181,6 +254,7 @@ muon_status muon_qk_norm_rope(const muon_norm_rope* spec, muon_heads q, muon_hea
     int sms = 0;
     const muon_status ds = device_sms(&sms);
     if (ds != MUON_OK) return ds;
+    if (!rope_apart(L, x, y, nullptr)) return MUON_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = counted_launch(st, MUON_K_NORM_ROPE, 0.0, rope_bytes(L, 2),
                                          [&] { return launch_norm_rope(L, false, sms, st); });
@@ -221,6 +295,7 @@ muon_status muon_qk_norm_rope_backward(const muon_norm_rope* spec, muon_heads dq
           return MUON_ERR_CUDA;
       return MUON_OK;
     }
+    if (!rope_apart(L, x, y, dy)) return MUON_ERR_INVALID_ARG;
     L.dw[0] = dq_weight;
     L.dw[1] = dk_weight;
     L.status = static_cast<const unsigned int*>(workspace);
@@ -251,6 +326,10 @@ muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_h
     if (!view_ok(&q, L.T, L.hq, L.dim, 2) || !view_ok(&k, L.T, L.hk, L.dim, 2) ||
         !view_ok(&v, L.T, L.hk, L.dim, 2) || !view_ok(&out, L.T, L.hq, L.dim, 2) ||
         !rows_apart(out, L.T, L.hq, L.dim) || !lse || !aligned16(lse))
+      return MUON_ERR_INVALID_ARG;
+    auto of_q = [&](const muon_heads& x) { return rows_of(x, L.T, L.hq, L.dim, 2); };
+    auto of_k = [&](const muon_heads& x) { return rows_of(x, L.T, L.hk, L.dim, 2); };
+    if (!apart({of_q(out), rows_of(lse, 1ll * L.hq * L.T)}, {of_q(q), of_k(k), of_k(v)}))
       return MUON_ERR_INVALID_ARG;
     int sms = 0;
     s = device_sms(&sms);
@@ -285,14 +364,20 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
     muon_status s = attention_launch(L, spec, workspace, workspace_bytes);
     if (s != MUON_OK) return s;
     if (L.T == 0) return MUON_OK;
-    muon_heads* of_q[] = {&dout, &q, &out, &dq};
-    muon_heads* of_k[] = {&k, &v, &dk, &dv};
-    for (muon_heads* x : of_q)
+    muon_heads* q_views[] = {&dout, &q, &out, &dq};
+    muon_heads* k_views[] = {&k, &v, &dk, &dv};
+    for (muon_heads* x : q_views)
       if (!view_ok(x, L.T, L.hq, L.dim, 2)) return MUON_ERR_INVALID_ARG;
-    for (muon_heads* x : of_k)
+    for (muon_heads* x : k_views)
       if (!view_ok(x, L.T, L.hk, L.dim, 2)) return MUON_ERR_INVALID_ARG;
     if (!rows_apart(dq, L.T, L.hq, L.dim) || !rows_apart(dk, L.T, L.hk, L.dim) ||
         !rows_apart(dv, L.T, L.hk, L.dim) || !lse || !aligned16(lse))
+      return MUON_ERR_INVALID_ARG;
+    // (the second launch reads q, k, v and dout again, after the first has written dq)
+    auto of_q = [&](const muon_heads& x) { return rows_of(x, L.T, L.hq, L.dim, 2); };
+    auto of_k = [&](const muon_heads& x) { return rows_of(x, L.T, L.hk, L.dim, 2); };
+    if (!apart({of_q(dq), of_k(dk), of_k(dv)},
+               {of_q(dout), of_q(q), of_k(k), of_k(v), of_q(out), rows_of(lse, 1ll * L.hq * L.T)}))
       return MUON_ERR_INVALID_ARG;
     int sms = 0;
     s = device_sms(&sms);

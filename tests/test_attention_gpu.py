@@ -580,3 +580,30 @@ def test_a_failed_default_workspace_is_seen_and_cleared():
     assert torch.equal(o2, out)
     # another stream has another one
     assert muon.workspace_status(None) == 0
+
+
+def test_outputs_over_inputs_are_refused():
+    q, k, v, do = _draw(91, 50, 4, 4, 64)
+    out, lse = muon.attention(q, k, v)
+    before = [x.clone() for x in (q, k, v, do, out, lse)]
+    for x in (q, k, v):
+        with pytest.raises(muon.MuonError):
+            muon.attention(q, k, v, out=x)
+    spare = torch.empty(50, 12, 64, dtype=q.dtype, device="cuda")
+    for name in ("dq", "dk", "dv"):
+        for x in (q, k, v, do, out):
+            with pytest.raises(muon.MuonError):
+                muon.attention_backward(do, q, k, v, out, lse, **{name: x})
+    with pytest.raises(muon.MuonError):
+        muon.attention_backward(do, q, k, v, out, lse, dk=spare[:, :4], dv=spare[:, 3:7])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v, do, out, lse), before))
+    # columns of one tensor that holds the inputs too
+    wide = torch.empty(50, 24, 64, dtype=q.dtype, device="cuda")
+    wide[:, :4], wide[:, 4:8], wide[:, 8:12], wide[:, 12:16] = q, k, v, do
+    part = [wide[:, i:i + 4] for i in range(0, 24, 4)]
+    o2, z2 = muon.attention(*part[:3], out=part[4])
+    assert torch.equal(o2, out) and torch.equal(z2, lse)
+    got = muon.attention_backward(part[3], *part[:3], o2, z2, dk=part[5])
+    for a, b in zip(got, muon.attention_backward(do, q, k, v, out, lse)):
+        assert torch.equal(a, b)

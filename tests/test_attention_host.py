@@ -4,6 +4,7 @@ before anything is enqueued, workspace sizes."""
 import ctypes
 import gc
 import os
+import random
 import threading
 import time
 import weakref
@@ -278,3 +279,79 @@ def test_status_of_the_default_workspace(default_workspaces, monkeypatch):
         assert muon.workspace_status(None, stream=7) == TIMEOUT
         assert muon.workspace_status(None, clear=True, stream=7) == TIMEOUT
         assert muon.workspace_status(None, stream=7) == OK
+
+
+def _spread(n, ts=512):
+    """n views that share nothing (16 tokens of 8 heads of 64)."""
+    return [_view(0x100000 * (i + 1), ts) for i in range(n)]
+
+
+@pytest.mark.parametrize("entry,outputs,inputs", [("fwd", [3], [0, 1, 2]),
+                                                  ("bwd", [5, 6, 7], [0, 1, 2, 3, 4])])
+def test_attention_refuses_outputs_over_inputs_and_each_other(lib, entry, outputs, inputs):
+    call, n = (_attn, 4) if entry == "fwd" else (_attn_back, 8)
+    lse = 0x8000000
+    row = 2 * 64                                # bytes of a head
+    for o in outputs:
+        for other in inputs + [x for x in outputs if x != o]:
+            at = 0x100000 * (other + 1)
+            # the same view, one a token on, its last row, one that ends in its first row
+            for shift in (0, 1024, 15 * 1024, -15 * 1024 - 3 * row):
+                views = _spread(n)
+                views[o] = _view(at + shift)
+                assert call(lib, _attn_spec(), views, lse=lse) == INVALID, (o, other, shift)
+    # log-sum-exps (8 heads of 16) inside a view
+    for at in (inputs + outputs if entry == "fwd" else outputs):
+        assert call(lib, _attn_spec(), _spread(n), lse=0x100000 * (at + 1) + 1024) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the views are no memory of a GPU")
+def test_attention_takes_views_that_only_interleave(lib):
+    # the columns of one tensor of 8 + 4 + 4 + 8 heads: q, k, v, out
+    ts, head = 24 * 64, 128
+    views = [_view(0x100000 + head * first, ts) for first in (0, 8, 12, 16)]
+    assert _attn(lib, _attn_spec(), views, lse=0x8000000) in (UNSUPPORTED, CUDA)
+    views[3] = _view(0x100000 + head * 15, ts)
+    assert _attn(lib, _attn_spec(), views, lse=0x8000000) == INVALID
+    # every third head each, as [tokens, heads, (q, k, out), dim]
+    spec = _attn_spec(kv_heads=8)
+    views = [_view(0x100000 + head * i, ts, 192) for i in (0, 1, 1, 2)]
+    assert _attn(lib, spec, views, lse=0x8000000) in (UNSUPPORTED, CUDA)
+    views[3] = _view(0x100000 + head, ts, 192)
+    assert _attn(lib, spec, views, lse=0x8000000) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the views are no memory of a GPU")
+def test_overlap_is_found_as_by_listing_the_bytes(lib):
+    rng = random.Random(0)
+    seen = set()
+    for _ in range(4000):
+        t, hq, hk = rng.choice([1, 2, 5]), rng.choice([1, 2, 4]), rng.choice([1, 2])
+        hk = min(hk, hq)
+        d = 8
+        ts = 8 * rng.randint(1, 24)
+
+        def rand(heads):
+            hs = 8 * rng.randint(1, 6)
+            return muon._Heads(0x100000 + 16 * rng.randint(0, 60), ts, hs), heads
+
+        def rows(v, heads):
+            hs = v.head_stride if heads > 1 else d
+            tok = v.token_stride if t > 1 else heads * d
+            return [v.data + 2 * (i * tok + h * hs) for i in range(t) for h in range(heads)]
+
+        (q, _), (out, _) = rand(hq), rand(hq)
+        far = _view(0x10000000, 512)
+        a = sorted(rows(out, hq))
+        if any(y - x < 2 * d for x, y in zip(a, a[1:])):
+            continue                            # rows of the output overlap
+        hs, tok = out.head_stride if hq > 1 else d, out.token_stride if t > 1 else hq * d
+        inner, outer, n = (hs, tok, hq) if hs <= tok else (tok, hs, t)
+        if t > 1 and hq > 1 and outer < inner * (n - 1) + d:
+            continue                            # (its rows do, by the rule of one span a row)
+        want = any(abs(x - y) < 2 * d for x in rows(q, hq) for y in a)
+        spec = _attn_spec(tokens=t, q_heads=hq, kv_heads=hk, head_dim=d)
+        got = _attn(lib, spec, [q, far, far, out], lse=0x20000000)
+        assert (got == INVALID) == want, (t, hq, ts, q.data, q.head_stride, out.data, hs)
+        seen.add((t, hq, want))
+    assert len(seen) >= 15

@@ -244,3 +244,32 @@ def test_position_outside_the_tables_with_lanes_past_the_head(hq, hk, d, rot, in
     good += muon.qk_norm_rope_backward(dy[0], dy[1], q, k, cos, sin, positions=pos, **kw)[:2]
     for x, want in zip((*y, *dx[:2]), good):
         assert torch.isnan(x[bad]).all() and torch.equal(x[~bad], want[~bad])
+
+
+def test_outputs_over_other_inputs_are_refused():
+    q, k, cos, sin, w, dy, pos = _draw(20, 50, 4, 4, 64, 64, torch.bfloat16)
+    kw = dict(q_weight=w[0], k_weight=w[1], positions=pos)
+    want = muon.qk_norm_rope(q, k, cos, sin, **kw)
+    dwant = muon.qk_norm_rope_backward(dy[0], dy[1], q, k, cos, sin, **kw)
+    before = [x.clone() for x in (q, k, *dy)]
+    spare = torch.empty(51, 8, 64, dtype=q.dtype, device="cuda")
+    for bad in (dict(q_out=k), dict(k_out=q), dict(q_out=spare[:50, :4], k_out=spare[1:, 3:7])):
+        with pytest.raises(muon.MuonError):
+            muon.qk_norm_rope(q, k, cos, sin, **bad, **kw)
+    for bad in (dict(dq=k), dict(dk=q), dict(dq=dy[1]), dict(dk=dy[0]),
+                dict(dq=spare[:50, :4], dk=spare[1:, 3:7])):
+        with pytest.raises(muon.MuonError):
+            muon.qk_norm_rope_backward(dy[0], dy[1], q, k, cos, sin, **bad, **kw)
+    with pytest.raises(muon.MuonError):                    # rows of its own input, a token on
+        muon.qk_norm_rope(spare[:50, :4], k, cos, sin, q_out=spare[1:, :4], **kw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((q, k, *dy), before))
+    # over the gradients of the outputs, and over the inputs
+    g = [x.clone() for x in dy]
+    got = muon.qk_norm_rope_backward(*g, q, k, cos, sin, dq=g[0], dk=g[1], **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, dwant))
+    x = [q.clone(), k.clone()]
+    got = muon.qk_norm_rope_backward(*dy, *x, cos, sin, dq=x[0], dk=x[1], **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, dwant))
+    got = muon.qk_norm_rope(q, k, cos, sin, q_out=q, k_out=k, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
