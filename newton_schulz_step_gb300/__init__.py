@@ -556,6 +556,16 @@ def _stream_workspace(ws, need: int, index: int, handle: int):
     return kept[:3]
 
 
+def _refuse_grad(where: str, **tensors):
+    """Forward calls record nothing for autograd: a tensor that asks for a gradient would not
+    get one."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad:
+            raise ValueError(f"{name} requires grad, and {where} records no gradient: call it under "
+                             f"torch.no_grad() or on detached tensors, and {where}_backward for "
+                             "the gradients")
+
+
 def _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
     """The spec of a call and its views of q and k."""
     _cuda_device(q, "q")
@@ -596,10 +606,13 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
     then the rotation of its first 2 * cos.shape[1] elements by rows `positions` (int32; the
     token's index when None) of the tables cos, sin (see rope_tables).  Pairs are (i, i + half),
     or (2i, 2i + 1) when interleaved.  Returns (q_out, k_out); they may be q and k themselves, and
-    overlap nothing else."""
+    overlap nothing else.  Nothing is recorded for autograd: tensors that require grad are refused
+    while it records, see qk_norm_rope_backward."""
     L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
+    if torch.is_grad_enabled():
+        _refuse_grad("qk_norm_rope", q=q, k=k, q_weight=q_weight, k_weight=k_weight)
     index = q.get_device()
     if stream is not None or index != _current_device():
         with _launch_on(q.device, stream):
@@ -692,9 +705,12 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     None.  Returns (out, lse): out like q, lse [q_heads, tokens] fp32.  Tokens past the last
     sequence get out 0 and lse -inf.  After a device-side wait that gave up, calls on the same
     workspace leave their outputs as they are (new ones undefined) until workspace_status(
-    workspace, clear=True); None there is the stream's default, as here."""
+    workspace, clear=True); None there is the stream's default, as here.  Nothing is recorded for
+    autograd: tensors that require grad are refused while it records, see attention_backward."""
     L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
+    if torch.is_grad_enabled():
+        _refuse_grad("attention", q=q, k=k, v=v)
     index = q.get_device()
     if stream is not None or index != _current_device():
         with _launch_on(q.device, stream):

@@ -607,3 +607,41 @@ def test_outputs_over_inputs_are_refused():
     got = muon.attention_backward(part[3], *part[:3], o2, z2, dk=part[5])
     for a, b in zip(got, muon.attention_backward(do, q, k, v, out, lse)):
         assert torch.equal(a, b)
+
+
+def test_tensors_that_require_grad_are_refused_while_autograd_records():
+    q, k, v, do = _draw(92, 40, 4, 2, 64, fused=False)
+    cos, sin = muon.rope_tables(40, 64)
+    w = torch.ones(64, device="cuda")
+    out, lse = muon.attention(q, k, v)
+    rotated = muon.qk_norm_rope(q, k, cos, sin, q_weight=w, k_weight=w)
+    for x in (q, k, v):
+        x.requires_grad_(True)
+        with pytest.raises(ValueError, match="attention_backward"):
+            muon.attention(q, k, v)
+        with torch.no_grad():
+            assert torch.equal(muon.attention(q, k, v)[0], out)
+        muon.attention_backward(do, q, k, v, out, lse)      # no gradient is lost here
+        x.requires_grad_(False)
+    for x in (q, k, w):
+        x.requires_grad_(True)
+        with pytest.raises(ValueError, match="qk_norm_rope_backward"):
+            muon.qk_norm_rope(q, k, cos, sin, q_weight=w, k_weight=w)
+        x.requires_grad_(False)
+
+    class Attention(torch.autograd.Function):               # the way into a module
+        @staticmethod
+        def forward(ctx, q, k, v):
+            o, z = muon.attention(q, k, v)
+            ctx.save_for_backward(q, k, v, o, z)
+            return o
+
+        @staticmethod
+        def backward(ctx, g):
+            q, k, v, o, z = ctx.saved_tensors
+            return muon.attention_backward(g, q, k, v, o, z)
+
+    leaves = [x.detach().clone().requires_grad_(True) for x in (q, k, v)]
+    Attention.apply(*leaves).backward(do)
+    for x, g in zip(leaves, muon.attention_backward(do, q, k, v, out, lse)):
+        assert torch.equal(x.grad, g)
