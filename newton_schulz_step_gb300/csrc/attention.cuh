@@ -233,8 +233,9 @@ __device__ __forceinline__ uint32_t tile_off(int row, int c) {
   return static_cast<uint32_t>(c >> 3) * kSlab + static_cast<uint32_t>(row) * 128u +
          ((static_cast<uint32_t>(c & 7) ^ static_cast<uint32_t>(row & 7)) << 4);
 }
-// Zeroes row `row` of a tile: padding may hold anything, and zero weights do not stop
-// Inf or NaN in a product.  (fence_proxy_async_smem before the product reads it.)
+// Zeroes row `row` of a tile.  Tokens that no row of a block's tile sees (padding, and the
+// sequences before or behind) may hold anything, and zero weights do not stop Inf or NaN in
+// a product.  (fence_proxy_async_smem before the product reads it.)
 template <int DP>
 __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 #pragma unroll
@@ -267,77 +268,151 @@ __device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi, uint32_t
 }
 
 // ---- rows by definition -------------------------------------------------
-// A matrix product over a tile multiplies invisible pairs by a weight of zero, and
-// zero times Inf or NaN is NaN.  A result row that is not finite is therefore
-// computed again from its visible pairs alone, by one warp: rows that depend on a
-// non-finite value stay non-finite, the others lose what leaked into them.  Nothing
-// of this runs on finite data.
+// A matrix product over a tile multiplies invisible pairs by a weight of zero, and zero
+// times Inf or NaN is NaN.  Operand rows that no row of the tile sees are cleared; what is
+// left to leak are tokens of the tile itself.  dk and dv know the queries that hold such
+// values by their log-sum-exp and delta, and clear these too.  out and dq do not know the
+// keys: a result row that is not finite is looked into by one warp.  It stays as it is where
+// its own sequence says so (a visible weight is not finite, and with it the whole row, or a
+// visible operand in the same column); otherwise it is computed again from its visible pairs
+// alone.  Nothing of this runs on finite data.
+// The looking keeps a diverged run from stalling: one row by definition takes 150 cycles a
+// key, and a NaN in a document's first key reaches all its rows.  (2048 tokens, 8/4 heads of
+// 64, every such row walked: 29 ms forward instead of 0.05.  What is walked now are a tile's
+// rows before a bad token: 4 ms.)
 // A lane holds the elements 2 lane, 2 lane + 1 of each 64-element half of a head.
 struct Row { float v[4]; };
+struct Packed { unsigned int w[2]; };    // the same in bf16
 
-__device__ __forceinline__ Row load_row(const __nv_bfloat16* p, int dim) {
+__device__ __forceinline__ Packed load_packed(const __nv_bfloat16* p, int dim) {
   const int lane = threadIdx.x & 31;
-  Row r;
+  Packed r;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int d = 64 * h + 2 * lane;
-    unsigned int x = 0;
-    if (d < dim) x = *reinterpret_cast<const unsigned int*>(p + d);
-    r.v[2 * h] = __uint_as_float(x << 16);
-    r.v[2 * h + 1] = __uint_as_float(x & 0xffff0000u);
+    r.w[h] = d < dim ? *reinterpret_cast<const unsigned int*>(p + d) : 0u;
   }
   return r;
 }
+__device__ __forceinline__ Row unpack(const Packed& x) {
+  Row r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    r.v[2 * h] = __uint_as_float(x.w[h] << 16);
+    r.v[2 * h + 1] = __uint_as_float(x.w[h] & 0xffff0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ Row load_row(const __nv_bfloat16* p, int dim) {
+  return unpack(load_packed(p, dim));
+}
 
-__device__ __forceinline__ float dot_row(const Row& a, const Row& b) {
+// Sums over the warp.
+template <int kN> __device__ __forceinline__ void warp_sums(float (&s)[kN]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+}
+__device__ __forceinline__ float dot_part(const Row& a, const Row& b) {
   float s = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) s = fmaf(a.v[j], b.v[j], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
-
 // acc += f x
 __device__ __forceinline__ void axpy(Row& acc, float f, const Row& x) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc.v[j] = fmaf(f, x.v[j], acc.v[j]);
 }
 
-// Every element of the row is NaN: further terms cannot change it.
-__device__ __forceinline__ bool all_nan(const Row& r, int dim) {
-  const int lane = threadIdx.x & 31;
-  bool n = true;
+// Elements of this lane that are not finite, a bit each.
+__device__ __forceinline__ unsigned int not_finite(const Packed& x) {
+  unsigned int bad = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) n &= 64 * (j >> 1) + 2 * lane >= dim || isnan(r.v[j]);
-  return __all_sync(0xffffffffu, n);
+  for (int h = 0; h < 2; ++h) {
+    if ((x.w[h] & 0x7f80u) == 0x7f80u) bad |= 1u << 2 * h;
+    if ((x.w[h] & 0x7f800000u) == 0x7f800000u) bad |= 2u << 2 * h;
+  }
+  return bad;
+}
+// Columns in which one of the rows a..b-1 of a head is not finite.
+static __device__ __noinline__ unsigned int bad_columns(const Heads<const __nv_bfloat16>& x, int head,
+                                                        int a, int b, int dim) {
+  constexpr int kN = 16;                 // rows in flight
+  unsigned int bad = 0;
+  for (int t = a; t < b; t += kN) {
+    Packed w[kN];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) w[n] = load_packed(x.row(min(t + n, b - 1), head), dim);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) bad |= not_finite(w[n]);
+  }
+  return bad;
 }
 
-// The row as bf16 into row `row` of a shared-memory tile.
-__device__ __forceinline__ void put_row(uint8_t* tile, int row, const Row& r, int slabs) {
+// A row as bf16 in row `row` of a shared-memory tile.
+__device__ __forceinline__ uint32_t* row_slot(uint8_t* tile, int row, int half) {
   const int lane = threadIdx.x & 31;
+  return reinterpret_cast<uint32_t*>(tile + tile_off(row, 8 * half + (lane >> 2)) +
+                                     4 * (lane & 3));
+}
+__device__ __forceinline__ void put_row(uint8_t* tile, int row, const Row& r, int slabs) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    if (h < slabs)
-      *reinterpret_cast<uint32_t*>(tile + tile_off(row, 8 * h + (lane >> 2)) + 4 * (lane & 3)) =
-          pack2(r.v[2 * h], r.v[2 * h + 1]);
+    if (h < slabs) *row_slot(tile, row, h) = pack2(r.v[2 * h], r.v[2 * h + 1]);
+}
+__device__ __forceinline__ unsigned int bad_elements(uint8_t* tile, int row, int slabs) {
+  Packed x = {{0u, 0u}};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (h < slabs) x.w[h] = *row_slot(tile, row, h);
+  return not_finite(x);
 }
 
 // Output row i of query head h over the keys begin..i.
 static __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int i, int begin) {
+  constexpr int kN = 8;                  // keys at a time; the next are on their way
   const int kh = h / L.group;
   const Row q = load_row(L.q.row(i, h), L.dim);
   Row acc = {{0.f, 0.f, 0.f, 0.f}};
   float m = -INFINITY, l = 0.f;
-  for (int j = i; j >= begin && !all_nan(acc, L.dim); --j) {
-    const float s = L.scale * dot_row(q, load_row(L.k.row(j, kh), L.dim));
-    const float mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = __expf(m - base), p = __expf(s - base);
-    l = l * f + p;
+  Packed k[kN], v[kN], k1[kN], v1[kN];
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      k1[n] = load_packed(L.k.row(min(j + n, i), kh), L.dim);
+      v1[n] = load_packed(L.v.row(min(j + n, i), kh), L.dim);
+    }
+  };
+  fetch(begin);
+#pragma unroll 1
+  for (int j = begin; j <= i; j += kN) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      k[n] = k1[n];
+      v[n] = v1[n];
+    }
+    fetch(j + kN);
+    float s[kN], mn = m;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] = dot_part(q, unpack(k[n]));
+    warp_sums(s);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      s[n] = j + n <= i ? L.scale * s[n] : -INFINITY;
+      mn = fmaxf(mn, s[n]);
+    }
+    const float base = mn == -INFINITY ? 0.f : mn, f = __expf(m - base);
+    l *= f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc.v[e] *= f;
-    axpy(acc, p, load_row(L.v.row(j, kh), L.dim));
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const float p = __expf(s[n] - base);
+      l += p;
+      axpy(acc, p, unpack(v[n]));
+    }
     m = mn;
   }
   const float inv = 1.f / l;               // (l = 0, all scores -inf: NaN)
@@ -346,42 +421,116 @@ static __device__ __noinline__ Row out_row(const AttentionLaunch& L, int h, int 
   return acc;
 }
 
+// Looks into output rows (bits of `bad`, from row r0 of the tile that starts at token row0)
+// that are not finite although their weights are.  row_begin: of the lane's row.
+static __device__ __noinline__ void mend_out(const AttentionLaunch& L, uint8_t* stage, int slabs,
+                                             int h, int row0, int r0, int row_begin,
+                                             unsigned int bad) {
+  const int kh = h / L.group;
+  unsigned int before = 0;                 // (rows that begin before the tile begin together)
+  bool looked = false;
+  while (bad) {
+    const int src = __ffs(bad) - 1, r = r0 + src, i = row0 + r;
+    bad &= bad - 1;
+    const int begin = __shfl_sync(0xffffffffu, row_begin, src);
+    unsigned int seen = bad_columns(L.v, kh, max(begin, row0), i + 1, L.dim);
+    if (begin < row0) {
+      if (!looked) before = bad_columns(L.v, kh, begin, row0, L.dim);
+      looked = true;
+      seen |= before;
+    }
+    if (__any_sync(0xffffffffu, bad_elements(stage, r, slabs) & ~seen))
+      put_row(stage, r, out_row(L, h, i, begin), slabs);
+  }
+}
+
 // Query gradient row i of head h.
 static __device__ __noinline__ Row dq_row(const AttentionLaunch& L, int h, int i, int begin) {
+  constexpr int kN = 4;
   const int kh = h / L.group;
   const Row q = load_row(L.q.row(i, h), L.dim);
   const Row g = load_row(L.dout.row(i, h), L.dim);
-  const float delta = dot_row(g, load_row(L.o.row(i, h), L.dim));
+  float delta[1] = {dot_part(g, load_row(L.o.row(i, h), L.dim))};
+  warp_sums(delta);
   const float lse = L.lse[static_cast<size_t>(h) * L.T + i];
   Row acc = {{0.f, 0.f, 0.f, 0.f}};
-  for (int j = i; j >= begin && !all_nan(acc, L.dim); --j) {
-    const Row k = load_row(L.k.row(j, kh), L.dim);
-    const float p = __expf(L.scale * dot_row(q, k) - lse);
-    axpy(acc, p * (dot_row(g, load_row(L.v.row(j, kh), L.dim)) - delta), k);
+  Packed k[kN], v[kN], k1[kN], v1[kN];
+  const __nv_bfloat16 *pk = L.k.row(begin, kh), *pv = L.v.row(begin, kh);
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int dim = j + n <= i ? L.dim : 0;              // (past the last key: zeros)
+      k1[n] = load_packed(pk, dim);
+      v1[n] = load_packed(pv, dim);
+      pk += L.k.ts;
+      pv += L.v.ts;
+    }
+  };
+  fetch(begin);
+#pragma unroll 1
+  for (int j = begin; j <= i; j += kN) {
+    float s[2 * kN];                       // scores, dp
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      k[n] = k1[n];
+      v[n] = v1[n];
+    }
+    fetch(j + kN);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      s[n] = dot_part(q, unpack(k[n]));
+      s[kN + n] = dot_part(g, unpack(v[n]));
+    }
+    warp_sums(s);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const float ds = __expf(L.scale * s[n] - lse) * (s[kN + n] - delta[0]);
+      if (j + n <= i) axpy(acc, ds, unpack(k[n]));
+    }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) acc.v[e] *= L.scale;
   return acc;
 }
 
-// Key and value gradient rows j of key head kh, over the queries j..end-1 of its group.
-static __device__ __noinline__ void dkv_row(const AttentionLaunch& L, int kh, int j, int end, Row& dk,
-                                     Row& dv) {
-  const Row k = load_row(L.k.row(j, kh), L.dim);
-  const Row v = load_row(L.v.row(j, kh), L.dim);
-  dk = dv = {{0.f, 0.f, 0.f, 0.f}};
-  for (int h = kh * L.group; h < (kh + 1) * L.group; ++h)
-    for (int i = j; i < end && !(all_nan(dk, L.dim) && all_nan(dv, L.dim)); ++i) {
-      const Row q = load_row(L.q.row(i, h), L.dim);
-      const Row g = load_row(L.dout.row(i, h), L.dim);
-      const float delta = dot_row(g, load_row(L.o.row(i, h), L.dim));
-      const float lse = L.lse[static_cast<size_t>(h) * L.T + i];
-      const float p = __expf(L.scale * dot_row(q, k) - lse);
-      axpy(dv, p, g);
-      axpy(dk, p * (dot_row(g, v) - delta), q);
+// The same look for rows of dq, whose ds are finite: one of them stays as it is only where a
+// visible key is not finite (and its weight 0).
+static __device__ __noinline__ void mend_dq(const AttentionLaunch& L, uint8_t* stage, int slabs, int h,
+                                            int row0, int r0, int row_begin, unsigned int bad) {
+  const int kh = h / L.group;
+  unsigned int before = 0;
+  bool looked = false;
+  while (bad) {
+    const int src = __ffs(bad) - 1, r = r0 + src, i = row0 + r;
+    bad &= bad - 1;
+    const int begin = __shfl_sync(0xffffffffu, row_begin, src);
+    unsigned int seen = bad_columns(L.k, kh, max(begin, row0), i + 1, L.dim);
+    if (begin < row0) {
+      if (!looked) before = bad_columns(L.k, kh, begin, row0, L.dim);
+      looked = true;
+      seen |= before;
     }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) dk.v[e] *= L.scale;
+    if (__any_sync(0xffffffffu, bad_elements(stage, r, slabs) & ~seen))
+      put_row(stage, r, dq_row(L, h, i, begin), slabs);
+  }
+}
+
+// Columns of dv that a visible query's dout makes not finite, for key j of key head kh: the queries
+// up to the end of the key's tile, and those behind it (the keys that see these end together).
+struct Behind {
+  bool looked = false;
+  unsigned int columns = 0;
+};
+static __device__ __noinline__ unsigned int lost_columns(const AttentionLaunch& L, int kh, int key0,
+                                                         int j, int end, Behind& behind) {
+  const int edge = key0 + kBlock, h0 = kh * L.group, h1 = h0 + L.group;
+  unsigned int lost = 0;
+  for (int h = h0; h < h1; ++h) lost |= bad_columns(L.dout, h, j, min(end, edge), L.dim);
+  if (end <= edge) return lost;
+  if (!behind.looked)
+    for (int h = h0; h < h1; ++h) behind.columns |= bad_columns(L.dout, h, edge, end, L.dim);
+  behind.looked = true;
+  return lost | behind.columns;
 }
 
 }  // namespace attn

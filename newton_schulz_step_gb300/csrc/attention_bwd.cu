@@ -354,8 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[2 * i] = __float_as_uint(y.x);
         x[2 * i + 1] = __float_as_uint(y.y);
       }
-      if (k0 < last_begin || j + 1 == n)
+      bool clear = false;
+      if (k0 < last_begin || j + 1 == n) {
+        clear = k0 < X.first || used < min(k0 + kBlock, L.T);
         hide(x, row_begin - k0 - 32 * group, row - k0 - 32 * group, 0u);
+      }
       if constexpr (decltype(own)::value) {
         // rows that see keys of this block only: their delta is the one of sum ds = 0
         float part = 0.f;
@@ -396,9 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tmem_st16(lanes + 128 + 32 * group, w);
       ptx::tmem_st8(lanes + 128 + 32 * group + 16, remainder);
-      if (used < min(k0 + kBlock, L.T)) {              // the block holds padding: clear its K
-        const int s = j % C::kK;                       // (landed: S has read it)
-        if (group == 0 && k0 + r >= used) zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
+      if (clear) {                       // the block holds padding, or keys before those that
+        const int s = j % C::kK;         // the tile sees: clear them (S has read the tile)
+        if (group == 0 && (k0 + r < X.first || k0 + r >= used))
+          zero_row<DP>(sm + C::kKRing + s * C::kTile, r);
         ptx::fence_proxy_async_smem();
       }
       ptx::tmem_st_wait();
@@ -437,14 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       if (group == 1)
         stats[128] = delta + ((X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]));
-      // any part of a row may be bad: the four warps of the rows share the joint set
-      unsigned int bad = X.repair[quarter] & (0x11111111u << group);
-      while (bad) {
-        const int src = __ffs(bad) - 1;
-        bad &= bad - 1;
-        put_row(sm, r - lane + src,
-                dq_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
-                DP / 64);
+      // Any part of a row may be bad: the four warps of the rows share the joint set.  (A row
+      // whose visible ds, summed up here, are not finite is so throughout.)
+      unsigned int bad = X.repair[quarter];
+      if (bad) {
+        const float sum = (X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]);
+        bad &= __ballot_sync(0xffffffffu, isfinite(sum)) & (0x11111111u << group);
+        mend_dq(L, sm, DP / 64, h, row0, r - lane, row_begin, bad);
       }
       ptx::fence_proxy_async_smem();
     }
@@ -498,7 +501,7 @@ struct DkvMisc {
   int used;                        // tokens that belong to a sequence
   int first_end, blocks;           // end of the first key's sequence; query blocks per head
   int key_end[kBlock];             // end of each key's sequence (no register is left for it)
-  unsigned int repair[2][4];       // rows of dv, dk to compute again, by warp of the tile
+  int lost;                        // dout has been cleared where keys see it
 };
 static_assert(sizeof(DkvMisc) <= 1024, "misc block");
 
@@ -509,6 +512,43 @@ template <int DP>
 __device__ __forceinline__ uint32_t sum_off(int which, int r, int c) {
   static_assert(2u * 128u * DP * 4u <= DkvCfg<DP>::kStats - DkvCfg<DP>::kQRing, "room for the sums");
   return DkvCfg<DP>::kQRing + ((which * 128 + r) * (DP / 4) + (c ^ (r & (DP / 4 - 1)))) * 16;
+}
+
+// Clears what is not finite in row r of a tile of Q or dO; whether there was any.
+template <int DP>
+static __device__ __noinline__ bool clear_row(uint8_t* tile, int r) {
+  bool any = false;
+  for (int c = 0; c < DP / 2; ++c) {
+    uint32_t* p = reinterpret_cast<uint32_t*>(tile + tile_off(r, c >> 2)) + (c & 3);
+    uint32_t w = *p;
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    if (w == *p) continue;
+    *p = w;
+    any = true;
+  }
+  return any;
+}
+
+// Puts NaN into dv where a dout that is not finite belongs and has been cleared: rows r0, r0 + 2,
+// ... r0 + 30, staged as bf16 (`stage`) or as sums.
+template <int DP>
+static __device__ __noinline__ void mark_lost(const AttentionLaunch& L, uint8_t* sm, uint8_t* stage,
+                                              int kh, int key0, int r0, const int* key_end) {
+  Behind behind;
+  for (int r = r0; r < r0 + 32; r += 2) {
+    if (key_end[r] <= key0 + r) continue;                  // no key of a sequence
+    const unsigned int lost = lost_columns(L, kh, key0, key0 + r, key_end[r], behind);
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e) {
+      if (!(lost >> e & 1u)) continue;
+      const int col = 64 * (e >> 1) + 2 * static_cast<int>(threadIdx.x & 31) + (e & 1);
+      if (stage)
+        *reinterpret_cast<uint16_t*>(stage + tile_off(r, col >> 3) + 2 * (col & 7)) = 0x7fff;
+      else
+        *reinterpret_cast<float*>(sm + sum_off<DP>(0, r, col >> 2) + 4 * (col & 3)) = NAN;
+    }
+  }
 }
 
 template <int DP>
@@ -574,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int end = 0;
     if (key0 < used) end = sequence_of(L, min(key0 + 127, used - 1)).end;
     X.used = used;
+    X.lost = 0;
     X.first_end = sequence_of(L, key0).end;
     X.blocks = end > key0 ? (end - 1) / kBlock + 1 - tile : 0;
   }
-  if (tid < 8) X.repair[tid >> 2][tid & 3] = 0;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -712,14 +752,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto step = [&](int i, auto own) {                 // own: the keys' own block, with ends
       const int q0 = b * kBlock;
       const bool masked = b == tile || q0 + kBlock > first_end;
-      const bool padded = masked && X.used < min(q0 + kBlock, L.T);
       auto hide_unseen = [&](uint32_t (&s)[32]) {
         hide(s, key - q0 - 32 * group, X.key_end[r] - 1 - q0 - 32 * group, 0u);
       };
       const float4* lse2 =
           reinterpret_cast<const float4*>(sm + C::kStats + at.slot * kStatBytes) + 8 * group;
-      ok = guard.warp_wait(&X.q_full[at.slot], at.parity) &&          // the stats
-           (C::kTwoS ? guard.warp_wait(&X.s_full[i & 1], (i >> 1) & 1)
+      ok = guard.warp_wait(&X.q_full[at.slot], at.parity);            // the stats
+      if (!ok) return;
+      // Where a key may not see a query, what is not finite in its q and dout would reach the key
+      // all the same.  A query that holds any, or that is padding, has a log-sum-exp or a delta
+      // that is not finite; its own keys have NaN for p or for ds then.
+      unsigned int gone = 0;                           // such queries of this warp's columns
+      if (masked) {
+        const float* z = reinterpret_cast<const float*>(lse2) + lane;
+        gone = __ballot_sync(0xffffffffu, q0 + 32 * group + lane < L.T &&
+                                              !(fabsf(z[0]) + fabsf(z[128]) < INFINITY));
+      }
+      ok = (C::kTwoS ? guard.warp_wait(&X.s_full[i & 1], (i >> 1) & 1)
                      : guard.warp_wait(&X.s_full[0], i & 1));
       if (!ok) return;
       ptx::tc_fence_after();
@@ -750,11 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tmem_st16(ts, w);
       }
-      if (padded) {                              // the block holds padding: clear its Q and dO
+      if (__builtin_expect(gone != 0, 0)) {
         ok = guard.warp_wait(&X.do_full[at.slot], at.parity);
         if (!ok) return;
-        if (group < 2 && q0 + r >= X.used)
-          zero_row<DP>(sm + (group ? C::kDoRing : C::kQRing) + at.slot * C::kTile, r);
+        if (quarter < 2 && (gone >> lane & 1u) &&
+            clear_row<DP>(sm + (quarter ? C::kDoRing : C::kQRing) + at.slot * C::kTile,
+                          32 * group + lane) &&
+            quarter == 1 && isfinite(reinterpret_cast<const float*>(lse2)[lane]))
+          X.lost = 1;                                  // single columns of dv need it
         ptx::fence_proxy_async_smem();
       }
       ptx::tmem_st_wait();
@@ -779,9 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[o + 1] = __float_as_uint(y.y);
         }
       }
-      // (p is 0 where a key is not seen, and 0 times a dp of real data is 0; a row that NaN
-      // or Inf there reached is computed again below.  Padding may hold anything.)
-      if (padded) hide_unseen(x);
+      // (p is 0 where a query is not seen, and 0 times the finite dp - delta of the others is 0)
+      if (__builtin_expect(gone != 0, 0)) hide_unseen(x);
       {
         uint32_t w[16];
 #pragma unroll
@@ -832,7 +883,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (ok) {
       ptx::tc_fence_after();
       const float f0 = which ? L.scale : 1.f;
-      float test = 0.f;                                // NaN if an element is not finite
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
         const int col = DP / 2 * side + 32 * i;
@@ -840,26 +890,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32_sync(lanes + 256 + DP * which + col, o);
         float f[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 32; ++e)
           f[e] = key < X.used && n > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
-          test = fmaf(f[e], 0.f, test);
-        }
         store_row32(stage, r, col / 8, f);
       }
-      const unsigned int bad = __ballot_sync(0xffffffffu, key < X.used && test != 0.f);
-      if (bad && lane == 0) atomicOr(&X.repair[which][quarter], bad);
     }
     half_barrier(which);                               // (reached by every compute thread)
-    if (ok && L.split == 1) {
-      // either side of a row may be bad: the two warps take every other row of the joint set
-      unsigned int bad = X.repair[which][quarter] & (side ? 0xaaaaaaaau : 0x55555555u);
-      while (bad) {
-        const int src = __ffs(bad) - 1;
-        bad &= bad - 1;
-        Row dk, dv;
-        dkv_row(L, kh, key - lane + src, X.key_end[r - lane + src], dk, dv);
-        put_row(stage, r - lane + src, which ? dk : dv, DP / 64);
-      }
+    if (ok) {
+      if (__builtin_expect(X.lost && !which, 0))       // (the two warps of a row's sides take
+        mark_lost<DP>(L, sm, L.split > 1 ? nullptr : stage, kh, key0, r - lane + side,   // every
+                      X.key_end);                                                 // other row)
       ptx::fence_proxy_async_smem();
     }
     half_barrier(which);
@@ -892,19 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
         if (key >= used) v = make_float4(0.f, 0.f, 0.f, 0.f);
         __nv_bfloat16* row = (which ? L.dk : L.dv).row(key, kh);
-        const float test = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
-        if (__any_sync(0xffffffffu, test != 0.f)) {
-          Row dk, dv;
-          dkv_row(L, kh, key, sequence_of(L, key).end, dk, dv);
-          const Row& x = which ? dk : dv;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (64 * e + 2 * lane < L.dim)
-              *reinterpret_cast<uint32_t*>(row + 64 * e + 2 * lane) =
-                  pack2(x.v[2 * e], x.v[2 * e + 1]);
-        } else if (key < L.T && 4 * lane < L.dim) {
+        if (key < L.T && 4 * lane < L.dim)
           *reinterpret_cast<uint2*>(row + 4 * lane) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
-        }
       }
     }
     ptx::cluster_arrive();                             // nobody reads this block's sums any more

@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&X.s_read[t]);
         }
+        bool clear = false;
         if (__builtin_expect(k0 < last_begin || b + 1 == blocks_end, 0)) {
+          clear = k0 < X.first[0] || used < min(k0 + kBlock, L.T);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             hide(s[i], row_begin - k0 - 32 * i, row - k0 - 32 * i, 0xff800000u);
@@ -389,12 +391,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (__builtin_expect(used < min(k0 + kBlock, L.T), 0)) {
-          // the block holds padding: clear its V
+        if (__builtin_expect(clear, 0)) {
+          // the block holds padding, or tokens that neither tile sees: clear their V
           const int n = 2 * (b - begin) + 1, slot = n % C::kStages;
           ok = guard.warp_wait(&X.full[slot], (n / C::kStages) & 1);
           if (!ok) break;
-          if (k0 + r >= used) zero_row<DP>(sm + C::kRing + slot * C::kTile, r);
+          if (k0 + r < X.first[0] || k0 + r >= used) zero_row<DP>(sm + C::kRing + slot * C::kTile, r);
           ptx::fence_proxy_async_smem();
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
@@ -449,14 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           L.lse[static_cast<size_t>(h) * L.T + row] =
               !keys ? -INFINITY : l == 0.f ? NAN : m * L.scale + __logf(l);
         __syncwarp();
-        unsigned int bad = __ballot_sync(0xffffffffu, row < L.T && test != 0.f);
-        while (bad) {
-          const int src = __ffs(bad) - 1;
-          bad &= bad - 1;
-          put_row(stage, r - lane + src,
-                  out_row(L, h, row - lane + src, __shfl_sync(0xffffffffu, row_begin, src)),
-                  DP / 64);
-        }
+        // (a row whose l is NaN or 0 is NaN throughout)
+        const unsigned int bad = __ballot_sync(0xffffffffu, row < L.T && test != 0.f && l > 0.f);
+        if (bad) mend_out(L, stage, DP / 64, h, row0 + 128 * t, r - lane, row_begin, bad);
         ptx::fence_proxy_async_smem();
       }
       if (blocks_end > 0) {

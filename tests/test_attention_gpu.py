@@ -645,3 +645,81 @@ def test_tensors_that_require_grad_are_refused_while_autograd_records():
     Attention.apply(*leaves).backward(do)
     for x, g in zip(leaves, muon.attention_backward(do, q, k, v, out, lse)):
         assert torch.equal(x.grad, g)
+
+
+# where a value that is not finite may stand: first, middle and last token of the second document,
+# the neighbours' tokens next to it (in its first and last tile), each in one element or a row
+BAD_TOKENS = [270, 271, 383, 384, 600, 768, 899, 269, 900]
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 64), (24, 24, 64), (2, 1, 128)])
+@pytest.mark.parametrize("whole", [False, True])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+def test_non_finite_values_over_several_tiles(which, whole, hq, hk, d):
+    lengths = [270, 630, 100]
+    cu = _cu(lengths)
+    for token in BAD_TOKENS:
+        for value in (float("nan"), float("inf")):
+            q, k, v, do = _draw(100 + token, 1000, hq, hk, d, fused=False)
+            x, h0 = {"q": q, "k": k, "v": v, "do": do}[which], 1 if which in "q do" else 0
+            if whole:
+                x[token, h0] = value
+            else:
+                x[token, h0, 5] = value
+            out, lse = muon.attention(q, k, v, cu)
+            grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+            some = sorted({0, 1, hq - 1})             # the rest holds finite values only
+            g = sorted({h // (hq // hk) for h in some})
+            pick = [h for h in range(hq) if h // (hq // hk) in g]
+            Q, K, V, D, O = (f64(y) for y in (q[:, pick], k[:, g], v[:, g], do[:, pick],
+                                              out[:, pick]))
+            Z = f64(lse[pick])
+            c = cu.cpu().numpy()
+            with np.errstate(all="ignore"):
+                r_out, r_lse = ref.attention(Q, K, V, c)
+                want = ref.attention_backward(D, Q, K, V, O, Z, c)
+            # out and dv element by element: other columns of a row keep their values
+            for name, got, w in [("out", O, r_out), ("dv", f64(grads[2][:, g]), want[2])]:
+                fin = np.isfinite(w)
+                assert np.array_equal(np.isfinite(got), fin), (name, token, value)
+                assert _rel(got[fin], w[fin]) <= REL, (name, token, value)
+            assert np.array_equal(np.isfinite(Z), np.isfinite(r_lse))
+            for name, got, w in [("dq", f64(grads[0][:, pick]), want[0]),
+                                 ("dk", f64(grads[1][:, g]), want[1])]:
+                clean = np.isfinite(w).all(axis=2)
+                assert np.isfinite(got[clean]).all(), (name, token, value)
+                assert _rel(got[clean], w[clean]) <= REL, (name, token, value)
+                assert not np.isfinite(got[~clean]).all(axis=1).any(), (name, token, value)
+            rest = [h for h in range(hk) if h not in g]
+            assert all(torch.isfinite(y[:, rest]).all() for y in grads[1:])
+
+
+@pytest.mark.parametrize("hq,hk,d", [(8, 4, 64), (8, 2, 128)])
+def test_non_finite_values_cost_no_walk_of_every_row(hq, hk, d):
+    # 8192 tokens take about 0.3 ms forward, 1 ms backward; a walk of all keys by every row that
+    # one value reaches took 470 and 360 ms.  What may still be walked: a tile's rows.
+    t = 8192
+    two = _cu([300, t - 300]), _cu([t - 300, 300])
+    cases = [(which, token, whole, None) for which in range(4)
+             for token in (0, t // 2 + 5, t - 1) for whole in (False, True)]
+    cases += [(None, 299, True, two[0]), (None, t - 300, True, two[1])]
+    for which, token, whole, cu in cases:
+        x = _draw(7, t, hq, hk, d, fused=False)
+        for i, y in enumerate(x):
+            if which is None or i == which:
+                y[token, 0, 3] = float("nan")
+                if whole:
+                    y[token] = float("nan")
+        q, k, v, do = x
+
+        def call():
+            out, lse = muon.attention(q, k, v, cu)
+            return muon.attention_backward(do, q, k, v, out, lse, cu)
+
+        call()
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        assert start.elapsed_time(end) < 60.0, (which, token, whole)
