@@ -53,12 +53,33 @@ __device__ __forceinline__ int tokens_in_use(const AttentionLaunch& L) {
   return L.cu == nullptr ? L.T : min(max(__ldg(L.cu + L.n_seqs), 0), L.T);
 }
 
-// The tile (of `rows` tokens; every thread of the block calls this) whose work is the
-// `want`-th largest: blocks start in the order of their index, and a long tile that
-// starts last ends last.  Worth its two block barriers (0.3 us) where documents of
-// different lengths take more than one wave of blocks: 8192 tokens of 5 to 2400, 12
-// heads of 64, went from 66 to 57 us forward.  work(i): the blocks that tile i walks.
-constexpr int kRankedTiles = 256;
+// The tile (every thread of the block calls this) whose work is the `want`-th largest: blocks
+// start in the order of their index, and a long tile that starts last ends last.
+// work(i): the blocks that tile i walks.
+// It costs every block its searches and two barriers, 1 us and more with many tiles, and a
+// wave the key blocks that neighbouring tiles share.  So it pays where documents of different
+// lengths take few waves, and a wave holds several tiles (the heads of a tile are blocks that
+// follow each other).  Time with it over time without, three packs of random lengths each:
+//   forward   4096 tokens, 12/12 heads of 64 (1.3 waves)     0.97  0.92  1.05
+//             8192 tokens, 8/4 heads of 64 (1.7)             0.85  0.80  0.98
+//             8192 tokens, 12/12 heads of 64 (2.5)           0.98  1.01  1.04
+//               (8 documents of 5 to 2400 tokens             0.94)
+//             16384 tokens, 8/4 heads of 64 (3.4)            0.96  0.95  0.96
+//             32768 tokens, 12/12 heads of 64 (10)           1.04  1.05  1.05
+//             4096 tokens, 24/8 heads of 64 (2.5)            1.08  1.05  1.09
+//   dq and dk, dv in a row, dk, dv ranked
+//             4096 tokens, 24/8 heads of 64 (1.7 waves)      0.91  0.96  0.98
+//             16384 tokens, 16/4 heads of 128 (3.4)          0.90  0.92  0.97
+//             32768 tokens, 16/4 heads of 128 (6.7)          1.02  1.01  0.99
+//             4096 tokens, 12/12 heads of 64 (2.5)           1.05  1.03  1.05
+//               (a key head with one query head has short walks: not ranked there)
+// dq, with a block for each query head, has many waves: 1.03 to 1.2, and it is not ranked.
+constexpr int kRankedTiles = 256;        // the scratch of the ranking
+inline bool rank_tiles(int n_seqs, int tiles, int heads, int sms) {
+  const long long blocks = 1ll * tiles * heads;
+  return n_seqs > 1 && tiles <= kRankedTiles && blocks > sms && blocks <= 4ll * sms &&
+         8 * heads <= sms;
+}
 template <typename F>
 __device__ __forceinline__ int ranked_tile(int tiles, int want, int* scratch, F&& work) {
   for (int i = threadIdx.x; i < tiles; i += blockDim.x) scratch[i] = work(i);

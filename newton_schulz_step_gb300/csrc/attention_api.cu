@@ -406,7 +406,7 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
     std::lock_guard<std::mutex> lk(pair_mu);
     cudaError_t e = counted_launch(
         st, MUON_K_ATTENTION_DQ, 6.0 * L.dim * pair_bound(L), row * (4.0 * L.hq + 2.0 * L.hk),
-        [&] { return launch_attention_dq(M, L, sms, st); });
+        [&] { return launch_attention_dq(M, L, st); });
     if (e != cudaSuccess) return MUON_ERR_CUDA;
     e = counted_launch(st, MUON_K_ATTENTION_DKV, 8.0 * L.dim * pair_bound(L),
                        row * (2.0 * L.hq + 4.0 * L.hk),

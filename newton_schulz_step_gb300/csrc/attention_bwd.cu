@@ -139,10 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of one sequence, the last tiles hold the most keys: they go first
   const int tiles = (L.T + 127) / 128;
   const int h = static_cast<int>(blockIdx.x) % L.hq;
-  int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
-  if (L.ranked)
-    tile = ranked_tile(tiles, static_cast<int>(blockIdx.x) / L.hq, reinterpret_cast<int*>(sm),
-                       [&](int i) { return i - sequence_of(L, 128 * i).begin / kBlock; });
+  const int tile = tiles - 1 - static_cast<int>(blockIdx.x) / L.hq;
   const int row0 = 128 * tile, kh = h / L.group;
 
   if (tid < 2) {
@@ -949,20 +946,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename K>
 cudaError_t launch(K kernel, int heads, int split, uint32_t smem, const AttentionMaps& m,
-                   AttentionLaunch& l, int sms, cudaStream_t s) {
-  const int tiles = (l.T + 127) / 128;
+                   AttentionLaunch& l, cudaStream_t s) {
   l.split = split;
-  l.ranked = l.n_seqs > 1 && tiles <= kRankedTiles && tiles * heads * split > sms;
-  return launch_behind(kernel, tiles * heads * split, kThreads, smem, m, l, s, split);
+  return launch_behind(kernel, (l.T + 127) / 128 * heads * split, kThreads, smem, m, l, s, split);
 }
 static_assert(DqCfg<128>::kSmem <= 232448 && DkvCfg<128>::kSmem <= 232448, "shared memory");
 
 }  // namespace
 
-cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, int sms,
-                                cudaStream_t s) {
-  return l.dim <= 64 ? launch(attention_dq_kernel<64>, l.hq, 1, DqCfg<64>::kSmem, m, l, sms, s)
-                     : launch(attention_dq_kernel<128>, l.hq, 1, DqCfg<128>::kSmem, m, l, sms, s);
+cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, cudaStream_t s) {
+  return l.dim <= 64 ? launch(attention_dq_kernel<64>, l.hq, 1, DqCfg<64>::kSmem, m, l, s)
+                     : launch(attention_dq_kernel<128>, l.hq, 1, DqCfg<128>::kSmem, m, l, s);
 }
 
 cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
@@ -976,9 +970,9 @@ cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int 
   // 51 split; 8192 tokens (1.2 times) 137 and 147.
   const bool uneven = l.n_seqs <= 1 && ((l.T + 127) / 128 + 1) * l.hk * 3 <= sms * 4;
   const int split = units * 4 <= sms ? 4 : units * 2 <= sms || uneven ? 2 : 1;
-  return l.dim <= 64
-             ? launch(attention_dkv_kernel<64>, l.hk, split, DkvCfg<64>::kSmem, m, l, sms, s)
-             : launch(attention_dkv_kernel<128>, l.hk, split, DkvCfg<128>::kSmem, m, l, sms, s);
+  l.ranked = split == 1 && l.group > 1 && rank_tiles(l.n_seqs, (l.T + 127) / 128, l.hk, sms);
+  return l.dim <= 64 ? launch(attention_dkv_kernel<64>, l.hk, split, DkvCfg<64>::kSmem, m, l, s)
+                     : launch(attention_dkv_kernel<128>, l.hk, split, DkvCfg<128>::kSmem, m, l, s);
 }
 
 }  // namespace muon

@@ -483,7 +483,7 @@ cudaError_t launch(const AttentionMaps& m, AttentionLaunch& l, int sms, cudaStre
   // instead of 28; 1024: 18 instead of 20)
   l.tiles = (l.T + 127) / 128 * l.hq <= sms ? 1 : kTiles;
   const int pairs = (l.T + 128 * l.tiles - 1) / (128 * l.tiles);
-  l.ranked = l.n_seqs > 1 && pairs <= kRankedTiles && pairs * l.hq > sms;
+  l.ranked = rank_tiles(l.n_seqs, pairs, l.hq, sms);
   return launch_behind(attention_fwd_kernel<DP>, pairs * l.hq, kThreads, Cfg<DP>::kSmem, m, l, s);
 }
 

@@ -297,7 +297,7 @@ struct AttentionLaunch {
   int n_seqs, T, hq, hk, group, dim;
   float scale;
   unsigned int* status;
-  int ranked;                       // blocks take the tiles by their work
+  int ranked;                       // out, dk, dv: blocks take the tiles by their work
   int tiles;                        // forward: tiles of 128 rows a block takes
   int split;                        // dk, dv: blocks of a cluster that share a tile
 };
@@ -337,8 +337,7 @@ cudaError_t launch_adam(const AdamLaunch& l, int blocks, cudaStream_t s);
 cudaError_t launch_fused(const FusedLaunch& l, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeLaunch& l, bool backward, int sms, cudaStream_t s);
 cudaError_t launch_attention(const AttentionMaps& m, AttentionLaunch l, int sms, cudaStream_t s);
-cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, int sms,
-                                cudaStream_t s);
+cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, cudaStream_t s);
 cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
                                  cudaStream_t s);
 

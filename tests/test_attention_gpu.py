@@ -723,3 +723,25 @@ def test_non_finite_values_cost_no_walk_of_every_row(hq, hk, d):
         end.record()
         torch.cuda.synchronize()
         assert start.elapsed_time(end) < 60.0, (which, token, whole)
+
+
+@pytest.mark.parametrize("d", [16, 128])
+def test_parity_where_blocks_take_the_tiles_by_their_work(d):
+    # 1 to 4 waves of blocks and few heads a tile, forward and dk/dv; documents of different lengths
+    lengths = [700, 3, 0, 1201, 130, 1, 641, 77, 900, 1340]
+    q, k, v, do = _draw(110 + d, sum(lengths), 16, 8, d)
+    cu = _cu(lengths)
+    out, lse = muon.attention(q, k, v, cu)
+    grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+    for g in (0, 7):                      # a key head at a time, with its two query heads
+        h = slice(2 * g, 2 * g + 2)
+        Q, D, K, V, L = (f64(x) for x in (q[:, h], do[:, h], k[:, g:g + 1], v[:, g:g + 1], lse[h]))
+        c = cu.cpu().numpy()
+        r_out, r_lse = ref.attention(Q, K, V, c)
+        b = _magnitudes(Q, K, V, D, r_out, L, c, d ** -0.5)
+        want = ref.attention_backward(D, Q, K, V, r_out, L, c)
+        assert np.all(np.abs(L - r_lse) <= b[1] + 1e-30)
+        got = (out[:, h], grads[0][:, h], grads[1][:, g:g + 1], grads[2][:, g:g + 1])
+        for name, x, w, e in zip(("out", "dq", "dk", "dv"), got, (r_out, *want), (b[0], *b[2:])):
+            err = np.abs(f64(x) - w) - (U * np.abs(w) + (1 + U) * e + 1e-30)
+            assert np.all(err <= 0), (name, g, float(err.max()))
