@@ -341,7 +341,8 @@ muon_status muon_attention(const muon_attention_spec* spec, muon_heads q, muon_h
 /*
  * Gradients of muon_attention's out with respect to q, k and v, from its out and
  * lse for the same q, k, v and offsets (of any other out the results are not
- * defined: delta is corrected by what out was rounded by).  With delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
+ * defined: delta is corrected by what out was rounded by).  With
+ * delta_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - delta_i):
  *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
  * (dk and dv summed over the query heads that share the key/value head, in fp32).
  * Fixed summation order, no atomics: repeated calls give equal bits.

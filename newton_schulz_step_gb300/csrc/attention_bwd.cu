@@ -24,7 +24,7 @@
 // from the block itself (sum ds = 0), and all remainders: 1.0 times.  The dk kernel takes
 // the remainders of the block where a sequence ends in the tile: its sums over few queries
 // scatter up to 1.7 times without them.  That is a block of a walk in both cases: 8192
-// packed tokens, 16/4 heads of 128, dq 143 to 147 us, dk/dv 201 to 205.
+// packed tokens, 16/4 heads of 128, dq 142 to 144 us, dk/dv 168 either way.
 //
 // Warps 0-15 compute, warp 16 issues the copies, warp 17 the products.  A compute thread
 // owns a row (TMEM lane) of S and dP and 32 of its columns; each of the 4 groups of warps
@@ -64,9 +64,9 @@ __device__ __forceinline__ void half_barrier(int half) {   // the lower or upper
 // exponentials have read this one), dq += dS K, dP of the next block; two buffers: dq,
 // dP of the next block, S of the one after.
 // What bounds it: heads of 128, the chain dP -> dS -> dq -> dP of the next block: dS is
-// written over dP, TMEM has no room for a second one.  8192 tokens, 32/8 heads: 660 us, its
-// products at 78 % of a library product's rate (tensor cores active 61 % of the cycles).
-// (Handing over dS before its remainders: 654 us.  Blocks of 64 keys: 815.)
+// written over dP, TMEM has no room for a second one.  8192 tokens, 32/8 heads: 670 us, its
+// products at 77 % of a library product's rate (tensor cores active 61 % of the cycles).
+// (Handing over dS before its remainders: 1 % less.  Blocks of 64 keys: 815.)
 template <int DP> struct DqCfg {
   static constexpr uint32_t kTile = DP / 64 * kSlab;
   static constexpr int kK = DP == 128 ? 3 : 4, kV = DP == 128 ? 2 : 4;   // ring slots
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dv += P^T dO, S^T of the next block (two buffers: of the one after), dk += dS^T Q, dP^T
 // of the next block; so P of a block is computed beside the last two products of the one
 // before, and dS beside the first two of its own.  With heads of 128 the four products
-// bound it: 88 % of the rate that a library product reaches (8192 tokens, 32/8 heads: 665
+// bound it: 87 % of the rate that a library product reaches (8192 tokens, 32/8 heads: 672
 // us).  With 64 the exponentials do, and the second buffer keeps the compute warps from
 // waiting for S.
 // Where the tiles leave SMs without work, 2 or 4 blocks of a cluster share a tile: each

@@ -20,8 +20,10 @@
 // bytes alone: 101).  So a position is read a step ahead, and the table row with the rows
 // it belongs to: 138 us; with the lanes of a row known at compile time and no division
 // a step 121 us (5.7 TB/s with the tables and positions, 84 % of the copy rate).
-// Backward of 16384 tokens, 16 + 16 heads of 128: 86 us (4.8 TB/s, 70 %).  Issued
-// instructions hold the rest: about 150 for 8 elements forward, 250 backward.
+// Backward of 16384 tokens, 16 + 16 heads of 128: 86 us (4.8 TB/s, 70 %).  What holds the
+// rest is that a warp loads, then computes, with too few others beside it: issue slots 60 %
+// with 24 warps an SM forward (about 150 instructions for 8 elements), 51 % with 16 backward
+// (250), waits for loads the first of the stalls.
 #include <type_traits>
 
 #include "internal.h"
