@@ -69,13 +69,19 @@ long long floor_div(long long a, long long b) { return a / b - (a % b != 0 && (a
 bool overlap(const Rows& a, const Rows& b) {
   if (a.at >= end_of(b) || b.at >= end_of(a)) return false;
   if (a.tokens > 1 && b.tokens > 1 && a.ts != b.ts) return true;
-  if (1ll * a.heads * b.heads > 1 << 16) return true;
   const long long ts = std::max(1ll, a.tokens > 1 ? a.ts : b.ts);
+  const long long apart = static_cast<long long>(a.at - b.at);
+  // all heads of a token as one piece: a's piece lies between two of b's
+  const long long gap = apart - floor_div(apart, ts) * ts;
+  if (gap >= b.hs * (b.heads - 1) + b.len && gap + a.hs * (a.heads - 1) + a.len <= ts)
+    return false;
+  if (1ll * a.heads * b.heads > 1 << 16) return true;
+  const bool one_stride = a.hs == b.hs;      // then head i - j of a over head 0 of b says it all
   for (int i = 0; i < a.heads; ++i)
     for (int j = 0; j < b.heads; ++j) {
+      if (one_stride && i > 0 && j > 0) break;
       // tokens d apart are off + d ts apart; they meet if -a.len < off + d ts < b.len
-      const long long off =
-          static_cast<long long>(a.at - b.at) + i * a.hs - j * b.hs;
+      const long long off = apart + i * a.hs - j * b.hs;
       const long long lo = floor_div(-a.len - off, ts) + 1, hi = -floor_div(off - b.len, ts) - 1;
       if (std::max(lo, 1ll - b.tokens) <= std::min(hi, a.tokens - 1ll)) return true;
     }
