@@ -557,8 +557,8 @@ def _stream_workspace(ws, need: int, index: int, handle: int):
 
 
 def _refuse_grad(where: str, **tensors):
-    """Forward calls record nothing for autograd: a tensor that asks for a gradient would not
-    get one."""
+    """Says which tensor asks for a gradient: forward calls record nothing for autograd, and it
+    would not get one."""
     for name, t in tensors.items():
         if t is not None and t.requires_grad:
             raise ValueError(f"{name} requires grad, and {where} records no gradient: call it under "
@@ -611,7 +611,9 @@ def qk_norm_rope(q, k, cos, sin, *, q_weight=None, k_weight=None, positions=None
     L = _lib or load_library()
     spec, vq, vk = _rope_spec(q, k, cos, sin, positions, q_weight, k_weight, norm, eps,
                               interleaved)
-    if torch.is_grad_enabled():
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or (
+            q_weight is not None and q_weight.requires_grad) or (
+            k_weight is not None and k_weight.requires_grad)):
         _refuse_grad("qk_norm_rope", q=q, k=k, q_weight=q_weight, k_weight=k_weight)
     index = q.get_device()
     if stream is not None or index != _current_device():
@@ -709,7 +711,7 @@ def attention(q, k, v, cu_seqlens=None, *, scale: float | None = None, out=None,
     autograd: tensors that require grad are refused while it records, see attention_backward."""
     L = _lib or load_library()
     spec, vq, vk, vv = _attention_spec(q, k, v, cu_seqlens, scale)
-    if torch.is_grad_enabled():
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         _refuse_grad("attention", q=q, k=k, v=v)
     index = q.get_device()
     if stream is not None or index != _current_device():
