@@ -423,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        f[e] = __uint_as_float(o[e]) * L.scale;
+        f[e] = row < used ? __uint_as_float(o[e]) * L.scale : 0.f;     // (no gradient of padding)
         test = fmaf(f[e], 0.f, test);
       }
       store_row32(sm, r, 4 * group, f);
-      const unsigned int bad = __ballot_sync(0xffffffffu, row < used && test != 0.f);
+      const unsigned int bad = __ballot_sync(0xffffffffu, test != 0.f);
       if (bad && lane == 0) atomicOr(&X.repair[quarter], bad);
     }
     if (ok) {

@@ -745,3 +745,17 @@ def test_parity_where_blocks_take_the_tiles_by_their_work(d):
         for name, x, w, e in zip(("out", "dq", "dk", "dv"), got, (r_out, *want), (b[0], *b[2:])):
             err = np.abs(f64(x) - w) - (U * np.abs(w) + (1 + U) * e + 1e-30)
             assert np.all(err <= 0), (name, g, float(err.max()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+def test_padding_gets_no_gradient_behind_values_that_are_not_finite(which, d):
+    # tokens past the last sequence in a tile with tokens that are not finite, and in tiles behind
+    q, k, v, do = _draw(120 + d, 500, 4, 2, d, fused=False)
+    cu = _cu([100, 190])
+    {"q": q, "k": k, "v": v, "do": do}[which][[40, 260, 280, 400], 1] = float("inf")
+    out, lse = muon.attention(q, k, v, cu)
+    grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+    assert torch.count_nonzero(out[290:]) == 0 and torch.isneginf(lse[:, 290:]).all()
+    for g in grads:
+        assert torch.count_nonzero(g[290:]) == 0
