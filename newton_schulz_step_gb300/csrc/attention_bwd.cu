@@ -436,8 +436,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     compute_barrier();                                 // (reached by every compute thread)
     if (ok) {
-      if (group == 1)
-        stats[128] = delta + ((X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]));
+      if (group == 1)                // (0 of rows that are not there: where nothing is hidden, a
+        stats[128] =                 // value that is not finite reaches their ds)
+            row < used
+                ? delta + ((X.delta[0][r] + X.delta[1][r]) + (X.delta[2][r] + X.delta[3][r]))
+                : 0.f;
       // Any part of a row may be bad: the four warps of the rows share the joint set.  (A row
       // whose visible ds, summed up here, are not finite is so throughout.)
       unsigned int bad = X.repair[quarter];

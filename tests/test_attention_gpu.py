@@ -759,3 +759,20 @@ def test_padding_gets_no_gradient_behind_values_that_are_not_finite(which, d):
     assert torch.count_nonzero(out[290:]) == 0 and torch.isneginf(lse[:, 290:]).all()
     for g in grads:
         assert torch.count_nonzero(g[290:]) == 0
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 1, 64), (8, 8, 128), (32, 8, 128)])
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+def test_non_finite_values_before_an_end_inside_a_tile(which, hq, hk, d):
+    # the last tile holds fewer than 128 tokens, and its sequence shares a tile with one before
+    lengths = [2, 88, 520, 0, 543]
+    cu = _cu(lengths)
+    for token in (671, 1100, 1152):
+        for value in (float("nan"), -float("inf")):
+            q, k, v, do = _draw(130 + token, 1153, hq, hk, d, fused=False)
+            {"q": q, "k": k, "v": v, "do": do}[which][token] = value
+            out, lse = muon.attention(q, k, v, cu)
+            grads = muon.attention_backward(do, q, k, v, out, lse, cu)
+            for x in (out, *grads):
+                assert torch.isfinite(x[:610]).all(), (token, value)
+            assert not torch.isfinite(grads[1][token]).all()
