@@ -98,7 +98,11 @@ typedef enum muon_kernel_kind {
   MUON_K_NORM_ROPE_BWD = 10, /* its gradients                                   */
   MUON_K_ATTENTION = 11,     /* attention, forward                              */
   MUON_K_ATTENTION_DQ = 12,  /* attention, gradient of the queries              */
-  MUON_K_ATTENTION_DKV = 13  /* attention, gradients of the keys and values     */
+  MUON_K_ATTENTION_DKV = 13, /* attention, gradients of the keys and values     */
+  MUON_K_LINEAR = 14,        /* products with a weight matrix                   */
+  MUON_K_LINEAR_FINISH = 15, /* sums of a split product, its epilogue           */
+  MUON_K_LINEAR_DZ = 16,     /* dz = dout act'(z), and the bias' gradient       */
+  MUON_K_LINEAR_TOKEN = 17   /* the product for up to 8 tokens                  */
 } muon_kernel_kind;
 
 /* Workspace bytes for one muon_step()/muon_ns5() call on [batch, rows, cols].
@@ -352,6 +356,67 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
                                     const float* lse, muon_heads dq, muon_heads dk,
                                     muon_heads dv, void* workspace, size_t workspace_bytes,
                                     void* stream);
+
+/*
+ * Products with a weight matrix, the operators between the attention path and the
+ * weights that muon_step trains (c_q, c_k, c_v, proj and the MLP's matrices).  The
+ * pages name the layers ([PG] CastedLinear, the relu^2 MLP) and print none of this;
+ * it is an addition.
+ *
+ * A matrix is passed as a strided view: element j of row i lies at
+ * data[i row_stride + j].  data and row_stride are 16-byte aligned (the stride of a
+ * single row is ignored), row_stride is at least the width: columns of a wider
+ * tensor are used in place, and a width that is no multiple of 8 needs padded rows.
+ * Padding is neither read into a result nor written.  An output shares no bytes
+ * with an input or another output, but where the text allows it (refused as an
+ * invalid argument; views that interleave have to have one stride).
+ */
+typedef struct muon_matrix {
+  void* data;
+  long long row_stride;
+} muon_matrix;
+
+typedef enum muon_activation {
+  MUON_ACT_NONE = 0,
+  MUON_ACT_RELU2 = 1,    /* max(z, 0)^2                                             */
+  MUON_ACT_GELU = 2      /* z / (1 + exp(-2 u)), u = (2/pi)^1/2 (z + 0.044715 z^3):
+                            GELU's tanh form                                        */
+} muon_activation;
+
+/*
+ * z = x W^T + b,  out = act(z) + r:  x [tokens, in_features], W [out_features,
+ * in_features], b [out_features] or NULL, r [tokens, out_features] or data NULL, all
+ * bf16.  Products in bf16 with fp32 sums; bias, activation and residual in fp32 on
+ * the sum; one rounding to bf16.  preact (or data NULL) receives z, rounded, for the
+ * gradients.  out may be the very view of the residual.
+ */
+typedef struct muon_linear_spec {
+  int tokens;                        /* 0..2^31 - 65537                             */
+  int in_features, out_features;     /* 1..2^20                                     */
+  int activation;                    /* muon_activation                             */
+  const void* bias;                  /* bf16, 16-byte aligned, or NULL              */
+} muon_linear_spec;
+
+/* Workspace bytes of muon_linear and muon_linear_backward; 0 if invalid. */
+size_t muon_linear_workspace_bytes(int tokens, int in_features, int out_features);
+
+muon_status muon_linear(const muon_linear_spec* spec, muon_matrix x, muon_matrix weight,
+                        muon_matrix residual, muon_matrix preact, muon_matrix out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of muon_linear: with dz = dout act'(z) (dout itself without activation),
+ *   dx = dz W,   dweight = dz^T x,   dbias = sum over tokens of dz
+ * in bf16 from fp32 sums.  With an activation, preact is the z that muon_linear
+ * left, and dz [tokens, out_features] is a buffer that the call fills with dz rounded
+ * to bf16 for the products (dbias sums the unrounded); without, both are unused.
+ * dbias: [out_features] or NULL; spec->bias is not read.  The residual's gradient is
+ * dout.  Fixed summation order: repeated calls give equal bits.
+ */
+muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout, muon_matrix x,
+                                 muon_matrix weight, muon_matrix preact, muon_matrix dz,
+                                 muon_matrix dx, muon_matrix dweight, void* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Path selection (no counterpart on the pages).  With enable = 1 (the default)

@@ -13,7 +13,8 @@ Entry points mirror the C ABI:
   adam_step([(p, g, m, v)...])   one DistAdam step on the non-matrix parameters
   qk_norm_rope(q, k, cos, sin)   RMS norm and rotary positions of the query and key heads
   attention(q, k, v, cu_seqlens) causal attention over packed sequences, grouped heads
-with qk_norm_rope_backward and attention_backward for their gradients.
+  linear(x, weight)              product with a weight matrix, bias, activation and residual
+with qk_norm_rope_backward, attention_backward and linear_backward for their gradients.
 """
 
 from __future__ import annotations
@@ -37,6 +38,7 @@ __all__ = [
     "set_streamed_apply", "streamed_apply", "KERNEL_KINDS",
     "ROPE_EPS", "rope_tables", "qk_norm_rope", "qk_norm_rope_backward",
     "norm_rope_workspace_bytes", "attention", "attention_backward", "attention_workspace_bytes",
+    "ACTIVATIONS", "linear", "linear_backward", "linear_workspace_bytes",
 ]
 
 # Quintic coefficients and rounds as printed in "Muon Custom Sizing 实战", section 2.3.
@@ -51,7 +53,8 @@ ADAM_EPS = 1e-8
 
 KERNEL_KINDS = {0: "prologue", 1: "small_ns", 2: "gram", 3: "poly", 4: "update", 5: "apply",
                 6: "adam", 7: "fused_ns", 8: "rounds", 9: "norm_rope", 10: "norm_rope_backward",
-                11: "attention", 12: "attention_dq", 13: "attention_dkv"}
+                11: "attention", 12: "attention_dq", 13: "attention_dkv", 14: "linear",
+                15: "linear_finish", 16: "linear_dz", 17: "linear_token"}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "timeout",
            5: "workspace"}
 
@@ -101,6 +104,16 @@ class _AttentionSpec(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("n_seqs", ctypes.c_int),
                 ("cu_seqlens", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class _Matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong)]
+
+
+class _LinearSpec(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("in_features", ctypes.c_int),
+                ("out_features", ctypes.c_int), ("activation", ctypes.c_int),
+                ("bias", ctypes.c_void_p)]
 
 
 class _TraceRecord(ctypes.Structure):
@@ -154,6 +167,13 @@ def load_library():
     L.muon_attention.restype = ci
     L.muon_attention_backward.argtypes = [spec, hd, hd, hd, hd, hd, vp, hd, hd, hd, vp, sz, vp]
     L.muon_attention_backward.restype = ci
+    lin, mat = ctypes.POINTER(_LinearSpec), _Matrix
+    L.muon_linear_workspace_bytes.argtypes = [ci, ci, ci]
+    L.muon_linear_workspace_bytes.restype = sz
+    L.muon_linear.argtypes = [lin, mat, mat, mat, mat, mat, vp, sz, vp]
+    L.muon_linear.restype = ci
+    L.muon_linear_backward.argtypes = [lin, mat, mat, mat, mat, mat, mat, mat, vp, vp, sz, vp]
+    L.muon_linear_backward.restype = ci
     L.muon_set_persistent_rounds.argtypes = [ci]
     L.muon_set_persistent_rounds.restype = ci
     L.muon_set_fused_ns.argtypes = [ci]
@@ -758,6 +778,144 @@ def attention_backward(dout, q, k, v, out, lse, cu_seqlens=None, *, scale: float
     _raise(L.muon_attention_backward(spec, vg, vq, vk, vv, vo, p_lse, vdq, vdk, vdv, ws,
                                      ws_bytes, handle), "muon_attention_backward")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------ around the weights
+ACTIVATIONS = {None: 0, "relu2": 1, "gelu": 2}
+
+
+def _refuse_matrix(t, name, shape, dtype, index):
+    """Says what is wrong with a [rows, columns] argument."""
+    device = torch.device("cuda", index)
+    _cuda_device(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, columns], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous along its rows")
+
+
+def _matrix(t, name: str, shape, dtype, index) -> _Matrix:
+    """The view of a [rows, columns] tensor of the given shape, dtype and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and len(shape) == 2:
+        sr, sc = t.stride()
+        if sc == 1 or shape[1] <= 1:
+            return _Matrix(t.data_ptr(), sr)
+    _refuse_matrix(t, name, shape, dtype, index)
+
+
+def _out_matrix(t, name: str, shape, dtype, index):
+    """(tensor, view) of an output: the caller's, or a new one, with its rows padded to 16 bytes
+    where the width asks for it."""
+    if t is not None:
+        return t, _matrix(t, name, shape, dtype, index)
+    rows, cols = shape
+    unit = 16 // dtype.itemsize
+    device = torch.device("cuda", index)
+    if cols % unit == 0:
+        t = torch.empty((rows, cols), dtype=dtype, device=device)
+        return t, _Matrix(t.data_ptr(), cols)
+    padded = -(-cols // unit) * unit
+    t = torch.empty((rows, padded), dtype=dtype, device=device)
+    return t[:, :cols], _Matrix(t.data_ptr(), padded)
+
+
+@functools.lru_cache(maxsize=1024)
+def linear_workspace_bytes(tokens: int, in_features: int, out_features: int) -> int:
+    return int(load_library().muon_linear_workspace_bytes(tokens, in_features, out_features))
+
+
+def _linear_spec(x, weight, activation, bias):
+    """The spec of a call and its views of x and weight."""
+    _cuda_device(x, "x")
+    index, bf16 = x.get_device(), torch.bfloat16
+    vx = _matrix(x, "x", x.shape, bf16, index)
+    t, k = x.shape
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [out_features, in_features], got {tuple(weight.shape)}")
+    n = weight.shape[0]
+    vw = _matrix(weight, "weight", (n, k), bf16, index)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    p_bias = _ptr(bias, "bias", index, bf16, (n,))
+    return _LinearSpec(t, k, n, ACTIVATIONS[activation], p_bias), vx, vw
+
+
+_NO_MATRIX = _Matrix(None, 0)
+
+
+def linear(x, weight, *, bias=None, activation: str | None = None, residual=None,
+           save_preact: bool = False, preact=None, out=None,
+           workspace: Workspace | None = None, stream=None):
+    """act(x weight^T + bias) + residual for bf16 x [tokens, in_features], weight [out_features,
+    in_features], bias [out_features] and residual [tokens, out_features] (matrices strided along
+    their rows, in 16-byte steps).  activation: None, "relu2" (max(z, 0)^2) or "gelu" (its tanh
+    form).  Sums in fp32, one rounding to bf16.  Returns out; with save_preact (out, preact), where
+    preact is z = x weight^T + bias for linear_backward (an argument of that name is the tensor to
+    fill, and asks for it too).  out may be the residual itself.  Nothing is recorded for autograd:
+    tensors that require grad are refused while it records, see linear_backward.  The workspace is
+    as for attention."""
+    L = _lib or load_library()
+    spec, vx, vw = _linear_spec(x, weight, activation, bias)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (
+            bias is not None and bias.requires_grad) or (
+            residual is not None and residual.requires_grad)):
+        _refuse_grad("linear", x=x, weight=weight, bias=bias, residual=residual)
+    index = x.get_device()
+    if stream is not None or index != _current_device():
+        with _launch_on(x.device, stream):
+            return linear(x, weight, bias=bias, activation=activation, residual=residual,
+                          save_preact=save_preact, preact=preact, out=out, workspace=workspace)
+    bf16, shape = torch.bfloat16, (spec.tokens, spec.out_features)
+    vr = vz = _NO_MATRIX
+    if residual is not None:
+        vr = _matrix(residual, "residual", shape, bf16, index)
+    if save_preact or preact is not None:
+        preact, vz = _out_matrix(preact, "preact", shape, bf16, index)
+    out, vo = _out_matrix(out, "out", shape, bf16, index)
+    handle = _current_handle(index)
+    ws, ws_bytes, _owner = _stream_workspace(
+        workspace, linear_workspace_bytes(spec.tokens, spec.in_features, spec.out_features), index,
+        handle)
+    _raise(L.muon_linear(spec, vx, vw, vr, vz, vo, ws, ws_bytes, handle), "muon_linear")
+    return out if preact is None else (out, preact)
+
+
+def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | None = None,
+                    preact=None, dx=None, dweight=None, workspace: Workspace | None = None,
+                    stream=None):
+    """Gradients of linear: from dout [tokens, out_features], its x and weight, and with an
+    activation the preact that it saved, returns (dx, dweight, dbias) in bf16; dbias is None
+    unless `bias`.  The residual's gradient is dout.  Outputs overlap no input."""
+    L = _lib or load_library()
+    spec, vx, vw = _linear_spec(x, weight, activation, None)
+    index, bf16 = x.get_device(), torch.bfloat16
+    if stream is not None or index != _current_device():
+        with _launch_on(x.device, stream):
+            return linear_backward(dout, x, weight, bias=bias, activation=activation,
+                                   preact=preact, dx=dx, dweight=dweight, workspace=workspace)
+    t, k, n = spec.tokens, spec.in_features, spec.out_features
+    vg = _matrix(dout, "dout", (t, n), bf16, index)
+    vz = vdz = _NO_MATRIX
+    if activation is not None:
+        if preact is None:
+            raise ValueError("an activation's gradient needs the preact that linear saved")
+        vz = _matrix(preact, "preact", (t, n), bf16, index)
+        _dz, vdz = _out_matrix(None, "dz", (t, n), bf16, index)
+    dx, vdx = _out_matrix(dx, "dx", (t, k), bf16, index)
+    dweight, vdw = _out_matrix(dweight, "dweight", (n, k), bf16, index)
+    dbias = torch.empty(n, dtype=bf16, device=x.device) if bias else None
+    handle = _current_handle(index)
+    ws, ws_bytes, _owner = _stream_workspace(workspace, linear_workspace_bytes(t, k, n), index,
+                                             handle)
+    _raise(L.muon_linear_backward(spec, vg, vx, vw, vz, vdz, vdx, vdw,
+                                  None if dbias is None else dbias.data_ptr(), ws, ws_bytes,
+                                  handle), "muon_linear_backward")
+    return dx, dweight, dbias
 
 
 def workspace_status(workspace: Workspace | None, clear: bool = False, stream=None) -> int:

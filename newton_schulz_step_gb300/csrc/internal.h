@@ -310,6 +310,61 @@ struct AttentionMaps {
   CUtensorMap dout, dq, dk, dv;       // backward
 };
 
+// ---- products with a weight matrix (linear.cu, linear_api.cu)
+// Pairs of CTAs that a plan counts on: one CTA on each of 152 SMs.
+constexpr int kLinearPairs = 76;
+constexpr int kTokenMax = 8;          // tokens that linear_token_kernel takes
+
+// One product D = A B^T: D is m x n, its tiles 256 rows x LinearLaunch::bn columns.
+struct LinearProblem {
+  int m, n, k_blocks;                 // k_blocks: contraction in 64-deep blocks
+  int tiles_m, tiles_n;
+  int splits;                         // parts of the contraction, <= k_blocks
+  int item_begin;                     // first work item: splits x tiles of them
+  int a_mn, b_mn;                     // operand lies with its rows along the contraction
+  int act, has_res, has_z;
+  const __nv_bfloat16* bias;
+  float* parts;                       // splits > 1: [splits][tiles][256 x bn] fp32 sums
+  // the epilogue's views, for linear_finish_kernel
+  __nv_bfloat16 *out, *z;
+  const __nv_bfloat16* res;
+  long long out_stride, z_stride, res_stride;
+};
+
+struct LinearLaunch {
+  LinearProblem prob[2];
+  int n_prob, items, bn;
+  // the bias' gradient: chunks of the rows' sums [db_chunks][db_n], added by the finish
+  __nv_bfloat16* dbias;
+  const float* db_parts;
+  int db_n, db_chunks;
+  unsigned int* status;
+};
+
+// 128-byte swizzle throughout.  K-major operands: boxes of 64 x (128 rows of A, bn / 2 of
+// B); MN-major: 64 x 64; blocks of the epilogue: 64 columns x 32 rows.
+struct LinearMaps {
+  CUtensorMap a[2], b[2], out[2], res[2], z[2];
+};
+
+struct LinearDz {
+  const __nv_bfloat16 *dy, *z;
+  __nv_bfloat16* dz;
+  long long dy_stride, z_stride, dz_stride;
+  float* parts;                       // [chunks][cols], or null without a bias
+  int rows, cols, chunk, act;
+  const unsigned int* status;
+};
+
+struct LinearToken {
+  const __nv_bfloat16 *x, *w, *bias, *res;
+  __nv_bfloat16 *z, *out;
+  long long x_stride, w_stride, res_stride, z_stride, out_stride;
+  int tokens, n, k, act;
+  int ks;                             // warps that share a row's columns (set by the launcher)
+  const unsigned int* status;
+};
+
 // Launchers (defined next to their kernels).  Each returns a cudaError_t from
 // the launch; grid sizes come from the caller's SM count.
 // The prologue may be launched as a programmatic dependent of the kernel
@@ -341,12 +396,20 @@ cudaError_t launch_attention_dq(const AttentionMaps& m, AttentionLaunch l, cudaS
 cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int sms,
                                  cudaStream_t s);
 
+cudaError_t launch_linear(const LinearMaps& m, const LinearLaunch& l, int sms, cudaStream_t s);
+cudaError_t launch_linear_finish(const LinearLaunch& l, cudaStream_t s);
+cudaError_t launch_linear_dz(const LinearDz& d, cudaStream_t s);
+cudaError_t launch_linear_token(LinearToken p, int sms, cudaStream_t s);
+
 // Host services of muon_api.cu for the other entry points' files.
 // Runs `fn` (which launches one kernel), counting and tracing it.
 cudaError_t counted_launch(cudaStream_t st, int kind, double flops, double bytes,
                            const std::function<cudaError_t()>& fn);
 // Tensor map of bf16 heads (see AttentionMaps); false if the driver refuses it.
 bool heads_tmap(CUtensorMap* tm, const muon_heads& v, int tokens, int heads, int dim);
+// Tensor map of a bf16 matrix, 128-byte swizzle, boxes of box_cols x box_rows.
+bool matrix_tmap(CUtensorMap* tm, const muon_matrix& v, int rows, int cols, int box_cols,
+                 int box_rows);
 // SM count of the current device; MUON_ERR_UNSUPPORTED unless it is sm_103a.
 muon_status device_sms(int* sms);
 constexpr size_t kStatusBytes = 256;  // status block at the start of a workspace

@@ -868,6 +868,22 @@ bool heads_tmap(CUtensorMap* tm, const muon_heads& v, int tokens, int heads, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool matrix_tmap(CUtensorMap* tm, const muon_matrix& v, int rows, int cols, int box_cols,
+                 int box_rows) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), 1u};
+  const cuuint64_t row = static_cast<cuuint64_t>(v.row_stride) * 2;
+  const cuuint64_t strides[2] = {row, row};           // (one matrix: the last is unused)
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
+                             1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.data, dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 muon_status device_sms(int* sms) { return current_device(sms); }
 
 }  // namespace muon
