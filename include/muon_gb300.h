@@ -102,7 +102,16 @@ typedef enum muon_kernel_kind {
   MUON_K_LINEAR = 14,        /* products with a weight matrix                   */
   MUON_K_LINEAR_FINISH = 15, /* sums of a split product, its epilogue           */
   MUON_K_LINEAR_DZ = 16,     /* dz = dout act'(z), and the bias' gradient       */
-  MUON_K_LINEAR_TOKEN = 17   /* the product for up to 8 tokens                  */
+  MUON_K_LINEAR_TOKEN = 17,  /* the product for up to 8 tokens                  */
+  MUON_K_RMS_NORM = 18,      /* residual's addition and RMS norm                */
+  MUON_K_RMS_NORM_BWD = 19,  /* its gradients                                   */
+  MUON_K_RMS_NORM_WEIGHT = 20, /* the weight's gradient: sum of the blocks' parts */
+  MUON_K_EMBEDDING = 21,     /* rows of a token table                           */
+  MUON_K_EMBEDDING_SORT = 22, /* tokens sorted by id, the table's gradient cleared */
+  MUON_K_EMBEDDING_SUM = 23, /* sums of the runs of equal ids                   */
+  MUON_K_EMBEDDING_JOIN = 24, /* ... of those that several warps share          */
+  MUON_K_GRAD_SQUARES = 25,  /* sum of squares of the gradients                 */
+  MUON_K_CLIP = 26           /* their norm, and the clipped gradients           */
 } muon_kernel_kind;
 
 /* Workspace bytes for one muon_step()/muon_ns5() call on [batch, rows, cols].
@@ -417,6 +426,105 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
                                  muon_matrix weight, muon_matrix preact, muon_matrix dz,
                                  muon_matrix dx, muon_matrix dweight, void* dbias,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The residual's addition and the RMS norm of the sum, the input of a block's halves.
+ * ([PG] has the norm before each half; the pages print no code of it.)  Per token:
+ *   h = x + residual  (x where residual's data is NULL),
+ *   y = h (mean h^2 + eps)^-1/2 w   (w = 1 where weight is NULL),
+ * with x, residual, out (y) and sum (h) [tokens, dim] in one type.  h stays in fp32 for
+ * the norm and is rounded to be stored; y is rounded once.  sum is given where residual
+ * is.  out and sum may each be the very view of x or of residual (not of each other).
+ */
+typedef struct muon_rms_norm_spec {
+  int dtype;               /* muon_dtype of every muon_matrix of the call           */
+  int tokens;              /* 0..2^31 - 65537                                       */
+  int dim;                 /* multiple of 8, 8..16384                               */
+  float eps;               /* finite, >= 0                                          */
+  const float* weight;     /* [dim], 16-byte aligned, or NULL                       */
+} muon_rms_norm_spec;
+
+muon_status muon_rms_norm(const muon_rms_norm_spec* spec, muon_matrix x, muon_matrix residual,
+                          muon_matrix out, muon_matrix sum, void* stream);
+
+/*
+ * The same with y in 8 bits: y = scale q, q in e4m3 (out: bytes, rows 8-byte aligned),
+ * one scale a row (group = 0; scales [tokens]) or for each 128 columns (group = 128;
+ * scales [tokens, ceil(dim / 128)]).  A scale is the least power of two (from 2^-126 on)
+ * that brings the group's largest |y| to 448 or less, 1 where that is 0: e4m3's is the only
+ * rounding.  Where a y of the group is not finite its scale and all its q are NaN.
+ */
+muon_status muon_rms_norm_fp8(const muon_rms_norm_spec* spec, int group, muon_matrix x,
+                              muon_matrix residual, muon_matrix out, float* scales,
+                              muon_matrix sum, void* stream);
+
+/*
+ * Gradients of muon_rms_norm from dout (y's) and h as stored (sum; x without a
+ * residual).  With r = (mean h^2 + eps)^-1/2, n = h r, G = dout w:
+ *   dx = r (G - n mean(G n)) + dresidual,   dweight = sum over tokens of dout n
+ * dresidual: h's gradient from where else it went, or data NULL; dx is the gradient of x
+ * and of residual alike.  dx may be the very view of dout, sum or dresidual.  dweight
+ * ([dim] fp32, overwritten) is given where the weight is.  Fixed summation order:
+ * repeated calls give equal bits.
+ */
+size_t muon_rms_norm_workspace_bytes(int dim);
+muon_status muon_rms_norm_backward(const muon_rms_norm_spec* spec, muon_matrix dout,
+                                   muon_matrix sum, muon_matrix dresidual, muon_matrix dx,
+                                   float* dweight, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * The token embedding, the table that muon_adam_step trains:
+ *   out[t] = scale table[ids[t]]
+ * for table [rows, dim] and out [tokens, dim], each fp32 or bf16.  A token whose id is
+ * outside the table gets NaN.
+ */
+typedef struct muon_embedding_spec {
+  int tokens;              /* 0..2^31 - 65537                                       */
+  int rows;                /* 1..2^30                                               */
+  int dim;                 /* multiple of 8, 8..65536                               */
+  int id_bytes;            /* 4 (int32) or 8 (int64)                                */
+  const void* ids;         /* [tokens] device memory, aligned to id_bytes           */
+  float scale;             /* finite                                                */
+} muon_embedding_spec;
+
+muon_status muon_embedding(const muon_embedding_spec* spec, int table_dtype, muon_matrix table,
+                           int out_dtype, muon_matrix out, void* stream);
+
+/*
+ * The table's gradient: dtable[v] = scale times the sum of dout[t] over the tokens with
+ * ids[t] = v, in fp32 and rounded once; rows that no token names are 0.  Tokens whose id
+ * is outside the table enter no sum.  dout and dtable are fp32 or bf16 each.  Fixed
+ * summation order (tokens sorted by id), no atomics: repeated calls give equal bits.
+ */
+size_t muon_embedding_workspace_bytes(int tokens, int dim);
+muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dtype,
+                                    muon_matrix dout, int dtable_dtype, muon_matrix dtable,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The norm of all gradients of a model together, and the gradients clipped by it, in
+ * front of muon_step_grouped and muon_adam_step:
+ *   norm = (sum over all tensors and elements of g^2)^1/2
+ *   out  = g min(1, max_norm / (norm + eps))
+ * norm: one float on the device.  out may be the gradient itself (in one type), or a
+ * tensor of either type; with max_norm = INFINITY only the norm is computed and out is
+ * not used.  The arrays of different tensors must not overlap.  A norm that is NaN or
+ * infinite makes the factor NaN or 0, as the formula has it.  Squares are summed in fp32
+ * per thread: magnitudes from 2^64 on make the norm infinite, those below 2^-75 add
+ * nothing.  Fixed summation order: repeated calls give equal bits.
+ */
+typedef struct muon_grad_tensor {
+  const void* grad;        /* [numel] in g_dtype, 16-byte aligned                   */
+  void* out;               /* [numel] in out_dtype, 16-byte aligned                 */
+  long long numel;         /* >= 0; 0 skips the tensor (its pointers may be NULL)   */
+  int g_dtype, out_dtype;  /* muon_dtype                                            */
+} muon_grad_tensor;
+
+size_t muon_clip_workspace_bytes(int n_tensors);
+muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, float max_norm,
+                                float eps, float* norm, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 /*
  * Path selection (no counterpart on the pages).  With enable = 1 (the default)

@@ -14,7 +14,11 @@ Entry points mirror the C ABI:
   qk_norm_rope(q, k, cos, sin)   RMS norm and rotary positions of the query and key heads
   attention(q, k, v, cu_seqlens) causal attention over packed sequences, grouped heads
   linear(x, weight)              product with a weight matrix, bias, activation and residual
-with qk_norm_rope_backward, attention_backward and linear_backward for their gradients.
+  rms_norm(x, weight)            RMS norm with the residual's addition (rms_norm_fp8: in 8 bits)
+  embedding(ids, table)          rows of the token table
+  clip_grad_norm(grads, ...)     norm of all gradients together, and clipping
+with qk_norm_rope_backward, attention_backward, linear_backward, rms_norm_backward and
+embedding_backward for their gradients.
 """
 
 from __future__ import annotations
@@ -39,6 +43,9 @@ __all__ = [
     "ROPE_EPS", "rope_tables", "qk_norm_rope", "qk_norm_rope_backward",
     "norm_rope_workspace_bytes", "attention", "attention_backward", "attention_workspace_bytes",
     "ACTIVATIONS", "linear", "linear_backward", "linear_workspace_bytes",
+    "NORM_EPS", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "rms_norm_workspace_bytes",
+    "embedding", "embedding_backward", "embedding_workspace_bytes",
+    "CLIP_EPS", "ClipGradNorm", "clip_grad_norm", "grad_norm",
 ]
 
 # Quintic coefficients and rounds as printed in "Muon Custom Sizing 实战", section 2.3.
@@ -54,7 +61,10 @@ ADAM_EPS = 1e-8
 KERNEL_KINDS = {0: "prologue", 1: "small_ns", 2: "gram", 3: "poly", 4: "update", 5: "apply",
                 6: "adam", 7: "fused_ns", 8: "rounds", 9: "norm_rope", 10: "norm_rope_backward",
                 11: "attention", 12: "attention_dq", 13: "attention_dkv", 14: "linear",
-                15: "linear_finish", 16: "linear_dz", 17: "linear_token"}
+                15: "linear_finish", 16: "linear_dz", 17: "linear_token", 18: "rms_norm",
+                19: "rms_norm_backward", 20: "rms_norm_weight", 21: "embedding",
+                22: "embedding_sort", 23: "embedding_sum", 24: "embedding_join",
+                25: "grad_squares", 26: "clip"}
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "timeout",
            5: "workspace"}
 
@@ -116,6 +126,22 @@ class _LinearSpec(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
+class _RmsNormSpec(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("tokens", ctypes.c_int), ("dim", ctypes.c_int),
+                ("eps", ctypes.c_float), ("weight", ctypes.c_void_p)]
+
+
+class _EmbeddingSpec(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("rows", ctypes.c_int), ("dim", ctypes.c_int),
+                ("id_bytes", ctypes.c_int), ("ids", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("numel", ctypes.c_longlong), ("g_dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int)]
+
+
 class _TraceRecord(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("round", ctypes.c_int), ("ms", ctypes.c_float),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -174,6 +200,25 @@ def load_library():
     L.muon_linear.restype = ci
     L.muon_linear_backward.argtypes = [lin, mat, mat, mat, mat, mat, mat, mat, vp, vp, sz, vp]
     L.muon_linear_backward.restype = ci
+    norm, emb = ctypes.POINTER(_RmsNormSpec), ctypes.POINTER(_EmbeddingSpec)
+    L.muon_rms_norm.argtypes = [norm, mat, mat, mat, mat, vp]
+    L.muon_rms_norm.restype = ci
+    L.muon_rms_norm_fp8.argtypes = [norm, ci, mat, mat, mat, vp, mat, vp]
+    L.muon_rms_norm_fp8.restype = ci
+    L.muon_rms_norm_workspace_bytes.argtypes = [ci]
+    L.muon_rms_norm_workspace_bytes.restype = sz
+    L.muon_rms_norm_backward.argtypes = [norm, mat, mat, mat, mat, vp, vp, sz, vp]
+    L.muon_rms_norm_backward.restype = ci
+    L.muon_embedding.argtypes = [emb, ci, mat, ci, mat, vp]
+    L.muon_embedding.restype = ci
+    L.muon_embedding_workspace_bytes.argtypes = [ci, ci]
+    L.muon_embedding_workspace_bytes.restype = sz
+    L.muon_embedding_backward.argtypes = [emb, ci, mat, ci, mat, vp, sz, vp]
+    L.muon_embedding_backward.restype = ci
+    L.muon_clip_workspace_bytes.argtypes = [ci]
+    L.muon_clip_workspace_bytes.restype = sz
+    L.muon_clip_grad_norm.argtypes = [ctypes.POINTER(_GradTensor), ci, cf, cf, vp, vp, sz, vp]
+    L.muon_clip_grad_norm.restype = ci
     L.muon_set_persistent_rounds.argtypes = [ci]
     L.muon_set_persistent_rounds.restype = ci
     L.muon_set_fused_ns.argtypes = [ci]
@@ -916,6 +961,275 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
                                   None if dbias is None else dbias.data_ptr(), ws, ws_bytes,
                                   handle), "muon_linear_backward")
     return dx, dweight, dbias
+
+
+NORM_EPS = 1e-6
+
+
+def _norm_spec(x, name, weight, eps):
+    """The spec of a call and its view of x."""
+    _cuda_device(x, name)
+    dtype, index = x.dtype, x.get_device()
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    vx = _matrix(x, name, x.shape, dtype, index)
+    t, d = x.shape
+    return _RmsNormSpec(1 if dtype is torch.bfloat16 else 0, t, d, eps,
+                        _ptr(weight, "weight", index, torch.float32, (d,))), vx
+
+
+def _refuse_norm_grad(where, x, weight, residual):
+    if torch.is_grad_enabled() and (x.requires_grad or (
+            weight is not None and weight.requires_grad) or (
+            residual is not None and residual.requires_grad)):
+        _refuse_grad(where, x=x, weight=weight, residual=residual)
+
+
+def rms_norm(x, weight=None, *, residual=None, eps: float = NORM_EPS, out=None,
+             residual_out=None, stream=None):
+    """RMS norm of h = x + residual (of x, without a residual) along the rows of x [tokens, dim]
+    (bf16 or fp32, strided along the tokens; dim a multiple of 8 up to 16384), times weight ([dim]
+    fp32).  Returns (out, h): h, rounded to x's type, is the next residual and what
+    rms_norm_backward takes; without a residual it is x itself.  out and residual_out (h's tensor)
+    may each be x or residual.  Nothing is recorded for autograd: tensors that require grad are
+    refused while it records, see rms_norm_backward."""
+    L = _lib or load_library()
+    spec, vx = _norm_spec(x, "x", weight, eps)
+    _refuse_norm_grad("rms_norm", x, weight, residual)
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    if stream is not None or index != _current_device():
+        with _launch_on(x.device, stream):
+            return rms_norm(x, weight, residual=residual, eps=eps, out=out,
+                            residual_out=residual_out)
+    vr = vh = _NO_MATRIX
+    h = x
+    if residual is not None:
+        vr = _matrix(residual, "residual", shape, dtype, index)
+        h, vh = _out_matrix(residual_out, "residual_out", shape, dtype, index)
+    elif residual_out is not None:
+        raise ValueError("residual_out is the sum with a residual, and there is none")
+    out, vo = _out_matrix(out, "out", shape, dtype, index)
+    _raise(L.muon_rms_norm(spec, vx, vr, vo, vh, _current_handle(index)), "muon_rms_norm")
+    return out, h
+
+
+def rms_norm_fp8(x, weight=None, *, residual=None, eps: float = NORM_EPS, group: int = 128,
+                 out=None, scales=None, residual_out=None, stream=None):
+    """rms_norm with its output in 8 bits: returns (out, scales, h), out [tokens, dim]
+    float8_e4m3fn, scales fp32 [tokens, 1] (group = 0: one a row) or [tokens, ceil(dim / 128)]
+    (group = 128: one for each 128 columns).  The values are scale * out.  A scale is the least
+    power of two that brings its group's largest magnitude to 448 or less; a group with a value
+    that is not finite reads as NaN."""
+    L = _lib or load_library()
+    spec, vx = _norm_spec(x, "x", weight, eps)
+    _refuse_norm_grad("rms_norm_fp8", x, weight, residual)
+    if group not in (0, 128):
+        raise ValueError(f"group must be 0 (a scale a row) or 128 columns, got {group}")
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    if stream is not None or index != _current_device():
+        with _launch_on(x.device, stream):
+            return rms_norm_fp8(x, weight, residual=residual, eps=eps, group=group, out=out,
+                                scales=scales, residual_out=residual_out)
+    vr = vh = _NO_MATRIX
+    h = x
+    if residual is not None:
+        vr = _matrix(residual, "residual", shape, dtype, index)
+        h, vh = _out_matrix(residual_out, "residual_out", shape, dtype, index)
+    elif residual_out is not None:
+        raise ValueError("residual_out is the sum with a residual, and there is none")
+    t, d = shape
+    s_shape = (t, 1 if group == 0 else -(-d // group))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    vo = _matrix(out, "out", shape, torch.float8_e4m3fn, index)
+    if scales is None:
+        scales = torch.empty(s_shape, dtype=torch.float32, device=x.device)
+    p_scales = _ptr(scales, "scales", index, torch.float32, s_shape)
+    _raise(L.muon_rms_norm_fp8(spec, group, vx, vr, vo, p_scales, vh, _current_handle(index)),
+           "muon_rms_norm_fp8")
+    return out, scales, h
+
+
+@functools.lru_cache(maxsize=256)
+def rms_norm_workspace_bytes(dim: int) -> int:
+    return int(load_library().muon_rms_norm_workspace_bytes(dim))
+
+
+def rms_norm_backward(dout, h, weight=None, *, dresidual=None, eps: float = NORM_EPS, dx=None,
+                      workspace: Workspace | None = None, stream=None):
+    """Gradients of rms_norm: from dout and the h that it returned (and the gradient of h from
+    where else it went, dresidual), returns (dx, dweight).  dx is the gradient of x and of residual
+    alike; dweight is fp32, None without a weight.  dx may be dout, h or dresidual itself."""
+    L = _lib or load_library()
+    spec, vh = _norm_spec(h, "h", weight, eps)
+    index, dtype, shape = h.get_device(), h.dtype, h.shape
+    if stream is not None or index != _current_device():
+        with _launch_on(h.device, stream):
+            return rms_norm_backward(dout, h, weight, dresidual=dresidual, eps=eps, dx=dx,
+                                     workspace=workspace)
+    vg = _matrix(dout, "dout", shape, dtype, index)
+    vr = _NO_MATRIX if dresidual is None else _matrix(dresidual, "dresidual", shape, dtype, index)
+    dx, vdx = _out_matrix(dx, "dx", shape, dtype, index)
+    dweight = None if weight is None else torch.empty_like(weight)
+    handle = _current_handle(index)
+    ws, ws_bytes, _owner = _stream_workspace(workspace, rms_norm_workspace_bytes(spec.dim), index,
+                                             handle)
+    _raise(L.muon_rms_norm_backward(spec, vg, vh, vr, vdx,
+                                    None if dweight is None else dweight.data_ptr(), ws, ws_bytes,
+                                    handle), "muon_rms_norm_backward")
+    return dx, dweight
+
+
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _embedding_spec(ids, rows, dim, scale):
+    _cuda_device(ids, "ids")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous [tokens], got {tuple(ids.shape)}")
+    return _EmbeddingSpec(ids.shape[0], rows, dim, ids.element_size(), ids.data_ptr(), scale)
+
+
+def _float_dtype(dtype, name):
+    if dtype not in _FLOATS:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _FLOATS[dtype]
+
+
+def embedding(ids, table, *, scale: float = 1.0, dtype=torch.bfloat16, out=None, stream=None):
+    """scale * table[ids] for ids [tokens] (int32 or int64) and table [rows, dim] (fp32 or bf16,
+    strided along the rows; dim a multiple of 8), rounded once to `dtype` (out's, where it is
+    given).  An id outside the table gives a row of NaN.  Nothing is recorded for autograd: a table
+    that requires grad is refused while it records, see embedding_backward."""
+    L = _lib or load_library()
+    _cuda_device(table, "table")
+    index, kind = table.get_device(), _float_dtype(table.dtype, "table")
+    vt = _matrix(table, "table", table.shape, table.dtype, index)
+    rows, dim = table.shape
+    spec = _embedding_spec(ids, rows, dim, scale)
+    if ids.get_device() != index:
+        raise ValueError(f"ids must be on {table.device}, got {ids.device}")
+    if table.requires_grad and torch.is_grad_enabled():
+        _refuse_grad("embedding", table=table)
+    if stream is not None or index != _current_device():
+        with _launch_on(table.device, stream):
+            return embedding(ids, table, scale=scale, dtype=dtype, out=out)
+    if out is not None:
+        dtype = out.dtype
+    out_kind = _float_dtype(dtype, "out")
+    out, vo = _out_matrix(out, "out", (spec.tokens, dim), dtype, index)
+    _raise(L.muon_embedding(spec, kind, vt, out_kind, vo, _current_handle(index)),
+           "muon_embedding")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def embedding_workspace_bytes(tokens: int, dim: int) -> int:
+    return int(load_library().muon_embedding_workspace_bytes(tokens, dim))
+
+
+def embedding_backward(dout, ids, rows: int, *, scale: float = 1.0, dtype=torch.float32, out=None,
+                       workspace: Workspace | None = None, stream=None):
+    """Gradient of embedding's table: [rows, dim] in `dtype` (fp32 or bf16; out's, where it is
+    given) from dout [tokens, dim] (fp32 or bf16).  Every row is written, those that no token names
+    with zeros; ids outside the table enter no sum.  Sums in fp32 in a fixed order."""
+    L = _lib or load_library()
+    _cuda_device(dout, "dout")
+    index, kind = dout.get_device(), _float_dtype(dout.dtype, "dout")
+    vg = _matrix(dout, "dout", dout.shape, dout.dtype, index)
+    t, dim = dout.shape
+    spec = _embedding_spec(ids, rows, dim, scale)
+    if spec.tokens != t:
+        raise ValueError(f"ids must be [{t}], got {tuple(ids.shape)}")
+    if ids.get_device() != index:
+        raise ValueError(f"ids must be on {dout.device}, got {ids.device}")
+    if stream is not None or index != _current_device():
+        with _launch_on(dout.device, stream):
+            return embedding_backward(dout, ids, rows, scale=scale, dtype=dtype, out=out,
+                                      workspace=workspace)
+    if out is not None:
+        dtype = out.dtype
+    out_kind = _float_dtype(dtype, "out")
+    out, vo = _out_matrix(out, "out", (rows, dim), dtype, index)
+    handle = _current_handle(index)
+    ws, ws_bytes, _owner = _stream_workspace(workspace, embedding_workspace_bytes(t, dim), index,
+                                             handle)
+    _raise(L.muon_embedding_backward(spec, kind, vg, out_kind, vo, ws, ws_bytes, handle),
+           "muon_embedding_backward")
+    return out
+
+
+CLIP_EPS = 1e-6
+
+
+class ClipGradNorm:
+    """A prepared clip_grad_norm call: the table of the tensors is marshalled once.  Calling it
+    enqueues the norm and the clipping on the current (or given) stream and returns the norm, a
+    new fp32 scalar on the device.  The tensors must stay alive and in place between calls."""
+
+    def __init__(self, grads, max_norm: float, *, outs=None, eps: float = CLIP_EPS,
+                 workspace: Workspace | None = None):
+        self._grads = list(grads)
+        self._outs = self._grads if outs is None else list(outs)
+        if not self._grads:
+            raise ValueError("there are no gradients")
+        if len(self._outs) != len(self._grads):
+            raise ValueError(f"outs must be one for each gradient: {len(self._outs)} for "
+                             f"{len(self._grads)}")
+        self._n = len(self._grads)
+        self._arr = (_GradTensor * self._n)()
+        self._device = self._grads[0].device
+        spans = []
+        for i, (g, o) in enumerate(zip(self._grads, self._outs)):
+            for t, name in ((g, "gradient"), (o, "out")):
+                if not t.is_cuda or not t.is_contiguous():
+                    raise ValueError(f"{name} {i} must be a contiguous CUDA tensor")
+                if t.device != self._device:
+                    raise ValueError(f"{name} {i} must be on {self._device}, got {t.device}")
+            if o.numel() != g.numel():
+                raise ValueError(f"out {i} must have {g.numel()} elements, got {o.numel()}")
+            a = self._arr[i]
+            a.grad, a.out, a.numel = g.data_ptr(), o.data_ptr(), g.numel()
+            a.g_dtype, a.out_dtype = _gdt(g), _gdt(o)
+            if g.numel():
+                same = a.grad == a.out and a.g_dtype == a.out_dtype
+                spans.append((a.grad, a.grad + g.numel() * g.element_size()))
+                if not same:
+                    spans.append((a.out, a.out + o.numel() * o.element_size()))
+        spans.sort()
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("gradients and outs must not overlap (an out may be its gradient)")
+        self._scalars = (float(max_norm), float(eps))
+        self._ws = workspace
+        self._need = int(load_library().muon_clip_workspace_bytes(self._n))
+
+    def __call__(self, stream=None):
+        index = self._device.index
+        if stream is not None or index != _current_device():
+            with _launch_on(self._device, stream):
+                return self()
+        norm = torch.empty((), dtype=torch.float32, device=self._device)
+        handle = _current_handle(index)
+        ws, ws_bytes, _owner = _stream_workspace(self._ws, self._need, index, handle)
+        _raise(load_library().muon_clip_grad_norm(self._arr, self._n, *self._scalars,
+                                                  norm.data_ptr(), ws, ws_bytes, handle),
+               "muon_clip_grad_norm")
+        return norm
+
+
+def clip_grad_norm(grads, max_norm: float, *, outs=None, eps: float = CLIP_EPS,
+                   workspace: Workspace | None = None, stream=None):
+    """The norm of all gradients together (contiguous fp32 or bf16 tensors of any shapes), and the
+    gradients times min(1, max_norm / (norm + eps)): in place, or into `outs`, which may be of
+    either type.  Returns the norm, an fp32 scalar on the device."""
+    return ClipGradNorm(grads, max_norm, outs=outs, eps=eps, workspace=workspace)(stream)
+
+
+def grad_norm(grads, *, workspace: Workspace | None = None, stream=None):
+    """The norm of all gradients together, an fp32 scalar on the device; they stay as they are."""
+    return ClipGradNorm(grads, math.inf, workspace=workspace)(stream)
 
 
 def workspace_status(workspace: Workspace | None, clear: bool = False, stream=None) -> int:

@@ -1,0 +1,448 @@
+// embedding.cu -- rows of a token table, scaled, and the table's gradient
+//
+//   out[t] = scale table[id_t],     d table[v] = scale sum over {t : id_t = v} of dout[t]
+//
+// The lookup is one read and one write of each token's row.  The gradient writes every row
+// of the table, zeros too, and reads dout once; each row's sum has a fixed order, by tokens
+// sorted by id (stable, so ascending in a row):
+//
+//   embedding_sort_kernel   one cluster of 8 CTAs sorts the tokens (radix, up to 10 bits a
+//                           pass) while the other CTAs of the launch clear the gradient: the
+//                           sort has 8 SMs' worth of work, the clearing is bound by HBM
+//   embedding_sum_kernel    a warp takes 32 sorted positions and 256 columns, adds the rows
+//                           of a run of equal ids in registers and stores the run; what
+//                           begins or ends outside of the 32 goes to the workspace
+//   embedding_join_kernel   runs that cross a border: their pieces, in order
+//
+// Runs are cut by position, not by id, so that a token that makes up a tenth of a text is
+// shared by many warps.  Rows that a run fills are written twice (cleared, then stored); they
+// are few against the table, and still in L2.
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void unpack(const uint4& a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  unpack(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// -1 for an id outside the table.
+__device__ __forceinline__ int id_at(const void* ids, bool wide, int t, int rows) {
+  const long long v = wide ? __ldg(static_cast<const long long*>(ids) + t)
+                           : static_cast<long long>(__ldg(static_cast<const int*>(ids) + t));
+  return v >= 0 && v < rows ? static_cast<int>(v) : -1;
+}
+
+// ------------------------------------------------------------ lookup
+// A warp takes a token's row, kAt vectors a lane in flight; the next token's id travels
+// with them.
+constexpr int kAt = 4;
+template <typename T, typename O>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ EmbeddingLaunch L) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int stride = gridDim.x * (kThreads / 32);
+  const int vecs = L.dim >> 3;
+  int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  int id = t < L.tokens ? id_at(L.ids, L.wide, t, L.rows) : -1;
+  for (; t < L.tokens; t += stride) {
+    const int next = t + stride < L.tokens ? id_at(L.ids, L.wide, t + stride, L.rows) : -1;
+    const T* const row = static_cast<const T*>(L.table) + max(id, 0) * L.table_stride;
+    O* const out = static_cast<O*>(L.out) + t * L.out_stride;
+    const float scale = id < 0 ? __int_as_float(0x7fffffff) : L.scale;
+    for (int c = lane; c < vecs; c += 32 * kAt) {
+      float v[kAt][8];
+#pragma unroll
+      for (int i = 0; i < kAt; ++i)
+        if (c + 32 * i < vecs) load8(row + 8 * (c + 32 * i), v[i]);
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        if (c + 32 * i >= vecs) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= scale;
+        store8(out + 8 * (c + 32 * i), v[i]);
+      }
+    }
+    id = next;
+  }
+}
+
+// ------------------------------------------------------------ sort, and zeros
+constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kMaxBins = 1024;
+constexpr int kSortSmem = (kSortWarps * kMaxBins + 2 * kMaxBins + 64) * 4;
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Sorts (id, token) by `passes` digits of `bits` bits, least first; ids outside the table sort
+// behind the last row.  CTA r has the r-th contiguous part of the items, a warp a contiguous
+// part of it, and each pass keeps equal digits in order: counts a warp, a digit's place from
+// the counts of smaller digits, earlier CTAs and earlier warps, and its rank among the lanes.
+__device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
+  uint32_t* const cnt = smem;                              // [warps][bins]
+  uint32_t* const total = smem + kSortWarps * kMaxBins;    // [bins], read by the other CTAs
+  uint32_t* const base = total + kMaxBins;                 // [bins]
+  uint32_t* const scan = base + kMaxBins;                  // [warps]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int bins = 1 << L.bits;
+  // whole rounds of 32 a warp
+  const int per_warp = ((L.tokens + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
+  const long long begin = (static_cast<long long>(rank) * kSortWarps + warp) * per_warp;
+  const int i0 = static_cast<int>(min(begin, static_cast<long long>(L.tokens)));
+  const int i1 = static_cast<int>(min(begin + per_warp, static_cast<long long>(L.tokens)));
+  uint32_t* const mine = cnt + warp * kMaxBins;
+  for (int pass = 0; pass < L.passes; ++pass) {
+    // the last pass ends in keys / order [0]
+    const int to = (L.passes - 1 - pass) & 1, from = to ^ 1;
+    const int shift = pass * L.bits;
+    auto key_at = [&](int i) -> uint32_t {
+      if (pass > 0) return __ldcg(L.keys[from] + i);
+      const int id = id_at(L.ids, L.wide, i, L.rows);
+      return id < 0 ? static_cast<uint32_t>(L.rows) : static_cast<uint32_t>(id);
+    };
+    for (int b = lane; b < bins; b += 32) mine[b] = 0u;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const bool live = i < i1;
+      const uint32_t d = live ? (key_at(i) >> shift) & (bins - 1) : 0xffffffffu;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      if (live && (__ffs(same) - 1) == lane) mine[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // a thread a digit: places of the warps, the CTA's total
+    if (tid < bins) {
+      uint32_t run = 0u;
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = cnt[w * kMaxBins + tid];
+        cnt[w * kMaxBins + tid] = run;
+        run += n;
+      }
+      total[tid] = run;
+    }
+    ptx::cluster_sync();
+    uint32_t before = 0u, all = 0u;
+    if (tid < bins) {
+      const uint32_t at = ptx::smem_u32(total + tid);
+#pragma unroll
+      for (uint32_t r = 0; r < kSortCtas; ++r) {
+        const uint32_t n = ld_cluster_u32(ptx::mapa_shared(at, r));
+        if (r < rank) before += n;
+        all += n;
+      }
+    }
+    // exclusive scan of the digits' totals over the block
+    uint32_t x = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      const uint32_t own = scan[lane];
+      uint32_t y = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      scan[lane] = y - own;
+    }
+    __syncthreads();
+    if (tid < bins) base[tid] = scan[warp] + x - all + before;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+      const bool live = i < i1;
+      const uint32_t key = live ? key_at(i) : 0u;
+      const uint32_t token = live && pass > 0 ? __ldcg(L.order[from] + i) : static_cast<uint32_t>(i);
+      const uint32_t d = live ? (key >> shift) & (bins - 1) : 0xffffffffu;
+      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      uint32_t at = 0u;
+      if (live) at = base[d] + mine[d] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (live && (__ffs(same) - 1) == lane) mine[d] += __popc(same);
+      __syncwarp();
+      if (live) {
+        __stcg(L.keys[to] + at, key);
+        __stcg(L.order[to] + at, token);
+      }
+    }
+    // the other CTAs' stores of this pass are read by the next, and `total` is free again
+    __threadfence();
+    ptx::cluster_sync();
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1)
+    embedding_sort_kernel(const __grid_constant__ EmbeddingLaunch L) {
+  extern __shared__ uint32_t s_sort[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (ptx::status_set(L.status)) return;      // (the same word for every CTA of the cluster)
+  if (blockIdx.x < kSortCtas) {
+    sort_tokens(L, s_sort);
+    return;
+  }
+  // zeros, 16 bytes a store
+  const int unit = L.out_bf16 ? 8 : 4;                    // elements
+  const long long size = L.out_bf16 ? 2 : 4;
+  const long long per_row = L.dim / unit;
+  const long long total = per_row * L.rows;
+  const long long step = static_cast<long long>(gridDim.x - kSortCtas) * kSortThreads;
+  uint8_t* const out = static_cast<uint8_t*>(L.out);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  long long i = static_cast<long long>(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
+  if (L.out_stride == L.dim) {
+    for (; i < total; i += step) *reinterpret_cast<uint4*>(out + i * 16) = zero;
+  } else {
+    for (; i < total; i += step) {
+      const long long r = i / per_row;
+      *reinterpret_cast<uint4*>(out + (r * L.out_stride + (i - r * per_row) * unit) * size) = zero;
+    }
+  }
+}
+
+// ------------------------------------------------------------ sums
+// Whether the sorted positions i and i + 1 hold one id; positions outside hold none.
+__device__ __forceinline__ bool joined(const uint32_t* keys, int i, int tokens) {
+  return i >= 0 && i + 1 < tokens && __ldcg(keys + i) == __ldcg(keys + i + 1);
+}
+
+template <typename O>
+__device__ __forceinline__ void store_row(const EmbeddingLaunch& L, uint32_t id, int c,
+                                          float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= L.scale;
+  store8(static_cast<O*>(L.out) + id * L.out_stride + c, v);
+}
+
+constexpr int kChunk = 32;             // sorted positions of a warp
+constexpr int kFlight = 8;             // rows of a warp in flight
+template <typename G, typename O>
+__global__ void __launch_bounds__(kThreads)
+    embedding_sum_kernel(const __grid_constant__ EmbeddingLaunch L) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (ptx::status_set(L.status)) return;
+  const int lane = threadIdx.x & 31;
+  const int groups = (L.dim + 255) / 256;
+  const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = static_cast<int>(task / groups);
+  const int c = static_cast<int>(task - static_cast<long long>(chunk) * groups) * 256 + lane * 8;
+  const int i0 = chunk * kChunk;
+  if (i0 >= L.tokens) return;
+  const int n = min(kChunk, L.tokens - i0);
+  const uint32_t key = lane < n ? __ldcg(L.keys[0] + i0 + lane) : 0xffffffffu;
+  const uint32_t token = lane < n ? __ldcg(L.order[0] + i0 + lane) : 0u;
+  // bit i: a run begins at position i; the run at position 0 may have begun earlier
+  const uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
+  const bool head_open = joined(L.keys[0], i0 - 1, L.tokens);
+  const bool tail_open = joined(L.keys[0], i0 + kChunk - 1, L.tokens);
+  const uint32_t begins = __ballot_sync(0xffffffffu, lane < n && (lane == 0 || key != prev));
+  const bool on = c < L.dim;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  int begin = 0;
+  for (int p = 0; p < n; p += kFlight) {
+    float v[kFlight][8];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const uint32_t t = __shfl_sync(0xffffffffu, token, (p + k) & 31);
+      const uint32_t id = __shfl_sync(0xffffffffu, key, (p + k) & 31);
+      // (rows of ids outside the table are not read)
+      if (on && p + k < n && id < static_cast<uint32_t>(L.rows)) {
+        load8(static_cast<const G*>(L.dout) + t * L.dout_stride + c, v[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int i = p + k;
+      if (i >= n) break;
+      if (begins >> i & 1u) {
+        begin = i;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+      if (i + 1 < n && !(begins >> (i + 1) & 1u)) continue;   // the run goes on in this chunk
+      const uint32_t id = __shfl_sync(0xffffffffu, key, i);
+      if (!on || id >= static_cast<uint32_t>(L.rows)) continue;
+      const bool from_before = begin == 0 && head_open;
+      const bool goes_on = i + 1 == n && tail_open;
+      if (from_before || goes_on) {
+        // [chunk][0]: of a run that began earlier; [1]: of one that begins here
+        store8(L.parts + (static_cast<size_t>(chunk) * 2 + (from_before ? 0 : 1)) * L.dim + c, acc);
+      } else {
+        store_row<O>(L, id, c, acc);
+      }
+    }
+  }
+}
+
+// A run that begins in a chunk and goes on: its piece there, then those of the chunks after.
+template <typename O>
+__global__ void __launch_bounds__(kThreads)
+    embedding_join_kernel(const __grid_constant__ EmbeddingLaunch L) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  if (ptx::status_set(L.status)) return;
+  const int lane = threadIdx.x & 31;
+  const int groups = (L.dim + 255) / 256;
+  const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = static_cast<int>(task / groups);
+  const int c = static_cast<int>(task - static_cast<long long>(chunk) * groups) * 256 + lane * 8;
+  const int last = chunk * kChunk + kChunk - 1;            // last position of the chunk
+  if (!joined(L.keys[0], last, L.tokens)) return;
+  const uint32_t id = __ldcg(L.keys[0] + last);
+  if (id >= static_cast<uint32_t>(L.rows)) return;
+  const int first = chunk * kChunk;
+  if (first > 0 && __ldcg(L.keys[0] + first - 1) == id) return;   // it began earlier
+  // chunks after this one that the run reaches: all up to the first that it does not fill
+  int reach = 1;
+  for (int k = chunk + 1;; k += 32) {
+    const long long end = (static_cast<long long>(k) + lane) * kChunk + kChunk - 1;
+    const bool through = end + 1 < L.tokens && __ldcg(L.keys[0] + end) == id &&
+                         __ldcg(L.keys[0] + end + 1) == id;
+    const uint32_t stop = __ballot_sync(0xffffffffu, !through);
+    if (stop != 0u) {
+      reach = k - chunk + __ffs(stop) - 1;
+      break;
+    }
+  }
+  if (c >= L.dim) return;
+  float acc[8];
+  load8(L.parts + (static_cast<size_t>(chunk) * 2 + 1) * L.dim + c, acc);
+  const float* p = L.parts + static_cast<size_t>(chunk + 1) * 2 * L.dim + c;
+#pragma unroll 4
+  for (int k = 0; k < reach; ++k) {
+    float v[8];
+    load8(p + static_cast<size_t>(k) * 2 * L.dim, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += v[j];
+  }
+  store_row<O>(L, id, c, acc);
+}
+
+// ------------------------------------------------------------ launchers
+template <typename K>
+cudaError_t launch_dependent(K kernel, long long blocks, int threads, int smem, int cluster,
+                             cudaStream_t s, const EmbeddingLaunch& l) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, l);
+}
+
+long long warp_tasks(const EmbeddingLaunch& l) {
+  return 1ll * ((l.tokens + kChunk - 1) / kChunk) * ((l.dim + 255) / 256);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const EmbeddingLaunch& l, bool table_bf16, int sms, cudaStream_t s) {
+  constexpr int kPer = kThreads / 32;
+  const long long blocks = std::min<long long>((1ll * l.tokens + kPer - 1) / kPer, 8ll * sms);
+  using B = __nv_bfloat16;
+  if (table_bf16)
+    return l.out_bf16 ? launch_dependent(embedding_kernel<B, B>, blocks, kThreads, 0, 1, s, l)
+                      : launch_dependent(embedding_kernel<B, float>, blocks, kThreads, 0, 1, s, l);
+  return l.out_bf16 ? launch_dependent(embedding_kernel<float, B>, blocks, kThreads, 0, 1, s, l)
+                    : launch_dependent(embedding_kernel<float, float>, blocks, kThreads, 0, 1, s, l);
+}
+
+cudaError_t launch_embedding_sort(EmbeddingLaunch l, int sms, cudaStream_t s) {
+  // passes of at most 10 bits that cover 0..rows (rows itself: outside the table)
+  int bits = 1;
+  while (bits < 31 && (l.rows >> bits) != 0) ++bits;
+  l.passes = (bits + 9) / 10;
+  l.bits = (bits + l.passes - 1) / l.passes;
+  const cudaError_t e = cudaFuncSetAttribute(
+      embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (e != cudaSuccess) return e;
+  // the sort's cluster, and clusters that clear: one CTA an SM, at least one
+  const long long bytes = 1ll * l.rows * l.dim * (l.out_bf16 ? 2 : 4);
+  const long long want = bytes / (kSortCtas * kSortThreads * 64) + 1;
+  const long long clear = std::max(1ll, std::min<long long>(sms / kSortCtas - 1, want));
+  return launch_dependent(embedding_sort_kernel, kSortCtas * (1 + clear), kSortThreads, kSortSmem,
+                          kSortCtas, s, l);
+}
+
+cudaError_t launch_embedding_sum(const EmbeddingLaunch& l, bool dout_bf16, cudaStream_t s) {
+  const long long blocks = (warp_tasks(l) + kThreads / 32 - 1) / (kThreads / 32);
+  using B = __nv_bfloat16;
+  auto go = [&](auto kernel) { return launch_dependent(kernel, blocks, kThreads, 0, 1, s, l); };
+  if (dout_bf16)
+    return l.out_bf16 ? go(embedding_sum_kernel<B, B>) : go(embedding_sum_kernel<B, float>);
+  return l.out_bf16 ? go(embedding_sum_kernel<float, B>) : go(embedding_sum_kernel<float, float>);
+}
+
+cudaError_t launch_embedding_join(const EmbeddingLaunch& l, cudaStream_t s) {
+  const long long blocks = (warp_tasks(l) + kThreads / 32 - 1) / (kThreads / 32);
+  return l.out_bf16
+             ? launch_dependent(embedding_join_kernel<__nv_bfloat16>, blocks, kThreads, 0, 1, s, l)
+             : launch_dependent(embedding_join_kernel<float>, blocks, kThreads, 0, 1, s, l);
+}
+
+size_t embedding_parts(int tokens, int dim) {
+  const size_t chunks = (static_cast<size_t>(tokens) + kChunk - 1) / kChunk;
+  return chunks > 1 ? chunks * 2 * dim : 0;
+}
+
+}  // namespace muon

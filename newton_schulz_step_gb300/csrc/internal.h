@@ -365,6 +365,63 @@ struct LinearToken {
   const unsigned int* status;
 };
 
+// ---- RMS norm with the residual's addition (rms_norm.cu, block_api.cu)
+constexpr int kRmsNormMaxDim = 16384;
+constexpr int kRmsNormMaxBlocks = 608;   // parts of the weight's gradient
+
+struct RmsNormLaunch {
+  const void *x, *dy, *res;         // backward: x is the sum as stored, res the sum's gradient
+  void *y, *sum;                    // backward: y is dx
+  const float* w;
+  float* scales;                    // 8 bits: [tokens][groups]
+  float* parts;                     // backward: [blocks][dim], or null without a weight
+  long long x_stride, dy_stride, res_stride, y_stride, sum_stride;   // y in 8 bits: bytes
+  int tokens, dim;
+  int team;                         // threads of a row (set by the launcher)
+  int group, groups;                // 8 bits: columns that share a scale (0: the row), their number
+  float eps;
+  const unsigned int* status;
+};
+
+// ---- embedding (embedding.cu, block_api.cu)
+struct EmbeddingLaunch {
+  const void *ids, *table, *dout;
+  void* out;                        // backward: the table's gradient
+  uint32_t *keys[2], *order[2];     // backward: ids and tokens, sorted ones in [0]
+  float* parts;                     // backward: [chunks][2][dim] pieces of runs
+  long long table_stride, dout_stride, out_stride;
+  int wide;                         // ids are int64
+  int tokens, rows, dim, out_bf16;
+  int bits, passes;                 // digits of the sort (set by the launcher)
+  float scale;
+  const unsigned int* status;
+};
+
+// ---- norm of all gradients, clipping (clip.cu, block_api.cu)
+constexpr int kClipUnit = 8192;        // elements per work unit
+constexpr int kMaxClipTensors = 64;    // tensors per launch
+constexpr int kClipBlocks = 608;       // parts of the sum of squares a launch, at most
+
+struct ClipTensor {
+  const void* g;
+  void* out;
+  long long n;                      // elements
+  long long unit_begin;             // first unit of this tensor in the launch
+  int g_bf16, out_bf16;
+};
+
+struct ClipLaunch {
+  ClipTensor t[kMaxClipTensors];
+  int n_tensors;
+  long long total_units;
+  double* parts;                    // [n_parts], the launches' parts one after the other
+  int part_begin, n_parts;          // this launch's first part; all launches' number
+  float* norm;                      // written by the first launch of the second pass, or null
+  float max_norm, eps;
+  int in_place;                     // every output is its gradient: nothing to do at factor 1
+  const unsigned int* status;
+};
+
 // Launchers (defined next to their kernels).  Each returns a cudaError_t from
 // the launch; grid sizes come from the caller's SM count.
 // The prologue may be launched as a programmatic dependent of the kernel
@@ -400,6 +457,20 @@ cudaError_t launch_linear(const LinearMaps& m, const LinearLaunch& l, int sms, c
 cudaError_t launch_linear_finish(const LinearLaunch& l, cudaStream_t s);
 cudaError_t launch_linear_dz(const LinearDz& d, cudaStream_t s);
 cudaError_t launch_linear_token(LinearToken p, int sms, cudaStream_t s);
+cudaError_t launch_rms_norm(RmsNormLaunch l, bool bf16, bool eight_bits, int sms, cudaStream_t s);
+// Blocks of the backward pass, each with a part of the weight's gradient.
+int rms_norm_blocks(int tokens, int dim);
+cudaError_t launch_rms_norm_backward(RmsNormLaunch l, bool bf16, cudaStream_t s);
+cudaError_t launch_rms_norm_weight(const RmsNormLaunch& l, float* dw, cudaStream_t s);
+cudaError_t launch_embedding(const EmbeddingLaunch& l, bool table_bf16, int sms, cudaStream_t s);
+cudaError_t launch_embedding_sort(EmbeddingLaunch l, int sms, cudaStream_t s);
+cudaError_t launch_embedding_sum(const EmbeddingLaunch& l, bool dout_bf16, cudaStream_t s);
+cudaError_t launch_embedding_join(const EmbeddingLaunch& l, cudaStream_t s);
+size_t embedding_parts(int tokens, int dim);   // floats of EmbeddingLaunch::parts
+// Blocks of a launch of the sum of squares (each leaves a part).
+int clip_blocks(const ClipLaunch& l, int sms);
+cudaError_t launch_grad_squares(const ClipLaunch& l, int blocks, cudaStream_t s);
+cudaError_t launch_clip(const ClipLaunch& l, int sms, cudaStream_t s);
 
 // Host services of muon_api.cu for the other entry points' files.
 // Runs `fn` (which launches one kernel), counting and tracing it.
