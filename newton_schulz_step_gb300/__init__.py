@@ -853,19 +853,14 @@ def _matrix(t, name: str, shape, dtype, index) -> _Matrix:
     _refuse_matrix(t, name, shape, dtype, index)
 
 
-def _out_matrix(t, name: str, shape, dtype, index):
-    """(tensor, view) of an output: the caller's, or a new one, with its rows padded to 16 bytes
-    where the width asks for it."""
-    if t is not None:
-        return t, _matrix(t, name, shape, dtype, index)
-    rows, cols = shape
-    unit = 16 // dtype.itemsize
-    device = torch.device("cuda", index)
-    if cols % unit == 0:
-        t = torch.empty((rows, cols), dtype=dtype, device=device)
+def _new_matrix(shape, dtype, device):
+    """(tensor, view) of a new output, its rows padded to 16 bytes where the width asks for it."""
+    cols = shape[1]
+    if cols % 8 == 0:
+        t = torch.empty(shape, dtype=dtype, device=device)
         return t, _Matrix(t.data_ptr(), cols)
-    padded = -(-cols // unit) * unit
-    t = torch.empty((rows, padded), dtype=dtype, device=device)
+    padded = (cols + 7) // 8 * 8
+    t = torch.empty((shape[0], padded), dtype=dtype, device=device)
     return t[:, :cols], _Matrix(t.data_ptr(), padded)
 
 
@@ -886,7 +881,7 @@ def _linear_spec(x, weight, activation, bias):
     vw = _matrix(weight, "weight", (n, k), bf16, index)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    p_bias = _ptr(bias, "bias", index, bf16, (n,))
+    p_bias = None if bias is None else _ptr(bias, "bias", index, bf16, (n,))
     return _LinearSpec(t, k, n, ACTIVATIONS[activation], p_bias), vx, vw
 
 
@@ -920,8 +915,14 @@ def linear(x, weight, *, bias=None, activation: str | None = None, residual=None
     if residual is not None:
         vr = _matrix(residual, "residual", shape, bf16, index)
     if save_preact or preact is not None:
-        preact, vz = _out_matrix(preact, "preact", shape, bf16, index)
-    out, vo = _out_matrix(out, "out", shape, bf16, index)
+        if preact is None:
+            preact, vz = _new_matrix(shape, bf16, x.device)
+        else:
+            vz = _matrix(preact, "preact", shape, bf16, index)
+    if out is None:
+        out, vo = _new_matrix(shape, bf16, x.device)
+    else:
+        vo = _matrix(out, "out", shape, bf16, index)
     handle = _current_handle(index)
     ws, ws_bytes, _owner = _stream_workspace(
         workspace, linear_workspace_bytes(spec.tokens, spec.in_features, spec.out_features), index,
@@ -943,17 +944,23 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
         with _launch_on(x.device, stream):
             return linear_backward(dout, x, weight, bias=bias, activation=activation,
                                    preact=preact, dx=dx, dweight=dweight, workspace=workspace)
-    t, k, n = spec.tokens, spec.in_features, spec.out_features
+    t, k, n, device = spec.tokens, spec.in_features, spec.out_features, x.device
     vg = _matrix(dout, "dout", (t, n), bf16, index)
     vz = vdz = _NO_MATRIX
     if activation is not None:
         if preact is None:
             raise ValueError("an activation's gradient needs the preact that linear saved")
         vz = _matrix(preact, "preact", (t, n), bf16, index)
-        _dz, vdz = _out_matrix(None, "dz", (t, n), bf16, index)
-    dx, vdx = _out_matrix(dx, "dx", (t, k), bf16, index)
-    dweight, vdw = _out_matrix(dweight, "dweight", (n, k), bf16, index)
-    dbias = torch.empty(n, dtype=bf16, device=x.device) if bias else None
+        _dz, vdz = _new_matrix((t, n), bf16, device)
+    if dx is None:
+        dx, vdx = _new_matrix((t, k), bf16, device)
+    else:
+        vdx = _matrix(dx, "dx", (t, k), bf16, index)
+    if dweight is None:
+        dweight, vdw = _new_matrix((n, k), bf16, device)
+    else:
+        vdw = _matrix(dweight, "dweight", (n, k), bf16, index)
+    dbias = torch.empty(n, dtype=bf16, device=device) if bias else None
     handle = _current_handle(index)
     ws, ws_bytes, _owner = _stream_workspace(workspace, linear_workspace_bytes(t, k, n), index,
                                              handle)
@@ -974,8 +981,19 @@ def _norm_spec(x, name, weight, eps):
         raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
     vx = _matrix(x, name, x.shape, dtype, index)
     t, d = x.shape
-    return _RmsNormSpec(1 if dtype is torch.bfloat16 else 0, t, d, eps,
-                        _ptr(weight, "weight", index, torch.float32, (d,))), vx
+    p_w = None if weight is None else _ptr(weight, "weight", index, torch.float32, (d,))
+    return _RmsNormSpec(1 if dtype is torch.bfloat16 else 0, t, d, eps, p_w), vx
+
+
+def _norm_out(t, name, like, index):
+    """(tensor, view) of an output shaped like `like`: the caller's, or a new contiguous one."""
+    if t is not None:
+        return t, _matrix(t, name, like.shape, like.dtype, index)
+    if like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return t, _Matrix(t.data_ptr(), like.shape[1])
 
 
 def _refuse_norm_grad(where, x, weight, residual):
@@ -1005,10 +1023,10 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = NORM_EPS, out=None,
     h = x
     if residual is not None:
         vr = _matrix(residual, "residual", shape, dtype, index)
-        h, vh = _out_matrix(residual_out, "residual_out", shape, dtype, index)
+        h, vh = _norm_out(residual_out, "residual_out", x, index)
     elif residual_out is not None:
         raise ValueError("residual_out is the sum with a residual, and there is none")
-    out, vo = _out_matrix(out, "out", shape, dtype, index)
+    out, vo = _norm_out(out, "out", x, index)
     _raise(L.muon_rms_norm(spec, vx, vr, vo, vh, _current_handle(index)), "muon_rms_norm")
     return out, h
 
@@ -1034,7 +1052,7 @@ def rms_norm_fp8(x, weight=None, *, residual=None, eps: float = NORM_EPS, group:
     h = x
     if residual is not None:
         vr = _matrix(residual, "residual", shape, dtype, index)
-        h, vh = _out_matrix(residual_out, "residual_out", shape, dtype, index)
+        h, vh = _norm_out(residual_out, "residual_out", x, index)
     elif residual_out is not None:
         raise ValueError("residual_out is the sum with a residual, and there is none")
     t, d = shape
@@ -1069,7 +1087,7 @@ def rms_norm_backward(dout, h, weight=None, *, dresidual=None, eps: float = NORM
                                      workspace=workspace)
     vg = _matrix(dout, "dout", shape, dtype, index)
     vr = _NO_MATRIX if dresidual is None else _matrix(dresidual, "dresidual", shape, dtype, index)
-    dx, vdx = _out_matrix(dx, "dx", shape, dtype, index)
+    dx, vdx = _norm_out(dx, "dx", h, index)
     dweight = None if weight is None else torch.empty_like(weight)
     handle = _current_handle(index)
     ws, ws_bytes, _owner = _stream_workspace(workspace, rms_norm_workspace_bytes(spec.dim), index,
@@ -1119,7 +1137,10 @@ def embedding(ids, table, *, scale: float = 1.0, dtype=torch.bfloat16, out=None,
     if out is not None:
         dtype = out.dtype
     out_kind = _float_dtype(dtype, "out")
-    out, vo = _out_matrix(out, "out", (spec.tokens, dim), dtype, index)
+    if out is None:
+        out, vo = _new_matrix((spec.tokens, dim), dtype, table.device)
+    else:
+        vo = _matrix(out, "out", (spec.tokens, dim), dtype, index)
     _raise(L.muon_embedding(spec, kind, vt, out_kind, vo, _current_handle(index)),
            "muon_embedding")
     return out
@@ -1152,7 +1173,10 @@ def embedding_backward(dout, ids, rows: int, *, scale: float = 1.0, dtype=torch.
     if out is not None:
         dtype = out.dtype
     out_kind = _float_dtype(dtype, "out")
-    out, vo = _out_matrix(out, "out", (rows, dim), dtype, index)
+    if out is None:
+        out, vo = _new_matrix((rows, dim), dtype, dout.device)
+    else:
+        vo = _matrix(out, "out", (rows, dim), dtype, index)
     handle = _current_handle(index)
     ws, ws_bytes, _owner = _stream_workspace(workspace, embedding_workspace_bytes(t, dim), index,
                                              handle)
