@@ -314,12 +314,34 @@ struct AttentionMaps {
 // Pairs of CTAs that a plan counts on: one CTA on each of 152 SMs.
 constexpr int kLinearPairs = 76;
 constexpr int kTokenMax = 8;          // tokens that linear_token_kernel takes
+constexpr int kBand = 8;              // pair rows of a band of tiles (see decode, linear.cu)
+
+// Division by a number known on the host: floor(n / d) for 0 <= n < 2^31 by a multiplication
+// (Granlund and Montgomery's method: m = floor(2^(31 + l) / d) + 1 with 2^(l - 1) < d <= 2^l).
+struct Divisor {
+  uint32_t m;
+  int shift;                          // -1: d = 1
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int n) const {
+    return shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), m) >> shift);
+  }
+#endif
+  static Divisor of(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    if (l == 0) return {0u, -1};
+    return {static_cast<uint32_t>((1ull << (31 + l)) / static_cast<uint32_t>(d) + 1), l - 1};
+  }
+};
 
 // One product D = A B^T: D is m x n, its tiles 256 rows x LinearLaunch::bn columns.
 struct LinearProblem {
   int m, n, k_blocks;                 // k_blocks: contraction in 64-deep blocks
   int tiles_m, tiles_n;
   int splits;                         // parts of the contraction, <= k_blocks
+  Divisor by_tiles, by_band, by_last; // tiles; tiles of a band; rows of the last band
+  int last_band;
+  int k_each, k_more;                 // blocks of a split; the first k_more have one more
   int item_begin;                     // first work item: splits x tiles of them
   int a_mn, b_mn;                     // operand lies with its rows along the contraction
   int act, has_res, has_z;

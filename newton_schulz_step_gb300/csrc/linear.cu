@@ -113,22 +113,21 @@ struct Item {
 // Linear item -> problem, split, tile.  All tiles of a split come before the next split.
 // Tiles go by bands of kBand pair rows, column by column within a band: the pairs at work
 // at one time then share a few row panels of A and column panels of B in L2.
-constexpr int kBand = 8;
 __device__ __forceinline__ Item decode(const LinearLaunch& L, int item) {
   Item it;
   it.p = L.n_prob > 1 && item >= L.prob[1].item_begin ? 1 : 0;
   const LinearProblem& P = L.prob[it.p];
   const int local = item - P.item_begin;
-  const int tiles = P.tiles_m * P.tiles_n;
-  it.split = local / tiles;
-  it.tile = local - it.split * tiles;
-  const int band = it.tile / (kBand * P.tiles_n);
+  it.split = P.by_tiles.quotient(local);
+  it.tile = local - it.split * (P.tiles_m * P.tiles_n);
+  const int band = P.by_band.quotient(it.tile);
   const int w = it.tile - band * kBand * P.tiles_n;
-  const int rows = min(kBand, P.tiles_m - band * kBand);
-  it.tn = w / rows;
-  it.pr = band * kBand + w - it.tn * rows;
-  it.kb0 = static_cast<int>(1ll * it.split * P.k_blocks / P.splits);
-  it.kb1 = static_cast<int>(1ll * (it.split + 1) * P.k_blocks / P.splits);
+  const bool whole = band < P.last_band;
+  it.tn = whole ? w / kBand : P.by_last.quotient(w);
+  it.pr = band * kBand + w - it.tn * (whole ? kBand : P.tiles_m - band * kBand);
+  const int each = P.k_each, more = P.k_more;
+  it.kb0 = it.split * each + min(it.split, more);
+  it.kb1 = it.kb0 + each + (it.split < more ? 1 : 0);
   return it;
 }
 
@@ -212,61 +211,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (skip) {
   } else if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int i = first; ok && i < L.items; i += stride) {
-        const Item it = decode(L, i);
-        const LinearProblem& P = L.prob[it.p];
-        const CUtensorMap *ma = &M.a[it.p], *mb = &M.b[it.p];
-        const int row = (2 * it.pr + rank) * kTileM, col = it.tn * kBN + rank * (kBN / 2);
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, ab.flag, ab.status)) {
-            give_up(ab, kErrTimeoutProducer);
-            ok = false;
-            break;
-          }
-          uint8_t* const sa = ring + stage * C::kStageBytes;
-          uint8_t* const sb = sa + C::kABytes;
-          const uint32_t bar = full0 + stage * 8;
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    // (the warp walks in step and an elected lane issues, as for the products: from a branch on
+    // a lane index the copies of a step took longer to issue than its products to run)
+    for (int i = first; ok && i < L.items; i += stride) {
+      const Item it = decode(L, i);
+      const LinearProblem& P = L.prob[it.p];
+      const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
+      const CUtensorMap *ma = &M.a[it.p], *mb = &M.b[it.p];
+      const int row = (2 * it.pr + rank) * kTileM, col = it.tn * kBN + rank * (kBN / 2);
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        ok = ptx::mbar_wait(&empty[stage], phase ^ 1u, ab.flag, ab.status);
+        __syncwarp();
+        if (!ok) break;
+        uint8_t* const sa = ring + stage * C::kStageBytes;
+        uint8_t* const sb = sa + C::kABytes;
+        const uint32_t bar = full0 + stage * 8;
+        if (ptx::elect_one()) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          if (P.a_mn) {          // slabs of 64 rows of the tile x 64 deep
+          if (a_mn) {            // slabs of 64 rows of the tile x 64 deep
             ptx::tma_load_3d_pair(sa, ma, row, kb * kTileK, 0, bar);
             ptx::tma_load_3d_pair(sa + 8192, ma, row + 64, kb * kTileK, 0, bar);
           } else {
             ptx::tma_load_3d_pair(sa, ma, kb * kTileK, row, 0, bar);
           }
-          if (P.b_mn) {
+          if (b_mn) {
 #pragma unroll
             for (int q = 0; q < kBN / 128; ++q)
               ptx::tma_load_3d_pair(sb + q * 8192, mb, col + q * 64, kb * kTileK, 0, bar);
           } else {
             ptx::tma_load_3d_pair(sb, mb, kb * kTileK, col, 0, bar);
           }
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-      }
-      // before exit every copy has landed and no commit is on its way to this CTA: the
-      // products have released every armed stage (after a failure, one bounded window)
-      const uint64_t t0 = ptx::globaltimer();
-      for (int s = 0; s < C::kStages; ++s) {
-        if (!(armed & (1u << s))) continue;
-        const uint64_t spent = ptx::globaltimer() - t0;
-        if (spent >= ptx::kWaitTimeoutNs ||
-            !ptx::mbar_wait(&empty[s], (armed_parity >> s) & 1u, nullptr, nullptr,
-                            ptx::kWaitTimeoutNs - spent)) {
-          give_up(ab, kErrTimeoutDrain);
-          break;
+        __syncwarp();
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
+    if (!ok && lane == 0) give_up(ab, kErrTimeoutProducer);
+    // before exit every copy has landed and no commit is on its way to this CTA: the
+    // products have released every armed stage (after a failure, one bounded window)
+    const uint64_t t0 = ptx::globaltimer();
+    for (int s = 0; s < C::kStages; ++s) {
+      if (!(armed & (1u << s))) continue;
+      const uint64_t spent = ptx::globaltimer() - t0;
+      if (spent >= ptx::kWaitTimeoutNs ||
+          !ptx::mbar_wait(&empty[s], (armed_parity >> s) & 1u, nullptr, nullptr,
+                          ptx::kWaitTimeoutNs - spent)) {
+        give_up(ab, kErrTimeoutDrain);
+        break;
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       int stage = 0, acc = 0;

@@ -48,9 +48,9 @@ struct Product {
 
 // Estimated clocks of a launch of `count` products with tiles bn wide and the given splits.
 // A 64-deep step of a 256 x 256 tile takes the tensor cores 512 clocks; of a 256 x 128 tile
-// half that, but the pair's 24 KB of operands a CTA then arrive no faster than in 290.
+// half that, but its operands, 24 KB a CTA, were not seen to arrive in less than 420.
 double plan_clocks(const Product* p, int count, int bn, const int* splits) {
-  const double step = bn == 256 ? 512.0 : 290.0, fixed = 2500.0;
+  const double step = bn == 256 ? 530.0 : 420.0, fixed = 2500.0;
   double work = 0.0, longest = 0.0, bytes = 0.0, waves = 0.0;
   for (int i = 0; i < count; ++i) {
     const double tiles = 1.0 * cdiv(p[i].m, 256) * cdiv(p[i].n, bn);
@@ -143,12 +143,18 @@ bool set_problem(LinearLaunch& L, int i, const Product& p, int splits, bool a_mn
   P.k_blocks = cdiv(p.k, kTileK);
   P.tiles_m = cdiv(p.m, 256);
   P.tiles_n = cdiv(p.n, L.bn);
+  const long long items = 1ll * P.tiles_m * P.tiles_n * splits + L.items;
+  if (items > kMaxItems) return false;
   P.splits = splits;
+  P.by_tiles = Divisor::of(P.tiles_m * P.tiles_n);
+  P.by_band = Divisor::of(kBand * P.tiles_n);
+  P.last_band = (P.tiles_m - 1) / kBand;
+  P.by_last = Divisor::of(P.tiles_m - P.last_band * kBand);
+  P.k_each = P.k_blocks / splits;
+  P.k_more = P.k_blocks - P.k_each * splits;
   P.a_mn = a_mn;
   P.b_mn = b_mn;
   P.item_begin = L.items;
-  const long long items = 1ll * P.tiles_m * P.tiles_n * splits + L.items;
-  if (items > kMaxItems) return false;
   L.items = static_cast<int>(items);
   L.n_prob = i + 1;
   return true;
