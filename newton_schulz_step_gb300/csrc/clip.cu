@@ -22,10 +22,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = kClipUnit / 8 / kThreads;      // vectors of 8 a thread and unit
 
-struct Raw {
+// 8 elements as stored.  kBf16: every gradient of the launch is bf16, so that half the
+// registers hold them and all vectors of a unit travel at once; else half a unit does.
+template <bool kBf16> struct Raw;
+template <> struct Raw<true> {
+  uint4 a;
+};
+template <> struct Raw<false> {
   uint4 a, b;                                        // b: fp32 only
 };
-__device__ __forceinline__ void load(const ClipTensor& T, long long e, Raw& r) {
+template <bool kBf16> constexpr int kFlight = kBf16 ? kVecs : kVecs / 2;
+
+__device__ __forceinline__ void load(const ClipTensor& T, long long e, Raw<true>& r) {
+  r.a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(T.g) + e));
+}
+__device__ __forceinline__ void load(const ClipTensor& T, long long e, Raw<false>& r) {
   if (T.g_bf16) {
     r.a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(T.g) + e));
   } else {
@@ -34,22 +45,25 @@ __device__ __forceinline__ void load(const ClipTensor& T, long long e, Raw& r) {
     r.b = __ldcg(p + 1);
   }
 }
-__device__ __forceinline__ void get(const ClipTensor& T, const Raw& r, float (&v)[8]) {
-  const uint32_t a[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-  if (T.g_bf16) {
+__device__ __forceinline__ void widen(const uint4& x, float (&v)[8]) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-    }
-  } else {
-    const uint32_t b[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(a[i]);
-      v[4 + i] = __uint_as_float(b[i]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(a[i] << 16);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
   }
+}
+__device__ __forceinline__ void get(const ClipTensor&, const Raw<true>& r, float (&v)[8]) {
+  widen(r.a, v);
+}
+__device__ __forceinline__ void get(const ClipTensor& T, const Raw<false>& r, float (&v)[8]) {
+  if (T.g_bf16) {
+    widen(r.a, v);
+    return;
+  }
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 }
 __device__ __forceinline__ float value(const ClipTensor& T, long long e) {
   return T.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(T.g)[e])
@@ -72,12 +86,18 @@ __device__ __forceinline__ void store(const ClipTensor& T, long long e, const fl
   }
 }
 
+// First units of the launch's tensors in shared memory (a search among the launch's
+// arguments is a chain of misses of the constant cache).
+__device__ __forceinline__ void load_begins(const ClipLaunch& L, long long* begins) {
+  if (threadIdx.x < static_cast<unsigned>(L.n_tensors)) begins[threadIdx.x] = L.t[threadIdx.x].unit_begin;
+}
 // Tensor of unit u: the last one that begins at or before it.
-__device__ __forceinline__ const ClipTensor& tensor_of(const ClipLaunch& L, long long u) {
+__device__ __forceinline__ const ClipTensor& tensor_of(const ClipLaunch& L, const long long* begins,
+                                                       long long u) {
   int lo = 0, hi = L.n_tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (L.t[mid].unit_begin <= u) lo = mid;
+    if (begins[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   return L.t[lo];
@@ -95,27 +115,41 @@ __device__ __forceinline__ double block_sum(double x, double* s) {
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ ClipLaunch L) {
+// (the root in fp32: in fp64 it takes longer than the sum; past 2^100 by a scale of 2^-64)
+__device__ __forceinline__ float root(double x) {
+  return x > 0x1p100 ? sqrtf(static_cast<float>(x * 0x1p-64)) * 0x1p32f
+                     : sqrtf(static_cast<float>(x));
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_constant__ ClipLaunch L) {
   __shared__ double s_sum[kThreads / 32];
+  __shared__ long long s_begins[kMaxClipTensors];
   ptx::griddep_launch_dependents();
+  load_begins(L, s_begins);
+  __syncthreads();
   ptx::griddep_wait();
   if (ptx::status_set(L.status)) return;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
   for (long long u = blockIdx.x; u < L.total_units; u += gridDim.x) {
-    const ClipTensor& T = tensor_of(L, u);
+    const ClipTensor& T = tensor_of(L, s_begins, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     if (base + kClipUnit <= T.n) {
-      Raw r[kVecs];
+#pragma unroll 1
+      for (int p = 0; p < kVecs; p += kFlight<kBf16>) {
+        Raw<kBf16> r[kFlight<kBf16>];
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) load(T, base + 8ll * (i * kThreads + threadIdx.x), r[i]);
+        for (int i = 0; i < kFlight<kBf16>; ++i)
+          load(T, base + 8ll * ((p + i) * kThreads + threadIdx.x), r[i]);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        float v[8];
-        get(T, r[i], v);
+        for (int i = 0; i < kFlight<kBf16>; ++i) {
+          float v[8];
+          get(T, r[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = fmaf(v[j], v[j], sum[j]);
+          for (int j = 0; j < 8; ++j) sum[j] = fmaf(v[j], v[j], sum[j]);
+        }
       }
     } else {
       for (int i = 0; i < kVecs; ++i) {
@@ -135,32 +169,54 @@ __global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_con
   if (threadIdx.x == 0) __stcg(L.parts + L.part_begin + blockIdx.x, total);
 }
 
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ ClipLaunch L) {
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant__ ClipLaunch L) {
   __shared__ double s_sum[kThreads / 32];
+  __shared__ long long s_begins[kMaxClipTensors];
   ptx::griddep_launch_dependents();
+  load_begins(L, s_begins);
+  __syncthreads();
   ptx::griddep_wait();
   if (ptx::status_set(L.status)) return;
+  // a block's first whole unit travels while the parts are added
+  long long u = L.total_units - 1 - blockIdx.x;
+  Raw<kBf16> r[kFlight<kBf16>];
+  auto fetch = [&](const ClipTensor& T, long long base) {
+#pragma unroll
+    for (int i = 0; i < kFlight<kBf16>; ++i)
+      load(T, base + 8ll * (i * kThreads + threadIdx.x), r[i]);
+  };
+  bool fetched = false;
+  if (u >= 0) {
+    const ClipTensor& T = tensor_of(L, s_begins, u);
+    const long long base = (u - T.unit_begin) * kClipUnit;
+    fetched = base + kClipUnit <= T.n;
+    if (fetched) fetch(T, base);
+  }
   double total = 0.0;
   for (int i = threadIdx.x; i < L.n_parts; i += kThreads) total += __ldcg(L.parts + i);
-  const float norm = static_cast<float>(sqrt(block_sum(total, s_sum)));
+  const float norm = root(block_sum(total, s_sum));
   if (L.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *L.norm = norm;
   const float ratio = L.max_norm / (norm + L.eps);
   const float c = ratio >= 1.f ? 1.f : ratio;         // (a norm that is NaN stays one)
   if (L.in_place && c == 1.f) return;
-  for (long long u = L.total_units - 1 - blockIdx.x; u >= 0; u -= gridDim.x) {
-    const ClipTensor& T = tensor_of(L, u);
+  for (; u >= 0; u -= gridDim.x) {
+    const ClipTensor& T = tensor_of(L, s_begins, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     if (base + kClipUnit <= T.n) {
-      Raw r[kVecs];
+#pragma unroll 1
+      for (int p = 0; p < kVecs; p += kFlight<kBf16>) {
+        const long long at = base + 8ll * p * kThreads;
+        if (!fetched) fetch(T, at);
+        fetched = false;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) load(T, base + 8ll * (i * kThreads + threadIdx.x), r[i]);
+        for (int i = 0; i < kFlight<kBf16>; ++i) {
+          float v[8];
+          get(T, r[i], v);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        float v[8];
-        get(T, r[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= c;
-        store(T, base + 8ll * (i * kThreads + threadIdx.x), v);
+          for (int j = 0; j < 8; ++j) v[j] *= c;
+          store(T, at + 8ll * (i * kThreads + threadIdx.x), v);
+        }
       }
     } else {
       for (int i = 0; i < kVecs; ++i) {
@@ -197,12 +253,20 @@ int clip_blocks(const ClipLaunch& l, int sms) {
       1, std::min<long long>({l.total_units, 4ll * sms, kClipBlocks})));
 }
 
+static bool all_bf16(const ClipLaunch& l) {
+  for (int i = 0; i < l.n_tensors; ++i)
+    if (!l.t[i].g_bf16) return false;
+  return true;
+}
+
 cudaError_t launch_grad_squares(const ClipLaunch& l, int blocks, cudaStream_t s) {
-  return launch_dependent(grad_squares_kernel, blocks, s, l);
+  return launch_dependent(all_bf16(l) ? grad_squares_kernel<true> : grad_squares_kernel<false>,
+                          blocks, s, l);
 }
 
 cudaError_t launch_clip(const ClipLaunch& l, int sms, cudaStream_t s) {
-  return launch_dependent(clip_kernel, clip_blocks(l, sms), s, l);
+  return launch_dependent(all_bf16(l) ? clip_kernel<true> : clip_kernel<false>,
+                          clip_blocks(l, sms), s, l);
 }
 
 }  // namespace muon

@@ -56,6 +56,28 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+// 8 elements as stored.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a = __ldg(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack(a, v); }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p + 4));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
 // -1 for an id outside the table.
 __device__ __forceinline__ int id_at(const void* ids, bool wide, int t, int rows) {
   const long long v = wide ? __ldg(static_cast<const long long*>(ids) + t)
@@ -109,6 +131,17 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
+// Lanes of the warp that hold the digit d of this one: a ballot a bit.  (__match_any_sync took
+// about six times as long for digits of 8 bits.)  Lanes that are not live hold none.
+__device__ __forceinline__ uint32_t equal_lanes(uint32_t d, int bits, bool live) {
+  uint32_t same = __ballot_sync(0xffffffffu, live);
+  for (int b = 0; b < bits; ++b) {
+    const uint32_t ones = __ballot_sync(0xffffffffu, d >> b & 1u);
+    same &= d >> b & 1u ? ones : ~ones;
+  }
+  return same;
+}
+
 // Sorts (id, token) by `passes` digits of `bits` bits, least first; ids outside the table sort
 // behind the last row.  CTA r has the r-th contiguous part of the items, a warp a contiguous
 // part of it, and each pass keeps equal digits in order: counts a warp, a digit's place from
@@ -141,8 +174,8 @@ __device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
 #pragma unroll 4
     for (int i = i0 + lane; i - lane < i1; i += 32) {
       const bool live = i < i1;
-      const uint32_t d = live ? (key_at(i) >> shift) & (bins - 1) : 0xffffffffu;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      const uint32_t d = live ? (key_at(i) >> shift) & (bins - 1) : 0u;
+      const uint32_t same = equal_lanes(d, L.bits, live);
       if (live && (__ffs(same) - 1) == lane) mine[d] += __popc(same);
       __syncwarp();
     }
@@ -196,8 +229,8 @@ __device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
       const bool live = i < i1;
       const uint32_t key = live ? key_at(i) : 0u;
       const uint32_t token = live && pass > 0 ? __ldcg(L.order[from] + i) : static_cast<uint32_t>(i);
-      const uint32_t d = live ? (key >> shift) & (bins - 1) : 0xffffffffu;
-      const uint32_t same = __match_any_sync(0xffffffffu, d);
+      const uint32_t d = (key >> shift) & (bins - 1);
+      const uint32_t same = equal_lanes(d, L.bits, live);
       uint32_t at = 0u;
       if (live) at = base[d] + mine[d] + __popc(same & ((1u << lane) - 1u));
       __syncwarp();
@@ -258,7 +291,7 @@ __device__ __forceinline__ void store_row(const EmbeddingLaunch& L, uint32_t id,
 }
 
 constexpr int kChunk = 32;             // sorted positions of a warp
-constexpr int kFlight = 8;             // rows of a warp in flight
+template <typename G> constexpr int kFlight = 32 / sizeof(G);   // rows of a warp in flight
 template <typename G, typename O>
 __global__ void __launch_bounds__(kThreads)
     embedding_sum_kernel(const __grid_constant__ EmbeddingLaunch L) {
@@ -285,22 +318,19 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   int begin = 0;
-  for (int p = 0; p < n; p += kFlight) {
-    float v[kFlight][8];
+  for (int p = 0; p < n; p += kFlight<G>) {
+    Raw<G> raw[kFlight<G>];
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
+    for (int k = 0; k < kFlight<G>; ++k) {
       const uint32_t t = __shfl_sync(0xffffffffu, token, (p + k) & 31);
       const uint32_t id = __shfl_sync(0xffffffffu, key, (p + k) & 31);
+      raw[k].clear();
       // (rows of ids outside the table are not read)
-      if (on && p + k < n && id < static_cast<uint32_t>(L.rows)) {
-        load8(static_cast<const G*>(L.dout) + t * L.dout_stride + c, v[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
-      }
+      if (on && p + k < n && id < static_cast<uint32_t>(L.rows))
+        raw[k].load(static_cast<const G*>(L.dout) + t * L.dout_stride + c);
     }
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
+    for (int k = 0; k < kFlight<G>; ++k) {
       const int i = p + k;
       if (i >= n) break;
       if (begins >> i & 1u) {
@@ -308,8 +338,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
       }
+      float v[8];
+      raw[k].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
       if (i + 1 < n && !(begins >> (i + 1) & 1u)) continue;   // the run goes on in this chunk
       const uint32_t id = __shfl_sync(0xffffffffu, key, i);
       if (!on || id >= static_cast<uint32_t>(L.rows)) continue;
@@ -359,7 +391,7 @@ __global__ void __launch_bounds__(kThreads)
   float acc[8];
   load8(L.parts + (static_cast<size_t>(chunk) * 2 + 1) * L.dim + c, acc);
   const float* p = L.parts + static_cast<size_t>(chunk + 1) * 2 * L.dim + c;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 0; k < reach; ++k) {
     float v[8];
     load8(p + static_cast<size_t>(k) * 2 * L.dim, v);

@@ -389,7 +389,7 @@ struct LinearToken {
 
 // ---- RMS norm with the residual's addition (rms_norm.cu, block_api.cu)
 constexpr int kRmsNormMaxDim = 16384;
-constexpr int kRmsNormMaxBlocks = 608;   // parts of the weight's gradient
+constexpr int kRmsNormMaxBlocks = 304;   // parts of the weight's gradient: two blocks an SM
 
 struct RmsNormLaunch {
   const void *x, *dy, *res;         // backward: x is the sum as stored, res the sum's gradient
@@ -420,7 +420,7 @@ struct EmbeddingLaunch {
 };
 
 // ---- norm of all gradients, clipping (clip.cu, block_api.cu)
-constexpr int kClipUnit = 8192;        // elements per work unit
+constexpr int kClipUnit = 16384;       // elements per work unit
 constexpr int kMaxClipTensors = 64;    // tensors per launch
 constexpr int kClipBlocks = 608;       // parts of the sum of squares a launch, at most
 

@@ -53,24 +53,50 @@ struct Cfg {
 static_assert(Cfg<256>::kSmem <= 232448 && Cfg<128>::kSmem <= 232448, "227 KB a CTA");
 
 // ------------------------------------------------------------ activations
-// 1 / (1 + exp(-2 u)), u = a (z + b z^3): the tanh form of GELU is z times this.
+// GELU's tanh form is z / (1 + exp(-2 u)), u = a (z + b z^3).  The exponential is taken as a
+// power of two: 2^(z (c + d z^2)) with c = -2 a log2(e), d = b c.
 constexpr float kGeluA = 0.7978845608028654f, kGeluB = 0.044715f;
+constexpr float kGeluC = -2.f * kGeluA * 1.4426950408889634f, kGeluD = kGeluB * kGeluC;
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float gelu_gate(float z) {
-  const float u = kGeluA * fmaf(kGeluB * z * z, z, z);
-  return __fdividef(1.f, 1.f + __expf(-2.f * u));
+  return reciprocal_approx(1.f + exp2_approx(z * fmaf(kGeluD * z, z, kGeluC)));
 }
 // (comparisons that a NaN fails lead to arithmetic on it, so it stays one)
-__device__ __forceinline__ float activate(float z, int act) {
-  if (act == MUON_ACT_RELU2) return z <= 0.f ? 0.f : z * z;
-  if (act == MUON_ACT_GELU) return z * gelu_gate(z);
-  return z;
+__device__ __forceinline__ float relu2(float z) { return z <= 0.f ? 0.f : z * z; }
+template <int kN>
+__device__ __forceinline__ void activate(float (&z)[kN], int act) {
+  if (act == MUON_ACT_RELU2) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) z[i] = relu2(z[i]);
+  } else if (act == MUON_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) z[i] *= gelu_gate(z[i]);
+  }
 }
-__device__ __forceinline__ float slope(float z, int act) {
-  if (act == MUON_ACT_RELU2) return z <= 0.f ? 0.f : 2.f * z;
-  // beyond +-30 the slope is 1 or 0 to the last bit, and z^3 may overflow
-  const float c = z > 30.f ? 30.f : z < -30.f ? -30.f : z;
-  const float s = gelu_gate(c);
-  return fmaf(2.f * c * s * (1.f - s), kGeluA * fmaf(3.f * kGeluB * c, c, 1.f), s);
+// v times the slope at z
+template <int kN>
+__device__ __forceinline__ void times_slope(float (&v)[kN], const float (&z)[kN], int act) {
+  if (act == MUON_ACT_RELU2) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] *= z[i] <= 0.f ? 0.f : 2.f * z[i];
+  } else if (act == MUON_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      // beyond +-30 the slope is 1 or 0 to the last bit, and z^3 may overflow
+      const float c = z[i] > 30.f ? 30.f : z[i] < -30.f ? -30.f : z[i];
+      const float s = gelu_gate(c);
+      v[i] *= fmaf(2.f * c * s * (1.f - s), kGeluA * fmaf(3.f * kGeluB * c, c, 1.f), s);
+    }
+  }
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -189,6 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     ptx::tmem_alloc_pair(tmem_slot, C::kTmemCols);
     ptx::tmem_relinquish_pair();
+  } else if (warp == 0 && ptx::elect_one()) {
+    for (int p = 0; p < L.n_prob; ++p) {
+      ptx::prefetch_tmap(&M.a[p]);
+      ptx::prefetch_tmap(&M.b[p]);
+    }
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -201,16 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ab.peer_flag = ptx::mapa_shared(ptx::smem_u32(const_cast<const int*>(abort_flag)),
                                   static_cast<uint32_t>(rank ^ 1));
   ab.status = L.status;
-  // an earlier failure on this workspace: the pair does nothing (decided for both CTAs)
-  if (threadIdx.x == 0 && ptx::status_set(ab.status)) {
-    *ab.flag = 1;
-    ptx::st_cluster_u32(ab.peer_flag, 1u);
-  }
-  ptx::cluster_sync();
-  const bool skip = *ab.flag != 0;
-
-  if (skip) {
-  } else if (warp == 0) {
+  if (warp == 0) {
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
@@ -330,12 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* const my_in = in_bar + e * kSlots;
     int acc = 0, slot = 0;
     uint32_t acc_phase = 0, in_par = 0, in_armed = 0;
+    // an earlier failure on this workspace: products run, but nothing is stored (the word is
+    // read beside the first loads; a check before them cost every launch a trip to L2)
+    const bool skip = ptx::status_set(ab.status);
     for (int i = first; i < L.items; i += stride) {
       const Item it = decode(L, i);
       const LinearProblem& P = L.prob[it.p];
       const int i0 = (2 * it.pr + rank) * kTileM + quarter * 32;    // first row of the warp
       const int c0 = it.tn * kBN + half * (kBN / 2);                // first column
-      const int units = i0 < P.m ? min(C::kUnits, max(0, (P.n - c0 + 63) / 64)) : 0;
+      const int units = !skip && i0 < P.m ? min(C::kUnits, max(0, (P.n - c0 + 63) / 64)) : 0;
       const bool split = P.splits > 1;
       const bool has_res = P.has_res != 0 && !split, has_z = P.has_z != 0 && !split;
       auto fetch = [&](int u) {       // the residual's block of unit u into slot u (lane 0)
@@ -350,6 +375,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         in_armed = units > 0 ? (has_z ? 1u : (1u << units) - 1u) : 0u;
         __syncwarp();
       }
+      // the first block's bias travels while the products run, the second's with the first's
+      const bool has_bias = P.bias != nullptr && !split;
+      uint4 bias[8];
+      auto fetch_bias = [&](int j0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int c = j0 + 8 * q;
+          if (c + 8 <= P.n) {
+            bias[q] = __ldg(reinterpret_cast<const uint4*>(P.bias + c));
+          } else {
+            float b[8];
+            load8(P.bias, c, P.n, b);
+            bias[q] = pack8(b);
+          }
+        }
+      };
+      if (has_bias && units > 0) fetch_bias(c0);
       bool ok = ptx::mbar_wait(&acc_full[acc], acc_phase, ab.flag, ab.status);
       __syncwarp();
       ptx::tc_fence_after();
@@ -378,14 +420,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int j0 = c0 + u * 64;
-        if (P.bias != nullptr) {
+        if (has_bias) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             float b[8];
-            load8(P.bias, j0 + 8 * q, P.n, b);
+            unpack8(bias[q], b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[8 * q + j] += b[j];
           }
+          if (u + 1 < units) fetch_bias(j0 + 64);
         }
         if (has_z) {
           const int zs = has_res ? 1 : slot;
@@ -404,10 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!has_res) slot ^= 1;
         }
-        if (P.act != MUON_ACT_NONE) {
-#pragma unroll
-          for (int q = 0; q < 64; ++q) z[q] = activate(z[q], P.act);
-        }
+        activate(z, P.act);
         int ys = slot;
         if (has_res) {
           ys = has_z ? 0 : u;
@@ -463,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) ptx::bulk_wait<0>();
+    if (lane == 0) ptx::bulk_wait_read<0>();
     __syncwarp();
   }
   __syncwarp();
@@ -534,8 +574,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
         for (int k = 0; k < 8; ++k) v[k] += x[k];
       }
       if (P.has_z) store8(P.z + i * P.z_stride, c, P.n, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = activate(v[k], P.act);
+      activate(v, P.act);
       if (P.has_res) {
         // (not through the read-only path: the output may be the residual itself)
         const __nv_bfloat16* row = P.res + i * P.res_stride;
@@ -601,8 +640,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
         if (D.act != MUON_ACT_NONE) {
           if (whole) unpack8(z[i], x);
           else load8(D.z + row * D.z_stride, c, D.cols, x);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] *= slope(x[k], D.act);
+          times_slope(v, x, D.act);
           store8(D.dz + row * D.dz_stride, c, D.cols, v);
         }
 #pragma unroll
@@ -694,7 +732,9 @@ __global__ void __launch_bounds__(256) linear_token_kernel(const __grid_constant
     for (int s = 0; s < P.ks; ++s) z += s_sum[grp * P.ks + s][r][t];
     if (P.bias != nullptr) z += __bfloat162float(P.bias[j]);
     if (P.z != nullptr) P.z[t * P.z_stride + j] = __float2bfloat16_rn(z);
-    z = activate(z, P.act);
+    float y[1] = {z};
+    activate(y, P.act);
+    z = y[0];
     if (P.res != nullptr) z += __bfloat162float(P.res[t * P.res_stride + j]);
     P.out[t * P.out_stride + j] = __float2bfloat16_rn(z);
   }

@@ -105,14 +105,34 @@ Plan make_plan(const Product* p, int count) {
   return best;
 }
 
-Plan forward_plan(int tokens, int in, int out) {
-  const Product p{tokens, out, in};
-  return make_plan(&p, 1);
-}
 // [0] dW, whose contraction over the tokens is the longer one as a rule, [1] dx
 void backward_products(int tokens, int in, int out, Product (&p)[2]) {
   p[0] = {out, in, tokens};
   p[1] = {tokens, in, out};
+}
+
+// The plan of a call, by its sizes.  Looking for one takes several microseconds (two products:
+// 450 estimates), so a thread keeps those of the sizes that it met last.
+Plan plan_of(int tokens, int in, int out, bool backward) {
+  struct Entry {
+    int tokens = -1, in, out;
+    bool backward;
+    Plan plan;
+  };
+  static thread_local Entry kept[64];
+  const unsigned h = (static_cast<unsigned>(tokens) * 2654435761u) ^
+                     (static_cast<unsigned>(in) * 40503u) ^ (static_cast<unsigned>(out) * 9176741u);
+  Entry& e = kept[((h >> 16) ^ h ^ (backward ? 1u : 0u)) & 63u];
+  if (e.tokens != tokens || e.in != in || e.out != out || e.backward != backward) {
+    Product p[2] = {{tokens, out, in}, {0, 0, 0}};
+    if (backward) backward_products(tokens, in, out, p);
+    e.plan = make_plan(p, backward ? 2 : 1);
+    e.tokens = tokens;
+    e.in = in;
+    e.out = out;
+    e.backward = backward;
+  }
+  return e.plan;
 }
 
 // Rows of a block of linear_dz_kernel: enough blocks for four an SM, whole sets of 32 rows.
@@ -124,13 +144,11 @@ int dz_chunk(int tokens, int out) {
 
 size_t forward_bytes(int tokens, int in, int out) {
   if (tokens <= kTokenMax) return kStatusBytes;
-  return kStatusBytes + align256(forward_plan(tokens, in, out).parts[0]);
+  return kStatusBytes + align256(plan_of(tokens, in, out, false).parts[0]);
 }
 size_t backward_bytes(int tokens, int in, int out) {
   if (tokens == 0) return kStatusBytes;
-  Product p[2];
-  backward_products(tokens, in, out, p);
-  const Plan plan = make_plan(p, 2);
+  const Plan plan = plan_of(tokens, in, out, true);
   return kStatusBytes + align256(plan.parts[0]) + align256(plan.parts[1]) +
          align256(static_cast<size_t>(cdiv(tokens, dz_chunk(tokens, out))) * out * sizeof(float));
 }
@@ -239,7 +257,7 @@ muon_status muon_linear(const muon_linear_spec* spec, muon_matrix x, muon_matrix
     }
     LinearLaunch L;
     std::memset(&L, 0, sizeof(L));
-    const Plan plan = forward_plan(t, k, n);
+    const Plan plan = plan_of(t, k, n, false);
     L.bn = plan.bn;
     L.status = status;
     if (!set_problem(L, 0, {t, n, k}, plan.splits[0], false, false)) return MUON_ERR_UNSUPPORTED;
@@ -318,7 +336,7 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
     if (s != MUON_OK) return s;
     Product p[2];
     backward_products(t, k, n, p);
-    const Plan plan = make_plan(p, 2);
+    const Plan plan = plan_of(t, k, n, true);
     uint8_t* const base = static_cast<uint8_t*>(workspace) + kStatusBytes;
     const int chunk = dz_chunk(t, n);
     LinearLaunch L;

@@ -388,40 +388,43 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// dw = sum of the blocks' parts, in a fixed order: 32 columns a block, 8 warps that take every
-// eighth part each.
-__global__ void __launch_bounds__(256)
+// dw = sum of the blocks' parts, in a fixed order: 32 columns a block, 32 warps that take every
+// 32nd part each (all of a warp's loads in flight at once).
+__global__ void __launch_bounds__(1024)
     rms_norm_weight_kernel(const float* parts, int blocks, int dim, float* dw,
                            const unsigned int* status) {
-  __shared__ float s_sum[8][32];
+  __shared__ float s_sum[32][33];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (ptx::status_set(status)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int d = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (d < dim) {
-#pragma unroll 8
-    for (int b = warp; b < blocks; b += 8) s += __ldcg(parts + static_cast<size_t>(b) * dim + d);
+  constexpr int kEach = (kRmsNormMaxBlocks + 31) / 32;
+  float v[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = warp + 32 * i;
+    v[i] = b < blocks && d < dim ? __ldcg(parts + static_cast<size_t>(b) * dim + d) : 0.f;
   }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) s += v[i];
   s_sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && d < dim) {
-    float t = 0.f;
+  s = s_sum[lane][warp];                     // column `warp`, one lane a warp's sum
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += s_sum[k][lane];
-    dw[d] = t;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < dim) dw[blockIdx.x * 32 + warp] = s;
 }
 
 template <typename K, typename... A>
-cudaError_t launch_dependent(K kernel, int blocks, int smem, cudaStream_t s, A... args) {
+cudaError_t launch_dependent(K kernel, int blocks, int threads, int smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
@@ -440,10 +443,10 @@ template <typename T, Mode kMode>
 cudaError_t forward(RmsNormLaunch l, int sms, cudaStream_t s) {
   const int per = kThreads / l.team, each = (l.dim / 8 + l.team - 1) / l.team;
   const int blocks = std::min((l.tokens + per - 1) / per, 8 * sms);
-  if (each <= 1) return launch_dependent(rms_norm_kernel<T, kMode, 1>, blocks, 0, s, l);
-  if (each <= 2) return launch_dependent(rms_norm_kernel<T, kMode, 2>, blocks, 0, s, l);
-  if (each <= 4) return launch_dependent(rms_norm_kernel<T, kMode, 4>, blocks, 0, s, l);
-  return launch_dependent(rms_norm_kernel<T, kMode, 8>, blocks, 0, s, l);
+  if (each <= 1) return launch_dependent(rms_norm_kernel<T, kMode, 1>, blocks, kThreads, 0, s, l);
+  if (each <= 2) return launch_dependent(rms_norm_kernel<T, kMode, 2>, blocks, kThreads, 0, s, l);
+  if (each <= 4) return launch_dependent(rms_norm_kernel<T, kMode, 4>, blocks, kThreads, 0, s, l);
+  return launch_dependent(rms_norm_kernel<T, kMode, 8>, blocks, kThreads, 0, s, l);
 }
 
 template <typename T>
@@ -456,7 +459,7 @@ cudaError_t backward(const RmsNormLaunch& l, int blocks, cudaStream_t s) {
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
     }
-    return launch_dependent(kernel, blocks, smem, s, l);
+    return launch_dependent(kernel, blocks, kThreads, smem, s, l);
   };
   if (each <= 1) return go(rms_norm_backward_kernel<T, 1>);
   if (each <= 2) return go(rms_norm_backward_kernel<T, 2>);
@@ -486,7 +489,7 @@ cudaError_t launch_rms_norm_backward(RmsNormLaunch l, bool bf16, cudaStream_t s)
 }
 
 cudaError_t launch_rms_norm_weight(const RmsNormLaunch& l, float* dw, cudaStream_t s) {
-  return launch_dependent(rms_norm_weight_kernel, (l.dim + 31) / 32, 0, s,
+  return launch_dependent(rms_norm_weight_kernel, (l.dim + 31) / 32, 1024, 0, s,
                           static_cast<const float*>(l.parts), rms_norm_blocks(l.tokens, l.dim),
                           l.dim, dw, l.status);
 }
