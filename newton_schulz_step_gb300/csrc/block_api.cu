@@ -124,9 +124,9 @@ bool embedding_spec_ok(const muon_embedding_spec* s) {
          (s->tokens == 0 ||
           (s->ids && (reinterpret_cast<uintptr_t>(s->ids) & (s->id_bytes - 1)) == 0));
 }
-// Status block, sorted and unsorted ids and tokens, pieces of runs.
+// Status block, number of sorted tokens, sorted and unsorted ids and tokens, pieces of runs.
 size_t embedding_workspace(int tokens, int dim) {
-  return kStatusBytes + 4 * align256(static_cast<size_t>(tokens) * 4) +
+  return kStatusBytes + 256 + 4 * align256(static_cast<size_t>(tokens) * 4) +
          align256(embedding_parts(tokens, dim) * sizeof(float));
 }
 void fill_embedding(EmbeddingLaunch& L, const muon_embedding_spec* s) {
@@ -303,6 +303,8 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
     L.out_bf16 = dtable_dtype == MUON_BF16;
     L.status = static_cast<const unsigned int*>(workspace);
     uint8_t* p = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    L.count = reinterpret_cast<uint32_t*>(p);
+    p += 256;
     const size_t list = align256(static_cast<size_t>(t) * 4);
     for (int i = 0; i < 2; ++i) {
       L.keys[i] = reinterpret_cast<uint32_t*>(p);

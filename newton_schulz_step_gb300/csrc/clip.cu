@@ -86,21 +86,26 @@ __device__ __forceinline__ void store(const ClipTensor& T, long long e, const fl
   }
 }
 
-// First units of the launch's tensors in shared memory (a search among the launch's
-// arguments is a chain of misses of the constant cache).
-__device__ __forceinline__ void load_begins(const ClipLaunch& L, long long* begins) {
-  if (threadIdx.x < static_cast<unsigned>(L.n_tensors)) begins[threadIdx.x] = L.t[threadIdx.x].unit_begin;
+// The launch's table of tensors in shared memory: a search among a kernel's arguments is a
+// chain of misses of the constant cache, and this copy, before the wait for the kernel before,
+// costs nothing.  (Read through a generic address: a different word a lane.)
+__device__ __forceinline__ void load_table(const ClipLaunch& L, ClipTensor* table) {
+  static_assert(sizeof(ClipTensor) % 8 == 0, "whole words");
+  const unsigned long long* from = reinterpret_cast<const unsigned long long*>(&L.t[0]);
+  asm("" : "+l"(from));
+  unsigned long long* to = reinterpret_cast<unsigned long long*>(table);
+  const int words = L.n_tensors * static_cast<int>(sizeof(ClipTensor) / 8);
+  for (int i = threadIdx.x; i < words; i += kThreads) to[i] = from[i];
 }
 // Tensor of unit u: the last one that begins at or before it.
-__device__ __forceinline__ const ClipTensor& tensor_of(const ClipLaunch& L, const long long* begins,
-                                                       long long u) {
-  int lo = 0, hi = L.n_tensors - 1;
+__device__ __forceinline__ const ClipTensor& tensor_of(const ClipTensor* table, int n, long long u) {
+  int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (begins[mid] <= u) lo = mid;
+    if (table[mid].unit_begin <= u) lo = mid;
     else hi = mid - 1;
   }
-  return L.t[lo];
+  return table[lo];
 }
 
 // Sum over the block, the same for every thread and run.
@@ -124,9 +129,9 @@ __device__ __forceinline__ float root(double x) {
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_constant__ ClipLaunch L) {
   __shared__ double s_sum[kThreads / 32];
-  __shared__ long long s_begins[kMaxClipTensors];
+  __shared__ ClipTensor s_table[kMaxClipTensors];
   ptx::griddep_launch_dependents();
-  load_begins(L, s_begins);
+  load_table(L, s_table);
   __syncthreads();
   ptx::griddep_wait();
   if (ptx::status_set(L.status)) return;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
   for (long long u = blockIdx.x; u < L.total_units; u += gridDim.x) {
-    const ClipTensor& T = tensor_of(L, s_begins, u);
+    const ClipTensor& T = tensor_of(s_table, L.n_tensors, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     if (base + kClipUnit <= T.n) {
 #pragma unroll 1
@@ -172,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant__ ClipLaunch L) {
   __shared__ double s_sum[kThreads / 32];
-  __shared__ long long s_begins[kMaxClipTensors];
+  __shared__ ClipTensor s_table[kMaxClipTensors];
   ptx::griddep_launch_dependents();
-  load_begins(L, s_begins);
+  load_table(L, s_table);
   __syncthreads();
   ptx::griddep_wait();
   if (ptx::status_set(L.status)) return;
@@ -188,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
   };
   bool fetched = false;
   if (u >= 0) {
-    const ClipTensor& T = tensor_of(L, s_begins, u);
+    const ClipTensor& T = tensor_of(s_table, L.n_tensors, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     fetched = base + kClipUnit <= T.n;
     if (fetched) fetch(T, base);
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
   const float c = ratio >= 1.f ? 1.f : ratio;         // (a norm that is NaN stays one)
   if (L.in_place && c == 1.f) return;
   for (; u >= 0; u -= gridDim.x) {
-    const ClipTensor& T = tensor_of(L, s_begins, u);
+    const ClipTensor& T = tensor_of(s_table, L.n_tensors, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     if (base + kClipUnit <= T.n) {
 #pragma unroll 1

@@ -142,42 +142,84 @@ __device__ __forceinline__ uint32_t equal_lanes(uint32_t d, int bits, bool live)
   return same;
 }
 
-// Sorts (id, token) by `passes` digits of `bits` bits, least first; ids outside the table sort
-// behind the last row.  CTA r has the r-th contiguous part of the items, a warp a contiguous
-// part of it, and each pass keeps equal digits in order: counts a warp, a digit's place from
-// the counts of smaller digits, earlier CTAs and earlier warps, and its rank among the lanes.
+constexpr int kRounds = 8;             // items of a lane at a time
+struct Batch {
+  uint32_t key[kRounds], off[kRounds];
+  uint32_t live;                       // bit r: item r is there
+};
+// Adds a batch's digits to the warp's counters; off: place of an item among the warp's items
+// of its digit.
+__device__ __forceinline__ void rank_batch(Batch& b, uint32_t* mine, int shift, int bits) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const bool live = b.live >> r & 1u;
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const uint32_t d = b.key[r] >> shift & ((1u << bits) - 1u);
+    const uint32_t same = equal_lanes(d, bits, live);
+    const uint32_t rank = __popc(same & ((1u << lane) - 1u));
+    if (live) b.off[r] = mine[d] + rank;
+    __syncwarp();
+    if (live && rank == 0u) mine[d] += __popc(same);
+    __syncwarp();
+  }
+}
+
+// Sorts (id, token) by `passes` digits of `bits` bits, least first; tokens whose id is outside
+// the table are dropped, and their number is left in *L.count.  CTA r has the r-th contiguous
+// part of the items, a warp a contiguous part of it, and each pass keeps equal digits in order:
+// counts a warp, a digit's place from the counts of smaller digits, earlier CTAs and earlier
+// warps, and an item's place among its warp's.  A warp's items stay in registers between the
+// count and the placing while they are kRounds a lane (up to 65536 tokens); more are read and
+// ranked again.  8 SMs take 14 us for 32768 tokens in two passes of 8 bits.
 __device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
   uint32_t* const cnt = smem;                              // [warps][bins]
   uint32_t* const total = smem + kSortWarps * kMaxBins;    // [bins], read by the other CTAs
   uint32_t* const base = total + kMaxBins;                 // [bins]
-  uint32_t* const scan = base + kMaxBins;                  // [warps]
+  uint32_t* const scan = base + kMaxBins;                  // [warps + 1]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const uint32_t rank = ptx::cluster_ctarank();
   const int bins = 1 << L.bits;
-  // whole rounds of 32 a warp
-  const int per_warp = ((L.tokens + kSortCtas * kSortWarps * 32 - 1) / (kSortCtas * kSortWarps * 32)) * 32;
-  const long long begin = (static_cast<long long>(rank) * kSortWarps + warp) * per_warp;
-  const int i0 = static_cast<int>(min(begin, static_cast<long long>(L.tokens)));
-  const int i1 = static_cast<int>(min(begin + per_warp, static_cast<long long>(L.tokens)));
   uint32_t* const mine = cnt + warp * kMaxBins;
+  int items = L.tokens;
   for (int pass = 0; pass < L.passes; ++pass) {
     // the last pass ends in keys / order [0]
     const int to = (L.passes - 1 - pass) & 1, from = to ^ 1;
     const int shift = pass * L.bits;
-    auto key_at = [&](int i) -> uint32_t {
-      if (pass > 0) return __ldcg(L.keys[from] + i);
-      const int id = id_at(L.ids, L.wide, i, L.rows);
-      return id < 0 ? static_cast<uint32_t>(L.rows) : static_cast<uint32_t>(id);
+    // whole rounds of 32 a warp
+    constexpr int kPer = kSortCtas * kSortWarps * 32;
+    const int per_warp = static_cast<int>((static_cast<long long>(items) + kPer - 1) / kPer) * 32;
+    const long long begin = (static_cast<long long>(rank) * kSortWarps + warp) * per_warp;
+    const int i0 = static_cast<int>(min(begin, static_cast<long long>(items)));
+    const int i1 = static_cast<int>(min(begin + per_warp, static_cast<long long>(items)));
+    const bool one_batch = per_warp <= 32 * kRounds;
+    Batch b;
+    auto load = [&](int i) {           // items i + 32 r + lane
+      b.live = 0u;
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int at = i + 32 * r + lane;
+        b.key[r] = 0u;
+        bool live = at < i1;
+        if (live) {
+          if (pass > 0) {
+            b.key[r] = __ldcg(L.keys[from] + at);
+          } else {
+            const int id = id_at(L.ids, L.wide, at, L.rows);
+            live = id >= 0;
+            b.key[r] = static_cast<uint32_t>(id);
+          }
+        }
+        b.live |= static_cast<uint32_t>(live) << r;
+      }
     };
-    for (int b = lane; b < bins; b += 32) mine[b] = 0u;
+    load(i0);
+    for (int k = lane; k < bins; k += 32) mine[k] = 0u;
     __syncwarp();
-#pragma unroll 4
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-      const bool live = i < i1;
-      const uint32_t d = live ? (key_at(i) >> shift) & (bins - 1) : 0u;
-      const uint32_t same = equal_lanes(d, L.bits, live);
-      if (live && (__ffs(same) - 1) == lane) mine[d] += __popc(same);
-      __syncwarp();
+    rank_batch(b, mine, shift, L.bits);
+    for (long long i = static_cast<long long>(i0) + 32 * kRounds; i < i1; i += 32 * kRounds) {
+      load(static_cast<int>(i));
+      rank_batch(b, mine, shift, L.bits);
     }
     __syncthreads();
     // a thread a digit: places of the warps, the CTA's total
@@ -220,31 +262,42 @@ __device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
         if (lane >= o) y += z;
       }
       scan[lane] = y - own;
+      if (lane == 31) scan[kSortWarps] = y;
     }
     __syncthreads();
     if (tid < bins) base[tid] = scan[warp] + x - all + before;
+    items = static_cast<int>(scan[kSortWarps]);            // (less the dropped ones)
     __syncthreads();
-#pragma unroll 4
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-      const bool live = i < i1;
-      const uint32_t key = live ? key_at(i) : 0u;
-      const uint32_t token = live && pass > 0 ? __ldcg(L.order[from] + i) : static_cast<uint32_t>(i);
-      const uint32_t d = (key >> shift) & (bins - 1);
-      const uint32_t same = equal_lanes(d, L.bits, live);
-      uint32_t at = 0u;
-      if (live) at = base[d] + mine[d] + __popc(same & ((1u << lane) - 1u));
-      __syncwarp();
-      if (live && (__ffs(same) - 1) == lane) mine[d] += __popc(same);
-      __syncwarp();
-      if (live) {
-        __stcg(L.keys[to] + at, key);
-        __stcg(L.order[to] + at, token);
+    auto place = [&](int i, bool ranked) {
+      uint32_t token[kRounds];
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        token[r] = static_cast<uint32_t>(i + 32 * r + lane);
+        if (pass > 0 && (b.live >> r & 1u)) token[r] = __ldcg(L.order[from] + token[r]);
+      }
+      if (!ranked) rank_batch(b, mine, shift, L.bits);
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        if (!(b.live >> r & 1u)) continue;
+        const uint32_t d = b.key[r] >> shift & (bins - 1);
+        const uint32_t at = base[d] + b.off[r] + (ranked ? mine[d] : 0u);
+        __stcg(L.keys[to] + at, b.key[r]);
+        __stcg(L.order[to] + at, token[r]);
+      }
+    };
+    if (one_batch) {
+      place(i0, true);
+    } else {
+      for (long long i = i0; i < i1; i += 32 * kRounds) {
+        load(static_cast<int>(i));
+        place(static_cast<int>(i), false);
       }
     }
     // the other CTAs' stores of this pass are read by the next, and `total` is free again
     __threadfence();
     ptx::cluster_sync();
   }
+  if (rank == 0 && tid == 0) __stcg(L.count, static_cast<uint32_t>(items));
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1)
@@ -277,11 +330,6 @@ __global__ void __launch_bounds__(kSortThreads, 1)
 }
 
 // ------------------------------------------------------------ sums
-// Whether the sorted positions i and i + 1 hold one id; positions outside hold none.
-__device__ __forceinline__ bool joined(const uint32_t* keys, int i, int tokens) {
-  return i >= 0 && i + 1 < tokens && __ldcg(keys + i) == __ldcg(keys + i + 1);
-}
-
 template <typename O>
 __device__ __forceinline__ void store_row(const EmbeddingLaunch& L, uint32_t id, int c,
                                           float (&v)[8]) {
@@ -291,43 +339,49 @@ __device__ __forceinline__ void store_row(const EmbeddingLaunch& L, uint32_t id,
 }
 
 constexpr int kChunk = 32;             // sorted positions of a warp
-template <typename G> constexpr int kFlight = 32 / sizeof(G);   // rows of a warp in flight
+template <typename G> constexpr int kFlight = 16 / sizeof(G);   // rows of a warp in flight
 template <typename G, typename O>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     embedding_sum_kernel(const __grid_constant__ EmbeddingLaunch L) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  if (ptx::status_set(L.status)) return;
   const int lane = threadIdx.x & 31;
   const int groups = (L.dim + 255) / 256;
   const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(task / groups);
   const int c = static_cast<int>(task - static_cast<long long>(chunk) * groups) * 256 + lane * 8;
-  const int i0 = chunk * kChunk;
-  if (i0 >= L.tokens) return;
-  const int n = min(kChunk, L.tokens - i0);
-  const uint32_t key = lane < n ? __ldcg(L.keys[0] + i0 + lane) : 0xffffffffu;
-  const uint32_t token = lane < n ? __ldcg(L.order[0] + i0 + lane) : 0u;
+  const long long i0 = static_cast<long long>(chunk) * kChunk;
+  // everything that the rows depend on in one trip: the lists are allocated to L.tokens, of
+  // which the first *L.count positions are sorted tokens
+  const bool there = i0 + lane < L.tokens;
+  const bool failed = ptx::status_set(L.status);
+  const long long items = __ldcg(L.count);
+  uint32_t key = there ? __ldcg(L.keys[0] + i0 + lane) : 0u;
+  uint32_t token = there ? __ldcg(L.order[0] + i0 + lane) : 0u;
+  const uint32_t before = i0 > 0 ? __ldcg(L.keys[0] + i0 - 1) : 0u;
+  const uint32_t after = i0 + kChunk < L.tokens ? __ldcg(L.keys[0] + i0 + kChunk) : 0u;
+  if (failed || i0 >= items) return;
+  const int n = static_cast<int>(min(static_cast<long long>(kChunk), items - i0));
+  if (lane >= n) token = 0u;
   // bit i: a run begins at position i; the run at position 0 may have begun earlier
   const uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
-  const bool head_open = joined(L.keys[0], i0 - 1, L.tokens);
-  const bool tail_open = joined(L.keys[0], i0 + kChunk - 1, L.tokens);
+  const bool head_open = i0 > 0 && before == __shfl_sync(0xffffffffu, key, 0);
+  const bool tail_open = i0 + kChunk < items && after == __shfl_sync(0xffffffffu, key, kChunk - 1);
   const uint32_t begins = __ballot_sync(0xffffffffu, lane < n && (lane == 0 || key != prev));
   const bool on = c < L.dim;
+  const G* const column = static_cast<const G*>(L.dout) + (on ? c : 0);
   float acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   int begin = 0;
+#pragma unroll 1
   for (int p = 0; p < n; p += kFlight<G>) {
     Raw<G> raw[kFlight<G>];
 #pragma unroll
     for (int k = 0; k < kFlight<G>; ++k) {
+      // (positions past the last read token 0's row and are not added)
       const uint32_t t = __shfl_sync(0xffffffffu, token, (p + k) & 31);
-      const uint32_t id = __shfl_sync(0xffffffffu, key, (p + k) & 31);
-      raw[k].clear();
-      // (rows of ids outside the table are not read)
-      if (on && p + k < n && id < static_cast<uint32_t>(L.rows))
-        raw[k].load(static_cast<const G*>(L.dout) + t * L.dout_stride + c);
+      raw[k].load(column + t * L.dout_stride);
     }
 #pragma unroll
     for (int k = 0; k < kFlight<G>; ++k) {
@@ -344,7 +398,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
       if (i + 1 < n && !(begins >> (i + 1) & 1u)) continue;   // the run goes on in this chunk
       const uint32_t id = __shfl_sync(0xffffffffu, key, i);
-      if (!on || id >= static_cast<uint32_t>(L.rows)) continue;
+      if (!on) continue;
       const bool from_before = begin == 0 && head_open;
       const bool goes_on = i + 1 == n && tail_open;
       if (from_before || goes_on) {
@@ -363,23 +417,25 @@ __global__ void __launch_bounds__(kThreads)
     embedding_join_kernel(const __grid_constant__ EmbeddingLaunch L) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  if (ptx::status_set(L.status)) return;
   const int lane = threadIdx.x & 31;
   const int groups = (L.dim + 255) / 256;
   const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int chunk = static_cast<int>(task / groups);
   const int c = static_cast<int>(task - static_cast<long long>(chunk) * groups) * 256 + lane * 8;
-  const int last = chunk * kChunk + kChunk - 1;            // last position of the chunk
-  if (!joined(L.keys[0], last, L.tokens)) return;
-  const uint32_t id = __ldcg(L.keys[0] + last);
-  if (id >= static_cast<uint32_t>(L.rows)) return;
-  const int first = chunk * kChunk;
-  if (first > 0 && __ldcg(L.keys[0] + first - 1) == id) return;   // it began earlier
+  const long long first = static_cast<long long>(chunk) * kChunk, last = first + kChunk - 1;
+  const bool inside = last + 1 < L.tokens;
+  const bool failed = ptx::status_set(L.status);
+  const long long items = __ldcg(L.count);
+  const uint32_t id = inside ? __ldcg(L.keys[0] + last) : 0u;
+  const uint32_t after = inside ? __ldcg(L.keys[0] + last + 1) : 0u;
+  const uint32_t before = inside && first > 0 ? __ldcg(L.keys[0] + first - 1) : 0u;
+  if (failed || last + 1 >= items || id != after) return;
+  if (first > 0 && before == id) return;                   // it began earlier
   // chunks after this one that the run reaches: all up to the first that it does not fill
   int reach = 1;
   for (int k = chunk + 1;; k += 32) {
     const long long end = (static_cast<long long>(k) + lane) * kChunk + kChunk - 1;
-    const bool through = end + 1 < L.tokens && __ldcg(L.keys[0] + end) == id &&
+    const bool through = end + 1 < items && __ldcg(L.keys[0] + end) == id &&
                          __ldcg(L.keys[0] + end + 1) == id;
     const uint32_t stop = __ballot_sync(0xffffffffu, !through);
     if (stop != 0u) {
@@ -440,9 +496,9 @@ cudaError_t launch_embedding(const EmbeddingLaunch& l, bool table_bf16, int sms,
 }
 
 cudaError_t launch_embedding_sort(EmbeddingLaunch l, int sms, cudaStream_t s) {
-  // passes of at most 10 bits that cover 0..rows (rows itself: outside the table)
+  // passes of at most 10 bits that cover 0..rows - 1
   int bits = 1;
-  while (bits < 31 && (l.rows >> bits) != 0) ++bits;
+  while (bits < 31 && ((l.rows - 1) >> bits) != 0) ++bits;
   l.passes = (bits + 9) / 10;
   l.bits = (bits + l.passes - 1) / l.passes;
   const cudaError_t e = cudaFuncSetAttribute(

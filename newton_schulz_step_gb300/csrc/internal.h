@@ -410,6 +410,7 @@ struct EmbeddingLaunch {
   const void *ids, *table, *dout;
   void* out;                        // backward: the table's gradient
   uint32_t *keys[2], *order[2];     // backward: ids and tokens, sorted ones in [0]
+  uint32_t* count;                  // backward: tokens whose id is in the table
   float* parts;                     // backward: [chunks][2][dim] pieces of runs
   long long table_stride, dout_stride, out_stride;
   int wide;                         // ids are int64
