@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kSortThreads, 1)
   const uint4 zero = make_uint4(0, 0, 0, 0);
   long long i = static_cast<long long>(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
   if (L.out_stride == L.dim) {
+#pragma unroll 4
     for (; i < total; i += step) *reinterpret_cast<uint4*>(out + i * 16) = zero;
   } else {
     for (; i < total; i += step) {
@@ -412,16 +413,22 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // A run that begins in a chunk and goes on: its piece there, then those of the chunks after.
+// A warp adds a few pieces by itself; the pieces of longer runs (a token that makes up much of
+// a text) are shared by the block's warps, every eighth one each, and the warps' sums added in
+// order.
+constexpr int kAlone = 8;              // pieces
 template <typename O>
 __global__ void __launch_bounds__(kThreads)
     embedding_join_kernel(const __grid_constant__ EmbeddingLaunch L) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float s_sum[kWarps][256];
+  __shared__ int s_reach[kWarps];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int groups = (L.dim + 255) / 256;
-  const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int chunk = static_cast<int>(task / groups);
-  const int c = static_cast<int>(task - static_cast<long long>(chunk) * groups) * 256 + lane * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk0 = blockIdx.x * kWarps;                  // a warp a chunk, 256 columns a block
+  const int c = blockIdx.y * 256 + lane * 8;
+  const int chunk = chunk0 + warp;
   const long long first = static_cast<long long>(chunk) * kChunk, last = first + kChunk - 1;
   const bool inside = last + 1 < L.tokens;
   const bool failed = ptx::status_set(L.status);
@@ -429,11 +436,11 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t id = inside ? __ldcg(L.keys[0] + last) : 0u;
   const uint32_t after = inside ? __ldcg(L.keys[0] + last + 1) : 0u;
   const uint32_t before = inside && first > 0 ? __ldcg(L.keys[0] + first - 1) : 0u;
-  if (failed || last + 1 >= items || id != after) return;
-  if (first > 0 && before == id) return;                   // it began earlier
+  // it goes on, and did not begin earlier
+  const bool open = !failed && last + 1 < items && id == after && !(first > 0 && before == id);
   // chunks after this one that the run reaches: all up to the first that it does not fill
-  int reach = 1;
-  for (int k = chunk + 1;; k += 32) {
+  int reach = 0;
+  for (int k = chunk + 1; open; k += 32) {
     const long long end = (static_cast<long long>(k) + lane) * kChunk + kChunk - 1;
     const bool through = end + 1 < items && __ldcg(L.keys[0] + end) == id &&
                          __ldcg(L.keys[0] + end + 1) == id;
@@ -443,23 +450,59 @@ __global__ void __launch_bounds__(kThreads)
       break;
     }
   }
-  if (c >= L.dim) return;
-  float acc[8];
-  load8(L.parts + (static_cast<size_t>(chunk) * 2 + 1) * L.dim + c, acc);
-  const float* p = L.parts + static_cast<size_t>(chunk + 1) * 2 * L.dim + c;
-#pragma unroll 8
-  for (int k = 0; k < reach; ++k) {
-    float v[8];
-    load8(p + static_cast<size_t>(k) * 2 * L.dim, v);
+  const bool on = c < L.dim;
+  const float* const column = L.parts + (on ? c : 0);
+  auto piece = [&](int k, float (&v)[8]) {                 // k pieces after a chunk's: [k][0]
+    load8(column + static_cast<size_t>(k) * 2 * L.dim, v);
+  };
+  if (open && reach <= kAlone) {
+    float acc[8], v[8];
+    load8(column + (static_cast<size_t>(chunk) * 2 + 1) * L.dim, acc);
+#pragma unroll 4
+    for (int k = 1; k <= reach; ++k) {
+      piece(chunk + k, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+    }
+    if (on) store_row<O>(L, id, c, acc);
   }
-  store_row<O>(L, id, c, acc);
+  if (lane == 0) s_reach[warp] = open && reach > kAlone ? reach : 0;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) {
+    const int far = s_reach[w];
+    if (far == 0) continue;                                // (the same for every thread)
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    if (warp == 0) load8(column + (static_cast<size_t>(chunk0 + w) * 2 + 1) * L.dim, acc);
+#pragma unroll 8
+    for (int k = 1 + warp; k <= far; k += kWarps) {
+      float v[8];
+      piece(chunk0 + w + k, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+    }
+    store8(&s_sum[warp][lane * 8], acc);
+    __syncthreads();
+    if (warp == w) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        float v[8];
+        load8(&s_sum[i][lane * 8], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      }
+      if (on) store_row<O>(L, id, c, acc);
+    }
+    __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------ launchers
 template <typename K>
-cudaError_t launch_dependent(K kernel, long long blocks, int threads, int smem, int cluster,
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, int cluster,
                              cudaStream_t s, const EmbeddingLaunch& l) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -469,13 +512,44 @@ cudaError_t launch_dependent(K kernel, long long blocks, int threads, int smem, 
   attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, l);
+}
+
+// Clusters of the sort that fit on the current device at once, asked once a device.
+cudaError_t sort_clusters(int sms, int* out) {
+  static int cache[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (cache[dev] == 0) {
+    e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSortSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kSortCtas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kSortSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(kSortCtas * (sms / kSortCtas));
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, embedding_sort_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    cache[dev] = n < 1 ? 1 : n;
+  }
+  *out = cache[dev];
+  return cudaSuccess;
 }
 
 long long warp_tasks(const EmbeddingLaunch& l) {
@@ -486,7 +560,8 @@ long long warp_tasks(const EmbeddingLaunch& l) {
 
 cudaError_t launch_embedding(const EmbeddingLaunch& l, bool table_bf16, int sms, cudaStream_t s) {
   constexpr int kPer = kThreads / 32;
-  const long long blocks = std::min<long long>((1ll * l.tokens + kPer - 1) / kPer, 8ll * sms);
+  const dim3 blocks(static_cast<unsigned>(
+      std::min<long long>((1ll * l.tokens + kPer - 1) / kPer, 8ll * sms)));
   using B = __nv_bfloat16;
   if (table_bf16)
     return l.out_bf16 ? launch_dependent(embedding_kernel<B, B>, blocks, kThreads, 0, 1, s, l)
@@ -501,19 +576,21 @@ cudaError_t launch_embedding_sort(EmbeddingLaunch l, int sms, cudaStream_t s) {
   while (bits < 31 && ((l.rows - 1) >> bits) != 0) ++bits;
   l.passes = (bits + 9) / 10;
   l.bits = (bits + l.passes - 1) / l.passes;
-  const cudaError_t e = cudaFuncSetAttribute(
-      embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  int fit = 0;
+  const cudaError_t e = sort_clusters(sms, &fit);
   if (e != cudaSuccess) return e;
-  // the sort's cluster, and clusters that clear: one CTA an SM, at least one
+  // the sort's cluster, and clusters that clear: those that fit beside it (a second wave would
+  // take as long as the first), at least one
   const long long bytes = 1ll * l.rows * l.dim * (l.out_bf16 ? 2 : 4);
   const long long want = bytes / (kSortCtas * kSortThreads * 64) + 1;
-  const long long clear = std::max(1ll, std::min<long long>(sms / kSortCtas - 1, want));
-  return launch_dependent(embedding_sort_kernel, kSortCtas * (1 + clear), kSortThreads, kSortSmem,
-                          kSortCtas, s, l);
+  const long long clear = std::max(1ll, std::min<long long>(fit - 1, want));
+  return launch_dependent(embedding_sort_kernel,
+                          dim3(static_cast<unsigned>(kSortCtas * (1 + clear))), kSortThreads,
+                          kSortSmem, kSortCtas, s, l);
 }
 
 cudaError_t launch_embedding_sum(const EmbeddingLaunch& l, bool dout_bf16, cudaStream_t s) {
-  const long long blocks = (warp_tasks(l) + kThreads / 32 - 1) / (kThreads / 32);
+  const dim3 blocks(static_cast<unsigned>((warp_tasks(l) + kThreads / 32 - 1) / (kThreads / 32)));
   using B = __nv_bfloat16;
   auto go = [&](auto kernel) { return launch_dependent(kernel, blocks, kThreads, 0, 1, s, l); };
   if (dout_bf16)
@@ -522,10 +599,11 @@ cudaError_t launch_embedding_sum(const EmbeddingLaunch& l, bool dout_bf16, cudaS
 }
 
 cudaError_t launch_embedding_join(const EmbeddingLaunch& l, cudaStream_t s) {
-  const long long blocks = (warp_tasks(l) + kThreads / 32 - 1) / (kThreads / 32);
+  constexpr int kPer = kChunk * (kThreads / 32);
+  const dim3 grid(static_cast<unsigned>((1ll * l.tokens + kPer - 1) / kPer), (l.dim + 255) / 256);
   return l.out_bf16
-             ? launch_dependent(embedding_join_kernel<__nv_bfloat16>, blocks, kThreads, 0, 1, s, l)
-             : launch_dependent(embedding_join_kernel<float>, blocks, kThreads, 0, 1, s, l);
+             ? launch_dependent(embedding_join_kernel<__nv_bfloat16>, grid, kThreads, 0, 1, s, l)
+             : launch_dependent(embedding_join_kernel<float>, grid, kThreads, 0, 1, s, l);
 }
 
 size_t embedding_parts(int tokens, int dim) {
