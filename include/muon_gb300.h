@@ -102,7 +102,7 @@ typedef enum muon_kernel_kind {
   MUON_K_LINEAR = 14,        /* products with a weight matrix                   */
   MUON_K_LINEAR_FINISH = 15, /* sums of a split product, its epilogue           */
   MUON_K_LINEAR_DZ = 16,     /* dz = dout act'(z), and the bias' gradient       */
-  MUON_K_LINEAR_TOKEN = 17,  /* the product for up to 8 tokens                  */
+  MUON_K_LINEAR_TOKEN = 17,  /* the product for up to 4 tokens                  */
   MUON_K_RMS_NORM = 18,      /* residual's addition and RMS norm                */
   MUON_K_RMS_NORM_BWD = 19,  /* its gradients                                   */
   MUON_K_RMS_NORM_WEIGHT = 20, /* the weight's gradient: sum of the blocks' parts */

@@ -313,7 +313,7 @@ struct AttentionMaps {
 // ---- products with a weight matrix (linear.cu, linear_api.cu)
 // Pairs of CTAs that a plan counts on: one CTA on each of 152 SMs.
 constexpr int kLinearPairs = 76;
-constexpr int kTokenMax = 8;          // tokens that linear_token_kernel takes
+constexpr int kTokenMax = 4;          // tokens that linear_token_kernel takes
 constexpr int kBand = 8;              // pair rows of a band of tiles (see decode, linear.cu)
 
 // Division by a number known on the host: floor(n / d) for 0 <= n < 2^31 by a multiplication
@@ -479,7 +479,7 @@ cudaError_t launch_attention_dkv(const AttentionMaps& m, AttentionLaunch l, int 
 cudaError_t launch_linear(const LinearMaps& m, const LinearLaunch& l, int sms, cudaStream_t s);
 cudaError_t launch_linear_finish(const LinearLaunch& l, cudaStream_t s);
 cudaError_t launch_linear_dz(const LinearDz& d, cudaStream_t s);
-cudaError_t launch_linear_token(LinearToken p, int sms, cudaStream_t s);
+cudaError_t launch_linear_token(const LinearToken& p, int sms, cudaStream_t s);
 cudaError_t launch_rms_norm(RmsNormLaunch l, bool bf16, bool eight_bits, int sms, cudaStream_t s);
 // Blocks of the backward pass, each with a part of the weight's gradient.
 int rms_norm_blocks(int tokens, int dim);

@@ -661,35 +661,52 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------ a few tokens
-// y of up to kTokenMax tokens on the CUDA cores: a warp holds kRowsPerWarp rows of W, a lane
-// 8 consecutive columns of them at a time, and the tokens' x come from L1.  `ks` warps of a
-// block share the rows and split the columns; their sums meet in shared memory.
-constexpr int kTokenRows = 4;
+// y of up to kTokenMax tokens on the CUDA cores: a warp holds kRows rows of W, a lane 8
+// consecutive columns of them at a time, and the tokens' x come from L1.  `ks` warps of a block
+// share the rows and split the columns; their sums meet in shared memory.  Bound by reading W:
+// 11008 x 4096 (90 MB) takes 16.9 us for one token and 17.2 for two, 5.3 TB/s; what is missing
+// to the copy's rate is the start, of which the prefetch hides 0.6 to 3.7 us (17.5 and 21.0
+// without; with 4 steps ahead 22.7).  For 3 and 4 tokens 24.6 us (tensor cores: 26), for 8
+// it was 46.7, so that these go to the tensor cores.
+constexpr int kTokenWarps = 8;              // of a block, at most
+constexpr int kTokenRows = 4;               // (with 2: 22.7 us instead of 17.5 at the size below)
+constexpr int kTokenAhead = 2;              // steps of W that are asked into L2 ahead
 template <int kT>
-__global__ void __launch_bounds__(256) linear_token_kernel(const __grid_constant__ LinearToken P) {
-  __shared__ float s_sum[8][kTokenRows][kT];
+__global__ void __launch_bounds__(32 * kTokenWarps)
+    linear_token_kernel(const __grid_constant__ LinearToken P) {
+  constexpr int kRows = kTokenRows;
+  __shared__ float s_sum[kTokenWarps][kRows][kT];
   ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  if (ptx::status_set(P.status)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = 8 / P.ks;                           // row groups of a block
-  const int row0 = (blockIdx.x * per + warp / P.ks) * kTokenRows;
+  const int per = (blockDim.x >> 5) / P.ks;           // row groups of a block
+  const int row0 = (blockIdx.x * per + warp / P.ks) * kRows;
   const int part = warp % P.ks;
-  uint64_t acc[kTokenRows][kT];
+  uint64_t acc[kRows][kT];
 #pragma unroll
-  for (int r = 0; r < kTokenRows; ++r)
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
     for (int t = 0; t < kT; ++t) acc[r][t] = 0;
   const int whole = P.k & ~7;
-  const __nv_bfloat16* wp[kTokenRows];
+  const __nv_bfloat16* wp[kRows];
 #pragma unroll
-  for (int r = 0; r < kTokenRows; ++r)                // (rows past the last repeat it)
+  for (int r = 0; r < kRows; ++r)                     // (rows past the last repeat it)
     wp[r] = P.w + min(row0 + r, P.n - 1) * P.w_stride;
+  // the first of W into L2 while the kernel before ends (its stores to W, if any, are seen by
+  // the loads, which wait for it)
+#pragma unroll
+  for (int i = 0; i < kTokenAhead; ++i) {
+    const int c = (part * 32 + lane) * 8 + i * P.ks * 256;
+    if (c >= whole) break;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) asm volatile("prefetch.global.L2 [%0];" ::"l"(wp[r] + c));
+  }
+  ptx::griddep_wait();
+  const bool failed = ptx::status_set(P.status);      // (nothing is stored then)
 #pragma unroll 2
   for (int c = (part * 32 + lane) * 8; c < whole; c += P.ks * 256) {
-    uint4 w[kTokenRows];
+    uint4 w[kRows];
 #pragma unroll
-    for (int r = 0; r < kTokenRows; ++r) w[r] = __ldcs(reinterpret_cast<const uint4*>(wp[r] + c));
+    for (int r = 0; r < kRows; ++r) w[r] = __ldcs(reinterpret_cast<const uint4*>(wp[r] + c));
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(P.x + min(t, P.tokens - 1) * P.x_stride + c));
@@ -698,7 +715,7 @@ __global__ void __launch_bounds__(256) linear_token_kernel(const __grid_constant
 #pragma unroll
       for (int k = 0; k < 4; ++k) xp[k] = ptx::pair(bf_lo(xs[k]), bf_hi(xs[k]));
 #pragma unroll
-      for (int r = 0; r < kTokenRows; ++r) {
+      for (int r = 0; r < kRows; ++r) {
         const uint32_t ws[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(256) linear_token_kernel(const __grid_constant
     }
   }
 #pragma unroll
-  for (int r = 0; r < kTokenRows; ++r) {
+  for (int r = 0; r < kRows; ++r) {
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       const float2 a = ptx::unpair(acc[r][t]);
@@ -722,11 +739,12 @@ __global__ void __launch_bounds__(256) linear_token_kernel(const __grid_constant
     }
   }
   __syncthreads();
+  if (failed) return;
   // one thread a result
-  for (int i = threadIdx.x; i < per * kTokenRows * P.tokens; i += 256) {
-    const int t = i / (per * kTokenRows), rr = i - t * (per * kTokenRows);
-    const int grp = rr / kTokenRows, r = rr - grp * kTokenRows;
-    const int j = (blockIdx.x * per + grp) * kTokenRows + r;
+  for (int i = threadIdx.x; i < per * kRows * P.tokens; i += blockDim.x) {
+    const int t = i / (per * kRows), rr = i - t * (per * kRows);
+    const int grp = rr / kRows, r = rr - grp * kRows;
+    const int j = (blockIdx.x * per + grp) * kRows + r;
     if (j >= P.n) continue;
     float z = 0.f;
     for (int s = 0; s < P.ks; ++s) z += s_sum[grp * P.ks + s][r][t];
@@ -823,19 +841,23 @@ cudaError_t launch_linear_dz(const LinearDz& d, cudaStream_t s) {
                           s, d);
 }
 
-cudaError_t launch_linear_token(LinearToken p, int sms, cudaStream_t s) {
+template <int kT>
+static cudaError_t launch_token(LinearToken p, int sms, cudaStream_t s) {
   // as many warps on the rows' columns as it takes to give every SM 16 warps
-  const int groups = (p.n + kTokenRows - 1) / kTokenRows;
+  constexpr int kRows = kTokenRows;
+  const int groups = (p.n + kRows - 1) / kRows;
   p.ks = 1;
-  while (p.ks < 8 && groups * p.ks < 16 * sms && p.ks * 256 < p.k) p.ks *= 2;
-  const int per = 8 / p.ks;
-  const dim3 grid((groups + per - 1) / per);
+  while (p.ks < kTokenWarps && groups * p.ks < 16 * sms && p.ks * 256 < p.k) p.ks *= 2;
+  const int warps = std::max(4, p.ks), per = warps / p.ks;
+  return launch_dependent(linear_token_kernel<kT>, dim3((groups + per - 1) / per), 32 * warps, 0, 1,
+                          s, p);
+}
+
+cudaError_t launch_linear_token(const LinearToken& p, int sms, cudaStream_t s) {
   switch (p.tokens) {
-    case 1: return launch_dependent(linear_token_kernel<1>, grid, 256, 0, 1, s, p);
-    case 2: return launch_dependent(linear_token_kernel<2>, grid, 256, 0, 1, s, p);
-    case 3:
-    case 4: return launch_dependent(linear_token_kernel<4>, grid, 256, 0, 1, s, p);
-    default: return launch_dependent(linear_token_kernel<8>, grid, 256, 0, 1, s, p);
+    case 1: return launch_token<1>(p, sms, s);
+    case 2: return launch_token<2>(p, sms, s);
+    default: return launch_token<4>(p, sms, s);
   }
 }
 

@@ -7,7 +7,7 @@
 //   dx = r (G - h r^2 mean(G h)) + dresidual,  G = dy w;   dw = sum over tokens of dy h r
 //
 // All of it is bound by HBM: each element is read once and written once.  A row is held in
-// registers by a team of 32 to 256 threads, vectors of 8 elements a thread: one pass over
+// registers by a team of 32 to 512 threads, vectors of 8 elements a thread: one pass over
 // the data, one sum over the team (the gradients' two sums travel together).  Teams of a
 // block work on rows of their own; the rows' loads are issued a row ahead, so that they
 // travel while the row before is summed.  A power of two as the scale makes the division
@@ -20,7 +20,8 @@
 namespace muon {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // of a block; 512 where a row's team has as many
+constexpr int kMaxTeam = 512;
 
 using ptx::pair;
 
@@ -67,7 +68,7 @@ template <> struct Raw<float> {
   }
 };
 
-// A team of `threads` (a power of two, 32..256) and its scratch: sums of two rows' worth, so
+// A team of `threads` (a power of two, 32..512) and its scratch: sums of two rows' worth, so
 // that one barrier a sum is enough (a slot is written again two sums later).
 struct Team {
   int threads, index, at;              // size, team of the block, thread of the team
@@ -175,9 +176,9 @@ struct Weights {
 enum Mode { kForward, kEightBits };
 
 template <typename T, Mode kMode, int kV>
-__global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constant__ RmsNormLaunch L) {
+__global__ void __launch_bounds__(kMaxTeam) rms_norm_kernel(const __grid_constant__ RmsNormLaunch L) {
   constexpr bool kAhead = kV <= 2;     // a row ahead in registers
-  __shared__ float s_sums[kThreads / 32 * 4];
+  __shared__ float s_sums[kMaxTeam / 32 * 4];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   Team team;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
   const float inv_dim = 1.f / static_cast<float>(L.dim);
   Weights<kV> w;
   w.init(L.w, team.at, L.team, vecs);
-  const int teams = kThreads / L.team, stride = gridDim.x * teams;
+  const int teams = blockDim.x / L.team, stride = gridDim.x * teams;
   const T* const x = static_cast<const T*>(L.x);
   const T* const res = static_cast<const T*>(L.res);
 
@@ -284,11 +285,11 @@ __global__ void __launch_bounds__(kThreads) rms_norm_kernel(const __grid_constan
 // dx and a block's part of dw.  The team of a row keeps its columns' sums of dy h r; the
 // teams' sums are added in order, and rms_norm_weight_kernel adds the blocks'.
 template <typename T, int kV>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMaxTeam)
     rms_norm_backward_kernel(const __grid_constant__ RmsNormLaunch L) {
-  constexpr bool kAhead = kV <= 2;
+  constexpr bool kAhead = kV * sizeof(T) <= 4;   // (two fp32 vectors ahead do not fit)
   extern __shared__ float s_dw[];      // [teams][dim], where there is a weight
-  __shared__ float s_sums[kThreads / 32 * 4];
+  __shared__ float s_sums[kMaxTeam / 32 * 4];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   if (ptx::status_set(L.status)) return;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads)
   const float inv_dim = 1.f / static_cast<float>(L.dim);
   Weights<kV> w;
   w.init(L.w, team.at, L.team, vecs);
-  const int teams = kThreads / L.team, stride = gridDim.x * teams;
+  const int teams = blockDim.x / L.team, stride = gridDim.x * teams;
   const T* const x = static_cast<const T*>(L.x);       // h as stored
   const T* const dy = static_cast<const T*>(L.dy);
   const T* const res = static_cast<const T*>(L.res);   // dresidual
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kThreads)
     if (c < vecs) Raw<float>::store(s_dw + team.index * L.dim + 8 * c, dw[i]);
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < L.dim; d += kThreads) {
+  for (int d = threadIdx.x; d < L.dim; d += blockDim.x) {
     float s = 0.f;
     for (int k = 0; k < teams; ++k) s += s_dw[k * L.dim + d];
     __stcg(L.parts + static_cast<size_t>(blockIdx.x) * L.dim + d, s);
@@ -432,39 +433,39 @@ cudaError_t launch_dependent(K kernel, int blocks, int threads, int smem, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Threads of a row's team: two vectors a thread, while that makes 32 to 256 of them.
+// Threads of a row's team: two vectors a thread, while that makes 32 to 512 of them.
 int team_of(int dim) {
   int t = 32;
-  while (t < kThreads && 2 * t < dim / 8) t *= 2;
+  while (t < kMaxTeam && 2 * t < dim / 8) t *= 2;
   return t;
 }
+int threads_of(int team) { return std::max(team, kThreads); }
 
 template <typename T, Mode kMode>
 cudaError_t forward(RmsNormLaunch l, int sms, cudaStream_t s) {
-  const int per = kThreads / l.team, each = (l.dim / 8 + l.team - 1) / l.team;
+  const int threads = threads_of(l.team), per = threads / l.team;
+  const int each = (l.dim / 8 + l.team - 1) / l.team;
   const int blocks = std::min((l.tokens + per - 1) / per, 8 * sms);
-  if (each <= 1) return launch_dependent(rms_norm_kernel<T, kMode, 1>, blocks, kThreads, 0, s, l);
-  if (each <= 2) return launch_dependent(rms_norm_kernel<T, kMode, 2>, blocks, kThreads, 0, s, l);
-  if (each <= 4) return launch_dependent(rms_norm_kernel<T, kMode, 4>, blocks, kThreads, 0, s, l);
-  return launch_dependent(rms_norm_kernel<T, kMode, 8>, blocks, kThreads, 0, s, l);
+  if (each <= 1) return launch_dependent(rms_norm_kernel<T, kMode, 1>, blocks, threads, 0, s, l);
+  if (each <= 2) return launch_dependent(rms_norm_kernel<T, kMode, 2>, blocks, threads, 0, s, l);
+  return launch_dependent(rms_norm_kernel<T, kMode, 4>, blocks, threads, 0, s, l);
 }
 
 template <typename T>
 cudaError_t backward(const RmsNormLaunch& l, int blocks, cudaStream_t s) {
-  const int each = (l.dim / 8 + l.team - 1) / l.team;
-  const int smem = l.parts != nullptr ? kThreads / l.team * l.dim * 4 : 0;
+  const int threads = threads_of(l.team), each = (l.dim / 8 + l.team - 1) / l.team;
+  const int smem = l.parts != nullptr ? threads / l.team * l.dim * 4 : 0;
   auto go = [&](auto kernel) -> cudaError_t {
     if (smem > 48 * 1024) {
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
     }
-    return launch_dependent(kernel, blocks, kThreads, smem, s, l);
+    return launch_dependent(kernel, blocks, threads, smem, s, l);
   };
   if (each <= 1) return go(rms_norm_backward_kernel<T, 1>);
   if (each <= 2) return go(rms_norm_backward_kernel<T, 2>);
-  if (each <= 4) return go(rms_norm_backward_kernel<T, 4>);
-  return go(rms_norm_backward_kernel<T, 8>);
+  return go(rms_norm_backward_kernel<T, 4>);
 }
 
 }  // namespace
@@ -478,7 +479,7 @@ cudaError_t launch_rms_norm(RmsNormLaunch l, bool bf16, bool eight_bits, int sms
 }
 
 int rms_norm_blocks(int tokens, int dim) {
-  const int per = kThreads / team_of(dim);
+  const int team = team_of(dim), per = threads_of(team) / team;
   return std::min((tokens + per - 1) / per, kRmsNormMaxBlocks);
 }
 
