@@ -232,6 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   ab.peer_flag = ptx::mapa_shared(ptx::smem_u32(const_cast<const int*>(abort_flag)),
                                   static_cast<uint32_t>(rank ^ 1));
   ab.status = L.status;
+  // An earlier failure on this workspace: the products run, and nothing is stored.  (Every warp
+  // reads the word beside its first steps: a decision common to the pair before them cost each
+  // launch 0.6 us.)  Waits that find it set later give up; after an earlier failure they do not
+  // look at it, so that the pair ends in step.
+  const bool failed = ptx::status_set(ab.status);
+  const unsigned int* const watched = failed ? nullptr : ab.status;
   if (warp == 0) {
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(full), 0);
     int stage = 0;
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap *ma = &M.a[it.p], *mb = &M.b[it.p];
       const int row = (2 * it.pr + rank) * kTileM, col = it.tn * kBN + rank * (kBN / 2);
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        ok = ptx::mbar_wait(&empty[stage], phase ^ 1u, ab.flag, ab.status);
+        ok = ptx::mbar_wait(&empty[stage], phase ^ 1u, ab.flag, watched);
         __syncwarp();
         if (!ok) break;
         uint8_t* const sa = ring + stage * C::kStageBytes;
@@ -303,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
         const uint32_t idesc = ptx::idesc_bf16(2 * kTileM, kBN, b_mn, a_mn);
         // both CTAs' epilogues have read this accumulator
-        ok = ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1u, ab.flag, ab.status);
+        ok = ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1u, ab.flag, watched);
         __syncwarp();
         ptx::tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * kBN);
         for (int kb = it.kb0; ok && kb < it.kb1; ++kb) {
-          ok = ptx::mbar_wait(&full[stage], phase, ab.flag, ab.status);
+          ok = ptx::mbar_wait(&full[stage], phase, ab.flag, watched);
           __syncwarp();
           if (!ok) break;
           const uint32_t sa = ptx::smem_u32(ring + stage * C::kStageBytes);
@@ -352,9 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* const my_in = in_bar + e * kSlots;
     int acc = 0, slot = 0;
     uint32_t acc_phase = 0, in_par = 0, in_armed = 0;
-    // an earlier failure on this workspace: products run, but nothing is stored (the word is
-    // read beside the first loads; a check before them cost every launch a trip to L2)
-    const bool skip = ptx::status_set(ab.status);
+    const bool skip = failed;
     for (int i = first; i < L.items; i += stride) {
       const Item it = decode(L, i);
       const LinearProblem& P = L.prob[it.p];
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (has_bias && units > 0) fetch_bias(c0);
-      bool ok = ptx::mbar_wait(&acc_full[acc], acc_phase, ab.flag, ab.status);
+      bool ok = ptx::mbar_wait(&acc_full[acc], acc_phase, ab.flag, watched);
       __syncwarp();
       ptx::tc_fence_after();
       const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -420,6 +424,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int j0 = c0 + u * 64;
+        // A TMA store writes whole units of 16 bytes: columns up to the next multiple of 8.  The
+        // block at the end of a row that ends inside a unit is stored by the lanes.
+        const bool ragged = j0 + 64 > P.n && (P.n & 7) != 0;
+        auto store_row = [&](__nv_bfloat16* to, long long stride) {
+          if (i0 + lane >= P.m) return;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = z[8 * q + j];
+            store8(to + (i0 + lane) * stride, j0 + 8 * q, P.n, v);
+          }
+        };
         if (has_bias) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -430,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (u + 1 < units) fetch_bias(j0 + 64);
         }
-        if (has_z) {
+        if (has_z && ragged) {
+          store_row(P.z, P.z_stride);
+        } else if (has_z) {
           const int zs = has_res ? 1 : slot;
           if (lane == 0) {
             // the slot's last store has read it (with a residual only slot 1 is free)
@@ -451,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ys = slot;
         if (has_res) {
           ys = has_z ? 0 : u;
-          ok = ptx::mbar_wait(&my_in[ys], (in_par >> ys) & 1u, ab.flag, ab.status);
+          ok = ptx::mbar_wait(&my_in[ys], (in_par >> ys) & 1u, ab.flag, watched);
           __syncwarp();
           if (!ok) break;
           in_par ^= 1u << ys;
@@ -468,16 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) ptx::bulk_wait_read<kSlots - 1>();
           __syncwarp();
         }
-        stage_row(slots + ys * kSlotBytes, lane, z);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::tma_store_3d(&M.out[it.p], j0, i0, 0, slots + ys * kSlotBytes);
-          ptx::bulk_commit();
+        if (ragged) {
+          store_row(P.out, P.out_stride);
+        } else {
+          stage_row(slots + ys * kSlotBytes, lane, z);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_3d(&M.out[it.p], j0, i0, 0, slots + ys * kSlotBytes);
+            ptx::bulk_commit();
+          }
+          if (!has_res) slot ^= 1;
         }
-        if (!has_res) {
-          slot ^= 1;
-        } else if (has_z && u + 1 < units) {
+        if (has_res && has_z && u + 1 < units) {
           if (lane == 0) {
             ptx::bulk_wait_read<0>();
             ptx::mbar_arrive_expect_tx(&my_in[0], kSlotBytes);

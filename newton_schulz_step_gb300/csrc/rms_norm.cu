@@ -175,8 +175,8 @@ struct Weights {
 
 enum Mode { kForward, kEightBits };
 
-template <typename T, Mode kMode, int kV>
-__global__ void __launch_bounds__(kMaxTeam) rms_norm_kernel(const __grid_constant__ RmsNormLaunch L) {
+template <typename T, Mode kMode, int kV, bool kRes>
+__global__ void __launch_bounds__(kMaxTeam, sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(const __grid_constant__ RmsNormLaunch L) {
   constexpr bool kAhead = kV <= 2;     // a row ahead in registers
   __shared__ float s_sums[kMaxTeam / 32 * 4];
   ptx::griddep_launch_dependents();
@@ -192,18 +192,18 @@ __global__ void __launch_bounds__(kMaxTeam) rms_norm_kernel(const __grid_constan
   w.init(L.w, team.at, L.team, vecs);
   const int teams = blockDim.x / L.team, stride = gridDim.x * teams;
   const T* const x = static_cast<const T*>(L.x);
-  const T* const res = static_cast<const T*>(L.res);
+  const T* const res = static_cast<const T*>(L.res);   // (kRes)
 
-  Raw<T> rx[kV], rr[kV];
+  Raw<T> rx[kV], rr[kRes ? kV : 1];
   auto load = [&](int row) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int c = team.at + i * L.team;
       rx[i].clear();
-      rr[i].clear();
+      if constexpr (kRes) rr[i].clear();
       if (row < L.tokens && c < vecs) {
         rx[i].load(x + row * L.x_stride + 8 * c);
-        if (res != nullptr) rr[i].load(res + row * L.res_stride + 8 * c);
+        if constexpr (kRes) rr[i].load(res + row * L.res_stride + 8 * c);
       }
     }
   };
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMaxTeam) rms_norm_kernel(const __grid_constan
     for (int i = 0; i < kV; ++i) {
       const int c = team.at + i * L.team;
       rx[i].get(h[i]);
-      if (res != nullptr) {
+      if constexpr (kRes) {
         float r[8];
         rr[i].get(r);
 #pragma unroll
@@ -433,22 +433,32 @@ cudaError_t launch_dependent(K kernel, int blocks, int threads, int smem, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Threads of a row's team: two vectors a thread, while that makes 32 to 512 of them.
-int team_of(int dim) {
+// Threads of a row's team: two vectors a thread, while that makes 32 to `most` of them.
+int team_of(int dim, int most) {
   int t = 32;
-  while (t < kMaxTeam && 2 * t < dim / 8) t *= 2;
+  while (t < most && 2 * t < dim / 8) t *= 2;
   return t;
 }
+// Forward, four vectors a thread and more blocks on an SM are better than a row ahead (4096 rows
+// of 8192: 43 us with teams of 256, 51 with 512); backward it is the other way (88 and 58).
+int forward_team(int dim) { return team_of(dim, dim / 8 <= 4 * kThreads ? kThreads : kMaxTeam); }
+int backward_team(int dim) { return team_of(dim, kMaxTeam); }
 int threads_of(int team) { return std::max(team, kThreads); }
 
-template <typename T, Mode kMode>
-cudaError_t forward(RmsNormLaunch l, int sms, cudaStream_t s) {
+template <typename T, Mode kMode, bool kRes>
+cudaError_t forward_as(const RmsNormLaunch& l, int sms, cudaStream_t s) {
   const int threads = threads_of(l.team), per = threads / l.team;
   const int each = (l.dim / 8 + l.team - 1) / l.team;
   const int blocks = std::min((l.tokens + per - 1) / per, 8 * sms);
-  if (each <= 1) return launch_dependent(rms_norm_kernel<T, kMode, 1>, blocks, threads, 0, s, l);
-  if (each <= 2) return launch_dependent(rms_norm_kernel<T, kMode, 2>, blocks, threads, 0, s, l);
-  return launch_dependent(rms_norm_kernel<T, kMode, 4>, blocks, threads, 0, s, l);
+  auto go = [&](auto kernel) { return launch_dependent(kernel, blocks, threads, 0, s, l); };
+  if (each <= 1) return go(rms_norm_kernel<T, kMode, 1, kRes>);
+  if (each <= 2) return go(rms_norm_kernel<T, kMode, 2, kRes>);
+  return go(rms_norm_kernel<T, kMode, 4, kRes>);
+}
+template <typename T, Mode kMode>
+cudaError_t forward(const RmsNormLaunch& l, int sms, cudaStream_t s) {
+  return l.res != nullptr ? forward_as<T, kMode, true>(l, sms, s)
+                          : forward_as<T, kMode, false>(l, sms, s);
 }
 
 template <typename T>
@@ -471,7 +481,7 @@ cudaError_t backward(const RmsNormLaunch& l, int blocks, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rms_norm(RmsNormLaunch l, bool bf16, bool eight_bits, int sms, cudaStream_t s) {
-  l.team = team_of(l.dim);
+  l.team = forward_team(l.dim);
   if (bf16)
     return eight_bits ? forward<__nv_bfloat16, kEightBits>(l, sms, s)
                       : forward<__nv_bfloat16, kForward>(l, sms, s);
@@ -479,12 +489,12 @@ cudaError_t launch_rms_norm(RmsNormLaunch l, bool bf16, bool eight_bits, int sms
 }
 
 int rms_norm_blocks(int tokens, int dim) {
-  const int team = team_of(dim), per = threads_of(team) / team;
+  const int team = backward_team(dim), per = threads_of(team) / team;
   return std::min((tokens + per - 1) / per, kRmsNormMaxBlocks);
 }
 
 cudaError_t launch_rms_norm_backward(RmsNormLaunch l, bool bf16, cudaStream_t s) {
-  l.team = team_of(l.dim);
+  l.team = backward_team(l.dim);
   const int blocks = rms_norm_blocks(l.tokens, l.dim);
   return bf16 ? backward<__nv_bfloat16>(l, blocks, s) : backward<float>(l, blocks, s);
 }

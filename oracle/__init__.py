@@ -20,3 +20,4 @@ from .muon_oracle import (  # noqa: F401
 )
 from .adam_oracle import ADAM_BETAS, ADAM_EPS, ADAM_LR, adam_step  # noqa: F401,E402
 from . import attention_oracle  # noqa: F401,E402
+from . import block_oracle  # noqa: F401,E402
