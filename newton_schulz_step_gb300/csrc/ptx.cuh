@@ -105,18 +105,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
       : "memory");
 }
 
-// One try suspends the thread for up to kTryNs: threads that wait by trying again and again
-// take shared-memory cycles from the products (products of 8192 x 2048 x 8192 to
-// 16384 x 4096 x 4096 took 8-13 % longer without the hint).
-constexpr uint32_t kTryNs = 10000;
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kTryNs)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -129,19 +125,47 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
                                           const unsigned int* status = nullptr,
                                           uint64_t timeout_ns = kWaitTimeoutNs) {
   if (mbar_try_wait(bar, parity)) return true;
-  // (reading %globaltimer takes longer than most waits: not before the 64th try)
-  uint64_t t0 = 0;
+  const uint64_t t0 = globaltimer();
   uint32_t spins = 0;
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((++spins & 63u) == 0u) {
       if (abort_flag != nullptr && *abort_flag) return false;
-      const uint64_t now = globaltimer();
-      if (t0 == 0) t0 = now;
-      const uint64_t dt = now - t0;
+      const uint64_t dt = globaltimer() - t0;
       if (dt > timeout_ns) return false;
       if (dt > kStatusPollNs && status_set(status)) return false;
     }
+  }
+}
+
+// The same with tries that suspend the thread for up to kTryNs: threads that try again and
+// again take shared-memory cycles from the products beside them.  (linear_gemm_kernel's products
+// of 8192 x 2048 x 8192 to 16384 x 4096 x 4096 took 8-13 % longer without; the attention kernels,
+// whose steps are shorter than the way back from the suspension, take 4-6 % longer with it.)
+constexpr uint32_t kTryNs = 10000;
+__device__ __forceinline__ bool mbar_try_suspend(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity,
+                                                    const volatile int* abort_flag,
+                                                    const unsigned int* status = nullptr,
+                                                    uint64_t timeout_ns = kWaitTimeoutNs) {
+  if (mbar_try_suspend(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (mbar_try_suspend(bar, parity)) return true;
+    if (abort_flag != nullptr && *abort_flag) return false;
+    const uint64_t dt = globaltimer() - t0;
+    if (dt > timeout_ns) return false;
+    if (dt > kStatusPollNs && status_set(status)) return false;
   }
 }
 
