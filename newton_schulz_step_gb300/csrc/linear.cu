@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap *ma = &M.a[it.p], *mb = &M.b[it.p];
       const int row = (2 * it.pr + rank) * kTileM, col = it.tn * kBN + rank * (kBN / 2);
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        ok = ptx::mbar_wait_suspended(&empty[stage], phase ^ 1u, ab.flag, watched);
+        ok = ptx::mbar_wait(&empty[stage], phase ^ 1u, ab.flag, watched);
         __syncwarp();
         if (!ok) break;
         uint8_t* const sa = ring + stage * C::kStageBytes;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(armed & (1u << s))) continue;
       const uint64_t spent = ptx::globaltimer() - t0;
       if (spent >= ptx::kWaitTimeoutNs ||
-          !ptx::mbar_wait_suspended(&empty[s], (armed_parity >> s) & 1u, nullptr, nullptr,
+          !ptx::mbar_wait(&empty[s], (armed_parity >> s) & 1u, nullptr, nullptr,
                           ptx::kWaitTimeoutNs - spent)) {
         give_up(ab, kErrTimeoutDrain);
         break;
@@ -309,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
         const uint32_t idesc = ptx::idesc_bf16(2 * kTileM, kBN, b_mn, a_mn);
         // both CTAs' epilogues have read this accumulator
-        ok = ptx::mbar_wait_suspended(&acc_empty[acc], acc_phase ^ 1u, ab.flag, watched);
+        ok = ptx::mbar_wait(&acc_empty[acc], acc_phase ^ 1u, ab.flag, watched);
         __syncwarp();
         ptx::tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * kBN);
         for (int kb = it.kb0; ok && kb < it.kb1; ++kb) {
-          ok = ptx::mbar_wait_suspended(&full[stage], phase, ab.flag, watched);
+          ok = ptx::mbar_wait(&full[stage], phase, ab.flag, watched);
           __syncwarp();
           if (!ok) break;
           const uint32_t sa = ptx::smem_u32(ring + stage * C::kStageBytes);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every product has completed before TMEM is freed
       if (ptx::elect_one()) ptx::mma_commit_pair(drain, 1);
       __syncwarp();
-      if (!ptx::mbar_wait_suspended(drain, 0, nullptr) && lane == 0) give_up(ab, kErrTimeoutDrain);
+      if (!ptx::mbar_wait(drain, 0, nullptr) && lane == 0) give_up(ab, kErrTimeoutDrain);
       __syncwarp();
     }
   } else {
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       if (has_bias && units > 0) fetch_bias(c0);
-      bool ok = ptx::mbar_wait_suspended(&acc_full[acc], acc_phase, ab.flag, watched);
+      bool ok = ptx::mbar_wait(&acc_full[acc], acc_phase, ab.flag, watched);
       __syncwarp();
       ptx::tc_fence_after();
       const uint32_t t0 = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ys = slot;
         if (has_res) {
           ys = has_z ? 0 : u;
-          ok = ptx::mbar_wait_suspended(&my_in[ys], (in_par >> ys) & 1u, ab.flag, watched);
+          ok = ptx::mbar_wait(&my_in[ys], (in_par >> ys) & 1u, ab.flag, watched);
           __syncwarp();
           if (!ok) break;
           in_par ^= 1u << ys;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) give_up(ab, kErrTimeoutEpilogue);
         // copies still in flight land within microseconds
         for (int s = 0; s < kSlots; ++s)
-          if (in_armed & (1u << s)) ptx::mbar_wait_suspended(&my_in[s], (in_par >> s) & 1u, nullptr);
+          if (in_armed & (1u << s)) ptx::mbar_wait(&my_in[s], (in_par >> s) & 1u, nullptr);
         __syncwarp();
         break;
       }

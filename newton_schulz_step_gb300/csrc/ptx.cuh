@@ -138,37 +138,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
-// The same with tries that suspend the thread for up to kTryNs: threads that try again and
-// again take shared-memory cycles from the products beside them.  (linear_gemm_kernel's products
-// of 8192 x 2048 x 8192 to 16384 x 4096 x 4096 took 8-13 % longer without; the attention kernels,
-// whose steps are shorter than the way back from the suspension, take 4-6 % longer with it.)
-constexpr uint32_t kTryNs = 10000;
-__device__ __forceinline__ bool mbar_try_suspend(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kTryNs)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ bool mbar_wait_suspended(uint64_t* bar, uint32_t parity,
-                                                    const volatile int* abort_flag,
-                                                    const unsigned int* status = nullptr,
-                                                    uint64_t timeout_ns = kWaitTimeoutNs) {
-  if (mbar_try_suspend(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  while (true) {
-    if (mbar_try_suspend(bar, parity)) return true;
-    if (abort_flag != nullptr && *abort_flag) return false;
-    const uint64_t dt = globaltimer() - t0;
-    if (dt > timeout_ns) return false;
-    if (dt > kStatusPollNs && status_set(status)) return false;
-  }
-}
-
 // ------------------------------------------------------- global counters
 __device__ __forceinline__ unsigned int ld_acquire_gpu(const unsigned int* p) {
   unsigned int v;
