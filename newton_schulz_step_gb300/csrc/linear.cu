@@ -166,6 +166,15 @@ __device__ __forceinline__ void stage_row(uint8_t* blk, int r, const float (&v)[
   for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(blk + sw128(r, 8 * q)) = pack8(v + 8 * q);
 }
 
+// Arrive on the even CTA's barrier, with no memory of this thread to publish: what it releases is
+// an accumulator that it has read into registers.  (ptx::mbar_arrive_cluster's release at cluster
+// scope waits for the stores before it, 2000 clocks a tile.)
+__device__ __forceinline__ void arrive_even(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                   ptx::mapa_shared(ptx::smem_u32(bar), 0))
+               : "memory");
+}
+
 struct Abort {
   volatile int* flag;          // ends every wait of this CTA
   uint32_t peer_flag;          // ... of the pair's other CTA (shared::cluster address)
@@ -371,12 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_arrive_expect_tx(&my_in[u], kSlotBytes);
         ptx::tma_load_3d(slots + u * kSlotBytes, &M.res[it.p], c0 + 64 * u, i0, 0, &my_in[u]);
       };
-      if (has_res) {
-        if (lane == 0) {
+      // Without z both slots are free for this tile's blocks once the last tile's stores have read
+      // them: one wait, before the one for the products (each takes 400 clocks, waited for or not).
+      if (!has_z || has_res) {
+        if (ptx::elect_one()) {
           ptx::bulk_wait_read<0>();
-          for (int u = 0; u < units && (u == 0 || !has_z); ++u) fetch(u);
+          if (has_res)
+            for (int u = 0; u < units && (u == 0 || !has_z); ++u) fetch(u);
         }
-        in_armed = units > 0 ? (has_z ? 1u : (1u << units) - 1u) : 0u;
+        if (has_res) in_armed = units > 0 ? (has_z ? 1u : (1u << units) - 1u) : 0u;
         __syncwarp();
       }
       // the first block's bias travels while the products run, the second's with the first's
@@ -451,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_row(P.z, P.z_stride);
         } else if (has_z) {
           const int zs = has_res ? 1 : slot;
-          if (lane == 0) {
+          if (ptx::elect_one()) {
             // the slot's last store has read it (with a residual only slot 1 is free)
             if (has_res) ptx::bulk_wait_read<0>();
             else ptx::bulk_wait_read<kSlots - 1>();
@@ -460,14 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage_row(slots + zs * kSlotBytes, lane, z);
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (ptx::elect_one()) {
             ptx::tma_store_3d(&M.z[it.p], j0, i0, 0, slots + zs * kSlotBytes);
             ptx::bulk_commit();
           }
           if (!has_res) slot ^= 1;
         }
         activate(z, P.act);
-        int ys = slot;
+        int ys = has_z ? slot : u;
         if (has_res) {
           ys = has_z ? 0 : u;
           ok = ptx::mbar_wait(&my_in[ys], (in_par >> ys) & 1u, ab.flag, watched);
@@ -483,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[8 * q + j] += r[j];
           }
-        } else {
-          if (lane == 0) ptx::bulk_wait_read<kSlots - 1>();
+        } else if (has_z) {
+          if (ptx::elect_one()) ptx::bulk_wait_read<kSlots - 1>();
           __syncwarp();
         }
         if (ragged) {
@@ -493,14 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage_row(slots + ys * kSlotBytes, lane, z);
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (ptx::elect_one()) {
             ptx::tma_store_3d(&M.out[it.p], j0, i0, 0, slots + ys * kSlotBytes);
             ptx::bulk_commit();
           }
-          if (!has_res) slot ^= 1;
+          if (has_z && !has_res) slot ^= 1;
         }
         if (has_res && has_z && u + 1 < units) {
-          if (lane == 0) {
+          if (ptx::elect_one()) {
             ptx::bulk_wait_read<0>();
             ptx::mbar_arrive_expect_tx(&my_in[0], kSlotBytes);
             ptx::tma_load_3d(slots, &M.res[it.p], j0 + 64, i0, 0, &my_in[0]);
@@ -519,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&acc_empty[acc]), 0));
+      if (ptx::elect_one()) arrive_even(&acc_empty[acc]);
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) ptx::bulk_wait_read<0>();
+    if (ptx::elect_one()) ptx::bulk_wait_read<0>();
     __syncwarp();
   }
   __syncwarp();
