@@ -6,6 +6,7 @@
 // allocates device memory.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -46,24 +47,29 @@ struct Product {
   int m, n, k;
 };
 
-// Estimated clocks of a launch of `count` products with tiles bn wide and the given splits.
-// A 64-deep step of a 256 x 256 tile takes the tensor cores 512 clocks; of a 256 x 128 tile
-// half that, but its operands, 24 KB a CTA, were not seen to arrive in less than 420.
+// Estimated clocks of a call's launches with `count` products, tiles bn wide and the given splits.
+// A 64-deep step of a 256 x 256 tile takes the tensor cores 512 clocks (530 measured); of a
+// 256 x 128 tile half that, but its operands, 24 KB a CTA, were not seen to arrive in less than
+// 420.  A tile takes its epilogue 8 clocks a column if the products are over sooner.  Sums of
+// splits: a launch, their way to L2 and back, and a trip to L2 for every four of them.
+// (Swept over both widths and 1 to 16 splits on 16 shapes of 33 to 8192 tokens, 64 to 11008 wide:
+// the choice was the fastest or within 14 % of it.)
 double plan_clocks(const Product* p, int count, int bn, const int* splits) {
   const double step = bn == 256 ? 530.0 : 420.0, fixed = 2500.0;
-  double work = 0.0, longest = 0.0, bytes = 0.0, waves = 0.0;
+  double work = 0.0, longest = 0.0, finish = 0.0, waves = 0.0;
   for (int i = 0; i < count; ++i) {
     const double tiles = 1.0 * cdiv(p[i].m, 256) * cdiv(p[i].n, bn);
-    const double len = std::max(cdiv(cdiv(p[i].k, kTileK), splits[i]) * step, 3.0 * bn);
+    const double len = std::max(cdiv(cdiv(p[i].k, kTileK), splits[i]) * step, 8.0 * bn);
     const double items = tiles * splits[i];
     work += items * len;
     longest = std::max(longest, len);
-    waves += static_cast<double>((static_cast<long long>(items) + kLinearPairs - 1) / kLinearPairs) * len;
-    if (splits[i] > 1) bytes += 2.0 * items * 256.0 * bn * 4.0;
+    waves += std::ceil(items / kLinearPairs) * len;
+    if (splits[i] > 1)
+      finish = std::max(finish, 5500.0 + 300.0 * splits[i]) + 8.0 / 6000.0 * splits[i] * p[i].m * p[i].n;
   }
   // one product: whole waves; two: the shorter items fill the last wave of the longer ones
   const double time = count == 1 ? waves : std::max(longest, work / kLinearPairs + 0.5 * longest);
-  return time + fixed + (bytes > 0.0 ? 4000.0 + bytes / 4000.0 : 0.0);
+  return time + fixed + finish;
 }
 
 struct Plan {

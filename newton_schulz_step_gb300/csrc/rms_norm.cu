@@ -4,7 +4,7 @@
 //   h = x + residual,   y = h r w,   r = (mean h^2 + eps)^-1/2
 //   8 bits: y = s q a group of columns (or a row), q in e4m3, s the least power of two that
 //           brings the group's largest |y| to 448 or less
-//   dx = r (G - h r^2 mean(G h)) + dresidual,  G = dy w;   dw = sum over tokens of dy h r
+//   dx = r (G - h r mean(G h r)) + dresidual,  G = dy w;   dw = sum over tokens of dy h r
 //
 // All of it is bound by HBM: each element is read once and written once.  A row is held in
 // registers by a team of 32 to 512 threads, vectors of 8 elements a thread: one pass over
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kMaxTeam)
     if (kAhead) load(row + stride);
     team.sum2(ss, gh);
     const float r = rsqrtf(fmaf(ss, inv_dim, L.eps));
-    const float m = -(r * r) * (gh * inv_dim);
+    const float m = -r * (gh * inv_dim);                 // (r^2 may overflow, h r does not)
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       const int c = team.at + i * L.team;
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kMaxTeam)
       float o[8], e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[i][j] = fmaf(g[i][j], h[i][j] * r, dw[i][j]);
+        h[i][j] *= r;
+        dw[i][j] = fmaf(g[i][j], h[i][j], dw[i][j]);
         o[j] = g[i][j];
       }
       w.times(i, c, o);
