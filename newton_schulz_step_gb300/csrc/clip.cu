@@ -65,9 +65,21 @@ __device__ __forceinline__ void get(const ClipTensor& T, const Raw<false>& r, fl
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
 }
-__device__ __forceinline__ float value(const ClipTensor& T, long long e) {
-  return T.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(T.g)[e])
-                  : static_cast<const float*>(T.g)[e];
+// Up to 8 elements from e on; those past the tensor are 0.
+__device__ __forceinline__ void load_some(const ClipTensor& T, long long e, float (&v)[8]) {
+  if (e + 8 <= T.n) {
+    Raw<false> r;
+    load(T, e, r);
+    get(T, r, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.f;
+    if (e + j < T.n)
+      v[j] = T.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(T.g)[e + j])
+                      : static_cast<const float*>(T.g)[e + j];
+  }
 }
 __device__ __forceinline__ void store(const ClipTensor& T, long long e, const float (&v)[8]) {
   if (T.out_bf16) {
@@ -157,13 +169,15 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
         }
       }
     } else {
+      // a tensor's last unit: whole vectors, then up to 7 elements
+#pragma unroll 2
       for (int i = 0; i < kVecs; ++i) {
         const long long e = base + 8ll * (i * kThreads + threadIdx.x);
-        for (int j = 0; j < 8; ++j) {
-          if (e + j >= T.n) break;
-          const float v = value(T, e + j);
-          sum[j] = fmaf(v, v, sum[j]);
-        }
+        if (e >= T.n) break;
+        float v[8];
+        load_some(T, e, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = fmaf(v[j], v[j], sum[j]);
       }
     }
   }
@@ -224,13 +238,21 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
         }
       }
     } else {
+#pragma unroll 2
       for (int i = 0; i < kVecs; ++i) {
         const long long e = base + 8ll * (i * kThreads + threadIdx.x);
-        for (int j = 0; j < 8; ++j) {
-          if (e + j >= T.n) break;
-          const float v = value(T, e + j) * c;
-          if (T.out_bf16) static_cast<__nv_bfloat16*>(T.out)[e + j] = __float2bfloat16_rn(v);
-          else static_cast<float*>(T.out)[e + j] = v;
+        if (e >= T.n) break;
+        float v[8];
+        load_some(T, e, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= c;
+        if (e + 8 <= T.n) {
+          store(T, e, v);
+        } else {
+          for (int j = 0; j < 8 && e + j < T.n; ++j) {
+            if (T.out_bf16) static_cast<__nv_bfloat16*>(T.out)[e + j] = __float2bfloat16_rn(v[j]);
+            else static_cast<float*>(T.out)[e + j] = v[j];
+          }
         }
       }
     }
