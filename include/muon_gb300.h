@@ -510,9 +510,9 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
  * norm: one float on the device.  out may be the gradient itself (in one type), or a
  * tensor of either type; with max_norm = INFINITY only the norm is computed and out is
  * not used.  The arrays of different tensors must not overlap.  A norm that is NaN or
- * infinite makes the factor NaN or 0, as the formula has it.  Squares are summed in fp32
- * per thread: magnitudes from 2^64 on make the norm infinite, those below 2^-75 add
- * nothing.  Fixed summation order: repeated calls give equal bits.
+ * infinite makes the factor NaN or 0, as the formula has it.  Squares are summed in fp32:
+ * magnitudes from 2^58 on may make the norm infinite, those below 2^-75 add nothing.
+ * Fixed summation order: repeated calls give equal bits.
  */
 typedef struct muon_grad_tensor {
   const void* grad;        /* [numel] in g_dtype, 16-byte aligned                   */

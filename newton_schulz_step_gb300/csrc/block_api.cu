@@ -331,7 +331,7 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
 size_t muon_clip_workspace_bytes(int n_tensors) {
   if (n_tensors < 0) return 0;
   const size_t launches = (static_cast<size_t>(n_tensors) + kMaxClipTensors - 1) / kMaxClipTensors;
-  return kStatusBytes + align256(std::max<size_t>(1, launches) * kClipBlocks * sizeof(double));
+  return kStatusBytes + align256(std::max<size_t>(1, launches) * kClipBlocks * sizeof(float2));
 }
 
 muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, float max_norm,
@@ -365,7 +365,7 @@ muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, 
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     ClipLaunch L;
     std::memset(&L, 0, sizeof(L));
-    L.parts = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+    L.parts = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
     L.status = static_cast<const unsigned int*>(workspace);
     L.max_norm = max_norm;
     L.eps = eps;

@@ -437,7 +437,7 @@ struct ClipLaunch {
   ClipTensor t[kMaxClipTensors];
   int n_tensors;
   long long total_units;
-  double* parts;                    // [n_parts], the launches' parts one after the other
+  float2* parts;                    // [n_parts], the launches' parts one after the other: sum, unit
   int part_begin, n_parts;          // this launch's first part; all launches' number
   float* norm;                      // written by the first launch of the second pass, or null
   float max_norm, eps;

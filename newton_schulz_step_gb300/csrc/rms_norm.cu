@@ -12,6 +12,11 @@
 // block work on rows of their own; the rows' loads are issued a row ahead, so that they
 // travel while the row before is summed.  A power of two as the scale makes the division
 // exact: the only rounding is e4m3's own, and the values that q stands for are exact in bf16.
+//
+// 16384 tokens of 2048 (bf16, with residual): forward 41.4 us (6.5 TB/s, 96 % of the copy's
+// rate), gradients 49.0 (5.5 TB/s, the sum of the weight's parts among it); of 4096 in 8 bits
+// 75.5 us (6.2 TB/s).  Blocks of 32 resident warps an SM forward (64 registers) gained 3 to 9 %
+// over 24; the gradients keep 16, their columns' sums of the weight take the registers.
 #include <algorithm>
 
 #include "internal.h"

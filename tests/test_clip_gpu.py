@@ -1,8 +1,8 @@
 """GPU parity of the norm and the clipping of all gradients with the float64 oracle.
 
-A thread sums squares in fp32, at most n / 8 of them an accumulator (n: its elements, a few hundred
-here), and the rest is fp64: the sum of squares is off by at most 2^-15 of itself, the norm by half
-of that and a few roundings, kNorm = 2^-15.  The factor adds two roundings, an output its own
+Squares are summed in fp32, at most n / 8 of them an accumulator (n: a thread's elements, a few
+hundred here), and the threads' and blocks' sums in some 30 further additions: the sum of squares is
+off by at most 2^-15 of itself, the norm by half of that and a few roundings, kNorm = 2^-15.  The factor adds two roundings, an output its own
 (2^-24 in fp32, 2^-8 in bf16).
 """
 
@@ -88,7 +88,7 @@ def test_factor_one_leaves_the_gradients_as_they_are():
 def test_extreme_values():
     zero = [torch.zeros(100, device=DEV), torch.zeros(33, dtype=B, device=DEV)]
     assert float(muon.clip_grad_norm(zero, 1.0)) == 0.0 and all(torch.all(z == 0) for z in zero)
-    # squares below fp32's smallest add nothing; sums past its largest are held in fp64
+    # squares below fp32's smallest add nothing; sums past its largest are held in another unit
     assert float(muon.grad_norm([torch.full((100,), 1e-30, device=DEV)])) == 0.0
     big = torch.full((1 << 20,), 1e18, device=DEV)
     assert abs(float(muon.grad_norm([big])) / (1e18 * 1024) - 1) < kNorm
