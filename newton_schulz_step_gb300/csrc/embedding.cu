@@ -19,8 +19,8 @@
 // are few against the table, and still in L2.
 //
 // 32768 tokens of a text's frequencies, 50257 rows of 768: lookup 11.9 us; gradient 48 us for
-// 205 MB (4.2 TB/s): clearing and sort 27, sums 17, joins 6 (the clearing alone, 154 MB, is
-// bound by HBM; the sort beside it takes 14).  With digits' equals found by __match_any_sync,
+// 205 MB (4.2 TB/s) back to back; each launch by itself with cold caches: clearing and sort 27
+// (the sort without clearing 22), sums 15, joins 10.  With digits' equals found by __match_any_sync,
 // items read again for their placing, and the joins of a token's 48 pieces by one warp it
 // was 96.
 #include <algorithm>
@@ -177,7 +177,7 @@ __device__ __forceinline__ void rank_batch(Batch& b, uint32_t* mine, int shift, 
 // counts a warp, a digit's place from the counts of smaller digits, earlier CTAs and earlier
 // warps, and an item's place among its warp's.  A warp's items stay in registers between the
 // count and the placing while they are kRounds a lane (up to 65536 tokens); more are read and
-// ranked again.  8 SMs take 14 us for 32768 tokens in two passes of 8 bits.
+// ranked again.  8 SMs take 22 us for 32768 tokens in two passes of 8 bits.
 __device__ void sort_tokens(const EmbeddingLaunch& L, uint32_t* smem) {
   uint32_t* const cnt = smem;                              // [warps][bins]
   uint32_t* const total = smem + kSortWarps * kMaxBins;    // [bins], read by the other CTAs
