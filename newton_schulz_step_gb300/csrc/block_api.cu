@@ -7,7 +7,6 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "views.h"
 
@@ -38,10 +37,6 @@ Rows rows_of(const muon_matrix& v, int rows, int cols, int size) {
 Rows flat(const void* p, long long bytes) {
   return {reinterpret_cast<uintptr_t>(p), 0, 0, bytes, 1, 1};
 }
-
-// The launches of one call read what the ones before them left in the workspace: no other
-// thread's launches on the stream come between.
-std::mutex g_block_mu;
 
 // ------------------------------------------------------------ RMS norm
 bool norm_dim_ok(int dim) { return dim >= 8 && dim <= kRmsNormMaxDim && dim % 8 == 0; }
@@ -216,7 +211,7 @@ muon_status muon_rms_norm_backward(const muon_rms_norm_spec* spec, muon_matrix d
     L.status = static_cast<const unsigned int*>(workspace);
     if (dweight)
       L.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-    std::lock_guard<std::mutex> lk(g_block_mu);
+    std::lock_guard<std::mutex> lk(g_workspace_mu);
     cudaError_t e = counted_launch(
         st, MUON_K_RMS_NORM_BWD, 0.0, 1.0 * t * d * size * (has_res ? 4.0 : 3.0),
         [&] { return launch_rms_norm_backward(L, spec->dtype == MUON_BF16, st); });
@@ -312,7 +307,7 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
       p += 2 * list;
     }
     L.parts = reinterpret_cast<float*>(p);
-    std::lock_guard<std::mutex> lk(g_block_mu);
+    std::lock_guard<std::mutex> lk(g_workspace_mu);
     cudaError_t e = counted_launch(st, MUON_K_EMBEDDING_SORT, 0.0,
                                    1.0 * spec->rows * d * size + 16.0 * t,
                                    [&] { return launch_embedding_sort(L, sms, st); });
@@ -393,7 +388,7 @@ muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, 
       }
       return j;
     };
-    std::lock_guard<std::mutex> lk(g_block_mu);
+    std::lock_guard<std::mutex> lk(g_workspace_mu);
     cudaError_t e = cudaSuccess;
     int i = 0, launches = 0;
     do {

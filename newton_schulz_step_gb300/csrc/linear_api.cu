@@ -8,7 +8,6 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "views.h"
 
@@ -189,10 +188,6 @@ bool operand(CUtensorMap* tm, const muon_matrix& v, int mn, int k, bool by_rows,
   return by_rows ? matrix_tmap(tm, v, k, mn, 64, 64) : matrix_tmap(tm, v, mn, k, 64, box_rows);
 }
 
-// The launches of one call read what the ones before them left in the workspace: no other
-// thread's launches on the stream come between.
-std::mutex g_linear_mu;
-
 }  // namespace
 
 extern "C" {
@@ -287,7 +282,7 @@ muon_status muon_linear(const muon_linear_spec* spec, muon_matrix x, muon_matrix
         (has_res && !matrix_tmap(&M.res[0], residual, t, n, 64, 32)) ||
         (has_z && !matrix_tmap(&M.z[0], preact, t, n, 64, 32)))
       return MUON_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_linear_mu);
+    std::lock_guard<std::mutex> lk(g_workspace_mu);
     cudaError_t e = counted_launch(st, MUON_K_LINEAR, flops, bytes,
                                    [&] { return launch_linear(M, L, sms, st); });
     if (e == cudaSuccess && P.splits > 1)
@@ -386,7 +381,7 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
       L.db_n = n;
       L.db_chunks = cdiv(t, chunk);
     }
-    std::lock_guard<std::mutex> lk(g_linear_mu);
+    std::lock_guard<std::mutex> lk(g_workspace_mu);
     cudaError_t e = cudaSuccess;
     if (act || dbias)
       e = counted_launch(st, MUON_K_LINEAR_DZ, 0.0, 2.0 * t * n * (act ? 3 : 1),

@@ -4,6 +4,7 @@ differentiation of the same model, the clipping, and that the steps run."""
 import importlib.util
 import math
 import os
+import threading
 
 import pytest
 import torch
@@ -92,3 +93,54 @@ def test_example_runs(ex):
 
 def test_a_step_is_the_same_in_every_run(ex):
     assert ex.main(steps=2) == ex.main(steps=2)
+
+
+def test_threads_with_calls_of_every_kind_on_one_stream():
+    # calls of several launches hand over through the one workspace of the stream
+    gen = torch.Generator().manual_seed(9)
+
+    def draw(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=gen).to(dtype).cuda()
+
+    x, w, dy = draw(300, 1032), draw(264, 1032), draw(300, 264)
+    h, dh, nw = draw(500, 1024), draw(500, 1024), draw(1024, dtype=torch.float32)
+    ids, de = torch.randint(0, 97, (1500,), generator=gen).cuda(), draw(1500, 264)
+    grads = [draw(n) for n in (70001, 33, 4096)]
+    q, k, v, do = draw(257, 4, 64), draw(257, 2, 64), draw(257, 2, 64), draw(257, 4, 64)
+    out, lse = muon.attention(q, k, v)
+    tables = muon.rope_tables(257, 64)
+    qw, kw = draw(64, dtype=torch.float32), draw(64, dtype=torch.float32)
+
+    def clip():
+        outs = [torch.empty_like(g) for g in grads]
+        return [muon.clip_grad_norm(grads, 0.5, outs=outs), *outs]
+
+    calls = [
+        lambda: [muon.linear(x, w), *muon.linear_backward(dy, x, w, bias=True)],
+        lambda: muon.rms_norm_backward(dh, h, nw),
+        lambda: [muon.embedding_backward(de, ids, 101)],
+        clip,
+        lambda: muon.attention_backward(do, q, k, v, out, lse),
+        lambda: muon.qk_norm_rope_backward(do, k, q, k, *tables, q_weight=qw, k_weight=kw),
+    ]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    stream, start = torch.cuda.Stream(), threading.Barrier(len(calls))
+    got = [[] for _ in calls]
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            start.wait()
+            for _ in range(60):
+                got[i].append(calls[i]())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert muon.workspace_status(None) == 0
+    for g, r in zip(got, want):
+        assert len(g) == 60
+        assert all(torch.equal(a, b) for one in g for a, b in zip(one, r))
