@@ -853,6 +853,12 @@ def _matrix(t, name: str, shape, dtype, index) -> _Matrix:
     _refuse_matrix(t, name, shape, dtype, index)
 
 
+def _check_sizes(bits, *sizes):
+    """bits: the sizes' OR.  ctypes would cut a size of more than 31 bits without a word."""
+    if bits >> 31:
+        raise ValueError(f"sizes must be less than 2^31, got {sizes}")
+
+
 def _new_matrix(shape, dtype, device):
     """(tensor, view) of a new output, its rows padded to 16 bytes where the width asks for it."""
     cols = shape[1]
@@ -866,6 +872,7 @@ def _new_matrix(shape, dtype, device):
 
 @functools.lru_cache(maxsize=1024)
 def linear_workspace_bytes(tokens: int, in_features: int, out_features: int) -> int:
+    _check_sizes(tokens | in_features | out_features, tokens, in_features, out_features)
     return int(load_library().muon_linear_workspace_bytes(tokens, in_features, out_features))
 
 
@@ -878,6 +885,7 @@ def _linear_spec(x, weight, activation, bias):
     if weight.dim() != 2:
         raise ValueError(f"weight must be [out_features, in_features], got {tuple(weight.shape)}")
     n = weight.shape[0]
+    _check_sizes(t | k | n, t, k, n)
     vw = _matrix(weight, "weight", (n, k), bf16, index)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
@@ -981,6 +989,7 @@ def _norm_spec(x, name, weight, eps):
         raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
     vx = _matrix(x, name, x.shape, dtype, index)
     t, d = x.shape
+    _check_sizes(t | d, t, d)
     p_w = None if weight is None else _ptr(weight, "weight", index, torch.float32, (d,))
     return _RmsNormSpec(1 if dtype is torch.bfloat16 else 0, t, d, eps, p_w), vx
 
@@ -1070,6 +1079,7 @@ def rms_norm_fp8(x, weight=None, *, residual=None, eps: float = NORM_EPS, group:
 
 @functools.lru_cache(maxsize=256)
 def rms_norm_workspace_bytes(dim: int) -> int:
+    _check_sizes(dim, dim)
     return int(load_library().muon_rms_norm_workspace_bytes(dim))
 
 
@@ -1107,7 +1117,9 @@ def _embedding_spec(ids, rows, dim, scale):
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     if ids.dim() != 1 or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous [tokens], got {tuple(ids.shape)}")
-    return _EmbeddingSpec(ids.shape[0], rows, dim, ids.element_size(), ids.data_ptr(), scale)
+    t = ids.shape[0]
+    _check_sizes(t | rows | dim, t, rows, dim)
+    return _EmbeddingSpec(t, rows, dim, ids.element_size(), ids.data_ptr(), scale)
 
 
 def _float_dtype(dtype, name):
@@ -1148,6 +1160,7 @@ def embedding(ids, table, *, scale: float = 1.0, dtype=torch.bfloat16, out=None,
 
 @functools.lru_cache(maxsize=1024)
 def embedding_workspace_bytes(tokens: int, dim: int) -> int:
+    _check_sizes(tokens | dim, tokens, dim)
     return int(load_library().muon_embedding_workspace_bytes(tokens, dim))
 
 
@@ -1258,7 +1271,7 @@ def grad_norm(grads, *, workspace: Workspace | None = None, stream=None):
 
 def workspace_status(workspace: Workspace | None, clear: bool = False, stream=None) -> int:
     """Synchronise and read the workspace's sticky device error word (0 = ok, 4 = timeout).
-    With None: that of the workspace which attention, its gradients and those of qk_norm_rope
+    With None: that of the workspace which attention, linear and the gradients of every kind
     keep for the current device and `stream` when the caller passes none.  (The one that a call
     captured into a CUDA graph takes is cleared by each replay and cannot be read: pass a
     Workspace to a captured call whose failure should be seen.)"""

@@ -886,7 +886,8 @@ cudaError_t launch_linear_finish(const LinearLaunch& l, cudaStream_t s) {
 
 cudaError_t launch_linear_dz(const LinearDz& d, cudaStream_t s) {
   return launch_dependent(linear_dz_kernel,
-                          dim3((d.cols + 255) / 256, (d.rows + d.chunk - 1) / d.chunk), 256, 0, 1,
+                          dim3((d.cols + 255) / 256, d.rows / d.chunk + (d.rows % d.chunk != 0)),
+                          256, 0, 1,
                           s, d);
 }
 

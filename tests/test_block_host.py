@@ -338,3 +338,25 @@ def test_structures_match_the_header(lib):
     assert ctypes.sizeof(muon._RmsNormSpec) == 24
     assert ctypes.sizeof(muon._EmbeddingSpec) == 32
     assert ctypes.sizeof(muon._GradTensor) == 32
+
+
+def test_binding_refuses_sizes_beyond_31_bits(lib, monkeypatch):
+    # (as C ints they would be small ones: 2^32 + 8 rows would be 8)
+    monkeypatch.setattr(muon, "_cuda_device", lambda t, name: None)
+    many = (1 << 32) + 8
+    tall, wide, small = (torch.empty(shape, dtype=torch.bfloat16, device="meta")
+                         for shape in ((many, 8), (8, many), (8, 8)))
+    ids = torch.zeros(8, dtype=torch.int64)
+    for call in (lambda: muon._linear_spec(tall, small, None, None),
+                 lambda: muon._linear_spec(small, tall, None, None),
+                 lambda: muon._linear_spec(wide, wide, None, None),
+                 lambda: muon._norm_spec(tall, "x", None, 0.0),
+                 lambda: muon._norm_spec(wide, "x", None, 0.0),
+                 lambda: muon._embedding_spec(ids, many, 8, 1.0),
+                 lambda: muon._embedding_spec(ids, -1, 8, 1.0),
+                 lambda: muon._embedding_spec(ids, 8, many, 1.0),
+                 lambda: muon.linear_workspace_bytes(many, 8, 8),
+                 lambda: muon.rms_norm_workspace_bytes(many),
+                 lambda: muon.embedding_workspace_bytes(many, 8)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
