@@ -337,15 +337,24 @@ muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, 
         (reinterpret_cast<uintptr_t>(norm) & 3u) || !(max_norm >= 0.f) || !std::isfinite(eps) ||
         eps < 0.f)
       return MUON_ERR_INVALID_ARG;
-    const bool clip = std::isfinite(max_norm);
+    // an infinite max_norm leaves the gradients as they are, but copies to other outputs
+    const bool clip = std::isfinite(max_norm) ||
+                      std::any_of(tensors, tensors + n_tensors, [](const muon_grad_tensor& T) {
+                        return T.numel > 0 && T.out &&
+                               (T.out != T.grad || T.out_dtype != T.g_dtype);
+                      });
+    const Rows r_norm = flat(norm, sizeof(float));
     bool in_place = true;
     for (int i = 0; i < n_tensors; ++i) {
       const muon_grad_tensor& T = tensors[i];
       if (T.numel < 0 || !dtype_ok(T.g_dtype)) return MUON_ERR_INVALID_ARG;
       if (T.numel == 0) continue;
-      if (!T.grad || !aligned16(T.grad)) return MUON_ERR_INVALID_ARG;
+      if (!T.grad || !aligned16(T.grad) || overlap(r_norm, flat(T.grad, T.numel * size_of(T.g_dtype))))
+        return MUON_ERR_INVALID_ARG;
       if (!clip) continue;
-      if (!T.out || !aligned16(T.out) || !dtype_ok(T.out_dtype)) return MUON_ERR_INVALID_ARG;
+      if (!T.out || !aligned16(T.out) || !dtype_ok(T.out_dtype) ||
+          overlap(r_norm, flat(T.out, T.numel * size_of(T.out_dtype))))
+        return MUON_ERR_INVALID_ARG;
       const bool same = T.out == T.grad && T.out_dtype == T.g_dtype;
       if (!same && overlap(flat(T.out, T.numel * size_of(T.out_dtype)),
                            flat(T.grad, T.numel * size_of(T.g_dtype))))

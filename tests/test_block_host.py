@@ -360,3 +360,15 @@ def test_binding_refuses_sizes_beyond_31_bits(lib, monkeypatch):
                  lambda: muon.embedding_workspace_bytes(many, 8)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_clip_norm_apart_and_outputs_without_clipping(lib):
+    good, out = (0x1000, 0x1000, 64, 1, 1), (0x1000, 0x2000, 64, 1, 0)
+    for norm in (0x1000, 0x107c, 0x2000, 0x20fc):
+        assert _clip(lib, [out], norm=norm) == INVALID
+    # an infinite max_norm: outs other than the gradients are written, and so have to be valid
+    inf = float("inf")
+    for bad in ((0x4000, 0x5008, 64, 1, 0), (0x4000, 0x4040, 64, 1, 1), (0x4000, None, 64, 1, 0)):
+        assert _clip(lib, [out, bad], max_norm=inf) == INVALID
+    for one in ([good], [good, (0x4000, None, 64, 1, 0)]):
+        assert _clip(lib, one, max_norm=inf, n=256) == WORKSPACE

@@ -167,3 +167,14 @@ def test_refusals():
             muon.clip_grad_norm(g, bad)
     with pytest.raises(muon.MuonError):                 # not 16-byte aligned
         muon.clip_grad_norm([wide[1:65]], 1.0)
+
+
+@pytest.mark.parametrize("o", [B, F])
+def test_an_infinite_max_norm_copies_to_outs(o):
+    grads = _draw(8, SHAPES, [B, F] * 5)
+    outs = [torch.full_like(g, 3.0, dtype=o) for g in grads]
+    before = [g.clone() for g in grads]
+    norm = muon.clip_grad_norm(grads, math.inf, outs=outs)
+    assert torch.equal(norm, muon.grad_norm(grads))
+    assert all(torch.equal(a, b) for a, b in zip(grads, before))
+    assert all(torch.equal(a, b.to(o)) for a, b in zip(outs, grads))
