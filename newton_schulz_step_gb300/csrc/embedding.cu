@@ -342,7 +342,7 @@ __device__ __forceinline__ void store_row(const EmbeddingLaunch& L, uint32_t id,
                                           float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] *= L.scale;
-  store8(static_cast<O*>(L.out) + id * L.out_stride + c, v);
+  if (id < static_cast<uint32_t>(L.rows)) store8(static_cast<O*>(L.out) + id * L.out_stride + c, v);
 }
 
 constexpr int kChunk = 32;             // sorted positions of a warp
@@ -362,14 +362,15 @@ __global__ void __launch_bounds__(kThreads, 3)
   // which the first *L.count positions are sorted tokens
   const bool there = i0 + lane < L.tokens;
   const bool failed = ptx::status_set(L.status);
-  const long long items = __ldcg(L.count);
+  const long long items = min(__ldcg(L.count), static_cast<uint32_t>(L.tokens));
   uint32_t key = there ? __ldcg(L.keys[0] + i0 + lane) : 0u;
   uint32_t token = there ? __ldcg(L.order[0] + i0 + lane) : 0u;
   const uint32_t before = i0 > 0 ? __ldcg(L.keys[0] + i0 - 1) : 0u;
   const uint32_t after = i0 + kChunk < L.tokens ? __ldcg(L.keys[0] + i0 + kChunk) : 0u;
   if (failed || i0 >= items) return;
   const int n = static_cast<int>(min(static_cast<long long>(kChunk), items - i0));
-  if (lane >= n) token = 0u;
+  // (a list that another call wrote into, against the contract, reaches no other memory)
+  if (lane >= n || token >= static_cast<uint32_t>(L.tokens)) token = 0u;
   // bit i: a run begins at position i; the run at position 0 may have begun earlier
   const uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
   const bool head_open = i0 > 0 && before == __shfl_sync(0xffffffffu, key, 0);
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads)
   const long long first = static_cast<long long>(chunk) * kChunk, last = first + kChunk - 1;
   const bool inside = last + 1 < L.tokens;
   const bool failed = ptx::status_set(L.status);
-  const long long items = __ldcg(L.count);
+  const long long items = min(__ldcg(L.count), static_cast<uint32_t>(L.tokens));
   const uint32_t id = inside ? __ldcg(L.keys[0] + last) : 0u;
   const uint32_t after = inside ? __ldcg(L.keys[0] + last + 1) : 0u;
   const uint32_t before = inside && first > 0 ? __ldcg(L.keys[0] + first - 1) : 0u;
