@@ -219,3 +219,32 @@ def test_refusals():
     tab.requires_grad_(True)
     with pytest.raises(ValueError, match="embedding_backward"):
         muon.embedding(i, tab)
+
+
+def test_offsets_past_32_bits():
+    rows, dim = 270_000, 8192                   # 2.2 10^9 elements
+    table = torch.empty(rows, dim, dtype=torch.bfloat16, device=DEV)
+    table.view(torch.int16).random_(0x1000, 0x3f80)
+    gen = torch.Generator().manual_seed(45)
+    ids = torch.cat((torch.tensor([0, rows - 1, rows - 1, rows, 262_144]),
+                     torch.randint(0, rows, (95,), generator=gen))).to(DEV)
+    out = muon.embedding(ids, table, scale=0.5)
+    ok = ids < rows
+    assert torch.equal(out[ok], table[ids[ok]] * 0.5) and torch.isnan(out[~ok]).all()
+    dout = torch.randn(len(ids), dim, generator=gen).bfloat16().to(DEV)
+    for dtype in (torch.bfloat16, torch.float32):
+        d = muon.embedding_backward(dout, ids, rows, dtype=dtype)
+        assert torch.equal(d[rows - 1].float(), (dout[1].float() + dout[2].float()).to(dtype).float())
+        d[ids[ok]] = 0
+        assert not d.any()
+        del d
+
+
+def test_many_tokens_past_the_registers_of_the_sort():
+    # more items a warp than are kept between count and placing, three passes of the sort
+    t, rows, dim = 2_200_000, 3_000_000, 8
+    ids = torch.randint(0, rows, (t,), device=DEV)
+    ids[::20] = 7
+    dout = torch.randint(-4, 5, (t, dim), device=DEV).bfloat16()
+    want = torch.zeros(rows, dim, device=DEV).index_add_(0, ids, dout.float())   # (whole numbers)
+    assert torch.equal(muon.embedding_backward(dout, ids, rows), want)

@@ -372,3 +372,27 @@ def test_refusals():
         with torch.no_grad():
             muon.linear(x, w, bias=b, residual=r)
         v.requires_grad_(False)
+
+
+def _spread(x, empty=False):
+    """x in rows so far apart that the last ones begin past 2^31 elements."""
+    rows, cols = x.shape
+    stride = ((1 << 31) // (rows - 2) // 8 + 1) * 8
+    buf = torch.empty((rows - 1) * stride + (cols + 7) // 8 * 8, dtype=x.dtype, device=DEV)
+    view = buf.as_strided((rows, cols), (stride, 1))
+    assert (rows - 1) * stride > 1 << 31
+    view.fill_(3.0) if empty else view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("t,k,n", [(4, 264, 136), (70, 264, 131), (40, 1032, 264)])
+def test_offsets_past_32_bits(t, k, n):
+    x, w, b, r, dy = _draw(41, t, k, n)
+    want = muon.linear(x, w, bias=b, activation="gelu", residual=r, save_preact=True)
+    wg = muon.linear_backward(dy, x, w, bias=True, activation="gelu", preact=want[1])
+    X, R, DY, O, Z, DX, W, DW = (_spread(v, e) for v, e in (
+        (x, False), (r, False), (dy, False), (r, True), (r, True), (x, True), (w, False), (w, True)))
+    muon.linear(X, W, bias=b, activation="gelu", residual=R, preact=Z, out=O)
+    got = muon.linear_backward(DY, X, W, bias=True, activation="gelu", preact=Z, dx=DX, dweight=DW)
+    assert torch.equal(O, want[0]) and torch.equal(Z, want[1])
+    assert all(torch.equal(a, c) for a, c in zip(got, wg))

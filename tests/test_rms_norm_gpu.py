@@ -292,3 +292,33 @@ def test_refusals():
         with pytest.raises(ValueError):
             muon.rms_norm_fp8(x, w, residual=r)
         v.requires_grad_(False)
+
+
+def _spread(x, empty=False):
+    """x in rows so far apart that the last ones begin past 2^31 elements."""
+    rows, cols = x.shape
+    stride = ((1 << 31) // (rows - 2) // 8 + 1) * 8
+    buf = torch.empty((rows - 1) * stride + (cols + 7) // 8 * 8, dtype=x.dtype, device=DEV)
+    view = buf.as_strided((rows, cols), (stride, 1))
+    assert (rows - 1) * stride > 1 << 31
+    view.fill_(3.0) if empty else view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_offsets_past_32_bits(dtype):
+    gen = torch.Generator().manual_seed(43)
+    x, r, dy = (torch.randn(50, 1024, generator=gen).to(dtype).to(DEV) for _ in range(3))
+    w = torch.randn(1024, generator=gen).to(DEV)
+    y, h = muon.rms_norm(x, w, residual=r)
+    dx, dw = muon.rms_norm_backward(dy, h, w, dresidual=r)
+    q, s, _ = muon.rms_norm_fp8(x, w, residual=r)
+    X, R, DY = (_spread(v) for v in (x, r, dy))
+    Y, H, DX = (_spread(x, True) for _ in range(3))
+    muon.rms_norm(X, w, residual=R, out=Y, residual_out=H)
+    assert torch.equal(Y, y) and torch.equal(H, h)
+    got = muon.rms_norm_backward(DY, H, w, dresidual=R, dx=DX)
+    assert torch.equal(DX, dx) and torch.equal(got[1], dw)
+    Q = _spread(q.view(torch.uint8), True).view(torch.float8_e4m3fn)
+    _, S, _ = muon.rms_norm_fp8(X, w, residual=R, out=Q, residual_out=H)
+    assert torch.equal(Q.view(torch.uint8), q.view(torch.uint8)) and torch.equal(S, s)
