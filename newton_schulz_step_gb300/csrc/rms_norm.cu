@@ -28,8 +28,6 @@ namespace {
 constexpr int kThreads = 256;        // of a block; 512 where a row's team has as many
 constexpr int kMaxTeam = 512;
 
-using ptx::pair;
-
 // 8 elements of a row as stored.
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
