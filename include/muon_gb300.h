@@ -508,10 +508,12 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
  *   norm = (sum over all tensors and elements of g^2)^1/2
  *   out  = g min(1, max_norm / (norm + eps))
  * norm: one float on the device.  out may be the gradient itself (in one type), or a
- * tensor of either type.  With max_norm = INFINITY the factor is 1, and where every out is
- * the gradient itself or NULL only the norm is computed.  The arrays of different tensors must not overlap.  A norm that is NaN or
- * infinite makes the factor NaN or 0, as the formula has it.  Squares are summed in fp32:
- * magnitudes from 2^58 on may make the norm infinite, those below 2^-75 add nothing.
+ * tensor of either type.  With max_norm = INFINITY the factor is 1 whatever the norm, and
+ * where every out is the gradient itself or NULL only the norm is computed.  At factor 1 a
+ * gradient whose out it is itself is not written.  The arrays of different tensors must not
+ * overlap.  With a finite max_norm a norm that is NaN or infinite makes the factor NaN or
+ * 0, as the formula has it.  Squares are summed in fp32: magnitudes from 2^58 on may make
+ * the norm infinite, those below 2^-75 add nothing.
  * Fixed summation order: repeated calls give equal bits.
  */
 typedef struct muon_grad_tensor {

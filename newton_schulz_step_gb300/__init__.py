@@ -1260,7 +1260,8 @@ def clip_grad_norm(grads, max_norm: float, *, outs=None, eps: float = CLIP_EPS,
                    workspace: Workspace | None = None, stream=None):
     """The norm of all gradients together (contiguous fp32 or bf16 tensors of any shapes), and the
     gradients times min(1, max_norm / (norm + eps)): in place, or into `outs`, which may be of
-    either type.  Returns the norm, an fp32 scalar on the device."""
+    either type.  An infinite max_norm is factor 1 whatever the norm.  Returns the norm, an fp32
+    scalar on the device."""
     return ClipGradNorm(grads, max_norm, outs=outs, eps=eps, workspace=workspace)(stream)
 
 

@@ -1,7 +1,7 @@
 // clip.cu -- the norm of all gradients of a model together, and the gradients clipped by it:
 //
 //   norm = (sum over all tensors and elements of g^2)^1/2
-//   out  = g c,  c = min(1, max_norm / (norm + eps))
+//   out  = g c,  c = min(1, max_norm / (norm + eps)), 1 where max_norm is infinite
 //
 // Two passes over the gradients, both bound by HBM: squares summed into one part a block,
 // then the factor (every block adds the few hundred parts, in order) and the products.  The
@@ -233,12 +233,17 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
   const float total = block_sum(large ? fmaf(plain, kUnit, scaled) : plain, s_sum);
   const float norm = large ? sqrtf(total) * 0x1p20f : sqrtf(total);
   if (L.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *L.norm = norm;
-  const float ratio = L.max_norm / (norm + L.eps);
-  const float c = ratio >= 1.f ? 1.f : ratio;         // (a norm that is NaN stays one)
+  // (infinity over a norm that is not finite would be NaN; a norm that is NaN stays one)
+  const float ratio = isinf(L.max_norm) ? 1.f : L.max_norm / (norm + L.eps);
+  const float c = ratio >= 1.f ? 1.f : ratio;
   if (L.in_place && c == 1.f) return;
   for (; u >= 0; u -= gridDim.x) {
     const ClipTensor& T = tensor_of(s_table, L.n_tensors, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
+    if (c == 1.f && T.out == T.g) {                   // in place: it stays as it is
+      fetched = false;
+      continue;
+    }
     if (base + kClipUnit <= T.n) {
 #pragma unroll 1
       for (int p = 0; p < kVecs; p += kFlight<kBf16>) {

@@ -178,3 +178,24 @@ def test_an_infinite_max_norm_copies_to_outs(o):
     assert torch.equal(norm, muon.grad_norm(grads))
     assert all(torch.equal(a, b) for a, b in zip(grads, before))
     assert all(torch.equal(a, b.to(o)) for a, b in zip(outs, grads))
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 1e20])
+def test_an_infinite_max_norm_is_factor_one_whatever_the_norm(value):
+    # (1e20: squares past fp32's range, an infinite norm of finite gradients)
+    grads = _draw(9, SHAPES, [B, F] * 5)
+    grads[5].view(-1)[7] = value
+    in_place = {1, 5, 6}                                # beside tensors with outs of their own
+    before = [g.clone() for g in grads]
+    outs = [g if i in in_place else torch.full_like(g, 3.0) for i, g in enumerate(grads)]
+    norm = float(muon.clip_grad_norm(grads, math.inf, outs=outs))
+    assert not math.isfinite(norm)
+    for g, o, b in zip(grads, outs, before):
+        bits = torch.int16 if g.dtype == B else torch.int32
+        assert torch.equal(g.view(bits), b.view(bits))
+        assert torch.equal(o.nan_to_num(nan=7.0), b.nan_to_num(nan=7.0))
+    # into the other type, where the value is not in place
+    outs = [torch.full_like(g, 3.0, dtype=F if g.dtype == B else B) for g in grads]
+    muon.clip_grad_norm(grads, math.inf, outs=outs)
+    for o, b in zip(outs, before):
+        assert torch.equal(o.nan_to_num(nan=7.0), b.to(o.dtype).nan_to_num(nan=7.0))
