@@ -433,8 +433,10 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
  *   h = x + residual  (x where residual's data is NULL),
  *   y = h (mean h^2 + eps)^-1/2 w   (w = 1 where weight is NULL),
  * with x, residual, out (y) and sum (h) [tokens, dim] in one type.  h stays in fp32 for
- * the norm and is rounded to be stored; y is rounded once.  sum is given where residual
- * is.  out and sum may each be the very view of x or of residual (not of each other).
+ * the norm and is rounded to be stored; y is rounded once.  Finite rows of any magnitude
+ * are right: one whose squares leave fp32's range is scaled by a power of two first (with a
+ * residual, its y is that of h as stored).  sum is given where residual is.  out and sum
+ * may each be the very view of x or of residual (not of each other).
  */
 typedef struct muon_rms_norm_spec {
   int dtype;               /* muon_dtype of every muon_matrix of the call           */
@@ -463,9 +465,9 @@ muon_status muon_rms_norm_fp8(const muon_rms_norm_spec* spec, int group, muon_ma
  * residual).  With r = (mean h^2 + eps)^-1/2, n = h r, G = dout w:
  *   dx = r (G - n mean(G n)) + dresidual,   dweight = sum over tokens of dout n
  * dresidual: h's gradient from where else it went, or data NULL; dx is the gradient of x
- * and of residual alike.  dx may be the very view of dout, sum or dresidual.  dweight
- * ([dim] fp32, overwritten) is given where the weight is.  Fixed summation order:
- * repeated calls give equal bits.
+ * and of residual alike, and infinite where 1 / r is below 2^-126.  dx may be the very
+ * view of dout, sum or dresidual.  dweight ([dim] fp32, overwritten) is given where the
+ * weight is.  Fixed summation order: repeated calls give equal bits.
  */
 size_t muon_rms_norm_workspace_bytes(int dim);
 muon_status muon_rms_norm_backward(const muon_rms_norm_spec* spec, muon_matrix dout,

@@ -322,3 +322,94 @@ def test_offsets_past_32_bits(dtype):
     Q = _spread(q.view(torch.uint8), True).view(torch.float8_e4m3fn)
     _, S, _ = muon.rms_norm_fp8(X, w, residual=R, out=Q, residual_out=H)
     assert torch.equal(Q.view(torch.uint8), q.view(torch.uint8)) and torch.equal(S, s)
+
+
+# magnitudes of rows whose squares leave fp32's range, between ordinary ones (the residual is three
+# times x: the largest sums stay below 2^128)
+MAGNITUDES = [1.0, 1e20, 1e-24, 1e37, 1e-12, 1e-36, 1e15, 1.0, 1e19, 1e-20]
+
+
+def _check_far(x, r, dy, dr, w, eps):
+    """As _check, but a residual's y may be that of h as stored: rounded, it moves an element and the
+    row's norm by kBf16 of themselves each."""
+    u = kBf16 if x.dtype == torch.bfloat16 else 0.0
+    X, R, W = (None if v is None else f64(v) for v in (x, r, w))
+    y, h = muon.rms_norm(x, w, residual=r, eps=eps)
+    want, wh = ref.rms_norm(X, W, R, eps)
+    s = np.abs(X) + (0 if R is None else np.abs(R))
+    rms = np.sqrt(np.mean(wh * wh, axis=1, keepdims=True) + eps)
+    e = kF32 * (np.abs(want) + s / rms * (1 if W is None else np.abs(W)))
+    e = e + (0.0 if R is None else 2 * u * np.abs(want))
+    _within(y, want, e + u * (np.abs(want) + e), "y")
+    _within(h, wh, 2.0 ** -24 * s + u * np.abs(wh) * (1 + 2.0 ** -23), "h")
+    # from h on there is no difference
+    _check(h, None, dy, dr, w, eps=eps)
+    # ... nor by where the outputs are
+    for out in (0, 1):
+        c = [x.clone(), None if r is None else r.clone()]
+        total = None if r is None else c[1 - out]
+        got = muon.rms_norm(c[0], w, residual=c[1], eps=eps, out=c[out], residual_out=total)
+        assert torch.equal(got[0], y) and (r is None or torch.equal(got[1], h))
+        if r is None:
+            break
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("d", [64, 264, 520, 2048, 4104, 16384])
+def test_rows_of_any_magnitude(d, eps, dtype):
+    x, r, dy, dr, w = _draw(44 + d, 30, d, torch.float32)
+    m = torch.tensor(MAGNITUDES * 3, device=DEV)[:, None]
+    x, r, dy, dr = (v.to(dtype) for v in (m * x, m * r, m * dy, dr))
+    _check_far(x, r, dy, dr, w, eps)
+    _check_far(x, None, dy, None, None, eps)
+    # one large element in a row of small ones
+    x[:, d // 2] = 1e25
+    _check_far(x, None, dy, dr, w, eps)
+    u = 2 * kBf16 if dtype == torch.bfloat16 else 0.0
+    for res in (None, r):
+        for group in (0, 128):
+            q, s, _ = muon.rms_norm_fp8(x, w, residual=res, eps=eps, group=group)
+            want, _ = ref.rms_norm(f64(x), f64(w), None if res is None else f64(res), eps)
+            at = ref.spread(f64(s), d, group)
+            err = np.abs(f64(q.float()) * at - want)
+            off = (0.0 if res is None else u) + 2.0 ** -12
+            assert np.all(err <= (2.0 ** -4 * (1 + off) + off) * np.abs(want) + 2.0 ** -10 * at)
+            top = np.abs(want[:, :128 if group else d]).max(axis=1)
+            assert np.all(top <= 448 * (1 + off) * at[:, 0])
+            # (2^-126 is the least scale, and a y below fp32's least value is 0, with scale 1)
+            assert np.all((top > 224 * (1 - off) * at[:, 0]) | (top < 2.0 ** -117))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_any_magnitude_leave_the_others_as_they_are(dtype):
+    # a team's later rows, by the loop or after it: the same bits
+    x, r, dy, dr, w = _draw(46, 20000, 264, dtype)
+    far = torch.arange(20000, device=DEV) % 97 == 5
+    for res in (None, r):
+        y, h = muon.rms_norm(x, w, residual=res)
+        dx, _ = muon.rms_norm_backward(dy, h, w, dresidual=dr)
+        q, s, _ = muon.rms_norm_fp8(x, w, residual=res)
+        X = x.clone()
+        X[far] *= 1e22
+        Y, H = muon.rms_norm(X, w, residual=res)
+        DX, _ = muon.rms_norm_backward(dy, H, w, dresidual=dr)
+        Q, S, _ = muon.rms_norm_fp8(X, w, residual=res)
+        for a, b in ((y, Y), (h, H), (dx, DX), (s, S), (q.view(torch.uint8), Q.view(torch.uint8))):
+            assert torch.equal(a[~far], b[~far])
+        want, _ = ref.rms_norm(f64(X[far]), f64(w))
+        assert np.all(np.abs(f64(Y[far]) - want) <= 3 * 2.0 ** -8 * np.abs(want) + 1e-12)
+
+
+def test_rows_that_are_not_finite_or_zero_without_eps():
+    x, _, dy, _, _ = _draw(45, 8, 520, torch.float32)
+    x[1], x[2], x[5] = 0.0, 1e25 * x[2], 1e-30 * x[5]
+    x[3, 7], x[4, 9] = float("inf"), float("nan")
+    y, _ = muon.rms_norm(x, eps=0.0)
+    dx, _ = muon.rms_norm_backward(dy, x, eps=0.0)
+    assert torch.isnan(y[[1, 4]]).all() and torch.isnan(dx[[1, 4]]).all()   # 0 / 0
+    assert torch.isnan(y[3, 7]) and torch.count_nonzero(y[3]) == 1
+    rest = [0, 2, 5, 6, 7]
+    want, _ = ref.rms_norm(f64(x)[rest], eps=0.0)
+    _within(y[rest], want, kF32 * np.abs(want), "y")
+    assert torch.isfinite(dx[rest]).all()
