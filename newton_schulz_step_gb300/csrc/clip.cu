@@ -11,9 +11,9 @@
 // reads and writes that reach HBM at 6.2 TB/s); 20 M in 47 tensors: 14.8 us together, of which
 // the bytes at the copy's rate take 9.
 //
-// Squares are taken and added in fp32: a thread's sums are eight chains of at most some hundred
-// squares (past 2^128 the norm is infinite, which magnitudes below 2^58 do not reach; a magnitude
-// below 2^-75 adds nothing).
+// Squares are taken and added in fp32: a thread's sums are eight chains of at most 512 squares
+// (past 2^128 the norm is infinite, which magnitudes below 2^58 do not reach; a magnitude below
+// 2^-75 adds nothing), which are put into a total in one of two units after that many.
 #include <algorithm>
 
 #include "internal.h"
@@ -127,6 +127,10 @@ __device__ __forceinline__ const ClipTensor& tensor_of(const ClipTensor* table, 
 // or of 2^40 once a thread's exceeds 2^96: fp64 runs at a sixtieth of fp32's rate here, and adding
 // the threads' sums in it took longer than reading the gradients (40 MB: 15 us, 9 without).
 constexpr float kLarge = 0x1p96f, kUnit = 0x1p-40f;
+// Units of 8 squares a chain between which a thread's chains go into its totals: gradients of up to
+// 64 x 608 x 16384 elements (637 M) need no such step.
+constexpr int kFoldUnits = 64;
+static_assert(kFoldUnits * kVecs == 512, "squares of a chain");
 // Sum over the block, the same for every thread and run.
 __device__ __forceinline__ float block_sum(float x, float* s) {
 #pragma unroll
@@ -151,7 +155,22 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+  float plain = 0.f, scaled = 0.f;                   // totals of earlier chains, in units of 1 and 2^40
+  int units = 0;
   for (long long u = blockIdx.x; u < L.total_units; u += gridDim.x) {
+    if (units++ == kFoldUnits) {
+      units = 1;
+      bool large = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) large |= sum[j] > kLarge;
+      float t = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t += large ? sum[j] * kUnit : sum[j];
+        sum[j] = 0.f;
+      }
+      (large ? scaled : plain) += t;
+    }
     const ClipTensor& T = tensor_of(s_table, L.n_tensors, u);
     const long long base = (u - T.unit_begin) * kClipUnit;
     if (base + kClipUnit <= T.n) {
@@ -182,11 +201,11 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
       }
     }
   }
-  bool over = false;
+  bool over = plain > kLarge || scaled != 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) over |= sum[j] > kLarge;
   const int large = __syncthreads_or(over);
-  float total = 0.f;
+  float total = large ? fmaf(plain, kUnit, scaled) : plain;
 #pragma unroll
   for (int j = 0; j < 8; ++j) total += large ? sum[j] * kUnit : sum[j];
   total = block_sum(total, s_sum);

@@ -199,3 +199,22 @@ def test_an_infinite_max_norm_is_factor_one_whatever_the_norm(value):
     muon.clip_grad_norm(grads, math.inf, outs=outs)
     for o, b in zip(outs, before):
         assert torch.equal(o.nan_to_num(nan=7.0), b.to(o.dtype).nan_to_num(nan=7.0))
+
+
+def test_magnitudes_below_2_58_of_more_elements_than_a_chain_takes():
+    # 6e9 of 1.875 2^57: the sum of squares passes 2^128 thousands of times, and a thread's share of
+    # them (4800 squares a chain, unless they are cut) passes it as well
+    n = 6_000_000_007
+    g = torch.full((n,), 1.875 * 2.0 ** 57, dtype=B, device=DEV)
+    small = torch.full((1000,), 3.0, device=DEV)
+    want = 1.875 * 2.0 ** 57 * math.sqrt(n)
+    assert abs(float(muon.grad_norm([g, small])) / want - 1) <= kNorm
+    # sums in units of 1: chains that are cut, ordinary values
+    g.fill_(0.0078125)
+    g[:n // 2].fill_(2.0)
+    want = math.sqrt(4.0 * (n // 2) + 0.0078125 ** 2 * (n - n // 2) + 9000)
+    assert abs(float(muon.grad_norm([g, small])) / want - 1) <= kNorm
+    # both: most threads' sums stay small, some do not
+    g[n - 100_000:] = 2.0 ** 56
+    want = math.sqrt(want * want + 100_000 * 2.0 ** 112)
+    assert abs(float(muon.grad_norm([small, g])) / want - 1) <= kNorm
