@@ -246,7 +246,7 @@ muon_status muon_qk_norm_rope_backward(const muon_norm_rope* spec, muon_heads dq
     L.status = static_cast<const unsigned int*>(workspace);
     L.ticket = static_cast<unsigned int*>(workspace) + 16;
     L.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(workspace);
     const cudaError_t e =
         counted_launch(st, MUON_K_NORM_ROPE_BWD, 0.0, rope_bytes(L, L.norm ? 3 : 2),
                        [&] { return launch_norm_rope(L, true, sms, st); });
@@ -347,7 +347,7 @@ muon_status muon_attention_backward(const muon_attention_spec* spec, muon_heads 
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double row = 2.0 * L.T * L.dim;
     // (dk, dv reads what dq leaves in the workspace)
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(workspace);
     cudaError_t e = counted_launch(
         st, MUON_K_ATTENTION_DQ, 6.0 * L.dim * pair_bound(L), row * (4.0 * L.hq + 2.0 * L.hk),
         [&] { return launch_attention_dq(M, L, st); });

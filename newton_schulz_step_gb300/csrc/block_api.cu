@@ -211,7 +211,7 @@ muon_status muon_rms_norm_backward(const muon_rms_norm_spec* spec, muon_matrix d
     L.status = static_cast<const unsigned int*>(workspace);
     if (dweight)
       L.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(dweight ? workspace : nullptr);
     cudaError_t e = counted_launch(
         st, MUON_K_RMS_NORM_BWD, 0.0, 1.0 * t * d * size * (has_res ? 4.0 : 3.0),
         [&] { return launch_rms_norm_backward(L, spec->dtype == MUON_BF16, st); });
@@ -307,7 +307,7 @@ muon_status muon_embedding_backward(const muon_embedding_spec* spec, int dout_dt
       p += 2 * list;
     }
     L.parts = reinterpret_cast<float*>(p);
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(workspace);
     cudaError_t e = counted_launch(st, MUON_K_EMBEDDING_SORT, 0.0,
                                    1.0 * spec->rows * d * size + 16.0 * t,
                                    [&] { return launch_embedding_sort(L, sms, st); });
@@ -397,7 +397,7 @@ muon_status muon_clip_grad_norm(const muon_grad_tensor* tensors, int n_tensors, 
       }
       return j;
     };
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(workspace);
     cudaError_t e = cudaSuccess;
     int i = 0, launches = 0;
     do {

@@ -282,7 +282,7 @@ muon_status muon_linear(const muon_linear_spec* spec, muon_matrix x, muon_matrix
         (has_res && !matrix_tmap(&M.res[0], residual, t, n, 64, 32)) ||
         (has_z && !matrix_tmap(&M.z[0], preact, t, n, 64, 32)))
       return MUON_ERR_CUDA;
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const WorkspaceTurn turn(P.splits > 1 ? workspace : nullptr);
     cudaError_t e = counted_launch(st, MUON_K_LINEAR, flops, bytes,
                                    [&] { return launch_linear(M, L, sms, st); });
     if (e == cudaSuccess && P.splits > 1)
@@ -381,7 +381,8 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
       L.db_n = n;
       L.db_chunks = cdiv(t, chunk);
     }
-    std::lock_guard<std::mutex> lk(g_workspace_mu);
+    const bool finish = dbias || plan.splits[0] > 1 || plan.splits[1] > 1;
+    const WorkspaceTurn turn(finish ? workspace : nullptr);
     cudaError_t e = cudaSuccess;
     if (act || dbias)
       e = counted_launch(st, MUON_K_LINEAR_DZ, 0.0, 2.0 * t * n * (act ? 3 : 1),
@@ -390,7 +391,7 @@ muon_status muon_linear_backward(const muon_linear_spec* spec, muon_matrix dout,
       e = counted_launch(st, MUON_K_LINEAR, 4.0 * t * k * n,
                          2.0 * (2.0 * t * n + 2.0 * t * k + 2.0 * n * k),
                          [&] { return launch_linear(M, L, sms, st); });
-    if (e == cudaSuccess && (dbias || plan.splits[0] > 1 || plan.splits[1] > 1))
+    if (e == cudaSuccess && finish)
       e = counted_launch(st, MUON_K_LINEAR_FINISH, 0.0,
                          static_cast<double>(plan.parts[0] + plan.parts[1]),
                          [&] { return launch_linear_finish(L, st); });

@@ -4,9 +4,9 @@
 
 #include <algorithm>
 #include <initializer_list>
-#include <mutex>
 
 #include "internal.h"
+#include "workspace_turn.h"
 
 namespace muon {
 
@@ -17,11 +17,6 @@ inline muon_status check_workspace(const void* ws, size_t have, size_t need) {
     return MUON_ERR_WORKSPACE;
   return MUON_OK;
 }
-
-// Held while the launches of one call are enqueued that leave something in its workspace: a later
-// launch of the call reads it, and calls of every kind share the workspace that the binding keeps
-// for a stream, so that no other thread's launches may come between.
-inline std::mutex g_workspace_mu;
 
 // Bytes that a call reads or writes: `len` at every (token, head).
 struct Rows {
