@@ -904,9 +904,10 @@ def linear(x, weight, *, bias=None, activation: str | None = None, residual=None
     their rows, in 16-byte steps).  activation: None, "relu2" (max(z, 0)^2) or "gelu" (its tanh
     form).  Sums in fp32, one rounding to bf16.  Returns out; with save_preact (out, preact), where
     preact is z = x weight^T + bias for linear_backward (an argument of that name is the tensor to
-    fill, and asks for it too).  out may be the residual itself.  Nothing is recorded for autograd:
-    tensors that require grad are refused while it records, see linear_backward.  The workspace is
-    as for attention."""
+    fill, and asks for it too).  The rows of new outputs are padded to 16 bytes where out_features
+    is no multiple of 8: views [:, :out_features] of wider tensors.  out may be the residual itself.
+    Nothing is recorded for autograd: tensors that require grad are refused while it records, see
+    linear_backward.  The workspace is as for attention."""
     L = _lib or load_library()
     spec, vx, vw = _linear_spec(x, weight, activation, bias)
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (
@@ -944,7 +945,9 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
                     stream=None):
     """Gradients of linear: from dout [tokens, out_features], its x and weight, and with an
     activation the preact that it saved, returns (dx, dweight, dbias) in bf16; dbias is None
-    unless `bias`.  The residual's gradient is dout.  Outputs overlap no input."""
+    unless `bias`.  The residual's gradient is dout.  Outputs overlap no input.  A new dweight is
+    contiguous, as clip_grad_norm and the optimizers take it (where in_features is no multiple of 8
+    that is a copy of it more); the rows of a new dx are padded to 16 bytes, as linear's are."""
     L = _lib or load_library()
     spec, vx, vw = _linear_spec(x, weight, activation, None)
     index, bf16 = x.get_device(), torch.bfloat16
@@ -964,7 +967,8 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
         dx, vdx = _new_matrix((t, k), bf16, device)
     else:
         vdx = _matrix(dx, "dx", (t, k), bf16, index)
-    if dweight is None:
+    own_dweight = dweight is None
+    if own_dweight:
         dweight, vdw = _new_matrix((n, k), bf16, device)
     else:
         vdw = _matrix(dweight, "dweight", (n, k), bf16, index)
@@ -975,6 +979,8 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
     _raise(L.muon_linear_backward(spec, vg, vx, vw, vz, vdz, vdx, vdw,
                                   None if dbias is None else dbias.data_ptr(), ws, ws_bytes,
                                   handle), "muon_linear_backward")
+    if own_dweight and k % 8:
+        dweight = dweight.contiguous()
     return dx, dweight, dbias
 
 

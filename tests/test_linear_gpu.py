@@ -396,3 +396,22 @@ def test_offsets_past_32_bits(t, k, n):
     got = muon.linear_backward(DY, X, W, bias=True, activation="gelu", preact=Z, dx=DX, dweight=DW)
     assert torch.equal(O, want[0]) and torch.equal(Z, want[1])
     assert all(torch.equal(a, c) for a, c in zip(got, wg))
+
+
+@pytest.mark.parametrize("t", [0, 3, 300])
+@pytest.mark.parametrize("k", [13, 130, 136])
+def test_weight_gradients_of_any_width_go_to_clipping_and_the_optimizers(t, k):
+    x, w, b, r, dy = _draw(50, t, k, 77)
+    given = torch.full((77, (k + 7) // 8 * 8), 5.0, dtype=torch.bfloat16, device=DEV)[:, :k]
+    _, want, _ = muon.linear_backward(dy, x, w, dweight=given)
+    assert want is given
+    _, dw, db = muon.linear_backward(dy, x, w, bias=True)
+    assert dw.is_contiguous() and torch.equal(dw, want)
+    norm = float(muon.clip_grad_norm([dw, db], 1.0))
+    sq = f64(want) ** 2
+    assert abs(norm - np.sqrt(sq.sum() + (f64(dy).sum(0) ** 2).sum())) <= 2.0 ** -7 * norm + 1e-6
+    p, m = (torch.zeros(77, k, device=DEV) for _ in range(2))
+    muon.step(p, dw, m, momentum=0.9, lr=0.02, weight_decay=0.0)
+    muon.adam_step([(p, dw, m, torch.zeros_like(p))], 1)
+    torch.cuda.synchronize()
+    assert torch.isfinite(p).all()
