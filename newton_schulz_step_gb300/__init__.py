@@ -853,6 +853,22 @@ def _matrix(t, name: str, shape, dtype, index) -> _Matrix:
     _refuse_matrix(t, name, shape, dtype, index)
 
 
+def _aligned(v: _Matrix, rows: int) -> bool:
+    """Whether the rows of a bf16 matrix begin on 16 bytes."""
+    return not (v.row_stride & 7 and rows > 1 or (v.data or 0) & 15)
+
+
+def _raise_rows(code: int, where: str, **views):
+    """_raise, which says of bf16 matrices (view, rows) whether one is refused for its rows."""
+    if code == 1:
+        for name, (v, rows) in views.items():
+            if not _aligned(v, rows):
+                raise MuonError(code, f"{where}: the rows of {name} must begin on 16 bytes (address "
+                                      f"{v.data or 0:#x}, row stride {v.row_stride} elements): copy "
+                                      "it into a tensor whose width is a multiple of 8")
+    _raise(code, where)
+
+
 def _check_sizes(bits, *sizes):
     """bits: the sizes' OR.  ctypes would cut a size of more than 31 bits without a word."""
     if bits >> 31:
@@ -936,7 +952,11 @@ def linear(x, weight, *, bias=None, activation: str | None = None, residual=None
     ws, ws_bytes, _owner = _stream_workspace(
         workspace, linear_workspace_bytes(spec.tokens, spec.in_features, spec.out_features), index,
         handle)
-    _raise(L.muon_linear(spec, vx, vw, vr, vz, vo, ws, ws_bytes, handle), "muon_linear")
+    code = L.muon_linear(spec, vx, vw, vr, vz, vo, ws, ws_bytes, handle)
+    if code:
+        t = spec.tokens
+        _raise_rows(code, "muon_linear", x=(vx, t), weight=(vw, spec.out_features),
+                    residual=(vr, t), preact=(vz, t), out=(vo, t))
     return out if preact is None else (out, preact)
 
 
@@ -947,7 +967,9 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
     activation the preact that it saved, returns (dx, dweight, dbias) in bf16; dbias is None
     unless `bias`.  The residual's gradient is dout.  Outputs overlap no input.  A new dweight is
     contiguous, as clip_grad_norm and the optimizers take it (where in_features is no multiple of 8
-    that is a copy of it more); the rows of a new dx are padded to 16 bytes, as linear's are."""
+    that is a copy of it more); the rows of a new dx are padded to 16 bytes, as linear's are.  dout's
+    rows may lie anywhere (the gradient of padded logits comes out of torch without the padding):
+    those that do not begin on 16 bytes are copied first, one pass over them."""
     L = _lib or load_library()
     spec, vx, vw = _linear_spec(x, weight, activation, None)
     index, bf16 = x.get_device(), torch.bfloat16
@@ -957,6 +979,9 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
                                    preact=preact, dx=dx, dweight=dweight, workspace=workspace)
     t, k, n, device = spec.tokens, spec.in_features, spec.out_features, x.device
     vg = _matrix(dout, "dout", (t, n), bf16, index)
+    if not _aligned(vg, t):
+        own, vg = _new_matrix((t, n), bf16, device)
+        own.copy_(dout.detach())
     vz = vdz = _NO_MATRIX
     if activation is not None:
         if preact is None:
@@ -976,9 +1001,11 @@ def linear_backward(dout, x, weight, *, bias: bool = False, activation: str | No
     handle = _current_handle(index)
     ws, ws_bytes, _owner = _stream_workspace(workspace, linear_workspace_bytes(t, k, n), index,
                                              handle)
-    _raise(L.muon_linear_backward(spec, vg, vx, vw, vz, vdz, vdx, vdw,
-                                  None if dbias is None else dbias.data_ptr(), ws, ws_bytes,
-                                  handle), "muon_linear_backward")
+    code = L.muon_linear_backward(spec, vg, vx, vw, vz, vdz, vdx, vdw,
+                                  None if dbias is None else dbias.data_ptr(), ws, ws_bytes, handle)
+    if code:
+        _raise_rows(code, "muon_linear_backward", x=(vx, t), weight=(vw, n), preact=(vz, t),
+                    dx=(vdx, t), dweight=(vdw, n))
     if own_dweight and k % 8:
         dweight = dweight.contiguous()
     return dx, dweight, dbias

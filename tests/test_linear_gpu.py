@@ -415,3 +415,57 @@ def test_weight_gradients_of_any_width_go_to_clipping_and_the_optimizers(t, k):
     muon.adam_step([(p, dw, m, torch.zeros_like(p))], 1)
     torch.cuda.synchronize()
     assert torch.isfinite(p).all()
+
+
+@pytest.mark.parametrize("t", [1, 3, 300])
+@pytest.mark.parametrize("kind", [None, "gelu"])
+def test_gradients_of_rows_that_begin_anywhere(t, kind):
+    x, w, b, r, dy = _draw(51, t, 136, 257)
+    y, z = muon.linear(x, w, bias=b, activation=kind, save_preact=True)
+    assert y.stride() == (264, 1)
+    z = z if kind else None
+    want = muon.linear_backward(dy, x, w, bias=True, activation=kind, preact=z)
+    wide = torch.full((t, 261), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, 3:260] = dy
+    for rows in (dy.contiguous(), wide[:, 3:260]):     # odd strides; an odd address
+        got = muon.linear_backward(rows, x, w, bias=True, activation=kind, preact=z)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    rows = dy.contiguous()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = muon.linear_backward(rows, x, w, bias=True, activation=kind, preact=z)
+    for v in got:
+        v.fill_(3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_an_output_head_whose_width_is_odd():
+    # logits, the gradient as torch makes it of them, and the head's gradients
+    t, d, n = 200, 72, 1001
+    x, w, _, _, _ = _draw(52, t, d, n, bias=False, residual=False)
+    targets = torch.randint(0, n, (t,), generator=torch.Generator().manual_seed(1)).to(DEV)
+    logits = muon.linear(x, w)
+    g = torch.softmax(logits.float(), 1)
+    g[torch.arange(t, device=DEV), targets] -= 1
+    g = (g / t).bfloat16()
+    assert g.stride() == (n, 1)
+    dx, dw, _ = muon.linear_backward(g, x, w)
+    _check_backward(g, x, w, None, None, False, (dx, dw, None))
+    muon.clip_grad_norm([dw], 1.0)
+
+
+def test_refused_rows_are_named():
+    x, w, b, r, dy = _draw(53, 20, 130, 77, pad=None)
+    for kw, name in ((dict(residual=r.contiguous()), "residual"),
+                     (dict(out=torch.empty(20, 77, dtype=x.dtype, device=DEV)), "out")):
+        with pytest.raises(muon.MuonError, match=f"rows of {name} "):
+            muon.linear(x, w, **kw)
+    with pytest.raises(muon.MuonError, match="rows of weight "):
+        muon.linear(x, w.contiguous())
+    with pytest.raises(muon.MuonError, match="rows of x "):
+        muon.linear_backward(dy, x.contiguous(), w)
+    with pytest.raises(muon.MuonError, match="rows of dweight "):
+        muon.linear_backward(dy, x, w, dweight=torch.empty(77, 130, dtype=x.dtype, device=DEV))
