@@ -7,8 +7,6 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
-#include <initializer_list>
-#include <mutex>
 
 #include "views.h"
 

@@ -66,7 +66,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void clear() { a = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     a = __ldg(reinterpret_cast<const uint4*>(p));
   }
@@ -74,7 +73,6 @@ template <> struct Raw<__nv_bfloat16> {
 };
 template <> struct Raw<float> {
   float4 a, b;
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void load(const float* p) {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p + 4));
