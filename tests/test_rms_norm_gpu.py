@@ -413,3 +413,27 @@ def test_rows_that_are_not_finite_or_zero_without_eps():
     want, _ = ref.rms_norm(f64(x)[rest], eps=0.0)
     _within(y[rest], want, kF32 * np.abs(want), "y")
     assert torch.isfinite(dx[rest]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 520, 4104])
+def test_rows_of_any_magnitude_in_place(d, dtype):
+    x, r, dy, dr, w = _draw(47, 3000, d, torch.float32)
+    m = torch.ones(3000, 1, device=DEV)
+    m[::7], m[3::50] = 1e22, 1e-24
+    x, r, dy, dr = (v.to(dtype) for v in (m * x, m * r, m * dy, dr))
+    y, h = muon.rms_norm(x, w, residual=r, eps=0.0)
+    dx, dw = muon.rms_norm_backward(dy, h, w, dresidual=dr, eps=0.0)
+    q, s, _ = muon.rms_norm_fp8(x, w, residual=r, eps=0.0)
+    assert torch.isfinite(y).all() and torch.isfinite(dx).all()
+    for over in range(3):
+        c = [dy.clone(), h.clone(), dr.clone()]
+        got = muon.rms_norm_backward(c[0], c[1], w, dresidual=c[2], eps=0.0, dx=c[over])
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+    for over in range(2):
+        c = [x.clone(), r.clone()]
+        got = muon.rms_norm_fp8(c[0], w, residual=c[1], eps=0.0, residual_out=c[over])
+        assert torch.equal(got[0].view(torch.uint8), q.view(torch.uint8))
+        assert torch.equal(got[1], s) and torch.equal(got[2], h)
+    assert all(torch.equal(a, b) for a, b in zip(
+        muon.rms_norm_backward(dy, h, w, dresidual=dr, eps=0.0), (dx, dw)))   # the same bits again
