@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_squares_kernel(const __grid_
   }
 }
 
+// (64 registers, for four blocks an SM; the bf16 form spills 32 bytes for it.)
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant__ ClipLaunch L) {
   __shared__ float s_sum[kThreads / 32];

@@ -24,10 +24,10 @@
 // epilogue, so the result does not depend on which split came first.  dx and dW go in one
 // launch (two problems): neither fills the card by itself where matrices are small.
 //
-// What bounds it: the tensor cores.  16384 x 4096 x 4096 takes 291 us (1890 TFLOP/s), a
-// library product 282; 8192 x 2048 x 8192 156 and 150; 8192 x 11008 x 4096 back to back, under
-// the power cap, 377 and 370; dx and dW of 8192 x 2048 x 8192 305 us, 88 % of the tensor
-// pipe's cycles.  (Sizes: tokens, width in, width out.)  The steps on the way, first size:
+// What bounds it: the tensor cores.  16384 x 4096 x 4096 takes 290 us (1896 TFLOP/s), a
+// library product 275; 8192 x 2048 x 8192 151 and 139; 8192 x 11008 x 4096 387 and 382, back to
+// back under the power limit 446 and 444; dx and dW of 8192 x 2048 x 8192 293 us, 88 % of the
+// tensor pipe's cycles.  (Sizes: tokens, width in, width out.)  The steps on the way, first size:
 //   copies issued from a branch on a lane index took 600 clocks a step of 512 clocks of
 //   products, whatever the ring's depth (4 to 6 stages), the order of the tiles or the L2
 //   hints; issued by an elected lane of a warp in step: 356 -> 308 us;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const __grid_constan
 // dz over the rows of a chunk.  Bound by HBM: 8192 x 8192 (403 MB) takes 66 us, 6.1 TB/s.
 // (z comes in as it was stored, in bf16: its half step and dz's each add as much to a
 // gradient's error as the gradient's own rounding.  fp32 would double the largest activation
-// that a training step keeps.)  A block takes 256 columns (8 a lane) and a chunk of rows,
+// that a training step keeps.  relu^2's z could be had from its output at half that rounding.)  A block takes 256 columns (8 a lane) and a chunk of rows,
 // a warp every eighth row of it; the chunks are added by linear_finish_kernel.
 constexpr int kDzRows = 4;                  // rows of a warp in flight
 __global__ void __launch_bounds__(256) linear_dz_kernel(const __grid_constant__ LinearDz D) {

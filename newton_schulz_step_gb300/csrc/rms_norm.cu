@@ -13,9 +13,9 @@
 // travel while the row before is summed.  A power of two as the scale makes the division
 // exact: the only rounding is e4m3's own, and the values that q stands for are exact in bf16.
 //
-// 16384 tokens of 2048 (bf16, with residual): forward 41.4 us (6.5 TB/s, 96 % of the copy's
-// rate), gradients 49.0 (5.5 TB/s, the sum of the weight's parts among it); of 4096 in 8 bits
-// 75.5 us (6.2 TB/s).  Blocks of 32 resident warps an SM forward (64 registers) gained 3 to 9 %
+// 16384 tokens of 2048 (bf16, with residual): forward 41.8 us (6.4 TB/s, 95 % of the copy's
+// rate), gradients 49.2 (5.5 TB/s, the sum of the weight's parts among it); of 4096 in 8 bits
+// 75.9 us (6.2 TB/s).  Blocks of 32 resident warps an SM forward (64 registers) gained 3 to 9 %
 // over 24; the gradients keep 16, their columns' sums of the weight take the registers.
 #include <algorithm>
 
@@ -185,7 +185,7 @@ enum Mode { kForward, kEightBits };
 // larger of the row's largest magnitude and eps^1/2 to [1, 4), so that nothing that counts leaves
 // the range.  A row with an element that is not finite keeps s = 1.
 // A team does its rows of that kind after the others, from memory, two or three times over; its loop
-// pays a comparison: 16384 rows of 2048 take 41.8 us forward (41.7 without), 49.4 (48.9) backward,
+// pays a comparison: 16384 rows of 2048 take 41.8 us forward (41.6 without), 49.2 (48.8) backward,
 // with 8 bits and no residual 26.7 (26.0), rows of 64 up to 4 % more.  (With the row scaled inside the
 // loop, in registers, calls took up to a third longer.)  With a residual such a row's y is that of h
 // as stored, one rounding more than in other rows: the sum may lie over what it was made of.
@@ -497,6 +497,8 @@ __global__ void __launch_bounds__(kMaxTeam, sizeof(T) == 2 ? 2 : 1) rms_norm_ker
   }
 }
 
+// (Four vectors a thread spill, 56 bytes in bf16 and 248 in fp32, and have no row ahead: rows of 8192
+// move at 4.7 TB/s, of 16384 at 3.2.)
 // dx and a block's part of dw.  The team of a row keeps its columns' sums of dy h r; the
 // teams' sums are added in order, and rms_norm_weight_kernel adds the blocks'.
 template <typename T, int kV>
