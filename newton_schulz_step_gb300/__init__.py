@@ -1051,8 +1051,8 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = NORM_EPS, out=None,
     (bf16 or fp32, strided along the tokens; dim a multiple of 8 up to 16384), times weight ([dim]
     fp32).  Returns (out, h): h, rounded to x's type, is the next residual and what
     rms_norm_backward takes; without a residual it is x itself.  out and residual_out (h's tensor)
-    may each be x or residual.  Finite rows of any magnitude are right.  Nothing is recorded for autograd: tensors that require grad are
-    refused while it records, see rms_norm_backward."""
+    may each be x or residual.  Finite rows of any magnitude are right.  Nothing is recorded for
+    autograd: tensors that require grad are refused while it records, see rms_norm_backward."""
     L = _lib or load_library()
     spec, vx = _norm_spec(x, "x", weight, eps)
     _refuse_norm_grad("rms_norm", x, weight, residual)
