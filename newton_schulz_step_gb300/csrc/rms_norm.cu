@@ -264,7 +264,7 @@ __device__ __forceinline__ void far_rows(const RmsNormLaunch& L, int row) {
       const float mean = fmaf(ss, 1.f / static_cast<float>(L.dim), L.eps * s * s);
       r = rsqrtf(mean);
       if (pass == 0) {
-        near = mean > 2.f * kLeastMean && mean < 0x1p126f;
+        near = mean > 2.f * kLeastMean && mean < 0x1p126f && ss < 0x1p126f;
         if (near) break;
         s = row_scale(team.max1(top), L.eps);
       }

@@ -437,3 +437,25 @@ def test_rows_of_any_magnitude_in_place(d, dtype):
         assert torch.equal(got[1], s) and torch.equal(got[2], h)
     assert all(torch.equal(a, b) for a, b in zip(
         muon.rms_norm_backward(dy, h, w, dresidual=dr, eps=0.0), (dx, dw)))   # the same bits again
+
+
+@pytest.mark.parametrize("d", [64, 1024])
+def test_a_sum_of_squares_that_leaves_the_range_by_its_rounding(d):
+    # In units of u = 2^122 (d = 64): 63 elements of (1 - 0.55 2^-8)^2 u and one of 1.34 u are past 64 u =
+    # 2^128; stored, the 63 are (1 - 2^-8)^2 u, and the sum is below it.  (d = 1024: u = 2^118.)
+    scale = 2.0 ** (61 if d == 64 else 59)
+    x = torch.full((5, d), (1 - 2.0 ** -8) * scale).bfloat16()
+    r = torch.full((5, d), 0.45 * 2.0 ** -8 * scale).bfloat16()
+    x[:, ::64], r[:, ::64] = 1.15625 * scale, 0.0
+    wide, stored = x.double() + r.double(), (x.float() + r.float()).bfloat16().double()
+    assert torch.all(wide.square().sum(1) > 2.0 ** 128)
+    assert torch.all(stored.square().sum(1) < 2.0 ** 128)
+    x, r = x.to(DEV), r.to(DEV)
+    y, h = muon.rms_norm(x, residual=r)
+    assert torch.equal(h.double().cpu(), stored)
+    want, _ = ref.rms_norm(f64(x), None, f64(r))
+    assert np.all(np.abs(f64(y) - want) <= 3 * kBf16 * np.abs(want))
+    for group in (0, 128):
+        q, s, _ = muon.rms_norm_fp8(x, residual=r, group=group)
+        values = f64(q.float()) * ref.spread(f64(s), d, group)
+        assert np.all(np.abs(values - want) <= (2.0 ** -4 + 3 * kBf16) * np.abs(want))
