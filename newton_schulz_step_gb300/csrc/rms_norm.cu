@@ -179,7 +179,7 @@ struct Weights {
 enum Mode { kForward, kEightBits };
 
 // ------------------------------------------------------------ rows whose squares leave the range
-// A row whose mean square and eps together lie outside of [2^-40, fp32's largest) is scaled by a
+// A row whose mean square and eps together lie outside of [2^-38, 2^112) may be scaled by a
 // power of two before its squares are summed: past 2^128 their sum would make every element 0, and
 // below 2^-126 squares lose bits or vanish (where eps does not cover them).  The scale s brings the
 // larger of the row's largest magnitude and eps^1/2 to [1, 4), so that nothing that counts leaves
@@ -190,9 +190,16 @@ enum Mode { kForward, kEightBits };
 // loop, in registers, calls took up to a third longer.)  With a residual such a row's y is that of h
 // as stored, one rounding more than in other rows: the sum may lie over what it was made of.
 // All threads of a team go or none: it goes by the team's sum.
-constexpr float kLeastMean = 0x1p-40f;
+// The scale is taken outside of twice that range, by h as stored, which rounding has moved less: so
+// it is by the row alone, and not by its neighbours, whether its y comes from the loop.  (The sum of
+// 16384 squares is below 2^127 while their mean is below 2^113.)
+constexpr float kLeastMean = 0x1p-38f, kMostMean = 0x1p112f;
+static_assert(kRmsNormMaxDim <= 1 << 14, "sums of squares of rows in range");
 __device__ __forceinline__ bool in_range(float mean) {
-  return mean >= kLeastMean && mean < __int_as_float(0x7f800000);
+  return mean >= kLeastMean && mean < kMostMean;
+}
+__device__ __forceinline__ bool near_range(float mean) {
+  return mean > 0.5f * kLeastMean && mean < 2.f * kMostMean;
 }
 // s for the row's largest magnitude as bits.
 __device__ __forceinline__ float row_scale(uint32_t top, float eps) {
@@ -228,8 +235,8 @@ __device__ __forceinline__ Team new_team(const RmsNormLaunch& L, float* sums) {
   return team;
 }
 
-// The team's rows forward: of all of them (kSome) those that are out of range or close to it (the
-// rounding of a sum may have moved it), or every row from `row` on.
+// The team's rows forward: of all of them (kSome) those that take the scale, or every row from `row`
+// on (those that take none get the bits that the loop would give).
 template <typename T, Mode kMode, bool kRes, bool kSome>
 __device__ __forceinline__ void far_rows(const RmsNormLaunch& L, int row) {
   __shared__ float s_sums[kMaxTeam / 32 * 4];
@@ -264,7 +271,7 @@ __device__ __forceinline__ void far_rows(const RmsNormLaunch& L, int row) {
       const float mean = fmaf(ss, 1.f / static_cast<float>(L.dim), L.eps * s * s);
       r = rsqrtf(mean);
       if (pass == 0) {
-        near = mean > 2.f * kLeastMean && mean < 0x1p126f && ss < 0x1p126f;
+        near = near_range(mean);
         if (near) break;
         s = row_scale(team.max1(top), L.eps);
       }

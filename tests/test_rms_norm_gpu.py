@@ -459,3 +459,32 @@ def test_a_sum_of_squares_that_leaves_the_range_by_its_rounding(d):
         q, s, _ = muon.rms_norm_fp8(x, residual=r, group=group)
         values = f64(q.float()) * ref.spread(f64(s), d, group)
         assert np.all(np.abs(values - want) <= (2.0 ** -4 + 3 * kBf16) * np.abs(want))
+
+
+@pytest.mark.parametrize("with_r", [False, True])
+def test_rows_at_the_ends_of_the_range_do_not_go_by_their_neighbours(with_r):
+    t, d = 20000, 264
+    x, r, _, _, w = _draw(48, t, d, torch.float32)
+    k = torch.arange(t, device=DEV) % 60
+    m = torch.exp2(torch.where(k < 30, -22 + k / 6, 54 + (k - 30) / 6).double())[:, None]
+    x, r = ((m * v.double() / 4).bfloat16() for v in (x, r))
+    r = r if with_r else None
+    far = torch.arange(t, device=DEV) % 97 == 5
+    X = x.clone()
+    X[far] = 1e25
+    for group in (None, 0, 128):
+        def call(v):
+            if group is None:
+                y, h = muon.rms_norm(v, w, residual=r, eps=0.0)
+                return y.view(torch.int16), h
+            q, s, h = muon.rms_norm_fp8(v, w, residual=r, eps=0.0, group=group)
+            return q.view(torch.uint8), s, h
+        for a, b in zip(call(x), call(X)):
+            assert torch.equal(a[~far], b[~far])
+    y, _ = muon.rms_norm(x, w, residual=r, eps=0.0)
+    want, _ = ref.rms_norm(f64(x), f64(w), None if r is None else f64(r), 0.0)
+    s = np.abs(f64(x)) + (0 if r is None else np.abs(f64(r)))
+    total = f64(x) + (0 if r is None else f64(r))
+    rms = np.sqrt(np.mean(total ** 2, axis=1, keepdims=True))
+    e = kF32 * (np.abs(want) + s / rms * np.abs(f64(w))) + (2 * kBf16 * np.abs(want) if with_r else 0)
+    _within(y, want, e + kBf16 * (np.abs(want) + e), "y")
