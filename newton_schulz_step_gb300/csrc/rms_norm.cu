@@ -381,6 +381,8 @@ __device__ __noinline__ void far_rows_backward(const RmsNormLaunch& L, int row, 
   }
 }
 
+// (Two blocks of 512, or four of 256, an SM: 64 registers.  Two bf16 vectors a thread with residual
+// spill 4 bytes for it, and 16 with 8 bits.)
 template <typename T, Mode kMode, int kV, bool kRes>
 __global__ void __launch_bounds__(kMaxTeam, sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(const __grid_constant__ RmsNormLaunch L) {
   constexpr bool kAhead = kV <= 2;     // a row ahead in registers
